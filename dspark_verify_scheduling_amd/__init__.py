@@ -20,7 +20,7 @@ import torch
 from . import _lib
 from ._lib import (
     BF16, COST_ADDITIVE, COST_SPS1D, DATA_BAD_CONF, DATA_BAD_COST, DATA_BAD_LENS,
-    DATA_BAD_LOGITS, F32, IN_COND,
+    DATA_BAD_LOGITS, DATA_BAD_PAGE, DATA_BAD_POS, DATA_BAD_TREE, E4M3, F16, F32, IN_COND,
     IN_CONF_LOGITS,
     IN_SURVIVAL, MAX_BATCH, MAX_CANDIDATES, MAX_GAMMA, MAX_TIERS, MAX_VOCAB, DsparkError,
 )
@@ -34,6 +34,10 @@ __all__ = [
     "IN_SURVIVAL", "DATA_BAD_COST", "DATA_BAD_CONF", "DATA_BAD_LENS", "DATA_BAD_LOGITS",
     "dspark_accept_sampling", "dspark_accept_sampling_workspace_size",
     "alloc_sampling_outputs",
+    "F16", "E4M3", "DATA_BAD_TREE", "DATA_BAD_PAGE", "DATA_BAD_POS", "KvCache", "alloc_kv_cache",
+    "dspark_kv_append", "alloc_append_outputs", "dspark_kv_read", "alloc_kv_read_outputs",
+    "dspark_tree_attention", "dspark_tree_attention_workspace_size", "alloc_attention_outputs",
+    "dspark_tree_accept", "alloc_tree_accept_outputs", "dspark_kv_commit",
 ]
 
 
@@ -594,3 +598,12 @@ def dspark_tv_accept(B: int, gamma: int, V: int, dt: int, draft_logits: torch.Te
     )
     _lib.check("dspark_tv_accept", _lib.lib().dspark_tv_accept(*args))
     return accept_rate, survival
+
+
+# the target pass (after the helpers above, which it shares)
+from .target import (  # noqa: E402
+    AppendOutputs, AttentionOutputs, KvCache, KvReadOutputs, TreeAcceptOutputs,
+    alloc_append_outputs, alloc_attention_outputs, alloc_kv_cache, alloc_kv_read_outputs,
+    alloc_tree_accept_outputs, dspark_kv_append, dspark_kv_commit, dspark_kv_read,
+    dspark_tree_accept, dspark_tree_attention, dspark_tree_attention_workspace_size,
+)

@@ -22,7 +22,8 @@ LIB = PKG / "libdspark.so"
 HOSTCHECK = PKG / "libdspark_hostcheck.so"
 ARCH = "gfx950"
 
-LIB_SOURCES = ["api.hip", "plan.hip", "pack.hip", "accept.hip", "tv.hip", "scatter.hip", "sts.hip", "sampling.hip"]
+LIB_SOURCES = ["api.hip", "plan.hip", "pack.hip", "accept.hip", "tv.hip", "scatter.hip", "sts.hip", "sampling.hip",
+               "api_target.hip", "kv_cache.hip", "tree_attention.hip"]
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}",

@@ -38,6 +38,14 @@
 // over all gamma drafts (the ceiling), then clipped to verify_len - 1, which
 // commits what compact mode commits.
 //
+// Tree accept runs the same argmax pass and accept_tree_kernel in place of the
+// finalize kernel: one wave per request, lane l holding row l + 1's parent and
+// draft token, walks from the root. A step is one LDS read (the prediction of
+// the present row), one ballot over the children that match it and a bit
+// scan, at most gamma of them; rows come after their parents, so the walk
+// ascends and ends. It is bound by the two dependent read rounds before it,
+// like the chain's finalize.
+//
 // The partials are fully rewritten by every call, so the workspace needs no
 // initialization and holds no state between calls.
 #include "argmax_unit.h"
@@ -224,6 +232,82 @@ __global__ __launch_bounds__(kWave) void accept_finalize_kernel(AcceptArgs a) {
   }
 }
 
+// One wave per request, and the grid-stride pass over every row's argmax.
+__global__ __launch_bounds__(kWave) void accept_tree_kernel(AcceptArgs a) {
+  __shared__ int am[DSPARK_MAX_GAMMA + 1];
+  const int lane = threadIdx.x;
+  const int G = a.gamma;
+  const int r = blockIdx.x;
+  const bool has_req = r < a.B;
+  const int total = a.cu[a.B];
+  int c0 = 0, end = 0, tok = 0, par = 0, prefix = 0;
+  if (has_req) {
+    c0 = a.cu[r];
+    end = a.cu[r + 1];
+    if (lane < G) {
+      tok = a.drafts[(size_t)r * G + lane];
+      par = a.parents ? a.parents[(size_t)r * G + lane] : lane;
+    }
+    prefix = a.prefix ? a.prefix[r] : 0;
+  }
+  const int total_eff = min(max(total, 0), a.max_rows);
+  const bool rows_ok = c0 >= 0 && end > c0 && end <= total_eff && end - c0 <= G + 1;
+  const int len = rows_ok ? end - c0 : 0;
+  const bool mine = lane + 1 < len;  // lane l has row l + 1
+  const bool tree_ok = __ballot(mine && (par < 0 || par > lane)) == 0;
+  const int i0 = blockIdx.x * kWave + lane;
+  int g0 = 0, m0 = 0;
+  if (total_eff > 0) {
+    const int last = total_eff - 1;
+    merge_two_rows(a, min(i0, last), min(min(max(c0, 0), last) + lane, last), g0, m0);
+  }
+  const int m1 = lane + kWave < len ? merge_row(a, c0 + lane + kWave) : 0;
+  if (i0 < total_eff) a.row_am[i0] = g0;
+  for (int i = i0 + gridDim.x * kWave; i < total_eff; i += gridDim.x * kWave) {
+    a.row_am[i] = merge_row(a, i);
+  }
+  if (!has_req) return;
+  if (lane < len) am[lane] = m0;
+  if (lane + kWave < len) am[lane + kWave] = m1;
+  __syncthreads();
+  const bool ok = rows_ok && tree_ok;
+  // what the lane's row says for column `lane` of the outputs; column G is
+  // lane 0's second one where G = 64
+  int32_t* out = a.out_tokens + (size_t)r * (G + 1);
+  int32_t* path = a.path + (size_t)r * (G + 1);
+  int c = 0, bon = -1;
+  unsigned long long on = 0;  // bit k - 1: row k is on the path
+  if (ok) {
+    int node = 0;
+    for (;;) {
+      bon = am[node];
+      const unsigned long long next = __ballot(mine && par == node && tok == bon);
+      if (!next) break;
+      const int k = (int)__builtin_ctzll(next);  // the lowest matching child
+      on |= 1ull << k;
+      node = k + 1;
+      ++c;
+    }
+  }
+  for (int j = lane; j <= G; j += kWave) {
+    out[j] = ok && j == c ? bon : -1;
+    path[j] = ok && j == 0 ? 0 : -1;
+  }
+  __syncthreads();
+  if (on >> lane & 1) {
+    const int at = (int)__popcll(on & ((1ull << lane) - 1));  // rows of the path before it
+    out[at] = tok;
+    path[at + 1] = lane + 1;
+  }
+  if (lane == 0) {
+    a.num_correct[r] = c;
+    a.bonus[r] = bon;
+    a.commit[r] = ok ? c + 1 : 0;
+    if (a.new_seq) a.new_seq[r] = ok ? prefix + c + 1 : prefix;
+    if (!ok) atomicOr(a.meta + 1, rows_ok ? DSPARK_DATA_BAD_TREE : DSPARK_DATA_BAD_LENS);
+  }
+}
+
 }  // namespace
 
 hipError_t launch_accept(const AcceptArgs& a, dspark_dtype dt, int grid, hipStream_t s) {
@@ -235,7 +319,9 @@ hipError_t launch_accept(const AcceptArgs& a, dspark_dtype dt, int grid, hipStre
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int fgrid = a.B > 0 ? a.B : 1;
-  if (a.fixed_rows >= 0) {
+  if (a.tree) {
+    hipLaunchKernelGGL(accept_tree_kernel, dim3(fgrid), dim3(kWave), 0, s, a);
+  } else if (a.fixed_rows >= 0) {
     hipLaunchKernelGGL(accept_finalize_kernel<true>, dim3(fgrid), dim3(kWave), 0, s, a);
   } else {
     hipLaunchKernelGGL(accept_finalize_kernel<false>, dim3(fgrid), dim3(kWave), 0, s, a);

@@ -9,11 +9,12 @@
 #include <algorithm>
 #include <atomic>
 
+#include "api_status.h"
 #include "common.h"
 
-namespace {
+namespace dspark {
 
-thread_local char g_last_error[512] = "";
+static thread_local char g_last_error[512] = "";
 
 dspark_status fail(dspark_status st, const char* fmt, ...) {
   va_list ap;
@@ -35,7 +36,15 @@ dspark_status launched(hipError_t e, const char* what) {
   return ok();
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace dspark
+
+using dspark::aligned16;
+using dspark::fail;
+using dspark::launched;
+using dspark::ok;
+using dspark::g_last_error;
+
+namespace {
 
 size_t elem_size(dspark_dtype dt) { return dt == DSPARK_BF16 ? 2 : 4; }
 
@@ -172,7 +181,7 @@ hipError_t current_cu_count(int* cus) {
 
 extern "C" {
 
-int32_t dspark_version(void) { return (1 << 16) | 2; }
+int32_t dspark_version(void) { return (1 << 16) | 3; }
 
 const char* dspark_status_str(dspark_status s) {
   switch (s) {
@@ -583,7 +592,8 @@ dspark_status accept_call(const char* fn, int32_t B, int32_t gamma, int32_t V, d
                           int32_t* bonus, int32_t* commit_lens, int32_t* out_tokens,
                           int32_t* new_seq_lens, uint8_t* prefix_mask, int32_t* accept_meta,
                           void* workspace, size_t workspace_bytes, bool own_scratch,
-                          void* stream) {
+                          void* stream, bool tree = false,
+                          const int32_t* tree_parents = nullptr, int32_t* path_rows = nullptr) {
   if (B < 0) return fail(DSPARK_E_INVALID, "%s: B = %d < 0", fn, B);
   if (gamma < 1 || gamma > DSPARK_MAX_GAMMA)
     return fail(DSPARK_E_INVALID, "%s: gamma = %d outside [1, %d]", fn, gamma,
@@ -605,6 +615,7 @@ dspark_status accept_call(const char* fn, int32_t B, int32_t gamma, int32_t V, d
     return fail(DSPARK_E_INVALID, "%s: cu_seqlens or accept_meta is NULL", fn);
   if (B > 0 && (!draft_tokens || !num_correct || !bonus || !commit_lens || !out_tokens))
     return fail(DSPARK_E_INVALID, "%s: a required per-request pointer is NULL", fn);
+  if (tree && B > 0 && !path_rows) return fail(DSPARK_E_INVALID, "%s: path_rows is NULL", fn);
   if (max_rows > 0 && !row_argmax)
     return fail(DSPARK_E_INVALID, "%s: row_argmax is NULL", fn);
   if (new_seq_lens && !prefix_lens)
@@ -654,6 +665,9 @@ dspark_status accept_call(const char* fn, int32_t B, int32_t gamma, int32_t V, d
   a.fixed_rows = -1;
   a.lens = nullptr;
   a.ceiling = nullptr;
+  a.tree = tree;
+  a.parents = tree_parents;
+  a.path = path_rows;
   // one workgroup per (row, unit) of the largest possible packed total; the
   // kernel reads the actual total on the device and idle workgroups exit
   const int64_t units_max = (int64_t)max_rows * g.chunks;
@@ -688,6 +702,20 @@ dspark_status dspark_accept_noalloc(int32_t B, int32_t gamma, int32_t V, dspark_
                      cu_seqlens, draft_tokens, prefix_lens, row_argmax, num_correct, bonus,
                      commit_lens, out_tokens, new_seq_lens, prefix_mask, accept_meta, nullptr, 0,
                      true, stream);
+}
+
+dspark_status dspark_tree_accept(int32_t B, int32_t gamma, int32_t V, dspark_dtype dt,
+                                 const void* packed_logits, int64_t ld, int32_t max_rows,
+                                 const int32_t* cu_seqlens, const int32_t* draft_tokens,
+                                 const int32_t* tree_parents, const int32_t* prefix_lens,
+                                 int32_t* row_argmax, int32_t* num_correct, int32_t* bonus,
+                                 int32_t* commit_lens, int32_t* out_tokens, int32_t* path_rows,
+                                 int32_t* new_seq_lens, int32_t* accept_meta, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  return accept_call("dspark_tree_accept", B, gamma, V, dt, packed_logits, ld, max_rows,
+                     cu_seqlens, draft_tokens, prefix_lens, row_argmax, num_correct, bonus,
+                     commit_lens, out_tokens, new_seq_lens, nullptr, accept_meta, workspace,
+                     workspace_bytes, false, stream, true, tree_parents, path_rows);
 }
 
 size_t dspark_accept_sampling_workspace_size(int32_t B, int32_t gamma, int32_t V, dspark_dtype dt) {

@@ -79,6 +79,10 @@ struct AcceptArgs {
   unsigned long long* partials;  // [max_rows * chunks] (key, index) per unit
   const int32_t* lens;  // cap-accept: verify_lens [B]
   int32_t* ceiling;     // cap-accept: uncapped leading matches [B]
+  // tree accept: the walk along parents ([B, gamma], null for the chain)
+  bool tree = false;
+  const int32_t* parents = nullptr;
+  int32_t* path = nullptr;  // [B, gamma + 1]
 };
 constexpr int kAccThreads = 256;
 constexpr int kAccVecsPerThread = 8;

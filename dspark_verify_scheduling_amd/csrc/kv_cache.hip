@@ -1,0 +1,502 @@
+// The paged key/value cache of the target pass: append with per-head norms and
+// rotation, read back, and the commit of an accepted path.
+//
+// All three move every byte once and compute next to nothing on it, so they
+// are bound by HBM (large calls) or by the latency of a launch and one or two
+// dependent reads (small ones). A row of one head is head_dim * 2 bytes; 16-byte
+// loads put it on head_dim / 8 lanes, so every reduction of a head (the sum of
+// squares, the largest magnitude) stays inside 8, 16 or 32 lanes.
+//
+// Status words: workgroup 0 of each launch checks every request by itself and
+// writes the status; the others repeat the checks of what they touch and leave
+// bad requests or rows out.
+#include "kv_dev.h"
+
+namespace dspark {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// ------------------------------------------------------------------ append
+
+// Status of request r, its pages and positions included; one thread.
+__device__ int append_status(const AppendArgs& a, int r, int total_eff) {
+  const ReqView& q = a.req;
+  int bits = request_status(q, r, total_eff);
+  if (bits) return bits;
+  const int len = q.cu[r + 1] - q.cu[r];
+  const int64_t lo = q.prefix[r], hi = lo + len;  // cache indices [lo, hi)
+  if (hi > ((int64_t)q.width << a.kv.page_shift)) return DSPARK_DATA_BAD_PAGE;
+  for (int64_t p = lo >> a.kv.page_shift; p <= (hi - 1) >> a.kv.page_shift; ++p) {
+    const int id = q.table[(size_t)r * q.width + p];
+    if (id < 0 || id >= a.kv.num_blocks) bits |= DSPARK_DATA_BAD_PAGE;
+  }
+  if (a.rope && hi > a.rope_rows) {
+    // a tree's depths may still be small enough
+    for (int j = 0; j < len; ++j) {
+      int depth = j;
+      if (q.parents) {
+        depth = 0;
+        for (int n = j; n > 0; n = q.parents[(size_t)r * q.gamma + n - 1]) ++depth;
+      }
+      if (lo + depth >= a.rope_rows) bits |= DSPARK_DATA_BAD_POS;
+    }
+  }
+  return bits;
+}
+
+template <typename T>
+struct Vec8;
+template <>
+struct Vec8<__bf16> { typedef bf16x8 type; };
+template <>
+struct Vec8<_Float16> { typedef f16x8 type; };
+
+// One workgroup per (request, row): LPH lanes per head take the heads of q, k
+// and v in turn.
+template <typename T, bool E8, int D>
+__global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
+  typedef typename Vec8<T>::type T8;
+  constexpr int LPH = D / 8, HPP = kThreads / LPH;
+  const ReqView& q = a.req;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  int total;
+  const int total_eff = rows_in_use(q, &total);
+  if (blockIdx.x == 0) {
+    int bits = total != total_eff ? DSPARK_DATA_BAD_LENS : 0;
+    for (int r = tid; r < q.B; r += kThreads) bits |= append_status(a, r, total_eff);
+    __shared__ int all;
+    if (tid == 0) all = 0;
+    __syncthreads();
+    if (bits) atomicOr(&all, bits);
+    __syncthreads();
+    if (tid == 0) {
+      a.meta[0] = total;
+      a.meta[1] = all;
+    }
+    return;
+  }
+  const int u = blockIdx.x - 1;
+  const int r = u / (q.gamma + 1);
+  const int j = u - r * (q.gamma + 1);
+  int c0, len;
+  if (!request_rows(q, r, total_eff, &c0, &len) || j >= len) return;
+  const int prefix = q.prefix[r];
+  if (prefix < 0 || (int64_t)prefix + len > ((int64_t)q.width << a.kv.page_shift)) return;
+  const int slot = prefix + j;
+  const int id = q.table[(size_t)r * q.width + (slot >> a.kv.page_shift)];
+  int depth = j;
+  if (q.parents) {
+    // lane l holds the parent of row l + 1; every wave walks by itself
+    const int par = lane + 1 < len ? q.parents[(size_t)r * q.gamma + lane] : 0;
+    if (__ballot(par < 0 || par > lane)) return;
+    depth = 0;
+    for (int n = j; n > 0; n = __builtin_amdgcn_readlane(par, n - 1)) ++depth;
+  }
+  if (id < 0 || id >= a.kv.num_blocks) return;
+  const int64_t pos = (int64_t)prefix + depth;
+  if (a.rope && pos >= a.rope_rows) return;
+
+  const int li = lane & (LPH - 1);  // the lane's eight elements: 8 li ..
+  const int hq = a.num_heads, hkv = a.kv.hkv;
+  const int heads = hq + 2 * hkv;
+  const int half = a.rope_dim >> 1;
+  // the lane's cosines and sines, the same for every head
+  float co[8], si[8];
+  bool turned = false;
+  int swap = lane;  // lane that holds the other elements of the pairs
+  if (a.rope) {
+    const float* cs = a.rope + (size_t)pos * a.rope_dim;
+    turned = 8 * li < a.rope_dim;
+    if (a.rope_interleaved) {
+      const int i0 = turned ? 4 * li : 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        co[2 * e] = co[2 * e + 1] = cs[i0 + e];
+        si[2 * e + 1] = cs[half + i0 + e];
+        si[2 * e] = -si[2 * e + 1];
+      }
+    } else {
+      const bool low = 8 * li < half;
+      const int i0 = turned ? (low ? 8 * li : 8 * li - half) : 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        co[e] = cs[i0 + e];
+        si[e] = low ? -cs[half + i0 + e] : cs[half + i0 + e];
+      }
+      if (turned) swap = low ? lane + half / 8 : lane - half / 8;
+    }
+  }
+  const unsigned char* rows[3] = {a.q + (size_t)(c0 + j) * a.q_ld, a.k + (size_t)(c0 + j) * a.k_ld,
+                                  a.v + (size_t)(c0 + j) * a.v_ld};
+  const int off = slot & ((1 << a.kv.page_shift) - 1);
+  for (int h0 = 0; h0 < heads; h0 += HPP) {
+    const int h = h0 + tid / LPH;
+    const bool live = h < heads;
+    const int kind = h < hq ? 0 : (h < hq + hkv ? 1 : 2);
+    const int hh = kind == 0 ? h : (kind == 1 ? h - hq : h - hq - hkv);
+    float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (live) {
+      const T8 raw = *reinterpret_cast<const T8*>(rows[kind] + (size_t)(hh * D + 8 * li) * 2);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = (float)raw[e];
+    }
+    const T* w = reinterpret_cast<const T*>(kind == 0 ? a.q_weight : a.k_weight);
+    if (a.q_weight || a.k_weight) {
+      float ss = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(x[e], x[e], ss);
+      for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor(ss, o, kWave);
+      if (live && kind < 2 && w) {
+        const float rstd = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+        const T8 ww = *reinterpret_cast<const T8*>(w + 8 * li);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = x[e] * rstd * (float)ww[e];
+      }
+    }
+    if (a.rope) {
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        // the pair's other element: a neighbour, or the same place of another lane
+        y[e] = a.rope_interleaved ? x[e ^ 1] : __shfl(x[e], swap, kWave);
+      }
+      if (turned && kind < 2) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __builtin_fmaf(x[e], co[e], y[e] * si[e]);
+      }
+    }
+    int e8 = 0;
+    float inv = 1.0f;
+    if constexpr (E8) {
+      float amax = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = finite_f32(x[e]) ? fmaxf(amax, fabsf(x[e])) : amax;
+      for (int o = LPH / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o, kWave));
+      e8 = e4m3_exponent(amax);
+      inv = pow2f(-e8);
+    }
+    if (!live) continue;
+    if (kind == 0 || !E8) {
+      T8 o;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = (T)x[e];
+      unsigned char* dst;
+      if (kind == 0) {
+        dst = a.q_out + (size_t)(c0 + j) * a.q_out_ld + (size_t)(hh * D + 8 * li) * 2;
+      } else {
+        dst = (kind == 1 ? a.kv.k : a.kv.v) + (size_t)id * a.kv.page_bytes +
+              ((((size_t)hh << a.kv.page_shift) + off) * D + 8 * li) * 2;
+      }
+      *reinterpret_cast<T8*>(dst) = o;
+    } else {
+      kv_u32x2 c;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        int wd = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_operand(x[4 * g], inv),
+                                                 e4m3_operand(x[4 * g + 1], inv), 0, false);
+        wd = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_operand(x[4 * g + 2], inv),
+                                             e4m3_operand(x[4 * g + 3], inv), wd, true);
+        c[g] = (unsigned)wd;
+      }
+      const size_t row = ((size_t)hh << a.kv.page_shift) + off;
+      *reinterpret_cast<kv_u32x2*>((kind == 1 ? a.kv.k : a.kv.v) + (size_t)id * a.kv.page_bytes +
+                                   row * D + 8 * li) = c;
+      if (li == 0) {
+        (kind == 1 ? a.kv.ks : a.kv.vs)[(size_t)id * a.kv.scale_page_bytes + row] =
+            (uint8_t)(e8 + 127);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ read
+
+constexpr int kReadRows = 16;  // rows per workgroup
+
+// One workgroup per kReadRows output rows: a thread per row finds its request
+// and page, then D / 8 lanes per (row, head) copy or widen eight elements each.
+template <bool E8, int D>
+__global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a) {
+  constexpr int LPH = D / 8, HPP = kThreads / LPH;
+  const ReqView& q = a.req;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  int total;
+  const int total_eff = rows_in_use(q, &total);
+  const int64_t reach = (int64_t)q.width << a.kv.page_shift;
+  if (blockIdx.x == 0) {
+    // one wave per request, a lane per page
+    __shared__ int all;
+    if (tid == 0) all = total != total_eff ? DSPARK_DATA_BAD_LENS : 0;
+    __syncthreads();
+    for (int r = tid / kWave; r < q.B; r += kThreads / kWave) {
+      const int s = q.cu[r], e = q.cu[r + 1], st = q.prefix[r];
+      int bits = 0;
+      if (s < 0 || e < s || e > total_eff || st < 0) {
+        bits = DSPARK_DATA_BAD_LENS;
+      } else if (e > s) {
+        const int64_t hi = (int64_t)st + (e - s);
+        if (hi > reach) {
+          bits = DSPARK_DATA_BAD_PAGE;
+        } else {
+          for (int64_t p = (st >> a.kv.page_shift) + lane; p <= (hi - 1) >> a.kv.page_shift;
+               p += kWave) {
+            const int id = q.table[(size_t)r * q.width + p];
+            if (id < 0 || id >= a.kv.num_blocks) bits = DSPARK_DATA_BAD_PAGE;
+          }
+        }
+      }
+      if (bits) atomicOr(&all, bits);
+    }
+    __syncthreads();
+    if (tid == 0) {
+      a.meta[0] = total;
+      a.meta[1] = all;
+    }
+    return;
+  }
+  __shared__ int page_of[kReadRows], off_of[kReadRows];
+  const int row0 = (blockIdx.x - 1) * kReadRows;
+  if (row0 >= total_eff) return;
+  if (tid < kReadRows) {
+    const int row = row0 + tid;
+    int id = -1, off = 0;
+    if (row < total_eff) {
+      // the last request that starts at or before the row
+      int lo = 0, hi = q.B;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (q.cu[mid] <= row) lo = mid; else hi = mid;
+      }
+      const int s = q.cu[lo], e = q.cu[lo + 1], st = q.prefix[lo];
+      if (s >= 0 && s <= row && row < e && e <= total_eff && st >= 0 &&
+          (int64_t)st + (e - s) <= reach) {
+        const int slot = st + (row - s);
+        id = q.table[(size_t)lo * q.width + (slot >> a.kv.page_shift)];
+        if (id >= a.kv.num_blocks) id = -1;
+        off = slot & ((1 << a.kv.page_shift) - 1);
+      }
+    }
+    page_of[tid] = id;
+    off_of[tid] = off;
+  }
+  __syncthreads();
+  const int li = lane & (LPH - 1);
+  for (int n = tid / LPH; n < kReadRows * a.kv.hkv; n += HPP) {
+    const int i = n / a.kv.hkv, h = n - i * a.kv.hkv;
+    const int id = page_of[i];
+    if (id < 0) continue;
+    const size_t at = ((size_t)h << a.kv.page_shift) + off_of[i];
+    const size_t dst = (size_t)(row0 + i) * a.out_ld + (size_t)(h * D + 8 * li) * 2;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const unsigned char* src = (w ? a.kv.v : a.kv.k) + (size_t)id * a.kv.page_bytes;
+      kv_u32x4 o;
+      if constexpr (E8) {
+        const kv_u32x2 c = *reinterpret_cast<const kv_u32x2*>(src + at * D + 8 * li);
+        const float sc =
+            pow2f((int)(w ? a.kv.vs : a.kv.ks)[(size_t)id * a.kv.scale_page_bytes + at] - 127);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          o[2 * g] = __builtin_bit_cast(
+              unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[g], sc, false));
+          o[2 * g + 1] = __builtin_bit_cast(
+              unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[g], sc, true));
+        }
+      } else {
+        o = *reinterpret_cast<const kv_u32x4*>(src + (at * D + 8 * li) * 2);
+      }
+      *reinterpret_cast<kv_u32x4*>((w ? a.v_out : a.k_out) + dst) = o;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ commit
+
+constexpr int kMoveBatch = 8;
+
+// The moves of request r, by the first wave's lanes: lane l has k = l + 1.
+// Returns the status bits; *src, *dst the lane's cache indices, *src = -1 where
+// it moves nothing.
+__device__ int path_moves(const CommitArgs& a, int r, int lane, int64_t* src, int64_t* dst) {
+  const ReqView& q = a.req;
+  *src = *dst = -1;
+  const int c = a.num_correct[r], prefix = q.prefix[r];
+  if (c < 0 || c > q.gamma || prefix < 0) return DSPARK_DATA_BAD_LENS;
+  const int32_t* path = a.path + (size_t)r * (q.gamma + 1);
+  const bool on = lane < c;
+  const int here = on ? path[lane + 1] : 0, before = on ? path[lane] : 0;
+  const bool ok = path[0] == 0 && (!on || (here > before && here <= q.gamma));
+  if (__ballot(!ok)) return DSPARK_DATA_BAD_TREE;
+  if (on && here != lane + 1) {
+    *src = (int64_t)prefix + here;
+    *dst = (int64_t)prefix + lane + 1;
+  }
+  const int64_t reach = (int64_t)q.width << a.kv.page_shift;
+  bool good = true;
+  if (*src >= 0) {
+    good = *src < reach;
+    if (good) {
+      const int s = q.table[(size_t)r * q.width + (*src >> a.kv.page_shift)];
+      const int d = q.table[(size_t)r * q.width + (*dst >> a.kv.page_shift)];
+      good = s >= 0 && s < a.kv.num_blocks && d >= 0 && d < a.kv.num_blocks;
+    }
+  }
+  if (__ballot(!good)) {
+    *src = -1;
+    return DSPARK_DATA_BAD_PAGE;
+  }
+  return 0;
+}
+
+// One workgroup per (request, layer); a thread owns 16-byte columns of it (one
+// place of one head of the keys or of the values) and moves the path's rows of
+// that column in ascending order. Path rows ascend and path[k] >= k, so a move
+// never overwrites the source of a later one, and a batch of kMoveBatch loads
+// may run ahead of its stores: the rows it stores to, k .. k + kMoveBatch - 1,
+// lie below every later source.
+__global__ __launch_bounds__(kThreads) void commit_kernel(CommitArgs a) {
+  const ReqView& q = a.req;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  if (blockIdx.x == 0) {
+    if (blockIdx.y != 0) return;
+    __shared__ int all, moved;
+    if (tid == 0) all = moved = 0;
+    __syncthreads();
+    for (int r = tid / kWave; r < q.B; r += kThreads / kWave) {
+      int64_t src, dst;
+      const int bits = path_moves(a, r, lane, &src, &dst);
+      const int n = __popcll(__ballot(src >= 0));
+      if (lane == 0) {
+        if (bits) atomicOr(&all, bits);
+        if (n) atomicAdd(&moved, n);
+      }
+    }
+    __syncthreads();
+    if (tid == 0) {
+      a.meta[0] = moved;
+      a.meta[1] = all;
+    }
+    return;
+  }
+  const int r = blockIdx.x - 1;
+  __shared__ int s_id[DSPARK_MAX_GAMMA], s_off[DSPARK_MAX_GAMMA], d_id[DSPARK_MAX_GAMMA],
+      d_off[DSPARK_MAX_GAMMA];
+  __shared__ int n_moves;
+  if (tid < kWave) {
+    int64_t src, dst;
+    path_moves(a, r, lane, &src, &dst);
+    const unsigned long long m = __ballot(src >= 0);
+    if (src >= 0) {
+      const int i = __popcll(m & ((1ull << lane) - 1));
+      const int mask = (1 << a.kv.page_shift) - 1;
+      s_id[i] = q.table[(size_t)r * q.width + (src >> a.kv.page_shift)];
+      d_id[i] = q.table[(size_t)r * q.width + (dst >> a.kv.page_shift)];
+      s_off[i] = (int)(src & mask);
+      d_off[i] = (int)(dst & mask);
+    }
+    if (lane == 0) n_moves = __popcll(m);
+  }
+  __syncthreads();
+  const int n = n_moves;
+  if (n == 0) return;
+  const int row_vecs = a.kv.dim * a.kv.cb / 16;
+  const size_t row_bytes = (size_t)a.kv.dim * a.kv.cb;
+  const int cols = 2 * a.kv.hkv * row_vecs;
+  for (int col = tid; col < cols; col += kThreads) {
+    const int row = col / row_vecs;  // keys' heads, then values' heads
+    const int w = row >= a.kv.hkv, h = row - w * a.kv.hkv;
+    unsigned char* base = (w ? a.kv.v : a.kv.k) + (size_t)blockIdx.y * a.kv.layer_bytes +
+                          (((size_t)h << a.kv.page_shift) * row_bytes) +
+                          (size_t)(col - row * row_vecs) * 16;
+    for (int k0 = 0; k0 < n; k0 += kMoveBatch) {
+      kv_u32x4 x[kMoveBatch];
+#pragma unroll
+      for (int i = 0; i < kMoveBatch; ++i) {
+        x[i] = (kv_u32x4){0u, 0u, 0u, 0u};
+        if (k0 + i < n)
+          x[i] = *reinterpret_cast<const kv_u32x4*>(base + (size_t)s_id[k0 + i] * a.kv.page_bytes +
+                                                    s_off[k0 + i] * row_bytes);
+      }
+#pragma unroll
+      for (int i = 0; i < kMoveBatch; ++i) {
+        if (k0 + i < n)
+          *reinterpret_cast<kv_u32x4*>(base + (size_t)d_id[k0 + i] * a.kv.page_bytes +
+                                       d_off[k0 + i] * row_bytes) = x[i];
+      }
+    }
+  }
+  if (a.kv.ks) {
+    for (int row = tid; row < 2 * a.kv.hkv; row += kThreads) {
+      const int w = row >= a.kv.hkv, h = row - w * a.kv.hkv;
+      uint8_t* base = (w ? a.kv.vs : a.kv.ks) + (size_t)blockIdx.y * a.kv.scale_layer_bytes +
+                      ((size_t)h << a.kv.page_shift);
+      for (int k = 0; k < n; ++k) {
+        base[(size_t)d_id[k] * a.kv.scale_page_bytes + d_off[k]] =
+            base[(size_t)s_id[k] * a.kv.scale_page_bytes + s_off[k]];
+      }
+    }
+  }
+}
+
+template <typename T, bool E8>
+void append_by_dim(const AppendArgs& a, unsigned grid, hipStream_t s) {
+  switch (a.kv.dim) {
+    case 64:
+      hipLaunchKernelGGL((append_kernel<T, E8, 64>), dim3(grid), dim3(kThreads), 0, s, a);
+      break;
+    case 128:
+      hipLaunchKernelGGL((append_kernel<T, E8, 128>), dim3(grid), dim3(kThreads), 0, s, a);
+      break;
+    default:
+      hipLaunchKernelGGL((append_kernel<T, E8, 256>), dim3(grid), dim3(kThreads), 0, s, a);
+  }
+}
+
+template <bool E8>
+void read_by_dim(const ReadArgs& a, unsigned grid, hipStream_t s) {
+  switch (a.kv.dim) {
+    case 64:
+      hipLaunchKernelGGL((read_kernel<E8, 64>), dim3(grid), dim3(kThreads), 0, s, a);
+      break;
+    case 128:
+      hipLaunchKernelGGL((read_kernel<E8, 128>), dim3(grid), dim3(kThreads), 0, s, a);
+      break;
+    default:
+      hipLaunchKernelGGL((read_kernel<E8, 256>), dim3(grid), dim3(kThreads), 0, s, a);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_append(const AppendArgs& a, dspark_dtype dt, hipStream_t s) {
+  const unsigned grid = 1u + (unsigned)a.req.B * (unsigned)(a.req.gamma + 1);
+  if (a.kv.cb == 1) {
+    append_by_dim<__bf16, true>(a, grid, s);
+  } else if (dt == DSPARK_BF16) {
+    append_by_dim<__bf16, false>(a, grid, s);
+  } else {
+    append_by_dim<_Float16, false>(a, grid, s);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_read(const ReadArgs& a, hipStream_t s) {
+  const int rows = a.req.B > 0 ? a.req.max_rows : 0;
+  const unsigned grid = 1u + (unsigned)((rows + (int64_t)kReadRows - 1) / kReadRows);
+  if (a.kv.cb == 1) {
+    read_by_dim<true>(a, grid, s);
+  } else {
+    read_by_dim<false>(a, grid, s);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_commit(const CommitArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL(commit_kernel, dim3(1u + (unsigned)a.req.B, (unsigned)a.kv.num_layers),
+                     dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace dspark

@@ -27,6 +27,16 @@
  *                    and its per-request cumulative product, which can feed
  *                    dspark_plan as survivals
  *
+ * and, for the target pass between pack and accept, over a paged cache, with
+ * the drafts of a request in a chain or in a tree:
+ *
+ *   dspark_kv_append norms and rotation of the packed rows' queries and keys,
+ *                    and the write of their keys and values into the cache
+ *   dspark_kv_read   cache rows back as dense rows
+ *   dspark_tree_attention  attention of the packed rows over the cache
+ *   dspark_tree_accept     greedy accept along a draft tree
+ *   dspark_kv_commit the accepted path's cache rows moved to consecutive slots
+ *
  * Page references used below:
  *   [Budget] akiyangdev, "DSpark 自适应 Verify 怎样分配候选预算"
  *   [Round]  akiyangdev, "DeepSeek-V4 DSpark 一轮 Draft、Verify、Accept 与 Commit"
@@ -69,7 +79,14 @@ typedef enum dspark_status {
   DSPARK_E_LAUNCH = 4       /* the HIP runtime refused a launch */
 } dspark_status;
 
-typedef enum dspark_dtype { DSPARK_F32 = 0, DSPARK_BF16 = 1 } dspark_dtype;
+/* F16 and E4M3 (8 bits: 4 of exponent, 3 of mantissa, no infinities) are types
+ * of the target-pass calls only. */
+typedef enum dspark_dtype {
+  DSPARK_F32 = 0,
+  DSPARK_BF16 = 1,
+  DSPARK_F16 = 2,
+  DSPARK_E4M3 = 3
+} dspark_dtype;
 
 /* What dspark_plan's `conf` holds. */
 typedef enum dspark_input {
@@ -86,6 +103,11 @@ typedef enum dspark_input {
 #define DSPARK_DATA_BAD_LENS 4 /* verify lengths or cu_seqlens malformed */
 #define DSPARK_DATA_BAD_LOGITS 8 /* a row a sampling request reads holds NaN or
                                     +inf, or has no finite maximum */
+#define DSPARK_DATA_BAD_TREE 16 /* a draft's parent row, or an accepted path, is
+                                   out of order or range */
+#define DSPARK_DATA_BAD_PAGE 32 /* a cache index lies beyond the block table, or
+                                   its page id is not one of the cache's */
+#define DSPARK_DATA_BAD_POS 64  /* a position lies beyond the rotation table */
 
 /* Limits. */
 #define DSPARK_MAX_GAMMA 64
@@ -97,6 +119,9 @@ typedef enum dspark_input {
 #define DSPARK_STS_MAX_GRID 128        /* temperature candidates of dspark_sts_fit */
 #define DSPARK_STS_MAX_BINS 64         /* calibration bins of dspark_sts_fit */
 #define DSPARK_STS_MAX_RECORDS 4194304 /* records of dspark_sts_fit */
+#define DSPARK_MAX_HEADS 256           /* query heads of the target-pass calls */
+#define DSPARK_MAX_GROUP 64            /* query heads per key/value head */
+#define DSPARK_MAX_LAYERS 1024         /* layers of one dspark_kv_commit */
 
 /* How the planner prices a budget (see dspark_plan_pack_ex). */
 typedef enum dspark_cost_mode {
@@ -601,6 +626,235 @@ dspark_status dspark_sts_fit(int32_t N, int32_t gamma, const float* z, const uin
 
 /* Bytes of workspace dspark_sts_fit needs (0 for invalid sizes). */
 size_t dspark_sts_workspace_size(int32_t N, int32_t gamma, int32_t n_t, int32_t n_bins);
+
+/*
+ * ---- The target pass: cache, attention, tree accept -----------------------
+ *
+ * Between dspark_pack and the accept the target model runs over the packed
+ * verify rows. [Round] §三 and [Budget] §五 define their layout (cu_seqlens,
+ * prefix_lens + j); [Round] §六 the commit. The pages draft chains; the calls
+ * below also take trees, of which a chain is the special case.
+ *
+ * Rows. Request r owns packed rows cu[r] .. cu[r+1]-1, len = 1..gamma+1 of
+ * them, row 0 its root; rows at or beyond cu_seqlens[B] are padding and are
+ * neither read nor written. Its prefix_lens[r] committed tokens are in the
+ * cache at indices 0..prefix-1, and its row j lives at cache index prefix + j.
+ *
+ * Tree. tree_parents[r * gamma + (j - 1)] is the parent row of row j = 1..
+ * len-1, in [0, j - 1]; entries past len - 1 are ignored. NULL is the chain
+ * (parent j - 1). Any front part of such a list is a tree again, so the
+ * planner's verify_lens shorten trees as they shorten chains. anc(j) is row j
+ * with its ancestors up to row 0, depth(j) the number of its ancestors, and
+ * the position of row j is prefix + depth(j).
+ *
+ * Cache. Pages of block_size tokens; page p of a layer holds keys as
+ * [num_kv_heads][block_size][head_dim] at k + p * block_stride elements, and
+ * values likewise at v. Cache index i of request r is token i % block_size of
+ * page block_table[r * table_width + i / block_size]. With dtype E4M3 each
+ * (token, head) row x of keys or of values is stored as codes and one exponent
+ * byte b, at [num_kv_heads][block_size] from p * scale_block_stride of k_scale
+ * or v_scale: value = code * 2^(b - 127). The exponent is the least with
+ * max |x| <= 448 * 2^(b - 127), held to [-100, 119] (0 for a row of zeros),
+ * taken over the finite elements. A power of two scales without rounding, and
+ * every such value is exact in bfloat16. Codes round to nearest, ties to even,
+ * and saturate at 448; a NaN or infinite element becomes NaN.
+ *
+ * Requests with data errors set a bit in the status word and are left out: a
+ * request whose rows are not 1..gamma+1 rows inside [0, min(cu_seqlens[B],
+ * max_rows)) or whose prefix is negative sets DSPARK_DATA_BAD_LENS, one with a
+ * parent out of range DSPARK_DATA_BAD_TREE, one that needs more pages than
+ * table_width DSPARK_DATA_BAD_PAGE. None of such a request's rows is written.
+ * Requests of one call must not share the pages that they write.
+ */
+typedef struct dspark_kv_cache {
+  void* k;           /* device, 16-byte aligned */
+  void* v;
+  uint8_t* k_scale;  /* device; E4M3 only, otherwise ignored */
+  uint8_t* v_scale;
+  int64_t block_stride;       /* elements from page to page, >= num_kv_heads *
+                                 block_size * head_dim, a multiple of 16 bytes */
+  int64_t scale_block_stride; /* bytes from page to page of the exponents */
+  int64_t layer_stride;       /* elements from layer to layer; dspark_kv_commit */
+  int64_t scale_layer_stride; /* bytes from layer to layer; dspark_kv_commit */
+  int32_t num_layers;         /* dspark_kv_commit; the other calls use layer 0 */
+  int32_t num_blocks;         /* pages of each layer, >= 1 */
+  int32_t num_kv_heads;       /* 1..DSPARK_MAX_HEADS */
+  int32_t block_size;         /* 16, 32, 64, 128 or 256 */
+  int32_t head_dim;           /* 64, 128 or 256 */
+  dspark_dtype dtype;         /* BF16, F16 or E4M3 */
+} dspark_kv_cache;
+
+/*
+ * dspark_kv_append - norms, rotation and cache write of the packed rows.
+ *
+ * For every packed row, in float32 and rounded once at the end:
+ *   queries, keys: y = x * (mean(x^2) + eps)^(-1/2) * weight over the head_dim
+ *     elements of each head (skipped where the weight is NULL), then the
+ *     rotation by the row's position: with h = rope_dim / 2 and (c_i, s_i) of
+ *     table row `position`, the pair (a, b) of elements (i, i + h), or (2 i,
+ *     2 i + 1) if rope_interleaved, becomes (a c_i - b s_i, b c_i + a s_i);
+ *     elements from rope_dim on stay (skipped where rope is NULL);
+ *   q_out = the queries; the cache gets the keys and the (unchanged) values at
+ *     cache index prefix + j.
+ *
+ * Arguments:
+ *   B, gamma           as for dspark_pack
+ *   num_heads          query heads, a multiple of the cache's num_kv_heads,
+ *                      at most DSPARK_MAX_GROUP times it
+ *   dt                 type of q, k, v, the weights and q_out: BF16 or F16; the
+ *                      cache holds the same type, or E4M3 with BF16
+ *   q, k, v            row i at q + i * q_ld (elements), its heads dense; all
+ *                      16-byte aligned, strides multiples of 8 elements. The
+ *                      three may be parts of the rows of one buffer.
+ *   max_rows           rows the buffers hold
+ *   tree_parents       [B, gamma] int32 or NULL (chain)
+ *   block_table        [B, table_width] int32
+ *   q_weight, k_weight [head_dim] or NULL, 16-byte aligned
+ *   eps                >= 0
+ *   rope               [rope_rows, rope_dim] float32: rope_dim / 2 cosines, then
+ *                      as many sines, of each position; or NULL. 16-byte
+ *                      aligned, rope_dim a multiple of 16 up to head_dim
+ *   q_out              rows as q, q_out_ld elements apart; q itself is allowed
+ *   append_meta        out [2] int32: cu_seqlens[B], status bits
+ * Further data errors: a row on a page id outside [0, num_blocks)
+ *   (DSPARK_DATA_BAD_PAGE) or at a position >= rope_rows (DSPARK_DATA_BAD_POS)
+ *   is left out alone.
+ */
+dspark_status dspark_kv_append(int32_t B, int32_t gamma, int32_t num_heads, dspark_dtype dt,
+                               const void* q, int64_t q_ld, const void* k, int64_t k_ld,
+                               const void* v, int64_t v_ld, int32_t max_rows,
+                               const int32_t* cu_seqlens, const int32_t* prefix_lens,
+                               const int32_t* tree_parents, const int32_t* block_table,
+                               int32_t table_width, const void* q_weight, const void* k_weight,
+                               float eps, const float* rope, int32_t rope_rows,
+                               int32_t rope_dim, int32_t rope_interleaved, void* q_out,
+                               int64_t q_out_ld, const dspark_kv_cache* cache,
+                               int32_t* append_meta, void* stream);
+
+/*
+ * dspark_kv_read - cache rows back as dense rows.
+ *
+ *   k_out[cu[r] + j], v_out[cu[r] + j] = the values at cache index starts[r] + j
+ *   for j < cu[r+1] - cu[r]
+ *
+ * Arguments:
+ *   B, cu_seqlens      requests (0..DSPARK_MAX_BATCH) and the rows of each: any
+ *                      number, also none
+ *   max_rows           rows the outputs hold
+ *   starts             [B] int32, the first cache index of each request
+ *   k_out, v_out       rows of [num_kv_heads][head_dim] of the cache's type
+ *                      (BF16 for E4M3: exact), out_ld elements apart; 16-byte
+ *                      aligned, out_ld a multiple of 8
+ *   read_meta          out [2] int32: cu_seqlens[B], status bits
+ * Data errors: a request whose rows lie outside [0, min(cu_seqlens[B],
+ *   max_rows)), or that starts below 0, sets DSPARK_DATA_BAD_LENS; one that
+ *   ends beyond its table row DSPARK_DATA_BAD_PAGE; none of its rows is
+ *   written. A row on a page id outside [0, num_blocks) sets
+ *   DSPARK_DATA_BAD_PAGE and is left out alone.
+ */
+dspark_status dspark_kv_read(int32_t B, int32_t max_rows, const int32_t* cu_seqlens,
+                             const int32_t* starts, const int32_t* block_table,
+                             int32_t table_width, const dspark_kv_cache* cache, void* k_out,
+                             void* v_out, int64_t out_ld, int32_t* read_meta, void* stream);
+
+/*
+ * dspark_tree_attention - attention of the packed verify rows over the cache.
+ *
+ * Row j of request r sees the cache indices 0..prefix-1 and prefix + i for i in
+ * anc(j), itself included. Query head h reads key/value head h / (num_heads /
+ * num_kv_heads):
+ *   s_k = scale * q . k_k,  out = sum_k exp(s_k) v_k / sum_k exp(s_k),
+ *   lse = log sum_k exp(s_k)
+ * over the indices seen. Scores, maxima, sums and the accumulated output are
+ * float32; the weights exp(s_k - max) round to the query type before their
+ * product with v (float32 accumulation), and the output rounds once. A value
+ * that a row does not see adds nothing to it, whatever it holds.
+ *
+ * Arguments:
+ *   B, gamma, num_heads, dt   as for dspark_kv_append
+ *   q, q_ld, max_rows  rows as for dspark_kv_append (its q_out)
+ *   scale              finite
+ *   out, out_ld        rows as q
+ *   lse                [max_rows, num_heads] float32 or NULL
+ *   attention_meta     out [2] int32: cu_seqlens[B], status bits
+ *   workspace          dspark_tree_attention_workspace_size() bytes, 256-byte
+ *                      aligned; contents irrelevant, no state between calls;
+ *                      calls that share it must not overlap in time
+ * The keys and values of the step's own rows must be in the cache
+ * (dspark_kv_append). Further data errors: the indices of a page id outside
+ *   [0, num_blocks) count as not seen and set DSPARK_DATA_BAD_PAGE; a row that
+ *   sees nothing at all then gets zeros and lse -inf.
+ */
+dspark_status dspark_tree_attention(int32_t B, int32_t gamma, int32_t num_heads, dspark_dtype dt,
+                                    const void* q, int64_t q_ld, int32_t max_rows,
+                                    const int32_t* cu_seqlens, const int32_t* prefix_lens,
+                                    const int32_t* tree_parents, const int32_t* block_table,
+                                    int32_t table_width, const dspark_kv_cache* cache,
+                                    float scale, void* out, int64_t out_ld, float* lse,
+                                    int32_t* attention_meta, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace dspark_tree_attention needs (0 for invalid sizes). */
+size_t dspark_tree_attention_workspace_size(int32_t B, int32_t gamma, int32_t num_heads,
+                                            int32_t num_kv_heads, int32_t head_dim);
+
+/*
+ * dspark_tree_accept - greedy accept along a draft tree.
+ *
+ * The argmax of every packed row is dspark_accept's (float32 order, NaN on
+ * top, lowest index on ties). From row 0 the walk goes on to the child row
+ * whose draft token is the argmax of the present row (the lowest such row if
+ * several are equal), and ends where there is none: path[0] = 0, path[1..c] the
+ * rows walked to, bonus = argmax of row path[c]. With the chain's parents this
+ * is dspark_accept.
+ *
+ * Arguments as for dspark_accept unless stated:
+ *   tree_parents       [B, gamma] int32 or NULL (chain)
+ *   num_correct        out [B] int32: c
+ *   bonus, commit_lens out [B] int32; commit_lens = c + 1
+ *   out_tokens         out [B, gamma + 1] int32: the drafts of path[1..c], the
+ *                      bonus, then -1
+ *   path_rows          out [B, gamma + 1] int32: path[0..c], then -1
+ *   new_seq_lens       out [B] int32 or NULL: prefix + c + 1
+ * Data errors: as for dspark_accept, and a parent out of range
+ *   (DSPARK_DATA_BAD_TREE): num_correct 0, bonus -1, commit 0, out_tokens and
+ *   path_rows -1, new_seq = prefix.
+ */
+dspark_status dspark_tree_accept(int32_t B, int32_t gamma, int32_t V, dspark_dtype dt,
+                                 const void* packed_logits, int64_t ld, int32_t max_rows,
+                                 const int32_t* cu_seqlens, const int32_t* draft_tokens,
+                                 const int32_t* tree_parents, const int32_t* prefix_lens,
+                                 int32_t* row_argmax, int32_t* num_correct, int32_t* bonus,
+                                 int32_t* commit_lens, int32_t* out_tokens, int32_t* path_rows,
+                                 int32_t* new_seq_lens, int32_t* accept_meta, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/*
+ * dspark_kv_commit - the accepted path's cache rows moved to consecutive slots.
+ *
+ * For k = 1..c (c = num_correct[r]) the keys and values at cache index prefix +
+ * path_rows[r, k] go to index prefix + k, in all heads and all num_layers
+ * layers of the cache (layer l at k + l * layer_stride), with their exponents.
+ * After it the cache holds the committed tokens at 0..prefix + c; the bonus
+ * token is the next step's root.
+ *
+ * Arguments:
+ *   B, gamma           as for dspark_pack
+ *   path_rows          [B, gamma + 1] int32, num_correct [B] int32: as written
+ *                      by dspark_tree_accept
+ *   prefix_lens        [B] int32: the lengths before the step
+ *   commit_meta        out [2] int32: rows moved per layer, status bits
+ * Data errors: c outside [0, gamma] or a negative prefix sets
+ *   DSPARK_DATA_BAD_LENS; a path that does not start at 0, ascend strictly and
+ *   stay within gamma DSPARK_DATA_BAD_TREE; a page beyond the table row or a
+ *   page id outside [0, num_blocks) DSPARK_DATA_BAD_PAGE. Nothing of such a
+ *   request is moved. (dspark_tree_accept's output for a malformed request, c =
+ *   0 and path -1, is one with DSPARK_DATA_BAD_TREE.)
+ */
+dspark_status dspark_kv_commit(int32_t B, int32_t gamma, const int32_t* path_rows,
+                               const int32_t* num_correct, const int32_t* prefix_lens,
+                               const int32_t* block_table, int32_t table_width,
+                               const dspark_kv_cache* cache, int32_t* commit_meta, void* stream);
 
 /* Name of a status code (static string). */
 const char* dspark_status_str(dspark_status s);

@@ -43,10 +43,16 @@ from .tv import tv_accept
 from .strided import cap_accept, scatter_to_strided
 from .sts import sts_fit
 from .sampling import DATA_BAD_LOGITS, accept_sampling
+from .target import (
+    DATA_BAD_PAGE, DATA_BAD_POS, DATA_BAD_TREE, commit_moves, e4m3_exponent, e4m3_round,
+    e4m3_values, norm_rope, tree_accept, tree_attention, tree_ok, tree_paths,
+)
 
 __all__ = [
     "sigmoid32", "survival", "plan", "pack", "accept", "row_argmax", "tv_accept",
     "cap_accept", "scatter_to_strided", "sts_fit", "accept_sampling", "DATA_BAD_LOGITS",
     "IN_CONF_LOGITS", "IN_COND", "IN_SURVIVAL", "COST_ADDITIVE", "COST_SPS1D", "sps_floor",
     "DATA_BAD_COST", "DATA_BAD_CONF", "DATA_BAD_LENS", "FX_SHIFT",
+    "DATA_BAD_TREE", "DATA_BAD_PAGE", "DATA_BAD_POS", "commit_moves", "e4m3_exponent", "e4m3_round",
+    "e4m3_values", "norm_rope", "tree_accept", "tree_attention", "tree_ok", "tree_paths",
 ]
