@@ -23,7 +23,8 @@ HOSTCHECK = PKG / "libdspark_hostcheck.so"
 ARCH = "gfx950"
 
 LIB_SOURCES = ["api.hip", "plan.hip", "pack.hip", "accept.hip", "tv.hip", "scatter.hip", "sts.hip", "sampling.hip",
-               "api_target.hip", "kv_cache.hip", "tree_attention.hip"]
+               "api_target.hip", "kv_cache.hip", "tree_attention.hip",
+               "tree_attention_d64.hip", "tree_attention_d128.hip", "tree_attention_d256.hip"]
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}",
@@ -33,6 +34,7 @@ COMMON_FLAGS = [
     "-shared",
     "-Wall",
     "-Wno-unused-function",
+    "-parallel-jobs=4",
     # no packed fp32 instructions: plain scalar fp32 code only
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     # no contraction of a product and a sum into one rounding anywhere, also

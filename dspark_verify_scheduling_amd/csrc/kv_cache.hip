@@ -84,7 +84,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
   if (!request_rows(q, r, total_eff, &c0, &len) || j >= len) return;
   const int prefix = q.prefix[r];
   if (prefix < 0 || (int64_t)prefix + len > ((int64_t)q.width << a.kv.page_shift)) return;
-  const int slot = prefix + j;
+  const int64_t slot = (int64_t)prefix + j;
   const int id = q.table[(size_t)r * q.width + (slot >> a.kv.page_shift)];
   int depth = j;
   if (q.parents) {
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
   }
   const unsigned char* rows[3] = {a.q + (size_t)(c0 + j) * a.q_ld, a.k + (size_t)(c0 + j) * a.k_ld,
                                   a.v + (size_t)(c0 + j) * a.v_ld};
-  const int off = slot & ((1 << a.kv.page_shift) - 1);
+  const int off = (int)(slot & ((1 << a.kv.page_shift) - 1));
   for (int h0 = 0; h0 < heads; h0 += HPP) {
     const int h = h0 + tid / LPH;
     const bool live = h < heads;
@@ -272,10 +272,10 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a) {
       const int s = q.cu[lo], e = q.cu[lo + 1], st = q.prefix[lo];
       if (s >= 0 && s <= row && row < e && e <= total_eff && st >= 0 &&
           (int64_t)st + (e - s) <= reach) {
-        const int slot = st + (row - s);
+        const int64_t slot = (int64_t)st + (row - s);
         id = q.table[(size_t)lo * q.width + (slot >> a.kv.page_shift)];
         if (id >= a.kv.num_blocks) id = -1;
-        off = slot & ((1 << a.kv.page_shift) - 1);
+        off = (int)(slot & ((1 << a.kv.page_shift) - 1));
       }
     }
     page_of[tid] = id;

@@ -1,159 +1,190 @@
-// Attention of packed verify rows (a chain or tree of drafts per request) over
-// the paged cache.
-#include "kv_dev.h"
+// Attention of packed verify rows over the paged cache: launch, workspace and
+// the joining kernel. The split kernel is in tree_attention.h.
+#include "tree_attention.h"
+
+#include <algorithm>
 
 namespace dspark {
 
+namespace attn {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
-
-__device__ inline float load_elem(const unsigned char* p, size_t i, int kind, float sc) {
-  if (kind == 2) {
-    const bf16x2 w = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((unsigned)p[i], sc, false);
-    return (float)w[0];
-  }
-  if (kind == 1) return (float)reinterpret_cast<const _Float16*>(p)[i];
-  return (float)reinterpret_cast<const __bf16*>(p)[i];
-}
-
-// One workgroup per (request, row, query head); its waves take every fourth
-// key, a lane head_dim / 64 elements, with a running maximum and sum each.
-template <typename T, int KIND, int D>
-__global__ __launch_bounds__(kThreads) void attention_kernel(AttnArgs a) {
+// One workgroup per (request, key/value head, share of its rows): joins the
+// parts that several workgroups of the split kernel left of a segment, in order,
+// a wave per row. The first of each request also checks it and its pages.
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, Parts ws, int mt_max,
+                                                        int shares) {
   constexpr int E = D / kWave;
+  typedef __attribute__((ext_vector_type(E))) float fE;
   const ReqView& q = a.req;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int share = blockIdx.x % shares, rh = blockIdx.x / shares;
+  const int r = rh / a.kv.hkv, h = rh - r * a.kv.hkv;
   int total;
   const int total_eff = rows_in_use(q, &total);
-  if (blockIdx.x == 0) {
+  Shape s;
+  const bool good = shape_of(a, r, total_eff, mt_max, &s);
+  if (h == 0 && share == 0) {
+    int bits = 0;
+    if (!good) {
+      bits = request_status(q, r, total_eff);
+      if (!bits) bits = DSPARK_DATA_BAD_PAGE;
+    } else {
+      if (wave == 0 && q.parents) {
+        const int up = lane + 1 < s.len ? q.parents[(size_t)r * q.gamma + lane] : 0;
+        if (__ballot(up < 0 || up > lane)) bits = DSPARK_DATA_BAD_TREE;
+      }
+      for (int64_t p = tid; p <= (s.keys - 1) >> a.kv.page_shift; p += kThreads) {
+        const int id = q.table[(size_t)r * q.width + p];
+        if (id < 0 || id >= a.kv.num_blocks) bits |= DSPARK_DATA_BAD_PAGE;
+      }
+    }
+    // a bad tree's pages are not looked at by the status of a malformed request
     __shared__ int all;
-    if (tid == 0) all = total != total_eff ? DSPARK_DATA_BAD_LENS : 0;
+    if (tid == 0) all = 0;
     __syncthreads();
-    for (int r = wave; r < q.B; r += kWaves) {
-      int bits = request_status(q, r, total_eff);
-      if (!bits) {
-        const int64_t hi = (int64_t)q.prefix[r] + (q.cu[r + 1] - q.cu[r]);
-        if (hi > ((int64_t)q.width << a.kv.page_shift)) {
-          bits = DSPARK_DATA_BAD_PAGE;
-        } else {
-          for (int64_t p = lane; p <= (hi - 1) >> a.kv.page_shift; p += kWave) {
-            const int id = q.table[(size_t)r * q.width + p];
-            if (id < 0 || id >= a.kv.num_blocks) bits = DSPARK_DATA_BAD_PAGE;
+    if (bits) atomicOr(&all, bits);
+    __syncthreads();
+    if (tid == 0 && all)
+      atomicOr(a.meta + 1, all & DSPARK_DATA_BAD_TREE ? DSPARK_DATA_BAD_TREE : all);
+  }
+  if (!good) return;
+  if (q.parents) {
+    const int up = lane + 1 < s.len ? q.parents[(size_t)r * q.gamma + lane] : 0;
+    if (__ballot(up < 0 || up > lane)) return;
+  }
+  const int64_t units = ws.base[q.B];
+  const int wgs = wgs_in_use(units, ws.wgs);
+  const SmallDiv by_group(a.group);
+  for (int seg = 0; seg < s.nseg; ++seg) {
+    const int64_t u0 = ws.base[r] + ((int64_t)h * s.nseg + seg) * s.nku, u1 = u0 + s.nku;
+    // workgroups of the first and the last unit
+    const int wa = (int)(((u0 + 1) * wgs - 1) / units), wb = (int)((u1 * wgs - 1) / units);
+    if (wa == wb) continue;
+    const int slot0 = 2 * wa + (wg_start(units, wa, wgs) == u0 ? 0 : 1);
+    const int n = wb - wa + 1;
+    const int tile0 = seg * s.per, tiles = min(s.per, s.mtiles - tile0);
+    const int rows = min(tiles * 16, s.mrows - tile0 * 16);
+    for (int row = share * kWaves + wave; row < rows; row += shares * kWaves) {
+      auto place = [&](int p) { return (size_t)(p ? 2 * (wa + p) : slot0) * ws.rows + row; };
+      float top = -__builtin_inff();
+      for (int p = lane; p < n; p += kWave) top = fmaxf(top, ws.m[place(p)]);
+      for (int o = kWave / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, kWave));
+      const float ref = top == -__builtin_inff() ? 0.0f : top;
+      float sum = 0.0f;
+      fE y;
+      for (int e = 0; e < E; ++e) y[e] = 0.0f;
+      for (int p0 = 0; p0 < n; p0 += kWave) {
+        // lane p0 + i: the factor of a part; then the parts in order
+        const int p = p0 + lane;
+        float f = 0.0f;
+        if (p < n) {
+          const float m = ws.m[place(p)];
+          f = top == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m - ref);
+          sum += ws.l[place(p)] * f;
+        }
+        const int cnt = min(n - p0, kWave);
+        for (int i = 0; i < cnt; i += 4) {
+          fE x[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            x[k] = *reinterpret_cast<const fE*>(ws.o + place(min(p0 + i + k, n - 1)) * D + lane * E);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (i + k < cnt) {
+              const float fk = read_lane(f, i + k);
+              for (int e = 0; e < E; ++e) y[e] += x[k][e] * fk;
+            }
           }
         }
       }
-      if (bits) atomicOr(&all, bits);
+      sum = wave_sum(sum);
+      const int m = tile0 * 16 + row;
+      const int j = by_group.quo(m);
+      const int head = h * a.group + (m - j * a.group);
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      T* dst = reinterpret_cast<T*>(a.out + (size_t)(s.c0 + j) * a.out_ld) + head * D + lane * E;
+      typedef __attribute__((ext_vector_type(E))) T TE;
+      TE z;
+      for (int e = 0; e < E; ++e) z[e] = (T)(y[e] * inv);
+      *reinterpret_cast<TE*>(dst) = z;
+      if (a.lse && lane == 0)
+        a.lse[(size_t)(s.c0 + j) * a.num_heads + head] =
+            sum == 0.0f ? -__builtin_inff() : (top + __builtin_amdgcn_logf(sum)) * kLn2;
     }
-    __syncthreads();
-    if (tid == 0) {
-      a.meta[0] = total;
-      a.meta[1] = all;
-    }
-    return;
   }
-  const int u = blockIdx.x - 1;
-  const int h = u % a.num_heads;
-  const int rj = u / a.num_heads;
-  const int r = rj / (q.gamma + 1), j = rj - r * (q.gamma + 1);
-  int c0, len;
-  if (!request_rows(q, r, total_eff, &c0, &len) || j >= len) return;
-  const int prefix = q.prefix[r];
-  if (prefix < 0 || (int64_t)prefix + len > ((int64_t)q.width << a.kv.page_shift)) return;
-  // bit i - 1: row i is row j or one of its ancestors; row 0 always is
-  unsigned long long seen = j >= 64 ? ~0ull : (1ull << j) - 1;
-  if (q.parents) {
-    const int par = lane + 1 < len ? q.parents[(size_t)r * q.gamma + lane] : 0;
-    if (__ballot(par < 0 || par > lane)) return;
-    seen = 0;
-    for (int n = j; n > 0; n = __builtin_amdgcn_readlane(par, n - 1)) seen |= 1ull << (n - 1);
-  }
-  const int kh = h / a.group;
-  float x[E], o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    x[e] = (float)reinterpret_cast<const T*>(a.q + (size_t)(c0 + j) * a.q_ld)[h * D + lane * E + e];
-    o[e] = 0.0f;
-  }
-  float m = -__builtin_inff(), l = 0.0f;
-  for (int k = wave; k < prefix + len; k += kWaves) {
-    const int i = k - prefix;
-    if (i > 0 && !((seen >> (i - 1)) & 1)) continue;
-    const int id = q.table[(size_t)r * q.width + (k >> a.kv.page_shift)];
-    if (id < 0 || id >= a.kv.num_blocks) continue;
-    const size_t row = ((size_t)kh << a.kv.page_shift) + (k & ((1 << a.kv.page_shift) - 1));
-    const size_t at = (size_t)id * a.kv.page_bytes;
-    float ksc = 1.0f, vsc = 1.0f;
-    if (KIND == 2) {
-      ksc = pow2f((int)a.kv.ks[(size_t)id * a.kv.scale_page_bytes + row] - 127);
-      vsc = pow2f((int)a.kv.vs[(size_t)id * a.kv.scale_page_bytes + row] - 127);
-    }
-    float s = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      s = __builtin_fmaf(x[e], load_elem(a.kv.k + at, row * D + lane * E + e, KIND, ksc), s);
-    s = wave_sum(s) * a.scale;
-    const float mn = fmaxf(m, s);
-    const float fix = m == mn ? 1.0f : expf(m - mn);
-    const float p = s == -__builtin_inff() ? 0.0f : expf(s - mn);
-    l = l * fix + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      o[e] = o[e] * fix + p * load_elem(a.kv.v + at, row * D + lane * E + e, KIND, vsc);
-    m = mn;
-  }
-  __shared__ float ms[kWaves], ls[kWaves], os[kWaves][D];
-  if (lane == 0) {
-    ms[wave] = m;
-    ls[wave] = l;
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) os[wave][lane * E + e] = o[e];
-  __syncthreads();
-  float mt = ms[0];
-  for (int w = 1; w < kWaves; ++w) mt = fmaxf(mt, ms[w]);
-  float lt = 0.0f;
-  for (int w = 0; w < kWaves; ++w) lt += ms[w] == -__builtin_inff() ? 0.0f : ls[w] * expf(ms[w] - mt);
-  for (int d = tid; d < D; d += kThreads) {
-    float y = 0.0f;
-    for (int w = 0; w < kWaves; ++w)
-      y += ms[w] == -__builtin_inff() ? 0.0f : os[w][d] * expf(ms[w] - mt);
-    reinterpret_cast<T*>(a.out + (size_t)(c0 + j) * a.out_ld)[h * D + d] =
-        (T)(lt == 0.0f ? 0.0f : y / lt);
-  }
-  if (a.lse && tid == 0)
-    a.lse[(size_t)(c0 + j) * a.num_heads + h] = lt == 0.0f ? -__builtin_inff() : mt + logf(lt);
 }
 
-template <typename T, int KIND>
-void by_dim(const AttnArgs& a, unsigned grid, hipStream_t s) {
-  switch (a.kv.dim) {
-    case 64:
-      hipLaunchKernelGGL((attention_kernel<T, KIND, 64>), dim3(grid), dim3(kThreads), 0, s, a);
-      break;
-    case 128:
-      hipLaunchKernelGGL((attention_kernel<T, KIND, 128>), dim3(grid), dim3(kThreads), 0, s, a);
-      break;
-    default:
-      hipLaunchKernelGGL((attention_kernel<T, KIND, 256>), dim3(grid), dim3(kThreads), 0, s, a);
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+constexpr int kMaxWgs = 512;
+
+struct Plan {
+  int mt_max, rows;
+  size_t m_off, l_off, o_off, bytes;
+};
+
+Plan plan(int B, int gamma, int group, int D) {
+  Plan p;
+  const int mtiles = (group * (gamma + 1) + 15) / 16;
+  p.mt_max = segment_tiles(D, mtiles);
+  p.rows = 16 * std::min(p.mt_max, mtiles);
+  const size_t stat = align256((size_t)2 * kMaxWgs * p.rows * sizeof(float));
+  p.m_off = align256((size_t)(B + 1) * sizeof(int64_t));
+  p.l_off = p.m_off + stat;
+  p.o_off = p.l_off + stat;
+  p.bytes = p.o_off + align256((size_t)2 * kMaxWgs * p.rows * D * sizeof(float));
+  return p;
+}
+
+template <int D>
+void launch_join(const AttnArgs& a, const Parts& ws, dspark_dtype dt, int mt_max, hipStream_t s) {
+  // enough waves to fill the card, and no more than there are rows
+  const int pairs = a.req.B * a.kv.hkv;
+  const int most = (a.group * (a.req.gamma + 1) + kWaves - 1) / kWaves;
+  const int shares = std::max(1, std::min(most, 1024 / std::max(pairs, 1)));
+  const dim3 grid((unsigned)pairs * shares), block(kThreads);
+  if (dt == DSPARK_BF16) {
+    hipLaunchKernelGGL((join_kernel<__bf16, D>), grid, block, 0, s, a, ws, mt_max, shares);
+  } else {
+    hipLaunchKernelGGL((join_kernel<_Float16, D>), grid, block, 0, s, a, ws, mt_max, shares);
   }
 }
 
 }  // namespace
+}  // namespace attn
+
+size_t attention_workspace(int B, int gamma, int num_heads, int num_kv_heads, int head_dim) {
+  return attn::plan(B, gamma, num_heads / num_kv_heads, head_dim).bytes;
+}
 
 hipError_t launch_attention(const AttnArgs& a, dspark_dtype dt, hipStream_t s) {
-  const unsigned grid = 1u + (unsigned)((int64_t)a.req.B * (a.req.gamma + 1) * a.num_heads);
-  if (a.kv.cb == 1) {
-    by_dim<__bf16, 2>(a, grid, s);
-  } else if (dt == DSPARK_BF16) {
-    by_dim<__bf16, 0>(a, grid, s);
-  } else {
-    by_dim<_Float16, 1>(a, grid, s);
+  int cus = 0;
+  hipError_t e = current_cu_count(&cus);
+  if (e != hipSuccess) return e;
+  const attn::Plan p = attn::plan(a.req.B, a.req.gamma, a.group, a.kv.dim);
+  unsigned char* w = static_cast<unsigned char*>(a.ws);
+  attn::Parts ws;
+  ws.base = reinterpret_cast<int64_t*>(w);
+  ws.m = reinterpret_cast<float*>(w + p.m_off);
+  ws.l = reinterpret_cast<float*>(w + p.l_off);
+  ws.o = reinterpret_cast<float*>(w + p.o_off);
+  ws.rows = p.rows;
+  ws.wgs = std::min(attn::kMaxWgs, cus * (p.mt_max > 2 ? 1 : 2));
+  switch (a.kv.dim) {
+    case 64: attn::launch_dim64(a, ws, dt, p.mt_max, s); break;
+    case 128: attn::launch_dim128(a, ws, dt, p.mt_max, s); break;
+    default: attn::launch_dim256(a, ws, dt, p.mt_max, s);
+  }
+  e = hipGetLastError();
+  if (e != hipSuccess || a.req.B == 0) return e;
+  switch (a.kv.dim) {
+    case 64: attn::launch_join<64>(a, ws, dt, p.mt_max, s); break;
+    case 128: attn::launch_join<128>(a, ws, dt, p.mt_max, s); break;
+    default: attn::launch_join<256>(a, ws, dt, p.mt_max, s);
   }
   return hipGetLastError();
 }
-
-size_t attention_workspace(int, int, int, int, int) { return 256; }
 
 }  // namespace dspark
