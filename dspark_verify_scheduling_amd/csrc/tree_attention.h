@@ -121,6 +121,12 @@ constexpr int wave_lds() {
                                                             : 16 * o_stride<D>() * 4;
 }
 
+// LDS of a workgroup: the waves' regions, then the queries of its row tiles.
+template <int D, int MT>
+constexpr int wg_lds() {
+  return kWaves * wave_lds<D>() + MT * 16 * D * 2;
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // A row's maximum follows its scores only when they pass it by this much (in
@@ -174,22 +180,32 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
     }
   }
 
+  // Scores in units of log2 with a positive factor, so that a masked score stays
+  // -infinity under it: the scale's sign and its zero go into the queries.
+  float sl = fminf(fabsf(a.scale) * kLog2e, 3.4028235e38f);
+  const unsigned sign = a.scale < 0.0f ? 0x80008000u : 0u;
+  const bool flat = sl == 0.0f;
+  if (flat) sl = 1.0f;
+  // the queries in LDS, in operand order: chunk f of tile t is one 16-byte read
+  // per lane. A lane's place in a key: of two 8-bit chunks in one load.
   const SmallDiv by_group(a.group);
-  V8 qf[MT][NF];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
+  V8* qs = reinterpret_cast<V8*>(lds + kWaves * wave_lds<D>());
+  for (int c = tid; c < MT * NF * kWave; c += kThreads) {
+    const int t = c / (NF * kWave), f = (c / kWave) % NF;
     const int m = (tile0 + t) * 16 + qi;
     const int j = by_group.quo(m);
-    const unsigned char* src =
-        a.q + (size_t)(s.c0 + j) * a.q_ld + (size_t)(h * a.group + (m - j * a.group)) * D * 2;
-#pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      // the place of a key's elements in a lane: of two 8-bit chunks in one load
-      const int d = E8 ? (f >> 1) * 64 + g * 16 + (f & 1) * 8 : f * 32 + g * 8;
-      qf[t][f] = (V8){0, 0, 0, 0, 0, 0, 0, 0};
-      if (m < s.mrows) qf[t][f] = *reinterpret_cast<const V8*>(src + d * 2);
+    const int d = E8 ? (f >> 1) * 64 + g * 16 + (f & 1) * 8 : f * 32 + g * 8;
+    V8 x = (V8){0, 0, 0, 0, 0, 0, 0, 0};
+    if (m < s.mrows && !flat) {
+      kv_u32x4 w = *reinterpret_cast<const kv_u32x4*>(
+          a.q + (size_t)(s.c0 + j) * a.q_ld +
+          ((size_t)(h * a.group + (m - j * a.group)) * D + d) * 2);
+      w ^= sign;
+      x = __builtin_bit_cast(V8, w);
     }
+    qs[c] = x;
   }
+  __syncthreads();
 
   f32x4 o[MT][ND];
   float mx[MT], l[MT];
@@ -247,7 +263,6 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
     }
   };
 
-  const float sl = a.scale * kLog2e;
   // steps of this wave: those whose first key exists
   const int64_t first = ku0 * kUnitKeys + wave * kTileKeys;
   const int steps =
@@ -256,140 +271,118 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
     fetch_ids(0);
     issue(0);
   }
+  // eight 8-bit elements, widened
+  auto widen = [](unsigned lo, unsigned hi, float e) {
+    kv_u32x4 w;
+    w[0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, e, false));
+    w[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, e, true));
+    w[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, e, false));
+    w[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, e, true));
+    return w;
+  };
+  // rows of the step's own tree that a query sees, bit l for row l + 1
+  auto seen_by = [&](int t) {
+    const int j = by_group.quo((tile0 + t) * 16 + qi);
+    if (!a.req.parents) return j >= 64 ? ~0ull : (1ull << j) - 1;
+    const unsigned long long path = __shfl(anc, max(j - 1, 0) & 63, kWave);
+    return j > 0 ? path : 0ull;
+  };
+
   for (int i = 0; i < steps; ++i) {
     const int key0 = (int)first + i * kUnitKeys;
-    const bool bad0 = id0 < 0, bad1 = id1 < 0;
+    const int page0 = id0, page1 = id1;
+    // the step holds keys that some query does not see (the request's own rows
+    // after its root, keys past its last), or lies on a page that is none
+    const bool edge = key0 + kTileKeys > prefix + 1 || page0 < 0 || page1 < 0;
     // scores
     f32x4 sc[MT][2];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      V8 kf[NF];
-      if constexpr (E8) {
-        const float e = __builtin_bit_cast(float, ksb[b] << 23);
+    for (int t = 0; t < MT; ++t) sc[t][0] = sc[t][1] = (f32x4){0, 0, 0, 0};
 #pragma unroll
-        for (int f = 0; f < NF; ++f) {
-          kv_u32x4 w;
+    for (int f = 0; f < NF; ++f) {
+      V8 kf[2];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const unsigned x = kr[b][f >> 1][(f & 1) * 2 + c];
-            w[2 * c] = __builtin_bit_cast(
-                unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, e, false));
-            w[2 * c + 1] = __builtin_bit_cast(
-                unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, e, true));
-          }
-          kf[f] = __builtin_bit_cast(V8, w);
+      for (int b = 0; b < 2; ++b) {
+        if constexpr (E8) {
+          kf[b] = __builtin_bit_cast(
+              V8, widen(kr[b][f >> 1][(f & 1) * 2], kr[b][f >> 1][(f & 1) * 2 + 1],
+                        __builtin_bit_cast(float, ksb[b] << 23)));
+        } else {
+          kf[b] = __builtin_bit_cast(V8, kr[b][f]);
         }
-      } else {
-#pragma unroll
-        for (int f = 0; f < NF; ++f) kf[f] = __builtin_bit_cast(V8, kr[b][f]);
       }
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
-        f32x4 c = (f32x4){0, 0, 0, 0};
-#pragma unroll
-        for (int f = 0; f < NF; ++f) c = TT::mfma(kf[f], qf[t][f], c);
-        sc[t][b] = c;
+        const V8 x = qs[(t * NF + f) * kWave + lane];
+        sc[t][0] = TT::mfma(kf[0], x, sc[t][0]);
+        sc[t][1] = TT::mfma(kf[1], x, sc[t][1]);
       }
     }
-    // the step that holds the request's own rows, or keys past its last, or
-    // lies on a page that is none
-    const bool edge = key0 + kTileKeys > prefix + 1 || bad0 || bad1;
-    // values into LDS
     unsigned long long odd = 0;  // rows of the step that hold NaN or infinity
-    if (!edge) {
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        unsigned char* dst = vt + (v * RPI + lane / LPR) * v_stride<D>() + (lane % LPR) * (32 / CB);
-        if constexpr (E8) {
-          const float e = __builtin_bit_cast(float, vsb[v] << 23);
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            kv_u32x4 w;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              w[2 * x] = __builtin_bit_cast(
-                  unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vr[v][2 * c + x], e, false));
-              w[2 * x + 1] = __builtin_bit_cast(
-                  unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vr[v][2 * c + x], e, true));
-            }
-            *reinterpret_cast<kv_u32x4*>(dst + 16 * c) = w;
-          }
-        } else {
-          *reinterpret_cast<kv_u32x4*>(dst) = vr[v];
-        }
-      }
-    } else {
-      // keys that do not exist hold anything: zeros in their place. NaN and
-      // infinity in a row that some query does not see must not meet its zero
-      // weight: such elements are left out here and added below.
+    if (edge) {
+      // values of keys that do not exist are anything: zeros in their place.
+      // NaN and infinity in a row that some query does not see must not meet
+      // its zero weight: such elements are left out here and added below.
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int row = v * RPI + lane / LPR;
-        const bool there = key0 + row < keys && !((row >> 4) ? bad1 : bad0);
-        unsigned char* dst = vt + row * v_stride<D>() + (lane % LPR) * (32 / CB);
-        bool strange = false;
+        const bool there = key0 + row < keys && (row >> 4 ? page1 : page0) >= 0;
+        unsigned strange = 0;
 #pragma unroll
-        for (int c = 0; c < 3 - CB; ++c) {
-          kv_u32x4 w = vr[v];
-          if constexpr (E8) {
-            const float e = __builtin_bit_cast(float, vsb[v] << 23);
+        for (int x = 0; x < 4; ++x) {
+          unsigned w = vr[v][x], out = 0;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              w[2 * x] = __builtin_bit_cast(
-                  unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vr[v][2 * c + x], e, false));
-              w[2 * x + 1] = __builtin_bit_cast(
-                  unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vr[v][2 * c + x], e, true));
-            }
+          for (int y = 0; y < 4 / CB; y += 1) {
+            constexpr unsigned E = E8 ? 0x7Fu : TT::kExpMask, all = E8 ? 0xFFu : 0xFFFFu;
+            const int at = y * 8 * CB;
+            if (((w >> at) & E) == E) out |= all << at;
           }
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            constexpr unsigned E = TT::kExpMask;
-            const bool lo = (w[x] & E) == E, hi = (w[x] & (E << 16)) == (E << 16);
-            strange |= lo || hi;
-            w[x] &= (lo ? 0xFFFF0000u : ~0u) & (hi ? 0x0000FFFFu : ~0u);
-            if (!there) w[x] = 0;
-          }
-          *reinterpret_cast<kv_u32x4*>(dst + 16 * c) = w;
+          strange |= out;
+          vr[v][x] = there ? w & ~out : 0;
         }
         unsigned long long found = __ballot(strange && there);
         while (found) {
-          const int at = (int)__builtin_ctzll(found);
+          odd |= 1ull << (v * RPI + (int)__builtin_ctzll(found) / LPR);
           found &= found - 1;
-          odd |= 1ull << (v * RPI + at / LPR);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const unsigned long long seen = seen_by(t);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int rel = key0 + (e >> 2) * 16 + g * 4 + (e & 3) - prefix;
+          const bool own = rel < len && ((seen >> ((rel - 1) & 63)) & 1);
+          if (((e >> 2) ? page1 : page0) < 0 || (rel > 0 && !own))
+            sc[t][e >> 2][e & 3] = -__builtin_inff();
         }
       }
     }
-    // the tile's loads are used up: the next tile's may start
-    const int page0 = id0, page1 = id1;
-    if (i + 1 < steps) issue(i + 1);
+    // values into LDS
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      unsigned char* dst = vt + (v * RPI + lane / LPR) * v_stride<D>() + (lane % LPR) * (32 / CB);
+#pragma unroll
+      for (int c = 0; c < 3 - CB; ++c) {
+        kv_u32x4 w = vr[v];
+        if constexpr (E8)
+          w = widen(vr[v][2 * c], vr[v][2 * c + 1], __builtin_bit_cast(float, vsb[v] << 23));
+        *reinterpret_cast<kv_u32x4*>(dst + 16 * c) = w;
+      }
+    }
+    // the step's loads are used up: the next one's start (the last step's again,
+    // unused, after it)
+    issue(min(i + 1, steps - 1));
 
     // weights
     V8 pf[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      float x[8];
+      float top = sc[t][0][0];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = sc[t][e >> 2][e & 3] * sl;
-      if (edge) {
-        const int j = by_group.quo((tile0 + t) * 16 + qi);
-        unsigned long long seen = j >= 64 ? ~0ull : (1ull << j) - 1;
-        if (a.req.parents) {
-          const unsigned long long path = __shfl(anc, max(j - 1, 0) & 63, kWave);
-          seen = j > 0 ? path : 0;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int rel = key0 + (e >> 2) * 16 + g * 4 + (e & 3) - prefix;
-          const bool vis = !((e >> 2) ? bad1 : bad0) &&
-                           (rel <= 0 || (rel < len && ((seen >> (rel - 1)) & 1)));
-          if (!vis) x[e] = -__builtin_inff();
-        }
-      }
-      float top = x[0];
-#pragma unroll
-      for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
-      if (__any(top > mx[t] + kSlack)) {
-        const float next = fmaxf(mx[t], group_max(top));
+      for (int e = 1; e < 8; ++e) top = fmaxf(top, sc[t][e >> 2][e & 3]);
+      if (__any(top * sl > mx[t] + kSlack)) {
+        const float next = fmaxf(mx[t], group_max(top * sl));
         const float fix =
             next == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(mx[t] - next);
         mx[t] = next;
@@ -400,7 +393,7 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
       const float ref = mx[t] == -__builtin_inff() ? 0.0f : mx[t];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float p = __builtin_amdgcn_exp2f(x[e] - ref);
+        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][e >> 2][e & 3], sl, -ref));
         l[t] += p;
         pf[t][e] = (T)p;
       }
@@ -425,28 +418,23 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
       const int64_t at = ((int64_t)h << ps) + ((key0 + row) & pm);
       const unsigned char* src = a.kv.v + id * a.kv.page_bytes + at * (D * CB);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const int j = by_group.quo((tile0 + t) * 16 + qi);
-        unsigned long long seen = j >= 64 ? ~0ull : (1ull << j) - 1;
-        if (a.req.parents) {
-          const unsigned long long path = __shfl(anc, max(j - 1, 0) & 63, kWave);
-          seen = j > 0 ? path : 0;
-        }
-        const bool vis = rel <= 0 || ((seen >> (rel - 1)) & 1);
+      for (int d = 0; d < ND; ++d) {
 #pragma unroll
-        for (int d = 0; d < ND; ++d) {
+        for (int e = 0; e < 4; ++e) {
+          const int col = d * 16 + g * 4 + e;
+          float v;
+          if (E8) {
+            v = (src[col] & 127) == 127 ? __builtin_nanf("") : 0.0f;
+          } else {
+            v = (float)reinterpret_cast<const T*>(src)[col];
+            v = finite_f32(v) ? 0.0f : v;
+          }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int col = d * 16 + g * 4 + e;
-            float v;
-            if (E8) {
-              v = (src[col] & 127) == 127 ? __builtin_nanf("") : 0.0f;
-            } else {
-              v = (float)reinterpret_cast<const T*>(src)[col];
-              v = finite_f32(v) ? 0.0f : v;
-            }
+          for (int t = 0; t < MT; ++t) {
+            const bool vis = rel <= 0 || ((seen_by(t) >> ((rel - 1) & 63)) & 1);
             if (vis) o[t][d][e] += v;
           }
+          asm volatile("" ::: "memory");  // one element at a time: no registers for a rare path
         }
       }
     }
@@ -520,8 +508,8 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
 // order: workgroup w takes the w-th equal share, so ragged contexts balance by
 // themselves and a long one is split over many workgroups.
 template <typename T, bool E8, int D, int MTMAX>
-__global__ __launch_bounds__(kThreads, MTMAX > 2 ? 1 : 2) void split_kernel(AttnArgs a, Parts ws) {
-  __shared__ __align__(16) unsigned char lds[kWaves * wave_lds<D>()];
+__global__ __launch_bounds__(kThreads, MTMAX > 3 || D == 256 ? 1 : 2) void split_kernel(AttnArgs a, Parts ws) {
+  __shared__ __align__(16) unsigned char lds[wg_lds<D, MTMAX>()];
   __shared__ float stat[kWaves][2][80];
   __shared__ int64_t wsum[kWaves];
   __shared__ int start_r;
@@ -604,11 +592,11 @@ __global__ __launch_bounds__(kThreads, MTMAX > 2 ? 1 : 2) void split_kernel(Attn
 // 16-row tiles of a segment, at most, for requests of up to `mtiles` of them.
 template <int D>
 constexpr int most_tiles() {
-  return D == 256 ? 2 : 5;
+  return D == 256 ? 3 : 5;
 }
 inline int segment_tiles(int D, int mtiles) {
-  const int most = D == 256 ? 2 : 5;
-  return mtiles <= 1 ? 1 : (mtiles <= 2 ? 2 : most);
+  const int most = D == 256 ? 3 : 5;
+  return mtiles <= 1 ? 1 : (mtiles <= 3 ? 3 : most);
 }
 
 template <typename T, bool E8, int D>
@@ -616,8 +604,8 @@ void launch_split(const AttnArgs& a, const Parts& ws, int mt_max, hipStream_t s)
   const dim3 grid((unsigned)ws.wgs), block(kThreads);
   if (mt_max == 1) {
     hipLaunchKernelGGL((split_kernel<T, E8, D, 1>), grid, block, 0, s, a, ws);
-  } else if (mt_max == 2) {
-    hipLaunchKernelGGL((split_kernel<T, E8, D, 2>), grid, block, 0, s, a, ws);
+  } else if (mt_max == 3) {
+    hipLaunchKernelGGL((split_kernel<T, E8, D, 3>), grid, block, 0, s, a, ws);
   } else {
     hipLaunchKernelGGL((split_kernel<T, E8, D, most_tiles<D>()>), grid, block, 0, s, a, ws);
   }
