@@ -12,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
@@ -25,6 +26,9 @@ ARCH = "gfx950"
 LIB_SOURCES = ["api.hip", "plan.hip", "pack.hip", "accept.hip", "tv.hip", "scatter.hip", "sts.hip", "sampling.hip",
                "api_target.hip", "kv_cache.hip", "tree_attention.hip",
                "tree_attention_d64.hip", "tree_attention_d128.hip", "tree_attention_d256.hip"]
+# sources whose generated code is checked for other uses of M0
+M0_SOURCES = ["tv.hip", "tree_attention_d64.hip", "tree_attention_d128.hip",
+              "tree_attention_d256.hip"]
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}",
@@ -62,14 +66,14 @@ def _run(cmd, verbose):
         raise RuntimeError(f"build failed: {cmd[-1]}")
 
 
-def check_m0_use(asm: str) -> None:
-    """The soft accept-rate kernels copy global memory straight into LDS with
-    inline assembly that sets M0 (the LDS address) itself, out of the
+def check_m0_use(asm: str, source: str = "tv.hip") -> None:
+    """The soft accept-rate and attention kernels copy global memory straight
+    into LDS with inline assembly that sets M0 (the LDS address) itself, out of the
     compiler's sight. That is sound only while nothing else in the code uses
     M0: raise unless every line of the gfx950 assembly that names m0 is one of
-    those inline-assembly statements (an `s_mov_b32 m0, sN` directly followed
-    by `s_nop 0` and `global_load_lds_dwordx4`, between the compiler's
-    ;;#ASMSTART / ;;#ASMEND markers)."""
+    those inline-assembly statements (an `s_mov_b32 m0` from a scalar register directly followed
+    by `s_nop 0` and `global_load_lds_dword` or `_dwordx4`, between the
+    compiler's ;;#ASMSTART / ;;#ASMEND markers)."""
     lines = asm.splitlines()
     inside = False
     for i, line in enumerate(lines):
@@ -82,11 +86,11 @@ def check_m0_use(asm: str) -> None:
             continue
         if t.startswith((";", ".")) or "m0" not in t.replace(",", " ").split():
             continue
-        ok = (inside and t.startswith("s_mov_b32 m0, s") and i + 2 < len(lines)
+        ok = (inside and t.startswith(("s_mov_b32 m0, s", "s_mov_b32 m0, vcc_")) and i + 2 < len(lines)
               and lines[i + 1].strip() == "s_nop 0"
-              and lines[i + 2].strip().startswith("global_load_lds_dwordx4"))
+              and lines[i + 2].strip().startswith(("global_load_lds_dwordx4 ", "global_load_lds_dword ")))
         if not ok:
-            raise RuntimeError(f"tv.hip: unexpected use of M0 in the generated code: {t!r}")
+            raise RuntimeError(f"{source}: unexpected use of M0 in the generated code: {t!r}")
 
 
 def build(verbose: bool = False) -> Path:
@@ -94,13 +98,17 @@ def build(verbose: bool = False) -> Path:
     hipcc = _hipcc()
     tmp = LIB.with_suffix(".so.tmp")
     _run([hipcc, *COMMON_FLAGS, "-o", tmp, *[CSRC / s for s in LIB_SOURCES]], verbose)
-    asm = LIB.with_suffix(".tv.s")
     flags = [f for f in COMMON_FLAGS if f not in ("-shared", "-fPIC")]
-    _run([hipcc, *flags, "-S", "--cuda-device-only", "-o", asm, CSRC / "tv.hip"], verbose)
+    asms = {s: LIB.with_suffix(f".{Path(s).stem}.s") for s in M0_SOURCES}
     try:
-        check_m0_use(asm.read_text())
+        with ThreadPoolExecutor(len(asms)) as pool:
+            list(pool.map(lambda s: _run([hipcc, *flags, "-S", "--cuda-device-only", "-o", asms[s],
+                                          CSRC / s], verbose), asms))
+        for s, asm in asms.items():
+            check_m0_use(asm.read_text(), s)
     finally:
-        asm.unlink()
+        for asm in asms.values():
+            asm.unlink(missing_ok=True)
     os.replace(tmp, LIB)
     tmp = HOSTCHECK.with_suffix(".so.tmp")
     _run([hipcc, *COMMON_FLAGS, "-o", tmp, CSRC / "hostcheck.hip"], verbose)

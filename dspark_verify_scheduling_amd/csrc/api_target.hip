@@ -39,11 +39,13 @@ dspark_status check_cache(const char* fn, const dspark_kv_cache* c, bool layers,
     return fail(DSPARK_E_INVALID,
                 "%s: block_stride = %lld must be >= %lld elements and a multiple of 16 bytes", fn,
                 (long long)c->block_stride, (long long)(tokens * c->head_dim));
-  if (e8 && (!c->k_scale || !c->v_scale || c->scale_block_stride < tokens ||
-             c->scale_block_stride > (1LL << 40)))
+  if (e8 && (!c->k_scale || !c->v_scale || !aligned16(c->k_scale) || !aligned16(c->v_scale) ||
+             c->scale_block_stride < tokens || c->scale_block_stride > (1LL << 40) ||
+             c->scale_block_stride % 16 != 0))
     return fail(DSPARK_E_INVALID,
-                "%s: an E4M3 cache needs k_scale, v_scale and scale_block_stride >= %lld", fn,
-                (long long)tokens);
+                "%s: an E4M3 cache needs k_scale and v_scale, 16-byte aligned, and "
+                "scale_block_stride >= %lld, a multiple of 16",
+                fn, (long long)tokens);
   if (layers) {
     if (c->num_layers < 1 || c->num_layers > DSPARK_MAX_LAYERS)
       return fail(DSPARK_E_INVALID, "%s: num_layers = %d outside [1, %d]", fn, c->num_layers,
@@ -51,7 +53,8 @@ dspark_status check_cache(const char* fn, const dspark_kv_cache* c, bool layers,
     if (c->num_layers > 1 &&
         (c->layer_stride < tokens * c->head_dim || c->layer_stride > (1LL << 50) ||
          c->layer_stride * cb % 16 != 0 ||
-         (e8 && (c->scale_layer_stride < tokens || c->scale_layer_stride > (1LL << 50)))))
+         (e8 && (c->scale_layer_stride < tokens || c->scale_layer_stride > (1LL << 50) ||
+                 c->scale_layer_stride % 16 != 0))))
       return fail(DSPARK_E_INVALID,
                   "%s: layers overlap, or their stride is not a multiple of 16 bytes", fn);
   }

@@ -10,8 +10,6 @@ namespace attn {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kTileKeys = 32;                      // keys of a wave's step
-constexpr int kUnitKeys = kWaves * kTileKeys;      // keys of a unit of work
 
 // What the split kernel leaves for the joining kernel: the schedule's prefix
 // sums, and per partial segment the running maximum and sum of each of its rows
@@ -26,17 +24,27 @@ struct Parts {
   int rows;       // rows of a segment, at most
 };
 
+// Tiles of 16 query rows of a segment, at most, and keys of a unit.
+template <int D>
+struct Size {
+  static constexpr int kTilesPerWave = D == 256 ? 1 : 2;
+  static constexpr int kTiles = kWaves * kTilesPerWave;
+  static constexpr int kKeys = D == 256 ? 32 : 64;
+};
+
 // Rows of a (request, key/value head): m = j * group + g for row j and the g-th
-// of the head's queries, in tiles of 16, up to `mt_max` tiles to a segment.
+// of the head's queries, in tiles of 16, several tiles to a segment.
 struct Shape {
   int len, prefix, c0;
   int mrows, mtiles;
-  int nseg, per;   // segments side by side, tiles of each
+  int nseg, per;  // segments side by side, tiles of each
   int64_t keys;
-  int nku;         // units along the keys
+  int nku;        // units along the keys
 };
 
-__device__ inline bool shape_of(const AttnArgs& a, int r, int total_eff, int mt_max, Shape* s) {
+template <int D>
+__device__ inline bool shape_of(const AttnArgs& a, int r, int total_eff, Shape* s) {
+  constexpr int kT = Size<D>::kTiles, kK = Size<D>::kKeys;
   if (!request_rows(a.req, r, total_eff, &s->c0, &s->len)) return false;
   s->prefix = a.req.prefix[r];
   s->keys = (int64_t)s->prefix + s->len;
@@ -45,15 +53,16 @@ __device__ inline bool shape_of(const AttnArgs& a, int r, int total_eff, int mt_
     return false;
   s->mrows = a.group * s->len;
   s->mtiles = (s->mrows + 15) >> 4;
-  s->nseg = (s->mtiles + mt_max - 1) / mt_max;
+  s->nseg = (s->mtiles + kT - 1) / kT;
   s->per = (s->mtiles + s->nseg - 1) / s->nseg;
-  s->nku = (int)((s->keys + kUnitKeys - 1) / kUnitKeys);
+  s->nku = (int)((s->keys + kK - 1) / kK);
   return true;
 }
 
-__device__ inline int64_t units_of(const AttnArgs& a, int r, int total_eff, int mt_max) {
+template <int D>
+__device__ inline int64_t units_of(const AttnArgs& a, int r, int total_eff) {
   Shape s;
-  return shape_of(a, r, total_eff, mt_max, &s) ? (int64_t)a.kv.hkv * s.nseg * s.nku : 0;
+  return shape_of<D>(a, r, total_eff, &s) ? (int64_t)a.kv.hkv * s.nseg * s.nku : 0;
 }
 
 // Workgroups that get units: never one without.
@@ -83,13 +92,66 @@ struct Types<_Float16> {
   }
 };
 
+typedef __attribute__((address_space(3))) unsigned char lds_u8;
+
 // Four rows of sixteen 16-bit elements, transposed: with the 16 lanes of a
 // group pointing at the rows' quarters in order, lane i gets column i.
 template <typename V4>
-__device__ inline V4 lds_columns(const void* p) {
+__device__ inline V4 lds_columns(unsigned at) {
   typedef __attribute__((ext_vector_type(4))) short s16x4;
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-  return __builtin_bit_cast(V4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p));
+  return __builtin_bit_cast(V4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)at));
+}
+
+// Eight rows of sixteen 8-bit elements, transposed: lanes point at the rows'
+// halves, lane i gets column i.
+__device__ inline kv_u32x2 lds_columns8(unsigned at) {
+  typedef __attribute__((ext_vector_type(2))) int i32x2;
+  typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
+  return __builtin_bit_cast(kv_u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)(uintptr_t)at));
+}
+
+template <typename X>
+__device__ inline X lds_read(unsigned at) {
+  return *(__attribute__((address_space(3))) const X*)(uintptr_t)at;
+}
+template <typename X>
+__device__ inline void lds_write(unsigned at, X x) {
+  *(__attribute__((address_space(3))) X*)(uintptr_t)at = x;
+}
+
+// Memory straight into LDS, 16 (or 4) bytes a lane at lds_at + 16 (4) * lane.
+// `from` and `lds_at` are wave-uniform; M0 holds lds_at (nothing else here uses
+// it). As inline assembly, the compiler's waits do not see the copies: its own
+// waits for loads only become more conservative by them, and wait_copies()
+// waits for the copies.
+__device__ inline void copy16(const unsigned char* from, unsigned lane_bytes, unsigned lds_at) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(lane_bytes), "s"(from), "s"(__builtin_amdgcn_readfirstlane((int)lds_at))
+               : "memory");
+}
+__device__ inline void copy4(const unsigned char* from, unsigned lane_bytes, unsigned lds_at) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+               :
+               : "v"(lane_bytes), "s"(from), "s"(__builtin_amdgcn_readfirstlane((int)lds_at))
+               : "memory");
+}
+// All but the last `N` loads of the wave are done (they end in order).
+template <int N>
+__device__ inline void wait_copies() {
+  static_assert(N >= 0 && N < 64, "the counter's width");
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+__device__ inline void barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
+}
+
+template <typename X>
+__device__ inline X* uniform(X* p) {
+  const uint64_t u = (uint64_t)p;
+  return (X*)(((uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((int)(u >> 32)) << 32) |
+              (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)u));
 }
 
 __device__ inline float group_max(float x) {
@@ -102,72 +164,213 @@ __device__ inline float group_sum(float x) {
   return x + __shfl_xor(x, 32, kWave);
 }
 
-// Row stride of the value tile in LDS: 32 bytes past the head's, so that the
-// four rows of a transposed read lie in different banks.
-template <int D>
-constexpr int v_stride() {
-  return 2 * D + 32;
-}
-
-// Row stride (floats) of a 16-row output tile in LDS.
-template <int D>
-constexpr int o_stride() {
-  return D + 4;
-}
-
-template <int D>
-constexpr int wave_lds() {
-  return kTileKeys * v_stride<D>() > 16 * o_stride<D>() * 4 ? kTileKeys * v_stride<D>()
-                                                            : 16 * o_stride<D>() * 4;
-}
-
-// LDS of a workgroup: the waves' regions, then the queries of its row tiles.
-template <int D, int MT>
-constexpr int wg_lds() {
-  return kWaves * wave_lds<D>() + MT * 16 * D * 2;
-}
-
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // A row's maximum follows its scores only when they pass it by this much (in
 // log2): weights then stay below 2^kSlack, and most steps rescale nothing.
 constexpr float kSlack = 8.0f;
 
-// One segment: the queries of `MT` 16-row tiles of one (request, key/value
-// head) over units [ku0, ku0 + n) of its keys. Each wave takes 32 keys of a
-// unit and keeps the statistics and outputs of all the segment's rows:
-//   S^T = K Q^T: keys are the rows of the product and queries its columns, so a
-//   lane holds 4 + 4 scores of one query (lane & 15), which are in place as the
-//   operand of  O^T = V^T P^T.  Keys go straight from memory into operands;
-//   values pass through the wave's LDS, where they are read by columns.
-template <typename T, bool E8, int D, int MT>
-__device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, const Shape& s, int r,
-                                        int h, int tile0, int64_t ku0, int n, bool whole,
-                                        int slot, unsigned char* lds, float (*stat)[2][80]) {
+// The tile of keys and values that a workgroup's waves share in LDS, in a ring
+// of kStages. Rows are unpadded (the copies into LDS write densely); 16-byte
+// chunk c of a row lies at chunk c ^ swizzle(row), so that the 16 rows which a
+// wave reads at one column spread over all banks.
+template <bool E8, int D>
+struct Ring {
+  static constexpr int CB = E8 ? 1 : 2;
+  static constexpr int kKeys = Size<D>::kKeys;
+  static constexpr int kGroups = kKeys / 16;
+  static constexpr int kRow = D * CB;                 // bytes of a row
+  static constexpr int kChunks = kRow / 16;
+  static constexpr int kRowsPerCopy = kWave / kChunks;
+  static constexpr int kCopies = 16 / kRowsPerCopy;   // copies of 16 rows
+  static constexpr int kTile = kKeys * kRow;          // keys, or values
+  static constexpr int kScales = 2 * kTile;           // offset of the exponents
+  static constexpr int kStage = 2 * kTile + (E8 ? 2 * kKeys : 0);
+  static constexpr int kStages = 65536 / (2 * kTile) < 4 ? 65536 / (2 * kTile) : 4;
+  // copies of a wave per stage: with 64 keys wave w has 16 keys and their
+  // values, with 32 keys 16 keys or their values
+  static constexpr int kPerWave = kGroups == 4 ? 2 * kCopies + (E8 ? 2 : 0) : kCopies + (E8 ? 1 : 0);
+  static constexpr int kFlags = kStages * kStage;     // bad pages, a byte per stage and wave
+  static constexpr int kOdd = kFlags + 4 * kStages;   // rows with NaN or infinity, 16 bits a group
+  static constexpr int kBytes = kOdd + 8 + (16 - (4 * kStages + 8) % 16) % 16;
+  static __device__ int swizzle(int row) {
+    return kChunks >= 16 ? row & 15 : (kChunks == 8 ? (row >> 1) & 7 : (row >> 2) & 3);
+  }
+};
+
+// One segment: the queries of several 16-row tiles of one (request, key/value
+// head) over units [ku0, ku0 + n) of its keys.
+struct Job {
+  Shape s;
+  int r, h, tile0, mt;
+  int n;         // units; 0: there is no such segment
+  int slot;      // its place among the parts
+  bool whole;    // it covers all the request's keys
+  int first;     // its first key
+};
+
+// Where a workgroup is in its share of the units.
+struct Cursor {
+  int64_t u, u1, off;  // next unit, end, next unit within request r
+  int64_t u0;
+  int64_t n_r;         // units of request r, -1: not known yet
+  int r;
+  Shape s;
+};
+
+template <int D>
+__device__ __forceinline__ Job next_job(const AttnArgs& a, int total_eff, Cursor& c) {
+  Job j;
+  j.n = 0;
+  while (c.u < c.u1) {
+    if (c.n_r < 0)
+      c.n_r = shape_of<D>(a, c.r, total_eff, &c.s) ? (int64_t)a.kv.hkv * c.s.nseg * c.s.nku : 0;
+    if (c.off >= c.n_r) {
+      ++c.r;
+      c.off = 0;
+      c.n_r = -1;
+      continue;
+    }
+    const Shape& s = c.s;
+    const int item = (int)(c.off / s.nku);
+    const int ku0 = (int)(c.off - (int64_t)item * s.nku);
+    j.s = s;
+    j.r = c.r;
+    j.n = (int)min((int64_t)(s.nku - ku0), c.u1 - c.u);
+    j.h = item / s.nseg;
+    const int seg = item - j.h * s.nseg;
+    j.tile0 = seg * s.per;
+    j.mt = min(s.per, s.mtiles - j.tile0);
+    j.whole = j.n == s.nku;
+    j.slot = 2 * blockIdx.x + (c.u == c.u0 ? 0 : 1);
+    j.first = ku0 * Size<D>::kKeys;
+    c.off += j.n;
+    c.u += j.n;
+    break;
+  }
+  return j;
+}
+
+// The producing side of the ring: this wave's copies of the next tile.
+template <bool E8, int D>
+struct Feeder {
+  typedef Ring<E8, D> R;
+  Cursor c;
+  Job j, nj;     // the job copied from, and the one after it
+  int i;         // its next tile
+  int ids, nids; // page ids of the wave's rows, lane l: tile id_first + l
+  int id_first;
+  int stage;
+
+  static __device__ int group_of(int wave) { return wave % R::kGroups; }
+
+  // The page ids have arrived here, and not at each of their uses: a wait for
+  // them would be one for the copies behind them too.
+  __device__ void settle() { asm volatile("" : "+v"(ids)); }
+
+  // lanes 0..63: the pages of 64 tiles from tile i on
+  __device__ int fetch(const AttnArgs& a, const Job& x, int t, int wave) const {
+    const int64_t key =
+        (int64_t)x.first + (int64_t)(t + lane_id()) * R::kKeys + group_of(wave) * 16;
+    const int p = (int)min(key, x.s.keys - 1) >> a.kv.page_shift;
+    return a.req.table[(size_t)x.r * a.req.width + p];
+  }
+
+  __device__ void start(const AttnArgs& a, int total_eff, const Cursor& at, int wave) {
+    c = at;
+    j = next_job<D>(a, total_eff, c);
+    ids = fetch(a, j, 0, wave);
+    settle();
+    nj = next_job<D>(a, total_eff, c);
+    nids = nj.n > 0 ? fetch(a, nj, 0, wave) : 0;
+    i = id_first = stage = 0;
+  }
+
+  __device__ void copies(const unsigned char* from, unsigned lds_at) const {
+    const int lane = lane_id();
+#pragma unroll
+    for (int n = 0; n < R::kCopies; ++n) {
+      const int row = n * R::kRowsPerCopy + lane / R::kChunks;
+      const unsigned chunk = (unsigned)((lane % R::kChunks) ^ R::swizzle(row));
+      copy16(from + n * R::kRowsPerCopy * R::kRow, (lane / R::kChunks) * R::kRow + chunk * 16,
+             lds_at + n * 1024);
+    }
+  }
+
+  __device__ void next(const AttnArgs& a, int total_eff, unsigned lds, int wave) {
+    if (j.n == 0) return;
+    const int g = group_of(wave);
+    const int key = j.first + i * R::kKeys + g * 16;
+    int id = __builtin_amdgcn_readlane(ids, i - id_first);
+    const bool bad = id < 0 || id >= a.kv.num_blocks;
+    if (bad) id = 0;  // any valid page: its keys are masked
+    const int64_t row =
+        ((int64_t)j.h << a.kv.page_shift) + (key & ((1 << a.kv.page_shift) - 1));
+    const unsigned base = lds + stage * R::kStage;
+    const unsigned char* k = uniform(a.kv.k + (int64_t)id * a.kv.page_bytes + row * R::kRow);
+    const unsigned char* v = uniform(a.kv.v + (int64_t)id * a.kv.page_bytes + row * R::kRow);
+    const unsigned kat = base + g * 16 * R::kRow, vat = kat + R::kTile;
+    if (R::kGroups == 4 || wave < 2) copies(k, kat);
+    if (R::kGroups == 4 || wave >= 2) copies(v, vat);
+    if constexpr (E8) {
+      const int64_t at = (int64_t)id * a.kv.scale_page_bytes + row;
+      const unsigned sc = base + R::kScales + g * 16;
+      if (lane_id() < 4) {
+        if (R::kGroups == 4 || wave < 2) copy4(uniform(a.kv.ks + at), lane_id() * 4, sc);
+        if (R::kGroups == 4 || wave >= 2)
+          copy4(uniform(a.kv.vs + at), lane_id() * 4, sc + R::kKeys);
+      }
+    }
+    if (lane_id() == 0)
+      lds_write<unsigned char>(lds + R::kFlags + stage * 4 + wave, bad ? 1 : 0);
+    stage = stage + 1 == R::kStages ? 0 : stage + 1;
+    if (++i == j.n) {
+      j = nj;
+      ids = nids;
+      settle();
+      i = id_first = 0;
+      if (j.n > 0) {
+        nj = next_job<D>(a, total_eff, c);
+        nids = nj.n > 0 ? fetch(a, nj, 0, wave) : 0;
+      }
+    } else if (i - id_first == kWave) {
+      ids = fetch(a, j, i, wave);
+      settle();
+      id_first = i;
+    }
+  }
+};
+
+// A wave's part of a segment: NT of its 16-row tiles (tile w, w + 4, ..; none for
+// a wave past the last) over all its keys, which the four waves bring into LDS
+// together. The products are
+//   S^T = K Q^T: keys are its rows and queries its columns, so a lane holds the
+//   scores of one query (lane & 15) for four keys of each sixteen, which are in
+//   place as the operand of  O^T = V^T P^T.
+template <typename T, bool E8, int D, int NT>
+__device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, const Job& job,
+                                        Feeder<E8, D>& feed, int total_eff, unsigned lds,
+                                        int64_t left, int& stage) {
   typedef Types<T> TT;
   typedef typename TT::V8 V8;
   typedef typename TT::V4 V4;
-  constexpr int CB = E8 ? 1 : 2;
-  constexpr int NF = D / 32;            // operand chunks of a key
-  constexpr int ND = D / 16;            // 16-column tiles of the output
-  constexpr int NK = E8 ? NF / 2 : NF;  // 16-byte loads of a key's share of a lane
-  constexpr int LPR = D * CB / 16;      // lanes of a value row
-  constexpr int RPI = kWave / LPR;      // value rows of a load
-  constexpr int NV = kTileKeys / RPI;   // loads of a value tile
-  const int tid = threadIdx.x, lane = tid & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int qi = lane & 15, g = lane >> 4;
-  const int ps = a.kv.page_shift, pm = (1 << ps) - 1;
+  typedef Ring<E8, D> R;
+  constexpr int NF = D / 32;         // operand chunks of a key
+  constexpr int ND = D / 16;         // 16-column tiles of the output
+  constexpr int NG = R::kGroups;     // 16-key groups of a tile
+  constexpr int NTX = NT ? NT : 1;
+  const Shape& s = job.s;
+  const int lane = lane_id(), qi = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int len = s.len, prefix = s.prefix;
   const int keys = (int)s.keys;
-  unsigned char* vt = lds + wave * wave_lds<D>();
+  const SmallDiv by_group(a.group);
 
   // the step's own tree: bit l of anc, in lane l, is row l + 1 itself, with its
   // ancestors' bits; row 0 is everybody's
   unsigned long long anc = 0;
-  if (a.req.parents) {
-    int up = lane + 1 < len ? a.req.parents[(size_t)r * a.req.gamma + lane] : 0;
-    if (__ballot(up < 0 || up > lane)) return;  // uniform over the workgroup
+  if (NT > 0 && a.req.parents) {
+    int up = lane + 1 < len ? a.req.parents[(size_t)job.r * a.req.gamma + lane] : 0;
     anc = 1ull << lane;
     for (int i = 0; i < 6; ++i) {
       const int from = max(up - 1, 0);
@@ -179,98 +382,37 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
       }
     }
   }
-
   // Scores in units of log2 with a positive factor, so that a masked score stays
   // -infinity under it: the scale's sign and its zero go into the queries.
   float sl = fminf(fabsf(a.scale) * kLog2e, 3.4028235e38f);
-  const unsigned sign = a.scale < 0.0f ? 0x80008000u : 0u;
   const bool flat = sl == 0.0f;
   if (flat) sl = 1.0f;
-  // the queries in LDS, in operand order: chunk f of tile t is one 16-byte read
-  // per lane. A lane's place in a key: of two 8-bit chunks in one load.
-  const SmallDiv by_group(a.group);
-  V8* qs = reinterpret_cast<V8*>(lds + kWaves * wave_lds<D>());
-  for (int c = tid; c < MT * NF * kWave; c += kThreads) {
-    const int t = c / (NF * kWave), f = (c / kWave) % NF;
-    const int m = (tile0 + t) * 16 + qi;
-    const int j = by_group.quo(m);
-    const int d = E8 ? (f >> 1) * 64 + g * 16 + (f & 1) * 8 : f * 32 + g * 8;
-    V8 x = (V8){0, 0, 0, 0, 0, 0, 0, 0};
-    if (m < s.mrows && !flat) {
-      kv_u32x4 w = *reinterpret_cast<const kv_u32x4*>(
-          a.q + (size_t)(s.c0 + j) * a.q_ld +
-          ((size_t)(h * a.group + (m - j * a.group)) * D + d) * 2);
-      w ^= sign;
-      x = __builtin_bit_cast(V8, w);
-    }
-    qs[c] = x;
-  }
-  __syncthreads();
-
-  f32x4 o[MT][ND];
-  float mx[MT], l[MT];
+  const unsigned sign = a.scale < 0.0f ? 0x80008000u : 0u;
+  // queries as operands. A lane's place in a key: of two 8-bit chunks in one read
+  V8 qf[NTX][NF];
+  f32x4 o[NTX][ND];
+  float mx[NTX], l[NTX];
+  int qrow[NTX];  // the request's row that the lane's query belongs to
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
+  for (int t = 0; t < NT; ++t) {
+    const int m = (job.tile0 + wave + kWaves * t) * 16 + qi;
+    const int row = by_group.quo(m);
+    qrow[t] = row;
+    const unsigned char* src = a.q + (size_t)(s.c0 + row) * a.q_ld +
+                               (size_t)(job.h * a.group + (m - row * a.group)) * D * 2;
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      const int d = E8 ? (f >> 1) * 64 + g * 16 + (f & 1) * 8 : f * 32 + g * 8;
+      kv_u32x4 w = (kv_u32x4){0, 0, 0, 0};
+      if (m < s.mrows && !flat) w = *reinterpret_cast<const kv_u32x4*>(src + d * 2) ^ sign;
+      qf[t][f] = __builtin_bit_cast(V8, w);
+    }
     mx[t] = -__builtin_inff();
     l[t] = 0.0f;
 #pragma unroll
     for (int d = 0; d < ND; ++d) o[t][d] = (f32x4){0, 0, 0, 0};
   }
 
-  const int32_t* table = a.req.table + (size_t)r * a.req.width;
-  const int last_page = (keys - 1) >> ps;
-  int ids = 0;       // page ids of the next 32 steps, two 16-key halves each
-  int id_first = 0;  // the step of lane 0
-  auto fetch_ids = [&](int i) {
-    id_first = i;
-    const int64_t key = (ku0 + i + (lane >> 1)) * kUnitKeys + wave * kTileKeys + (lane & 1) * 16;
-    const int p = (int)min(key >> ps, (int64_t)last_page);
-    const int id = table[p];
-    ids = id >= 0 && id < a.kv.num_blocks ? id : -1;
-  };
-
-  kv_u32x4 kr[2][NK], vr[NV];
-  unsigned ksb[2] = {0, 0}, vsb[NV];
-  int id0 = 0, id1 = 0;  // pages of the halves in flight
-  auto issue = [&](int i) {
-    if (i - id_first >= 32) fetch_ids(i);
-    id0 = __builtin_amdgcn_readlane(ids, 2 * (i - id_first));
-    id1 = __builtin_amdgcn_readlane(ids, 2 * (i - id_first) + 1);
-    const int key0 = (int)((ku0 + i) * kUnitKeys) + wave * kTileKeys;
-    const unsigned char *kp[2], *vp[2];
-    size_t sp[2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      // a page that is none: any valid address, its keys are masked
-      const int64_t id = max(b ? id1 : id0, 0);
-      const int64_t row = ((int64_t)h << ps) + ((key0 + 16 * b) & pm);
-      kp[b] = a.kv.k + id * a.kv.page_bytes + row * (D * CB);
-      vp[b] = a.kv.v + id * a.kv.page_bytes + row * (D * CB);
-      if (E8) sp[b] = (size_t)(id * a.kv.scale_page_bytes + row);
-    }
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-#pragma unroll
-      for (int f = 0; f < NK; ++f)
-        kr[b][f] = *reinterpret_cast<const kv_u32x4*>(kp[b] + qi * (D * CB) + f * 64 + g * 16);
-      if (E8) ksb[b] = a.kv.ks[sp[b] + qi];
-    }
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int b = (v * RPI) >> 4;
-      vr[v] = *reinterpret_cast<const kv_u32x4*>(vp[b] + ((v * RPI) & 15) * (D * CB) + lane * 16);
-      if (E8) vsb[v] = a.kv.vs[sp[b] + ((v * RPI) & 15) + lane / LPR];
-    }
-  };
-
-  // steps of this wave: those whose first key exists
-  const int64_t first = ku0 * kUnitKeys + wave * kTileKeys;
-  const int steps =
-      first >= keys ? 0 : (int)min((int64_t)n, (keys - first + kUnitKeys - 1) / kUnitKeys);
-  if (steps > 0) {
-    fetch_ids(0);
-    issue(0);
-  }
   // eight 8-bit elements, widened
   auto widen = [](unsigned lo, unsigned hi, float e) {
     kv_u32x4 w;
@@ -278,251 +420,292 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
     w[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, e, true));
     w[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, e, false));
     w[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, e, true));
-    return w;
+    return __builtin_bit_cast(V8, w);
   };
-  // rows of the step's own tree that a query sees, bit l for row l + 1
+  // rows of the step's own tree that the lane's query sees, bit l for row l + 1
   auto seen_by = [&](int t) {
-    const int j = by_group.quo((tile0 + t) * 16 + qi);
+    const int j = qrow[t];
     if (!a.req.parents) return j >= 64 ? ~0ull : (1ull << j) - 1;
     const unsigned long long path = __shfl(anc, max(j - 1, 0) & 63, kWave);
     return j > 0 ? path : 0ull;
   };
 
-  for (int i = 0; i < steps; ++i) {
-    const int key0 = (int)first + i * kUnitKeys;
-    const int page0 = id0, page1 = id1;
-    // the step holds keys that some query does not see (the request's own rows
-    // after its root, keys past its last), or lies on a page that is none
-    const bool edge = key0 + kTileKeys > prefix + 1 || page0 < 0 || page1 < 0;
-    // scores
-    f32x4 sc[MT][2];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) sc[t][0] = sc[t][1] = (f32x4){0, 0, 0, 0};
-#pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      V8 kf[2];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        if constexpr (E8) {
-          kf[b] = __builtin_bit_cast(
-              V8, widen(kr[b][f >> 1][(f & 1) * 2], kr[b][f >> 1][(f & 1) * 2 + 1],
-                        __builtin_bit_cast(float, ksb[b] << 23)));
-        } else {
-          kf[b] = __builtin_bit_cast(V8, kr[b][f]);
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const V8 x = qs[(t * NF + f) * kWave + lane];
-        sc[t][0] = TT::mfma(kf[0], x, sc[t][0]);
-        sc[t][1] = TT::mfma(kf[1], x, sc[t][1]);
-      }
-    }
-    unsigned long long odd = 0;  // rows of the step that hold NaN or infinity
-    if (edge) {
-      // values of keys that do not exist are anything: zeros in their place.
-      // NaN and infinity in a row that some query does not see must not meet
-      // its zero weight: such elements are left out here and added below.
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const int row = v * RPI + lane / LPR;
-        const bool there = key0 + row < keys && (row >> 4 ? page1 : page0) >= 0;
-        unsigned strange = 0;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          unsigned w = vr[v][x], out = 0;
-#pragma unroll
-          for (int y = 0; y < 4 / CB; y += 1) {
-            constexpr unsigned E = E8 ? 0x7Fu : TT::kExpMask, all = E8 ? 0xFFu : 0xFFFFu;
-            const int at = y * 8 * CB;
-            if (((w >> at) & E) == E) out |= all << at;
-          }
-          strange |= out;
-          vr[v][x] = there ? w & ~out : 0;
-        }
-        unsigned long long found = __ballot(strange && there);
-        while (found) {
-          odd |= 1ull << (v * RPI + (int)__builtin_ctzll(found) / LPR);
-          found &= found - 1;
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const unsigned long long seen = seen_by(t);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int rel = key0 + (e >> 2) * 16 + g * 4 + (e & 3) - prefix;
-          const bool own = rel < len && ((seen >> ((rel - 1) & 63)) & 1);
-          if (((e >> 2) ? page1 : page0) < 0 || (rel > 0 && !own))
-            sc[t][e >> 2][e & 3] = -__builtin_inff();
-        }
-      }
-    }
-    // values into LDS
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      unsigned char* dst = vt + (v * RPI + lane / LPR) * v_stride<D>() + (lane % LPR) * (32 / CB);
-#pragma unroll
-      for (int c = 0; c < 3 - CB; ++c) {
-        kv_u32x4 w = vr[v];
-        if constexpr (E8)
-          w = widen(vr[v][2 * c], vr[v][2 * c + 1], __builtin_bit_cast(float, vsb[v] << 23));
-        *reinterpret_cast<kv_u32x4*>(dst + 16 * c) = w;
-      }
-    }
-    // the step's loads are used up: the next one's start (the last step's again,
-    // unused, after it)
-    issue(min(i + 1, steps - 1));
+  // lane's offsets in a tile: its chunk of a key, its piece of a value row
+  const int key_at = qi * R::kRow + ((g ^ R::swizzle(qi)) << 4);
+  const int vrow = E8 ? g * 4 + ((qi >> 1) & 3) : g * 4 + (qi >> 2);
+  const int val_at = R::kTile +
+                     (E8 ? ((qi >> 3) * 16 + vrow) * R::kRow + (R::swizzle(vrow) << 4)
+                         : vrow * R::kRow + ((((qi >> 1) & 1) ^ R::swizzle(vrow)) << 4)) +
+                     (qi & 1) * 8;
 
-    // weights
-    V8 pf[MT];
+  for (int i = 0; i < job.n; ++i, --left) {
+    // this tile's copies are done when those of the stages after it may not be
+    if (left > R::kStages - 2) {
+      wait_copies<(R::kStages - 2) * R::kPerWave>();
+    } else {
+      wait_copies<0>();
+    }
+    barrier();
+    const unsigned buf = lds + stage * R::kStage;
+    const unsigned flags = lds_read<unsigned>(lds + R::kFlags + stage * 4);
+    feed.next(a, total_eff, lds, wave);
+    stage = stage + 1 == R::kStages ? 0 : stage + 1;
+    const int key0 = job.first + i * R::kKeys;
+    // the tile holds keys that some query does not see (the request's own rows
+    // after its root, keys past its last), or rows of a page that is none
+    const bool edge = key0 + R::kKeys > prefix + 1 ||
+                      __builtin_amdgcn_readfirstlane((int)flags) != 0;
+    auto missing = [&](int group) { return (flags >> (8 * group)) & 255u; };
+    unsigned long long odd = 0;  // rows of the tile that hold NaN or infinity
+    if (edge) {
+      // Values of keys that do not exist are anything: zeros in their place. NaN
+      // and infinity in a row that some query does not see must not meet its
+      // zero weight: such elements are left out here and added below.
+      if (wave < NG) {
+        unsigned strange_rows = 0;
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      float top = sc[t][0][0];
+        for (int n = 0; n < R::kCopies; ++n) {
+          const int row16 = n * R::kRowsPerCopy + lane / R::kChunks;
+          const bool there = key0 + wave * 16 + row16 < keys && !missing(wave);
+          const unsigned at = buf + R::kTile + wave * 16 * R::kRow + n * 1024 + lane * 16;
+          kv_u32x4 w = lds_read<kv_u32x4>(at);
+          unsigned strange = 0;
 #pragma unroll
-      for (int e = 1; e < 8; ++e) top = fmaxf(top, sc[t][e >> 2][e & 3]);
-      if (__any(top * sl > mx[t] + kSlack)) {
-        const float next = fmaxf(mx[t], group_max(top * sl));
-        const float fix =
-            next == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(mx[t] - next);
-        mx[t] = next;
-        l[t] *= fix;
+          for (int x = 0; x < 4; ++x) {
+            unsigned out = 0;
 #pragma unroll
-        for (int d = 0; d < ND; ++d) o[t][d] *= fix;
+            for (int y = 0; y < 4 / R::CB; ++y) {
+              constexpr unsigned E = E8 ? 0x7Fu : TT::kExpMask, all = E8 ? 0xFFu : 0xFFFFu;
+              const int sh = y * 8 * R::CB;
+              if (((w[x] >> sh) & E) == E) out |= all << sh;
+            }
+            strange |= out;
+            w[x] = there ? w[x] & ~out : 0;
+          }
+          lds_write(at, w);
+          unsigned long long found = __ballot(strange && there);
+          while (found) {
+            strange_rows |= 1u << (n * R::kRowsPerCopy + (int)__builtin_ctzll(found) / R::kChunks);
+            found &= found - 1;
+          }
+        }
+        if (E8 && lane < 16 && (key0 + wave * 16 + lane >= keys || missing(wave)))
+          lds_write<unsigned char>(buf + R::kScales + R::kKeys + wave * 16 + lane, 127);
+        if (lane == 0) lds_write<unsigned short>(lds + R::kOdd + wave * 2, (unsigned short)strange_rows);
       }
-      const float ref = mx[t] == -__builtin_inff() ? 0.0f : mx[t];
+      barrier();
+      if constexpr (NG == 4) {
+        odd = lds_read<unsigned long long>(lds + R::kOdd);
+      } else {
+        odd = lds_read<unsigned>(lds + R::kOdd);
+      }
+      odd = read_lane(odd, 0);
+    }
+    if constexpr (NT > 0) {
+      // scores
+      f32x4 sc[NT][NG];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][e >> 2][e & 3], sl, -ref));
-        l[t] += p;
-        pf[t][e] = (T)p;
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int b = 0; b < NG; ++b) sc[t][b] = (f32x4){0, 0, 0, 0};
+#pragma unroll
+      for (int b = 0; b < NG; b += 2) {
+        if constexpr (E8) {
+          float e[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            e[x] = __builtin_bit_cast(
+                float,
+                (unsigned)lds_read<unsigned char>(buf + R::kScales + (b + x) * 16 + qi) << 23);
+#pragma unroll
+          for (int p = 0; p < NF / 2; ++p) {
+            kv_u32x4 w[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              w[x] = lds_read<kv_u32x4>(buf + ((key_at ^ (p << 6)) + (b + x) * 16 * R::kRow));
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const V8 kf = widen(w[x][2 * y], w[x][2 * y + 1], e[x]);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                  sc[t][b + x] = TT::mfma(kf, qf[t][2 * p + y], sc[t][b + x]);
+              }
+          }
+        } else {
+#pragma unroll
+          for (int f = 0; f < NF; ++f)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const V8 kf = lds_read<V8>(buf + ((key_at ^ (f << 6)) + (b + x) * 16 * R::kRow));
+#pragma unroll
+              for (int t = 0; t < NT; ++t)
+                sc[t][b + x] = TT::mfma(kf, qf[t][f], sc[t][b + x]);
+            }
+        }
+      }
+      if (edge) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const unsigned long long seen = seen_by(t);
+#pragma unroll
+          for (int b = 0; b < NG; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int rel = key0 + b * 16 + g * 4 + e - prefix;
+              const bool own = rel < len && ((seen >> ((rel - 1) & 63)) & 1);
+              if (missing(b) || (rel > 0 && !own)) sc[t][b][e] = -__builtin_inff();
+            }
+        }
+      }
+      // weights
+      float vs[E8 ? NG : 1][4];
+      if constexpr (E8) {
+#pragma unroll
+        for (int b = 0; b < NG; ++b) {
+          const unsigned w = lds_read<unsigned>(buf + R::kScales + R::kKeys + b * 16 + g * 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            vs[b][e] = __builtin_bit_cast(float, ((w >> (8 * e)) & 255u) << 23);
+        }
+      }
+      V8 pf[NT][NG / 2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float top = sc[t][0][0];
+#pragma unroll
+        for (int b = 0; b < NG; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[t][b][e]);
+        if (__any(top * sl > mx[t] + kSlack)) {
+          const float next = fmaxf(mx[t], group_max(top * sl));
+          const float fix =
+              next == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(mx[t] - next);
+          mx[t] = next;
+          l[t] *= fix;
+#pragma unroll
+          for (int d = 0; d < ND; ++d) o[t][d] *= fix;
+        }
+        const float ref = mx[t] == -__builtin_inff() ? 0.0f : mx[t];
+#pragma unroll
+        for (int b = 0; b < NG; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][b][e], sl, -ref));
+            l[t] += p;
+            // an 8-bit value's power of two goes to its weight, exactly
+            if constexpr (E8) p *= vs[b][e];
+            pf[t][b >> 1][(b & 1) * 4 + e] = (T)p;
+          }
+      }
+      // O^T += V^T P^T
+#pragma unroll
+      for (int d0 = 0; d0 < ND; d0 += 2)
+#pragma unroll
+        for (int c = 0; c < NG / 2; ++c)
+#pragma unroll
+          for (int d = d0; d < d0 + 2; ++d) {
+            V8 vf;
+            if constexpr (E8) {
+              const kv_u32x2 w = lds_columns8(buf + ((val_at ^ (d << 4)) + c * 32 * R::kRow));
+              vf = widen(w[0], w[1], 1.0f);
+            } else {
+              const unsigned at = buf + ((val_at ^ (d << 5)) + c * 32 * R::kRow);
+              const V4 lo = lds_columns<V4>(at);
+              const V4 hi = lds_columns<V4>(at + 16 * R::kRow);
+              vf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) o[t][d] = TT::mfma(vf, pf[t][c], o[t][d]);
+          }
+      while (odd) {
+        // a row with NaN or infinity: they go to the queries that see it
+        const int row = (int)__builtin_ctzll(odd);
+        odd &= odd - 1;
+        const int key = key0 + row, rel = key - prefix;
+        const int64_t id = a.req.table[(size_t)job.r * a.req.width + (key >> a.kv.page_shift)];
+        const int64_t at =
+            ((int64_t)job.h << a.kv.page_shift) + (key & ((1 << a.kv.page_shift) - 1));
+        const unsigned char* src = a.kv.v + id * a.kv.page_bytes + at * R::kRow;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int col = d * 16 + g * 4 + e;
+            float v;
+            if (E8) {
+              v = (src[col] & 127) == 127 ? __builtin_nanf("") : 0.0f;
+            } else {
+              v = (float)reinterpret_cast<const T*>(src)[col];
+              v = finite_f32(v) ? 0.0f : v;
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const bool vis = rel <= 0 || ((seen_by(t) >> ((rel - 1) & 63)) & 1);
+              if (vis) o[t][d][e] += v;
+            }
+            asm volatile("" ::: "memory");  // one element at a time: no registers for a rare path
+          }
+        }
       }
     }
-    // O^T += V^T P^T
+  }
+
 #pragma unroll
-    for (int d = 0; d < ND; ++d) {
-      const unsigned char* at =
-          vt + (g * 4 + (qi >> 2)) * v_stride<D>() + d * 32 + (qi & 3) * 8;
-      const V4 lo = lds_columns<V4>(at);
-      const V4 hi = lds_columns<V4>(at + 16 * v_stride<D>());
-      const V8 vf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-      for (int t = 0; t < MT; ++t) o[t][d] = TT::mfma(vf, pf[t], o[t][d]);
-    }
-    while (odd) {
-      // a row with NaN or infinity: they go to the queries that see it
-      const int row = (int)__builtin_ctzll(odd);
-      odd &= odd - 1;
-      const int64_t id = row >> 4 ? page1 : page0;
-      const int rel = key0 + row - prefix;
-      const int64_t at = ((int64_t)h << ps) + ((key0 + row) & pm);
-      const unsigned char* src = a.kv.v + id * a.kv.page_bytes + at * (D * CB);
+  for (int t = 0; t < NT; ++t) {
+    const float sum = group_sum(l[t]);
+    const int m = (job.tile0 + wave + kWaves * t) * 16 + qi;
+    if (m >= s.mrows) continue;
+    if (job.whole) {
+      const int head = job.h * a.group + (m - qrow[t] * a.group);
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      T* dst = reinterpret_cast<T*>(a.out + (size_t)(s.c0 + qrow[t]) * a.out_ld) + head * D + g * 4;
 #pragma unroll
       for (int d = 0; d < ND; ++d) {
+        V4 z;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int col = d * 16 + g * 4 + e;
-          float v;
-          if (E8) {
-            v = (src[col] & 127) == 127 ? __builtin_nanf("") : 0.0f;
-          } else {
-            v = (float)reinterpret_cast<const T*>(src)[col];
-            v = finite_f32(v) ? 0.0f : v;
-          }
+        for (int e = 0; e < 4; ++e) z[e] = (T)(o[t][d][e] * inv);
+        *reinterpret_cast<V4*>(dst + d * 16) = z;
+      }
+      if (a.lse && g == 0)
+        a.lse[(size_t)(s.c0 + qrow[t]) * a.num_heads + head] =
+            sum == 0.0f ? -__builtin_inff() : (mx[t] + __builtin_amdgcn_logf(sum)) * kLn2;
+    } else {
+      const size_t at = (size_t)job.slot * ws.rows + (wave + kWaves * t) * 16 + qi;
+      float* dst = ws.o + at * D + g * 4;
 #pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            const bool vis = rel <= 0 || ((seen_by(t) >> ((rel - 1) & 63)) & 1);
-            if (vis) o[t][d][e] += v;
-          }
-          asm volatile("" ::: "memory");  // one element at a time: no registers for a rare path
-        }
+      for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4*>(dst + d * 16) = o[t][d];
+      if (g == 0) {
+        ws.m[at] = mx[t];
+        ws.l[at] = sum;
       }
     }
-  }
-
-  // the waves' parts, through LDS: statistics first, then a 16-row tile at a time
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    l[t] = group_sum(l[t]);
-    if (g == 0) {
-      stat[wave][0][t * 16 + qi] = mx[t];
-      stat[wave][1][t * 16 + qi] = l[t];
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    float top = stat[0][0][t * 16 + qi];
-    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, stat[w][0][t * 16 + qi]);
-    const float fix = top == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(mx[t] - top);
-    float* mine = reinterpret_cast<float*>(vt) + qi * o_stride<D>() + g * 4;
-#pragma unroll
-    for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4*>(mine + d * 16) = o[t][d] * fix;
-    __syncthreads();
-    for (int c = tid; c < 16 * (D / 8); c += kThreads) {
-      const int row = c / (D / 8), col = (c % (D / 8)) * 8;
-      const int m = (tile0 + t) * 16 + row;
-      if (m >= s.mrows) continue;
-      f32x4 y[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-      float rtop = stat[0][0][t * 16 + row], rsum = 0.0f;
-      for (int w = 1; w < kWaves; ++w) rtop = fmaxf(rtop, stat[w][0][t * 16 + row]);
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const float* from =
-            reinterpret_cast<const float*>(lds + w * wave_lds<D>()) + row * o_stride<D>() + col;
-        y[0] += *reinterpret_cast<const f32x4*>(from);
-        y[1] += *reinterpret_cast<const f32x4*>(from + 4);
-        rsum += rtop == -__builtin_inff()
-                    ? stat[w][1][t * 16 + row]
-                    : stat[w][1][t * 16 + row] *
-                          __builtin_amdgcn_exp2f(stat[w][0][t * 16 + row] - rtop);
-      }
-      if (whole) {
-        const int j = by_group.quo(m);
-        const int head = h * a.group + (m - j * a.group);
-        const float inv = rsum == 0.0f ? 0.0f : 1.0f / rsum;
-        V8 z;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] = (T)(y[e >> 2][e & 3] * inv);
-        *reinterpret_cast<V8*>(a.out + (size_t)(s.c0 + j) * a.out_ld + (size_t)(head * D + col) * 2) =
-            z;
-        if (a.lse && col == 0)
-          a.lse[(size_t)(s.c0 + j) * a.num_heads + head] =
-              rsum == 0.0f ? -__builtin_inff() : (rtop + __builtin_amdgcn_logf(rsum)) * kLn2;
-      } else {
-        const size_t at = (size_t)slot * ws.rows + t * 16 + row;
-        f32x4* to = reinterpret_cast<f32x4*>(ws.o + at * D + col);
-        to[0] = y[0];
-        to[1] = y[1];
-        if (col == 0) {
-          ws.m[at] = rtop;
-          ws.l[at] = rsum;
-        }
-      }
-    }
-    __syncthreads();
   }
 }
 
 // Persistent over the units of all (request, key/value head, row segment)s in
 // order: workgroup w takes the w-th equal share, so ragged contexts balance by
-// themselves and a long one is split over many workgroups.
-template <typename T, bool E8, int D, int MTMAX>
-__global__ __launch_bounds__(kThreads, MTMAX > 3 || D == 256 ? 1 : 2) void split_kernel(AttnArgs a, Parts ws) {
-  __shared__ __align__(16) unsigned char lds[wg_lds<D, MTMAX>()];
-  __shared__ float stat[kWaves][2][80];
+// themselves and a long one is split over many workgroups. The ring of tiles
+// runs on across segments.
+template <typename T, bool E8, int D>
+__global__ __launch_bounds__(kThreads, 2) void split_kernel(AttnArgs a, Parts ws) {
+  typedef Ring<E8, D> R;
+  __shared__ __align__(1024) unsigned char lds_mem[R::kBytes];
   __shared__ int64_t wsum[kWaves];
   __shared__ int start_r;
   __shared__ int64_t start_off;
   const ReqView& q = a.req;
   const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const unsigned lds = (unsigned)(uintptr_t)(lds_u8*)lds_mem;
   int rows_total;
   const int total_eff = rows_in_use(q, &rows_total);
   // every workgroup sums the requests' units by itself
   const int per = (q.B + kThreads - 1) / kThreads;
   const int r0 = min(tid * per, q.B), r1 = min(r0 + per, q.B);
   int64_t mine = 0;
-  for (int r = r0; r < r1; ++r) mine += units_of(a, r, total_eff, MTMAX);
+  for (int r = r0; r < r1; ++r) mine += units_of<D>(a, r, total_eff);
   int64_t total;
   int64_t at = block_excl_scan<int64_t, kThreads>(mine, wsum, &total);
   const int wgs = wgs_in_use(total, gridDim.x);
@@ -530,7 +713,7 @@ __global__ __launch_bounds__(kThreads, MTMAX > 3 || D == 256 ? 1 : 2) void split
     int64_t b = at;
     for (int r = r0; r < r1; ++r) {
       ws.base[r] = b;
-      b += units_of(a, r, total_eff, MTMAX);
+      b += units_of<D>(a, r, total_eff);
     }
     if (tid == 0) {
       ws.base[q.B] = total;
@@ -542,7 +725,7 @@ __global__ __launch_bounds__(kThreads, MTMAX > 3 || D == 256 ? 1 : 2) void split
   const int64_t u0 = wg_start(total, blockIdx.x, wgs), u1 = wg_start(total, blockIdx.x + 1, wgs);
   if (at <= u0 && u0 < at + mine) {
     for (int r = r0; r < r1; ++r) {
-      const int64_t n = units_of(a, r, total_eff, MTMAX);
+      const int64_t n = units_of<D>(a, r, total_eff);
       if (u0 < at + n) {
         start_r = r;
         start_off = u0 - at;
@@ -552,79 +735,54 @@ __global__ __launch_bounds__(kThreads, MTMAX > 3 || D == 256 ? 1 : 2) void split
     }
   }
   __syncthreads();
-  int r = __builtin_amdgcn_readfirstlane(start_r);
-  int64_t off = start_off;
-  int64_t u = u0;
-  while (u < u1) {
-    Shape s;
-    const int64_t n_r =
-        shape_of(a, r, total_eff, MTMAX, &s) ? (int64_t)a.kv.hkv * s.nseg * s.nku : 0;
-    if (off >= n_r) {
-      ++r;
-      off = 0;
-      continue;
+  Cursor cur;
+  cur.u0 = cur.u = u0;
+  cur.u1 = u1;
+  cur.r = __builtin_amdgcn_readfirstlane(start_r);
+  cur.off = read_lane(start_off, 0);
+  cur.n_r = -1;
+  Feeder<E8, D> feed;
+  feed.start(a, total_eff, cur, wave);
+#pragma unroll
+  for (int i = 0; i < R::kStages - 1; ++i) feed.next(a, total_eff, lds, wave);
+  int64_t left = u1 - u0;
+  int stage = 0;
+  for (;;) {
+    const Job job = next_job<D>(a, total_eff, cur);
+    if (job.n == 0) break;
+    // tiles of this wave; none of a request whose tree is none
+    int nt = max(0, (job.mt - wave + kWaves - 1) / kWaves);
+    if (q.parents) {
+      const int lane = lane_id();
+      const int up = lane + 1 < job.s.len ? q.parents[(size_t)job.r * q.gamma + lane] : 0;
+      if (__ballot(up < 0 || up > lane)) nt = 0;
     }
-    const int item = (int)(off / s.nku);
-    const int64_t ku0 = off - (int64_t)item * s.nku;
-    const int n = (int)min(s.nku - ku0, u1 - u);
-    const int h = item / s.nseg, seg = item - h * s.nseg;
-    const bool whole = n == s.nku;
-    const int slot = 2 * blockIdx.x + (u == u0 ? 0 : 1);
-    const int tile0 = seg * s.per, mt = min(s.per, s.mtiles - tile0);
-#define DSPARK_SEGMENT(MT)                                                                     \
-  case MT:                                                                                     \
-    if constexpr (MT <= MTMAX)                                                                 \
-      segment<T, E8, D, MT>(a, ws, s, r, h, tile0, ku0, n, whole, slot, lds, stat);            \
-    break;
-    switch (mt) {
-      DSPARK_SEGMENT(1)
-      DSPARK_SEGMENT(2)
-      DSPARK_SEGMENT(3)
-      DSPARK_SEGMENT(4)
-      DSPARK_SEGMENT(5)
+    if (nt == 0) {
+      segment<T, E8, D, 0>(a, ws, job, feed, total_eff, lds, left, stage);
+    } else if (nt == 1) {
+      segment<T, E8, D, 1>(a, ws, job, feed, total_eff, lds, left, stage);
+    } else if constexpr (Size<D>::kTilesPerWave > 1) {
+      segment<T, E8, D, 2>(a, ws, job, feed, total_eff, lds, left, stage);
     }
-#undef DSPARK_SEGMENT
-    off += n;
-    u += n;
+    left -= job.n;
   }
 }
 
-// 16-row tiles of a segment, at most, for requests of up to `mtiles` of them.
 template <int D>
-constexpr int most_tiles() {
-  return D == 256 ? 3 : 5;
-}
-inline int segment_tiles(int D, int mtiles) {
-  const int most = D == 256 ? 3 : 5;
-  return mtiles <= 1 ? 1 : (mtiles <= 3 ? 3 : most);
-}
-
-template <typename T, bool E8, int D>
-void launch_split(const AttnArgs& a, const Parts& ws, int mt_max, hipStream_t s) {
+void launch_dim(const AttnArgs& a, const Parts& ws, dspark_dtype dt, hipStream_t s) {
   const dim3 grid((unsigned)ws.wgs), block(kThreads);
-  if (mt_max == 1) {
-    hipLaunchKernelGGL((split_kernel<T, E8, D, 1>), grid, block, 0, s, a, ws);
-  } else if (mt_max == 3) {
-    hipLaunchKernelGGL((split_kernel<T, E8, D, 3>), grid, block, 0, s, a, ws);
-  } else {
-    hipLaunchKernelGGL((split_kernel<T, E8, D, most_tiles<D>()>), grid, block, 0, s, a, ws);
-  }
-}
-
-template <int D>
-void launch_dim(const AttnArgs& a, const Parts& ws, dspark_dtype dt, int mt_max, hipStream_t s) {
   if (a.kv.cb == 1) {
-    launch_split<__bf16, true, D>(a, ws, mt_max, s);
+    hipLaunchKernelGGL((split_kernel<__bf16, true, D>), grid, block, 0, s, a, ws);
   } else if (dt == DSPARK_BF16) {
-    launch_split<__bf16, false, D>(a, ws, mt_max, s);
+    hipLaunchKernelGGL((split_kernel<__bf16, false, D>), grid, block, 0, s, a, ws);
   } else {
-    launch_split<_Float16, false, D>(a, ws, mt_max, s);
+    hipLaunchKernelGGL((split_kernel<_Float16, false, D>), grid, block, 0, s, a, ws);
   }
 }
 
-void launch_dim64(const AttnArgs& a, const Parts& ws, dspark_dtype dt, int mt_max, hipStream_t s);
-void launch_dim128(const AttnArgs& a, const Parts& ws, dspark_dtype dt, int mt_max, hipStream_t s);
-void launch_dim256(const AttnArgs& a, const Parts& ws, dspark_dtype dt, int mt_max, hipStream_t s);
+void launch_dim64(const AttnArgs& a, const Parts& ws, dspark_dtype dt, hipStream_t s);
+void launch_dim128(const AttnArgs& a, const Parts& ws, dspark_dtype dt, hipStream_t s);
+void launch_dim256(const AttnArgs& a, const Parts& ws, dspark_dtype dt, hipStream_t s);
 
 }  // namespace attn
 }  // namespace dspark

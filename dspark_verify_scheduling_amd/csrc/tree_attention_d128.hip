@@ -4,8 +4,8 @@
 namespace dspark {
 namespace attn {
 
-void launch_dim128(const AttnArgs& a, const Parts& ws, dspark_dtype dt, int mt_max, hipStream_t s) {
-  launch_dim<128>(a, ws, dt, mt_max, s);
+void launch_dim128(const AttnArgs& a, const Parts& ws, dspark_dtype dt, hipStream_t s) {
+  launch_dim<128>(a, ws, dt, s);
 }
 
 }  // namespace attn

@@ -669,13 +669,14 @@ size_t dspark_sts_workspace_size(int32_t N, int32_t gamma, int32_t n_t, int32_t 
 typedef struct dspark_kv_cache {
   void* k;           /* device, 16-byte aligned */
   void* v;
-  uint8_t* k_scale;  /* device; E4M3 only, otherwise ignored */
+  uint8_t* k_scale;  /* device, 16-byte aligned; E4M3 only, otherwise ignored */
   uint8_t* v_scale;
   int64_t block_stride;       /* elements from page to page, >= num_kv_heads *
                                  block_size * head_dim, a multiple of 16 bytes */
-  int64_t scale_block_stride; /* bytes from page to page of the exponents */
+  int64_t scale_block_stride; /* bytes from page to page of the exponents, a
+                                 multiple of 16 */
   int64_t layer_stride;       /* elements from layer to layer; dspark_kv_commit */
-  int64_t scale_layer_stride; /* bytes from layer to layer; dspark_kv_commit */
+  int64_t scale_layer_stride; /* bytes, a multiple of 16; dspark_kv_commit */
   int32_t num_layers;         /* dspark_kv_commit; the other calls use layer 0 */
   int32_t num_blocks;         /* pages of each layer, >= 1 */
   int32_t num_kv_heads;       /* 1..DSPARK_MAX_HEADS */

@@ -74,7 +74,7 @@ BAD_CACHES = [
     (_cache(num_blocks=0), INV), (_cache(k=None), INV), (_cache(v=0x1008), INV),
     (_cache(block_stride=2047), INV), (_cache(block_stride=2052), INV),
     (_e8(k_scale=None), INV), (_e8(v_scale=None), INV), (_e8(scale_block_stride=31), INV),
-    (_e8(block_stride=2056), INV),
+    (_e8(block_stride=2056), INV), (_e8(k_scale=0x3004), INV), (_e8(scale_block_stride=40), INV),
 ]
 
 
@@ -151,7 +151,7 @@ def test_read_and_commit_refusals():
     assert _commit(_cache(num_layers=0), meta=FAKE) == INV
     assert _commit(_cache(num_layers=1025), meta=FAKE) == INV
     assert _commit(_cache(num_layers=2, layer_stride=1024), meta=FAKE) == INV  # layers overlap
-    assert _commit(_e8(num_layers=2, layer_stride=2048, scale_layer_stride=1), meta=FAKE) == INV
+    assert _commit(_e8(num_layers=2, layer_stride=2048, scale_layer_stride=40), meta=FAKE) == INV
 
 
 @pytest.mark.parametrize("kw,code", [
