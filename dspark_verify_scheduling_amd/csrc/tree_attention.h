@@ -29,7 +29,7 @@ template <int D>
 struct Size {
   static constexpr int kTilesPerWave = D == 256 ? 1 : 2;
   static constexpr int kTiles = kWaves * kTilesPerWave;
-  static constexpr int kKeys = D == 256 ? 32 : 64;
+  static constexpr int kKeys = D >= 128 ? 32 : 64;
 };
 
 // Rows of a (request, key/value head): m = j * group + g for row j and the g-th
@@ -38,31 +38,42 @@ struct Shape {
   int len, prefix, c0;
   int mrows, mtiles;
   int nseg, per;  // segments side by side, tiles of each
-  int64_t keys;
+  int keys;
   int nku;        // units along the keys
 };
 
-template <int D>
-__device__ inline bool shape_of(const AttnArgs& a, int r, int total_eff, Shape* s) {
-  constexpr int kT = Size<D>::kTiles, kK = Size<D>::kKeys;
-  if (!request_rows(a.req, r, total_eff, &s->c0, &s->len)) return false;
-  s->prefix = a.req.prefix[r];
-  s->keys = (int64_t)s->prefix + s->len;
-  if (s->prefix < 0 || s->keys > ((int64_t)a.req.width << a.kv.page_shift) ||
-      s->keys > 0x7FFFFF00LL)  // cache indices in 32 bits, a unit beyond included
-    return false;
-  s->mrows = a.group * s->len;
-  s->mtiles = (s->mrows + 15) >> 4;
-  s->nseg = (s->mtiles + kT - 1) / kT;
-  s->per = (s->mtiles + s->nseg - 1) / s->nseg;
-  s->nku = (int)((s->keys + kK - 1) / kK);
-  return true;
+// Whether a request's rows are well formed (its tree and pages apart); their
+// place and its prefix.
+__device__ inline bool rows_of(const AttnArgs& a, int r, int total_eff, int* c0, int* len,
+                               int* prefix) {
+  const bool ok = request_rows(a.req, r, total_eff, c0, len);
+  *prefix = a.req.prefix[r];
+  const int64_t keys = (int64_t)*prefix + *len;
+  // (cache indices in 32 bits, a unit beyond included)
+  return ok && *prefix >= 0 && keys <= ((int64_t)a.req.width << a.kv.page_shift) &&
+         keys <= 0x7FFFFF00LL;
 }
 
 template <int D>
-__device__ inline int64_t units_of(const AttnArgs& a, int r, int total_eff) {
+__device__ inline Shape shape_of(const AttnArgs& a, int c0, int len, int prefix) {
+  constexpr int kT = Size<D>::kTiles, kK = Size<D>::kKeys;
   Shape s;
-  return shape_of<D>(a, r, total_eff, &s) ? (int64_t)a.kv.hkv * s.nseg * s.nku : 0;
+  s.c0 = c0;
+  s.len = len;
+  s.prefix = prefix;
+  s.keys = prefix + len;
+  s.mrows = a.group * len;
+  s.mtiles = (s.mrows + 15) >> 4;
+  s.nseg = (s.mtiles + kT - 1) / kT;
+  s.per = (s.mtiles + s.nseg - 1) / s.nseg;
+  s.nku = (s.keys + kK - 1) / kK;
+  return s;
+}
+
+template <int D>
+__device__ inline int64_t units_of(const AttnArgs& a, int c0, int len, int prefix) {
+  const Shape s = shape_of<D>(a, c0, len, prefix);
+  return (int64_t)a.kv.hkv * s.nseg * s.nku;
 }
 
 // Workgroups that get units: never one without.
@@ -103,14 +114,6 @@ __device__ inline V4 lds_columns(unsigned at) {
   return __builtin_bit_cast(V4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)at));
 }
 
-// Eight rows of sixteen 8-bit elements, transposed: lanes point at the rows'
-// halves, lane i gets column i.
-__device__ inline kv_u32x2 lds_columns8(unsigned at) {
-  typedef __attribute__((ext_vector_type(2))) int i32x2;
-  typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
-  return __builtin_bit_cast(kv_u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)(uintptr_t)at));
-}
-
 template <typename X>
 __device__ inline X lds_read(unsigned at) {
   return *(__attribute__((address_space(3))) const X*)(uintptr_t)at;
@@ -126,7 +129,7 @@ __device__ inline void lds_write(unsigned at, X x) {
 // waits for loads only become more conservative by them, and wait_copies()
 // waits for the copies.
 __device__ inline void copy16(const unsigned char* from, unsigned lane_bytes, unsigned lds_at) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt"
                :
                : "v"(lane_bytes), "s"(from), "s"(__builtin_amdgcn_readfirstlane((int)lds_at))
                : "memory");
@@ -170,82 +173,124 @@ constexpr float kLn2 = 0.6931471805599453f;
 // log2): weights then stay below 2^kSlack, and most steps rescale nothing.
 constexpr float kSlack = 8.0f;
 
-// The tile of keys and values that a workgroup's waves share in LDS, in a ring
-// of kStages. Rows are unpadded (the copies into LDS write densely); 16-byte
-// chunk c of a row lies at chunk c ^ swizzle(row), so that the 16 rows which a
-// wave reads at one column spread over all banks.
+// LDS of a workgroup. A tile of keys and values in 16 bits is shared by its
+// waves; rows are unpadded (copies into LDS write densely), and 16-byte chunk c
+// of a row lies at chunk c ^ swizzle(row), so that the 16 rows which a wave reads
+// at one column spread over all banks.
+//   16-bit caches: a ring of kStages tiles, filled straight from memory.
+//   8-bit caches: each wave has a ring of kStages pieces of codes and exponents
+//   for itself, and widens its piece of the next tile into one of two tiles.
 template <bool E8, int D>
 struct Ring {
   static constexpr int CB = E8 ? 1 : 2;
   static constexpr int kKeys = Size<D>::kKeys;
   static constexpr int kGroups = kKeys / 16;
-  static constexpr int kRow = D * CB;                 // bytes of a row
-  static constexpr int kChunks = kRow / 16;
-  static constexpr int kRowsPerCopy = kWave / kChunks;
-  static constexpr int kCopies = 16 / kRowsPerCopy;   // copies of 16 rows
+  static constexpr int kRow = 2 * D;                  // bytes of a row of a tile
   static constexpr int kTile = kKeys * kRow;          // keys, or values
-  static constexpr int kScales = 2 * kTile;           // offset of the exponents
-  static constexpr int kStage = 2 * kTile + (E8 ? 2 * kKeys : 0);
-  static constexpr int kStages = 65536 / (2 * kTile) < 4 ? 65536 / (2 * kTile) : 4;
-  // copies of a wave per stage: with 64 keys wave w has 16 keys and their
-  // values, with 32 keys 16 keys or their values
-  static constexpr int kPerWave = kGroups == 4 ? 2 * kCopies + (E8 ? 2 : 0) : kCopies + (E8 ? 1 : 0);
-  static constexpr int kFlags = kStages * kStage;     // bad pages, a byte per stage and wave
-  static constexpr int kOdd = kFlags + 4 * kStages;   // rows with NaN or infinity, 16 bits a group
-  static constexpr int kBytes = kOdd + 8 + (16 - (4 * kStages + 8) % 16) % 16;
+  static constexpr int kTiles = 2 * kTile;            // both
+  // copies of 16 rows: kWave 16-byte chunks each
+  static constexpr int kChunks = D * CB / 16;         // of a cache row
+  static constexpr int kRowsPerCopy = kWave / kChunks;
+  static constexpr int kCopies = 16 / kRowsPerCopy;
+  // a wave's share of a tile: with 64 keys the wave's 16 and their values, with
+  // 32 keys 16 of them (waves 0 and 1) or their values (2 and 3)
+  static constexpr int kParts = kGroups == 4 ? 2 : 1;
+  static constexpr int kPerWave = kParts * (kCopies + (E8 ? 1 : 0));
+  static constexpr int kPart = 16 * D + 64;           // codes, exponents; 8 bits
+  static constexpr int kPiece = kParts * kPart;
+  static constexpr int kRaw = 2 * kTiles;             // offset of the waves' rings
+  static constexpr int kStages =
+      E8 ? (D == 256 ? 2 : 4) : (65536 / kTiles < 4 ? 65536 / kTiles : 4);
+  static constexpr int kFlags = E8 ? kRaw + kStages * kWaves * kPiece : kStages * kTiles;
+  // bad pages, a byte per stage and wave (8 bits: per tile and wave, after the
+  // wave's own per stage)
+  static constexpr int kOdd = kFlags + 4 * kStages + 8;  // rows with NaN or infinity, 16 bits a
+                                                         // group, two tiles
+  static constexpr int kBytes = kOdd + 16;
+  // workgroups to a CU, of its 160 KiB
+  static constexpr int kPerCu = kBytes <= 81920 - 256 ? 2 : 1;
+  static_assert(kBytes <= 163840 - 256, "a CU's LDS");
   static __device__ int swizzle(int row) {
-    return kChunks >= 16 ? row & 15 : (kChunks == 8 ? (row >> 1) & 7 : (row >> 2) & 3);
+    return D >= 128 ? row & 15 : (row >> 1) & 7;
   }
 };
 
 // One segment: the queries of several 16-row tiles of one (request, key/value
-// head) over units [ku0, ku0 + n) of its keys.
+// head) over some units of its keys. What the copies need of it,
+struct Span {
+  int r, h;
+  int first;  // its first key
+  int n;      // units; 0: there is no such segment
+  int keys;   // of the request
+};
+// and the rest.
 struct Job {
   Shape s;
-  int r, h, tile0, mt;
-  int n;         // units; 0: there is no such segment
-  int slot;      // its place among the parts
-  bool whole;    // it covers all the request's keys
-  int first;     // its first key
+  int tile0, mt;
+  int slot;    // its place among the parts
+  bool whole;  // it covers all the request's keys
 };
 
-// Where a workgroup is in its share of the units.
+// Where a wave is in its workgroup's share of the units. Lane l holds the rows
+// of request `window + l` (len 0: malformed), so that most steps from request to
+// request read nothing.
 struct Cursor {
-  int64_t u, u1, off;  // next unit, end, next unit within request r
-  int64_t u0;
-  int64_t n_r;         // units of request r, -1: not known yet
-  int r;
-  Shape s;
+  int64_t left;  // units of the share still to come
+  int64_t off;   // next unit within request r
+  int64_t n_r;   // units of request r, -1: not known yet
+  int r, window;
+  int begun;     // 0 before the share's first segment
+  int w_c0, w_len, w_prefix;
 };
+
+__device__ inline void load_window(const AttnArgs& a, int total_eff, int first, Cursor& c) {
+  const int r = first + lane_id();
+  c.window = first;
+  c.w_c0 = c.w_len = c.w_prefix = 0;
+  if (r < a.req.B) {
+    int c0, len, prefix;
+    if (rows_of(a, r, total_eff, &c0, &len, &prefix)) {
+      c.w_c0 = c0;
+      c.w_len = len;
+      c.w_prefix = prefix;
+    }
+  }
+}
 
 template <int D>
-__device__ __forceinline__ Job next_job(const AttnArgs& a, int total_eff, Cursor& c) {
-  Job j;
+__device__ __forceinline__ Span next_span(const AttnArgs& a, int total_eff, Cursor& c, Job* job) {
+  Span j;
   j.n = 0;
-  while (c.u < c.u1) {
-    if (c.n_r < 0)
-      c.n_r = shape_of<D>(a, c.r, total_eff, &c.s) ? (int64_t)a.kv.hkv * c.s.nseg * c.s.nku : 0;
+  while (c.left > 0) {
+    if (c.r - c.window >= kWave) load_window(a, total_eff, c.r, c);
+    const int l = c.r - c.window;
+    const int len = read_lane(c.w_len, l);
+    const Shape s = shape_of<D>(a, read_lane(c.w_c0, l), len, read_lane(c.w_prefix, l));
+    if (c.n_r < 0) c.n_r = len ? (int64_t)a.kv.hkv * s.nseg * s.nku : 0;
     if (c.off >= c.n_r) {
       ++c.r;
       c.off = 0;
       c.n_r = -1;
       continue;
     }
-    const Shape& s = c.s;
     const int item = (int)(c.off / s.nku);
     const int ku0 = (int)(c.off - (int64_t)item * s.nku);
-    j.s = s;
     j.r = c.r;
-    j.n = (int)min((int64_t)(s.nku - ku0), c.u1 - c.u);
+    j.n = (int)min((int64_t)(s.nku - ku0), c.left);
     j.h = item / s.nseg;
-    const int seg = item - j.h * s.nseg;
-    j.tile0 = seg * s.per;
-    j.mt = min(s.per, s.mtiles - j.tile0);
-    j.whole = j.n == s.nku;
-    j.slot = 2 * blockIdx.x + (c.u == c.u0 ? 0 : 1);
     j.first = ku0 * Size<D>::kKeys;
+    j.keys = s.keys;
+    if (job) {
+      const int seg = item - j.h * s.nseg;
+      job->s = s;
+      job->tile0 = seg * s.per;
+      job->mt = min(s.per, s.mtiles - job->tile0);
+      job->whole = j.n == s.nku;
+      job->slot = 2 * blockIdx.x + c.begun;
+    }
+    c.begun = 1;
     c.off += j.n;
-    c.u += j.n;
+    c.left -= j.n;
     break;
   }
   return j;
@@ -256,7 +301,7 @@ template <bool E8, int D>
 struct Feeder {
   typedef Ring<E8, D> R;
   Cursor c;
-  Job j, nj;     // the job copied from, and the one after it
+  Span j, nj;    // the segment copied from, and the one after it
   int i;         // its next tile
   int ids, nids; // page ids of the wave's rows, lane l: tile id_first + l
   int id_first;
@@ -269,34 +314,37 @@ struct Feeder {
   __device__ void settle() { asm volatile("" : "+v"(ids)); }
 
   // lanes 0..63: the pages of 64 tiles from tile i on
-  __device__ int fetch(const AttnArgs& a, const Job& x, int t, int wave) const {
+  __device__ int fetch(const AttnArgs& a, const Span& x, int t, int wave) const {
     const int64_t key =
         (int64_t)x.first + (int64_t)(t + lane_id()) * R::kKeys + group_of(wave) * 16;
-    const int p = (int)min(key, x.s.keys - 1) >> a.kv.page_shift;
+    const int p = (int)min(key, (int64_t)x.keys - 1) >> a.kv.page_shift;
     return a.req.table[(size_t)x.r * a.req.width + p];
   }
 
   __device__ void start(const AttnArgs& a, int total_eff, const Cursor& at, int wave) {
     c = at;
-    j = next_job<D>(a, total_eff, c);
+    j = next_span<D>(a, total_eff, c, nullptr);
     ids = fetch(a, j, 0, wave);
     settle();
-    nj = next_job<D>(a, total_eff, c);
+    nj = next_span<D>(a, total_eff, c, nullptr);
     nids = nj.n > 0 ? fetch(a, nj, 0, wave) : 0;
     i = id_first = stage = 0;
   }
 
-  __device__ void copies(const unsigned char* from, unsigned lds_at) const {
+  // 16 rows of the cache; SWIZZLE: as rows of a tile
+  template <bool SWIZZLE>
+  static __device__ void copies(const unsigned char* from, unsigned lds_at) {
     const int lane = lane_id();
 #pragma unroll
     for (int n = 0; n < R::kCopies; ++n) {
       const int row = n * R::kRowsPerCopy + lane / R::kChunks;
-      const unsigned chunk = (unsigned)((lane % R::kChunks) ^ R::swizzle(row));
-      copy16(from + n * R::kRowsPerCopy * R::kRow, (lane / R::kChunks) * R::kRow + chunk * 16,
-             lds_at + n * 1024);
+      const int chunk = SWIZZLE ? (lane % R::kChunks) ^ R::swizzle(row) : lane % R::kChunks;
+      copy16(from + n * R::kRowsPerCopy * D * R::CB,
+             (lane / R::kChunks) * D * R::CB + (unsigned)chunk * 16, lds_at + n * 1024);
     }
   }
 
+  // Starts the wave's copies of the next tile.
   __device__ void next(const AttnArgs& a, int total_eff, unsigned lds, int wave) {
     if (j.n == 0) return;
     const int g = group_of(wave);
@@ -306,19 +354,20 @@ struct Feeder {
     if (bad) id = 0;  // any valid page: its keys are masked
     const int64_t row =
         ((int64_t)j.h << a.kv.page_shift) + (key & ((1 << a.kv.page_shift) - 1));
-    const unsigned base = lds + stage * R::kStage;
-    const unsigned char* k = uniform(a.kv.k + (int64_t)id * a.kv.page_bytes + row * R::kRow);
-    const unsigned char* v = uniform(a.kv.v + (int64_t)id * a.kv.page_bytes + row * R::kRow);
-    const unsigned kat = base + g * 16 * R::kRow, vat = kat + R::kTile;
-    if (R::kGroups == 4 || wave < 2) copies(k, kat);
-    if (R::kGroups == 4 || wave >= 2) copies(v, vat);
-    if constexpr (E8) {
-      const int64_t at = (int64_t)id * a.kv.scale_page_bytes + row;
-      const unsigned sc = base + R::kScales + g * 16;
-      if (lane_id() < 4) {
-        if (R::kGroups == 4 || wave < 2) copy4(uniform(a.kv.ks + at), lane_id() * 4, sc);
-        if (R::kGroups == 4 || wave >= 2)
-          copy4(uniform(a.kv.vs + at), lane_id() * 4, sc + R::kKeys);
+#pragma unroll
+    for (int p = 0; p < R::kParts; ++p) {
+      const bool values = R::kParts == 2 ? p == 1 : wave >= 2;
+      const unsigned char* from = uniform((values ? a.kv.v : a.kv.k) +
+                                          (int64_t)id * a.kv.page_bytes + row * (D * R::CB));
+      if constexpr (E8) {
+        const unsigned to =
+            lds + R::kRaw + (stage * kWaves + wave) * R::kPiece + p * R::kPart;
+        copies<false>(from, to);
+        if (lane_id() < 4)
+          copy4(uniform((values ? a.kv.vs : a.kv.ks) + (int64_t)id * a.kv.scale_page_bytes + row),
+                lane_id() * 4, to + 16 * D);
+      } else {
+        copies<true>(from, lds + stage * R::kTiles + (values ? R::kTile : 0) + g * 16 * R::kRow);
       }
     }
     if (lane_id() == 0)
@@ -330,7 +379,7 @@ struct Feeder {
       settle();
       i = id_first = 0;
       if (j.n > 0) {
-        nj = next_job<D>(a, total_eff, c);
+        nj = next_span<D>(a, total_eff, c, nullptr);
         nids = nj.n > 0 ? fetch(a, nj, 0, wave) : 0;
       }
     } else if (i - id_first == kWave) {
@@ -348,9 +397,9 @@ struct Feeder {
 //   scores of one query (lane & 15) for four keys of each sixteen, which are in
 //   place as the operand of  O^T = V^T P^T.
 template <typename T, bool E8, int D, int NT>
-__device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, const Job& job,
-                                        Feeder<E8, D>& feed, int total_eff, unsigned lds,
-                                        int64_t left, int& stage) {
+__device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, const Span& span,
+                                        const Job& job, Feeder<E8, D>& feed, int total_eff,
+                                        unsigned lds, int64_t left, int& stage) {
   typedef Types<T> TT;
   typedef typename TT::V8 V8;
   typedef typename TT::V4 V4;
@@ -363,14 +412,14 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
   const int lane = lane_id(), qi = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int len = s.len, prefix = s.prefix;
-  const int keys = (int)s.keys;
+  const int keys = s.keys;
   const SmallDiv by_group(a.group);
 
   // the step's own tree: bit l of anc, in lane l, is row l + 1 itself, with its
   // ancestors' bits; row 0 is everybody's
   unsigned long long anc = 0;
   if (NT > 0 && a.req.parents) {
-    int up = lane + 1 < len ? a.req.parents[(size_t)job.r * a.req.gamma + lane] : 0;
+    int up = lane + 1 < len ? a.req.parents[(size_t)span.r * a.req.gamma + lane] : 0;
     anc = 1ull << lane;
     for (int i = 0; i < 6; ++i) {
       const int from = max(up - 1, 0);
@@ -388,7 +437,7 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
   const bool flat = sl == 0.0f;
   if (flat) sl = 1.0f;
   const unsigned sign = a.scale < 0.0f ? 0x80008000u : 0u;
-  // queries as operands. A lane's place in a key: of two 8-bit chunks in one read
+  // queries as operands
   V8 qf[NTX][NF];
   f32x4 o[NTX][ND];
   float mx[NTX], l[NTX];
@@ -399,10 +448,10 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
     const int row = by_group.quo(m);
     qrow[t] = row;
     const unsigned char* src = a.q + (size_t)(s.c0 + row) * a.q_ld +
-                               (size_t)(job.h * a.group + (m - row * a.group)) * D * 2;
+                               (size_t)(span.h * a.group + (m - row * a.group)) * D * 2;
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
-      const int d = E8 ? (f >> 1) * 64 + g * 16 + (f & 1) * 8 : f * 32 + g * 8;
+      const int d = f * 32 + g * 8;
       kv_u32x4 w = (kv_u32x4){0, 0, 0, 0};
       if (m < s.mrows && !flat) w = *reinterpret_cast<const kv_u32x4*>(src + d * 2) ^ sign;
       qf[t][f] = __builtin_bit_cast(V8, w);
@@ -413,15 +462,6 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
     for (int d = 0; d < ND; ++d) o[t][d] = (f32x4){0, 0, 0, 0};
   }
 
-  // eight 8-bit elements, widened
-  auto widen = [](unsigned lo, unsigned hi, float e) {
-    kv_u32x4 w;
-    w[0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, e, false));
-    w[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, e, true));
-    w[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, e, false));
-    w[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, e, true));
-    return __builtin_bit_cast(V8, w);
-  };
   // rows of the step's own tree that the lane's query sees, bit l for row l + 1
   auto seen_by = [&](int t) {
     const int j = qrow[t];
@@ -432,119 +472,180 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
 
   // lane's offsets in a tile: its chunk of a key, its piece of a value row
   const int key_at = qi * R::kRow + ((g ^ R::swizzle(qi)) << 4);
-  const int vrow = E8 ? g * 4 + ((qi >> 1) & 3) : g * 4 + (qi >> 2);
-  const int val_at = R::kTile +
-                     (E8 ? ((qi >> 3) * 16 + vrow) * R::kRow + (R::swizzle(vrow) << 4)
-                         : vrow * R::kRow + ((((qi >> 1) & 1) ^ R::swizzle(vrow)) << 4)) +
+  const int vrow = g * 4 + (qi >> 2);
+  const int val_at = R::kTile + vrow * R::kRow + ((((qi >> 1) & 1) ^ R::swizzle(vrow)) << 4) +
                      (qi & 1) * 8;
 
-  for (int i = 0; i < job.n; ++i, --left) {
-    // this tile's copies are done when those of the stages after it may not be
-    if (left > R::kStages - 2) {
-      wait_copies<(R::kStages - 2) * R::kPerWave>();
-    } else {
-      wait_copies<0>();
-    }
-    barrier();
-    const unsigned buf = lds + stage * R::kStage;
-    const unsigned flags = lds_read<unsigned>(lds + R::kFlags + stage * 4);
-    feed.next(a, total_eff, lds, wave);
-    stage = stage + 1 == R::kStages ? 0 : stage + 1;
-    const int key0 = job.first + i * R::kKeys;
+  for (int i = 0; i < span.n; ++i, --left) {
+    const int key0 = span.first + i * R::kKeys;
     // the tile holds keys that some query does not see (the request's own rows
-    // after its root, keys past its last), or rows of a page that is none
-    const bool edge = key0 + R::kKeys > prefix + 1 ||
-                      __builtin_amdgcn_readfirstlane((int)flags) != 0;
-    auto missing = [&](int group) { return (flags >> (8 * group)) & 255u; };
-    unsigned long long odd = 0;  // rows of the tile that hold NaN or infinity
-    if (edge) {
-      // Values of keys that do not exist are anything: zeros in their place. NaN
-      // and infinity in a row that some query does not see must not meet its
-      // zero weight: such elements are left out here and added below.
-      if (wave < NG) {
+    // after its root, keys past its last), or (found below) rows of a page that
+    // is none
+    bool edge = key0 + R::kKeys > prefix + 1;
+    unsigned buf, flags;
+    unsigned odd_at = lds + R::kOdd;
+    // Values of keys that do not exist are anything: zeros in their place. NaN and
+    // infinity in a row that some query does not see must not meet its zero
+    // weight: such elements are left out here and added below. Four 16-bit (8-bit
+    // codes: eight) elements at a time; returns what was left out.
+    auto clean = [&](kv_u32x4& w, bool there) {
+      unsigned strange = 0;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        unsigned out = 0;
+#pragma unroll
+        for (int y = 0; y < 4 / R::CB; ++y) {
+          constexpr unsigned E = E8 ? 0x7Fu : TT::kExpMask, all = E8 ? 0xFFu : 0xFFFFu;
+          const int sh = y * 8 * R::CB;
+          if (((w[x] >> sh) & E) == E) out |= all << sh;
+        }
+        strange |= out;
+        w[x] = there ? w[x] & ~out : 0;
+      }
+      return strange != 0 && there;
+    };
+    // rows (16 bits) that a ballot over copy n's lanes names
+    auto rows_in = [&](unsigned long long found, int n) {
+      unsigned rows = 0;
+      while (found) {
+        rows |= 1u << (n * R::kRowsPerCopy + (int)__builtin_ctzll(found) / R::kChunks);
+        found &= found - 1;
+      }
+      return rows;
+    };
+    if constexpr (E8) {
+      // the wave's piece of this tile: done when the pieces after it may not be
+      if (left > R::kStages - 1) {
+        wait_copies<(R::kStages - 1) * R::kPerWave>();
+      } else {
+        wait_copies<0>();
+      }
+      const int tile = (int)(left & 1);
+      buf = lds + tile * R::kTiles;
+      odd_at += tile * 8;
+      const int gr = Feeder<E8, D>::group_of(wave);
+      const unsigned mine = (unsigned)__builtin_amdgcn_readfirstlane(
+          (int)lds_read<unsigned char>(lds + R::kFlags + stage * 4 + wave));
+#pragma unroll
+      for (int p = 0; p < R::kParts; ++p) {
+        const bool values = R::kParts == 2 ? p == 1 : wave >= 2;
+        const unsigned from = lds + R::kRaw + (stage * kWaves + wave) * R::kPiece + p * R::kPart;
+        const unsigned to = buf + (values ? R::kTile : 0) + gr * 16 * R::kRow;
         unsigned strange_rows = 0;
 #pragma unroll
         for (int n = 0; n < R::kCopies; ++n) {
-          const int row16 = n * R::kRowsPerCopy + lane / R::kChunks;
-          const bool there = key0 + wave * 16 + row16 < keys && !missing(wave);
-          const unsigned at = buf + R::kTile + wave * 16 * R::kRow + n * 1024 + lane * 16;
-          kv_u32x4 w = lds_read<kv_u32x4>(at);
-          unsigned strange = 0;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            unsigned out = 0;
-#pragma unroll
-            for (int y = 0; y < 4 / R::CB; ++y) {
-              constexpr unsigned E = E8 ? 0x7Fu : TT::kExpMask, all = E8 ? 0xFFu : 0xFFFFu;
-              const int sh = y * 8 * R::CB;
-              if (((w[x] >> sh) & E) == E) out |= all << sh;
-            }
-            strange |= out;
-            w[x] = there ? w[x] & ~out : 0;
+          const int row = n * R::kRowsPerCopy + lane / R::kChunks;
+          const int c = lane % R::kChunks;
+          kv_u32x4 w = lds_read<kv_u32x4>(from + n * 1024 + lane * 16);
+          unsigned b = lds_read<unsigned char>(from + 16 * D + row);
+          if (values && (edge || mine)) {
+            const bool there = key0 + gr * 16 + row < keys && !mine;
+            strange_rows |= rows_in(__ballot(clean(w, there)), n);
+            b = there ? b : 127u;
           }
-          lds_write(at, w);
-          unsigned long long found = __ballot(strange && there);
-          while (found) {
-            strange_rows |= 1u << (n * R::kRowsPerCopy + (int)__builtin_ctzll(found) / R::kChunks);
-            found &= found - 1;
+          const float e = __builtin_bit_cast(float, b << 23);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            kv_u32x4 z;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              z[2 * y] = __builtin_bit_cast(
+                  unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * x + y], e, false));
+              z[2 * y + 1] = __builtin_bit_cast(
+                  unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * x + y], e, true));
+            }
+            lds_write(to + row * R::kRow + (((2 * c + x) ^ R::swizzle(row)) << 4), z);
           }
         }
-        if (E8 && lane < 16 && (key0 + wave * 16 + lane >= keys || missing(wave)))
-          lds_write<unsigned char>(buf + R::kScales + R::kKeys + wave * 16 + lane, 127);
-        if (lane == 0) lds_write<unsigned short>(lds + R::kOdd + wave * 2, (unsigned short)strange_rows);
+        if (values && lane == 0)
+          lds_write<unsigned short>(odd_at + gr * 2, (unsigned short)strange_rows);
+      }
+      if (lane == 0)
+        lds_write<unsigned char>(lds + R::kFlags + 4 * R::kStages + tile * 4 + wave,
+                                 (unsigned char)mine);
+      feed.next(a, total_eff, lds, wave);
+      barrier();
+      flags = lds_read<unsigned>(lds + R::kFlags + 4 * R::kStages + tile * 4);
+      edge |= __builtin_amdgcn_readfirstlane((int)flags) != 0;
+    } else {
+      // this tile's copies are done when those of the stages after it may not be
+      if (left > R::kStages - 2) {
+        wait_copies<(R::kStages - 2) * R::kPerWave>();
+      } else {
+        wait_copies<0>();
       }
       barrier();
-      if constexpr (NG == 4) {
-        odd = lds_read<unsigned long long>(lds + R::kOdd);
-      } else {
-        odd = lds_read<unsigned>(lds + R::kOdd);
+      buf = lds + stage * R::kTiles;
+      flags = lds_read<unsigned>(lds + R::kFlags + stage * 4);
+      feed.next(a, total_eff, lds, wave);
+      edge |= __builtin_amdgcn_readfirstlane((int)flags) != 0;
+      if (edge) {
+        if (wave < NG) {
+          unsigned strange_rows = 0;
+#pragma unroll
+          for (int n = 0; n < R::kCopies; ++n) {
+            const int row = wave * 16 + n * R::kRowsPerCopy + lane / R::kChunks;
+            const bool there = key0 + row < keys && !((flags >> (8 * wave)) & 255u);
+            const unsigned at = buf + R::kTile + wave * 16 * R::kRow + n * 1024 + lane * 16;
+            kv_u32x4 w = lds_read<kv_u32x4>(at);
+            strange_rows |= rows_in(__ballot(clean(w, there)), n);
+            lds_write(at, w);
+          }
+          if (lane == 0) lds_write<unsigned short>(odd_at + wave * 2, (unsigned short)strange_rows);
+        }
+        barrier();
       }
-      odd = read_lane(odd, 0);
+    }
+    stage = stage + 1 == R::kStages ? 0 : stage + 1;
+    auto missing = [&](int group) { return (flags >> (8 * group)) & 255u; };
+    unsigned long long odd = 0;  // rows of the tile that hold NaN or infinity
+    if (edge) {
+      if constexpr (NG == 4) {
+        odd = read_lane(lds_read<unsigned long long>(odd_at), 0);
+      } else {
+        odd = (unsigned)read_lane((int)lds_read<unsigned>(odd_at), 0);
+      }
     }
     if constexpr (NT > 0) {
-      // scores
+      // Scores. Reads from LDS go out in batches, ahead of the products that use
+      // them and, for the values, of the softmax: one at a time, their latency is
+      // most of the loop.
       f32x4 sc[NT][NG];
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int b = 0; b < NG; ++b) sc[t][b] = (f32x4){0, 0, 0, 0};
+      constexpr int FB = NF < 4 ? NF : 4;
 #pragma unroll
-      for (int b = 0; b < NG; b += 2) {
-        if constexpr (E8) {
-          float e[2];
+      for (int b = 0; b < NG; b += 2)
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
-            e[x] = __builtin_bit_cast(
-                float,
-                (unsigned)lds_read<unsigned char>(buf + R::kScales + (b + x) * 16 + qi) << 23);
+        for (int f0 = 0; f0 < NF; f0 += FB) {
+          V8 kf[FB][2];
 #pragma unroll
-          for (int p = 0; p < NF / 2; ++p) {
-            kv_u32x4 w[2];
+          for (int f = 0; f < FB; ++f)
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-              w[x] = lds_read<kv_u32x4>(buf + ((key_at ^ (p << 6)) + (b + x) * 16 * R::kRow));
+              kf[f][x] =
+                  lds_read<V8>(buf + ((key_at ^ ((f0 + f) << 6)) + (b + x) * 16 * R::kRow));
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int y = 0; y < 2; ++y)
+          for (int f = 0; f < FB; ++f)
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const V8 kf = widen(w[x][2 * y], w[x][2 * y + 1], e[x]);
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                  sc[t][b + x] = TT::mfma(kf, qf[t][2 * p + y], sc[t][b + x]);
-              }
-          }
-        } else {
-#pragma unroll
-          for (int f = 0; f < NF; ++f)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const V8 kf = lds_read<V8>(buf + ((key_at ^ (f << 6)) + (b + x) * 16 * R::kRow));
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
               for (int t = 0; t < NT; ++t)
-                sc[t][b + x] = TT::mfma(kf, qf[t][f], sc[t][b + x]);
-            }
+                sc[t][b + x] = TT::mfma(kf[f][x], qf[t][f0 + f], sc[t][b + x]);
         }
-      }
+      V4 vl[ND][NG / 2], vh[ND][NG / 2];
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int c = 0; c < NG / 2; ++c) {
+          const unsigned at = buf + ((val_at ^ (d << 5)) + c * 32 * R::kRow);
+          vl[d][c] = lds_columns<V4>(at);
+          vh[d][c] = lds_columns<V4>(at + 16 * R::kRow);
+        }
+      __builtin_amdgcn_sched_barrier(0);
       if (edge) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -560,16 +661,6 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
         }
       }
       // weights
-      float vs[E8 ? NG : 1][4];
-      if constexpr (E8) {
-#pragma unroll
-        for (int b = 0; b < NG; ++b) {
-          const unsigned w = lds_read<unsigned>(buf + R::kScales + R::kKeys + b * 16 + g * 4);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            vs[b][e] = __builtin_bit_cast(float, ((w >> (8 * e)) & 255u) << 23);
-        }
-      }
       V8 pf[NT][NG / 2];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -592,42 +683,29 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
         for (int b = 0; b < NG; ++b)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][b][e], sl, -ref));
+            const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][b][e], sl, -ref));
             l[t] += p;
-            // an 8-bit value's power of two goes to its weight, exactly
-            if constexpr (E8) p *= vs[b][e];
             pf[t][b >> 1][(b & 1) * 4 + e] = (T)p;
           }
       }
       // O^T += V^T P^T
 #pragma unroll
-      for (int d0 = 0; d0 < ND; d0 += 2)
+      for (int c = 0; c < NG / 2; ++c)
 #pragma unroll
-        for (int c = 0; c < NG / 2; ++c)
+        for (int d = 0; d < ND; ++d) {
+          const V8 vf = __builtin_shufflevector(vl[d][c], vh[d][c], 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
-          for (int d = d0; d < d0 + 2; ++d) {
-            V8 vf;
-            if constexpr (E8) {
-              const kv_u32x2 w = lds_columns8(buf + ((val_at ^ (d << 4)) + c * 32 * R::kRow));
-              vf = widen(w[0], w[1], 1.0f);
-            } else {
-              const unsigned at = buf + ((val_at ^ (d << 5)) + c * 32 * R::kRow);
-              const V4 lo = lds_columns<V4>(at);
-              const V4 hi = lds_columns<V4>(at + 16 * R::kRow);
-              vf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) o[t][d] = TT::mfma(vf, pf[t][c], o[t][d]);
-          }
+          for (int t = 0; t < NT; ++t) o[t][d] = TT::mfma(vf, pf[t][c], o[t][d]);
+        }
       while (odd) {
         // a row with NaN or infinity: they go to the queries that see it
         const int row = (int)__builtin_ctzll(odd);
         odd &= odd - 1;
         const int key = key0 + row, rel = key - prefix;
-        const int64_t id = a.req.table[(size_t)job.r * a.req.width + (key >> a.kv.page_shift)];
+        const int64_t id = a.req.table[(size_t)span.r * a.req.width + (key >> a.kv.page_shift)];
         const int64_t at =
-            ((int64_t)job.h << a.kv.page_shift) + (key & ((1 << a.kv.page_shift) - 1));
-        const unsigned char* src = a.kv.v + id * a.kv.page_bytes + at * R::kRow;
+            ((int64_t)span.h << a.kv.page_shift) + (key & ((1 << a.kv.page_shift) - 1));
+        const unsigned char* src = a.kv.v + id * a.kv.page_bytes + at * (D * R::CB);
 #pragma unroll
         for (int d = 0; d < ND; ++d) {
 #pragma unroll
@@ -658,7 +736,7 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
     const int m = (job.tile0 + wave + kWaves * t) * 16 + qi;
     if (m >= s.mrows) continue;
     if (job.whole) {
-      const int head = job.h * a.group + (m - qrow[t] * a.group);
+      const int head = span.h * a.group + (m - qrow[t] * a.group);
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
       T* dst = reinterpret_cast<T*>(a.out + (size_t)(s.c0 + qrow[t]) * a.out_ld) + head * D + g * 4;
 #pragma unroll
@@ -701,70 +779,96 @@ __global__ __launch_bounds__(kThreads, 2) void split_kernel(AttnArgs a, Parts ws
   const unsigned lds = (unsigned)(uintptr_t)(lds_u8*)lds_mem;
   int rows_total;
   const int total_eff = rows_in_use(q, &rows_total);
-  // every workgroup sums the requests' units by itself
-  const int per = (q.B + kThreads - 1) / kThreads;
-  const int r0 = min(tid * per, q.B), r1 = min(r0 + per, q.B);
-  int64_t mine = 0;
-  for (int r = r0; r < r1; ++r) mine += units_of<D>(a, r, total_eff);
-  int64_t total;
-  int64_t at = block_excl_scan<int64_t, kThreads>(mine, wsum, &total);
-  const int wgs = wgs_in_use(total, gridDim.x);
-  if (blockIdx.x == 0) {
-    int64_t b = at;
-    for (int r = r0; r < r1; ++r) {
-      ws.base[r] = b;
-      b += units_of<D>(a, r, total_eff);
-    }
-    if (tid == 0) {
-      ws.base[q.B] = total;
-      a.meta[0] = rows_total;
-      a.meta[1] = rows_total != total_eff ? DSPARK_DATA_BAD_LENS : 0;
-    }
-  }
-  if ((int)blockIdx.x >= wgs) return;
-  const int64_t u0 = wg_start(total, blockIdx.x, wgs), u1 = wg_start(total, blockIdx.x + 1, wgs);
-  if (at <= u0 && u0 < at + mine) {
-    for (int r = r0; r < r1; ++r) {
-      const int64_t n = units_of<D>(a, r, total_eff);
-      if (u0 < at + n) {
-        start_r = r;
-        start_off = u0 - at;
-        break;
-      }
-      at += n;
-    }
-  }
-  __syncthreads();
+  // every wave finds its workgroup's share by itself where a wave's lanes hold
+  // the batch; the workgroup together where they do not
   Cursor cur;
-  cur.u0 = cur.u = u0;
-  cur.u1 = u1;
-  cur.r = __builtin_amdgcn_readfirstlane(start_r);
-  cur.off = read_lane(start_off, 0);
   cur.n_r = -1;
+  cur.begun = 0;
+  int64_t u0, u1;
+  int64_t total;
+  const int wgs_all = gridDim.x;
+  if (q.B <= kWave) {
+    load_window(a, total_eff, 0, cur);
+    const int64_t mine =
+        cur.w_len ? units_of<D>(a, cur.w_c0, cur.w_len, cur.w_prefix) : 0;
+    const int64_t incl = wave_incl_scan_op(mine, (int64_t)0, OpAdd{});
+    total = read_lane(incl, kWave - 1);
+    if (blockIdx.x == 0 && tid < q.B) ws.base[tid] = incl - mine;
+    const int wgs = wgs_in_use(total, wgs_all);
+    u0 = (int)blockIdx.x < wgs ? wg_start(total, blockIdx.x, wgs) : total;
+    u1 = (int)blockIdx.x < wgs ? wg_start(total, blockIdx.x + 1, wgs) : total;
+    const unsigned long long past = __ballot(u0 < incl);
+    cur.r = past ? (int)__builtin_ctzll(past) : 0;
+    cur.off = u0 - read_lane(incl - mine, cur.r);
+  } else {
+    auto units = [&](int r) {
+      int c0, len, prefix;
+      return rows_of(a, r, total_eff, &c0, &len, &prefix) ? units_of<D>(a, c0, len, prefix)
+                                                          : (int64_t)0;
+    };
+    const int per = (q.B + kThreads - 1) / kThreads;
+    const int r0 = min(tid * per, q.B), r1 = min(r0 + per, q.B);
+    int64_t mine = 0;
+    for (int r = r0; r < r1; ++r) mine += units(r);
+    int64_t at = block_excl_scan<int64_t, kThreads>(mine, wsum, &total);
+    if (blockIdx.x == 0) {
+      int64_t b = at;
+      for (int r = r0; r < r1; ++r) {
+        ws.base[r] = b;
+        b += units(r);
+      }
+    }
+    const int wgs = wgs_in_use(total, wgs_all);
+    u0 = (int)blockIdx.x < wgs ? wg_start(total, blockIdx.x, wgs) : total;
+    u1 = (int)blockIdx.x < wgs ? wg_start(total, blockIdx.x + 1, wgs) : total;
+    if (at <= u0 && u0 < at + mine) {
+      for (int r = r0; r < r1; ++r) {
+        const int64_t n = units(r);
+        if (u0 < at + n) {
+          start_r = r;
+          start_off = u0 - at;
+          break;
+        }
+        at += n;
+      }
+    }
+    __syncthreads();
+    cur.r = __builtin_amdgcn_readfirstlane(start_r);
+    cur.off = read_lane(start_off, 0);
+    if (u0 < u1) load_window(a, total_eff, cur.r, cur);
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    ws.base[q.B] = total;
+    a.meta[0] = rows_total;
+    a.meta[1] = rows_total != total_eff ? DSPARK_DATA_BAD_LENS : 0;
+  }
+  if (u0 >= u1) return;
+  cur.left = u1 - u0;
   Feeder<E8, D> feed;
   feed.start(a, total_eff, cur, wave);
 #pragma unroll
-  for (int i = 0; i < R::kStages - 1; ++i) feed.next(a, total_eff, lds, wave);
+  for (int i = 0; i < (E8 ? R::kStages : R::kStages - 1); ++i) feed.next(a, total_eff, lds, wave);
   int64_t left = u1 - u0;
   int stage = 0;
   for (;;) {
-    const Job job = next_job<D>(a, total_eff, cur);
-    if (job.n == 0) break;
+    Job job;
+    const Span span = next_span<D>(a, total_eff, cur, &job);
+    if (span.n == 0) break;
     // tiles of this wave; none of a request whose tree is none
     int nt = max(0, (job.mt - wave + kWaves - 1) / kWaves);
     if (q.parents) {
       const int lane = lane_id();
-      const int up = lane + 1 < job.s.len ? q.parents[(size_t)job.r * q.gamma + lane] : 0;
+      const int up = lane + 1 < job.s.len ? q.parents[(size_t)span.r * q.gamma + lane] : 0;
       if (__ballot(up < 0 || up > lane)) nt = 0;
     }
     if (nt == 0) {
-      segment<T, E8, D, 0>(a, ws, job, feed, total_eff, lds, left, stage);
+      segment<T, E8, D, 0>(a, ws, span, job, feed, total_eff, lds, left, stage);
     } else if (nt == 1) {
-      segment<T, E8, D, 1>(a, ws, job, feed, total_eff, lds, left, stage);
+      segment<T, E8, D, 1>(a, ws, span, job, feed, total_eff, lds, left, stage);
     } else if constexpr (Size<D>::kTilesPerWave > 1) {
-      segment<T, E8, D, 2>(a, ws, job, feed, total_eff, lds, left, stage);
+      segment<T, E8, D, 2>(a, ws, span, job, feed, total_eff, lds, left, stage);
     }
-    left -= job.n;
+    left -= span.n;
   }
 }
 

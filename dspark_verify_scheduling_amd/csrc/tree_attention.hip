@@ -11,27 +11,27 @@ namespace {
 
 // One workgroup per (request, key/value head, share of its rows): joins the
 // parts that several workgroups of the split kernel left of a segment, in order,
-// a wave per row. The first of each request also checks it and its pages.
+// D / 8 lanes to a row with eight elements each. A part's statistics and outputs
+// are read together, so a row costs about one memory latency. The first
+// workgroup of each request also checks it and its pages.
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, Parts ws, int shares) {
-  constexpr int E = D / kWave;
-  typedef __attribute__((ext_vector_type(E))) float fE;
-  typedef __attribute__((ext_vector_type(E))) T TE;
+  typedef typename Types<T>::V8 V8;
+  constexpr int kLanes = D / 8, kRows = kThreads / kLanes;
   const ReqView& q = a.req;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int share = blockIdx.x % shares, rh = blockIdx.x / shares;
   const int r = rh / a.kv.hkv, h = rh - r * a.kv.hkv;
+  const int64_t units = ws.base[q.B], base = ws.base[r];
   int total;
   const int total_eff = rows_in_use(q, &total);
-  Shape s;
-  const bool good = shape_of<D>(a, r, total_eff, &s);
-  const bool tree =
-      !good || !q.parents ||
-      !__ballot([&] {
-        const int up = lane + 1 < s.len ? q.parents[(size_t)r * q.gamma + lane] : 0;
-        return up < 0 || up > lane;
-      }());
+  int c0, len, prefix;
+  const bool good = rows_of(a, r, total_eff, &c0, &len, &prefix);
+  bool tree = true;
+  if (good && q.parents) {
+    const int up = lane + 1 < len ? q.parents[(size_t)r * q.gamma + lane] : 0;
+    tree = __ballot(up < 0 || up > lane) == 0;
+  }
   if (h == 0 && share == 0) {
     int bits = 0;
     if (!good) {
@@ -40,80 +40,82 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, Parts ws, in
     } else if (!tree) {
       bits = DSPARK_DATA_BAD_TREE;
     } else {
-      for (int64_t p = tid; p <= (s.keys - 1) >> a.kv.page_shift; p += kThreads) {
+      const int64_t keys = (int64_t)prefix + len;
+      for (int64_t p = tid; p <= (keys - 1) >> a.kv.page_shift; p += kThreads) {
         const int id = q.table[(size_t)r * q.width + p];
         if (id < 0 || id >= a.kv.num_blocks) bits = DSPARK_DATA_BAD_PAGE;
       }
     }
-    if (__any(bits != 0)) {
-      if (bits) atomicOr(a.meta + 1, bits);
-    }
+    if (bits) atomicOr(a.meta + 1, bits);
   }
   if (!good || !tree) return;
-  const int64_t units = ws.base[q.B], base = ws.base[r];
+  const Shape s = shape_of<D>(a, c0, len, prefix);
   const int wgs = wgs_in_use(units, ws.wgs);
   const SmallDiv by_group(a.group);
-  // rows in order over the segments, a wave each
-  for (int m = share * kWaves + wave; m < s.mrows; m += shares * kWaves) {
-    const int seg = (m >> 4) / s.per;
+  const int col = (tid % kLanes) * 8;
+  // rows in order over the segments, kRows of one at a time
+  const int steps = (s.per * 16 + kRows - 1) / kRows;
+  for (int step = share; step < s.nseg * steps; step += shares) {
+    const int seg = step / steps;
     const int64_t u0 = base + ((int64_t)h * s.nseg + seg) * s.nku, u1 = u0 + s.nku;
     // workgroups of the first and the last unit
     const int wa = (int)(((u0 + 1) * wgs - 1) / units), wb = (int)((u1 * wgs - 1) / units);
     if (wa == wb) continue;
     const int slot0 = 2 * wa + (wg_start(units, wa, wgs) == u0 ? 0 : 1);
     const int n = wb - wa + 1;
-    const int row = m - seg * s.per * 16;
-    auto place = [&](int p) { return (size_t)(p ? 2 * (wa + p) : slot0) * ws.rows + row; };
-    // the first eight parts are under way while their statistics are looked at
-    constexpr int kAhead = 8;
-    fE x[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      x[k] = *reinterpret_cast<const fE*>(ws.o + place(min(k, n - 1)) * D + lane * E);
-    float top = -__builtin_inff();
-    for (int p = lane; p < n; p += kWave) top = fmaxf(top, ws.m[place(p)]);
-    for (int o = kWave / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, kWave));
-    float sum = 0.0f;
-    fE y;
-    for (int e = 0; e < E; ++e) y[e] = 0.0f;
-    for (int p0 = 0; p0 < n; p0 += kWave) {
-      // lane i: the factor of part p0 + i; then the parts in order
-      const int p = p0 + lane;
-      float f = 0.0f;
-      if (p < n) {
-        f = top == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(ws.m[place(p)] - top);
-        sum += ws.l[place(p)] * f;
-      }
-      const int cnt = min(n - p0, kWave);
-      for (int i = 0; i < cnt; i += kAhead) {
-        fE z[kAhead];
+    const int rows = min(s.per * 16, s.mrows - seg * s.per * 16);
+    const int row = (step - seg * steps) * kRows + tid / kLanes;
+    if (row < rows) {
+      constexpr int kAhead = 4;
+      float top = -__builtin_inff(), sum = 0.0f;
+      f32x4 y[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+      for (int p0 = 0; p0 < n; p0 += kAhead) {
+        float m[kAhead], l[kAhead];
+        f32x4 x[kAhead][2];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-          z[k] = x[k];
-          if (p0 + i + kAhead < n)
-            x[k] = *reinterpret_cast<const fE*>(
-                ws.o + place(min(p0 + i + kAhead + k, n - 1)) * D + lane * E);
-        }
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          if (i + k < cnt) {
-            const float fk = read_lane(f, i + k);
-            for (int e = 0; e < E; ++e) y[e] += z[k][e] * fk;
+          const int p = p0 + k;
+          m[k] = -__builtin_inff();
+          l[k] = 0.0f;
+          x[k][0] = x[k][1] = (f32x4){0, 0, 0, 0};
+          if (p < n) {
+            const size_t at = (size_t)(p ? 2 * (wa + p) : slot0) * ws.rows + row;
+            m[k] = ws.m[at];
+            l[k] = ws.l[at];
+            x[k][0] = *reinterpret_cast<const f32x4*>(ws.o + at * D + col);
+            x[k][1] = *reinterpret_cast<const f32x4*>(ws.o + at * D + col + 4);
           }
         }
+        float next = top;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) next = fmaxf(next, m[k]);
+        const bool none = next == -__builtin_inff();  // nothing seen, or NaN scores only
+        const float fix = none ? 1.0f : __builtin_amdgcn_exp2f(top - next);
+        sum *= fix;
+        y[0] *= fix;
+        y[1] *= fix;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const float f = none ? 1.0f : __builtin_amdgcn_exp2f(m[k] - next);
+          sum += l[k] * f;
+          y[0] += x[k][0] * f;
+          y[1] += x[k][1] * f;
+        }
+        top = next;
       }
+      const int mm = seg * s.per * 16 + row;
+      const int j = by_group.quo(mm);
+      const int head = h * a.group + (mm - j * a.group);
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      V8 z;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] = (T)(y[e >> 2][e & 3] * inv);
+      *reinterpret_cast<V8*>(reinterpret_cast<T*>(a.out + (size_t)(c0 + j) * a.out_ld) + head * D +
+                             col) = z;
+      if (a.lse && col == 0)
+        a.lse[(size_t)(c0 + j) * a.num_heads + head] =
+            sum == 0.0f ? -__builtin_inff() : (top + __builtin_amdgcn_logf(sum)) * kLn2;
     }
-    sum = wave_sum(sum);
-    const int j = by_group.quo(m);
-    const int head = h * a.group + (m - j * a.group);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    TE z;
-    for (int e = 0; e < E; ++e) z[e] = (T)(y[e] * inv);
-    *reinterpret_cast<TE*>(reinterpret_cast<T*>(a.out + (size_t)(s.c0 + j) * a.out_ld) + head * D +
-                           lane * E) = z;
-    if (a.lse && lane == 0)
-      a.lse[(size_t)(s.c0 + j) * a.num_heads + head] =
-          sum == 0.0f ? -__builtin_inff() : (top + __builtin_amdgcn_logf(sum)) * kLn2;
   }
 }
 
@@ -141,9 +143,10 @@ Plan plan(int B, int gamma, int group, int D) {
 
 template <int D>
 void launch_join(const AttnArgs& a, const Parts& ws, dspark_dtype dt, hipStream_t s) {
-  // enough waves to fill the card, and no more than there are rows
+  // a workgroup's rows at once, and more workgroups where there are few pairs
   const int pairs = a.req.B * a.kv.hkv;
-  const int most = (a.group * (a.req.gamma + 1) + kWaves - 1) / kWaves;
+  const int rows = a.group * (a.req.gamma + 1), at_once = kThreads / (D / 8);
+  const int most = (rows + at_once - 1) / at_once;
   const int shares = std::max(1, std::min(most, 4096 / std::max(pairs, 1)));
   const dim3 grid((unsigned)pairs * shares), block(kThreads);
   if (dt == DSPARK_BF16) {
@@ -172,7 +175,12 @@ hipError_t launch_attention(const AttnArgs& a, dspark_dtype dt, hipStream_t s) {
   ws.l = reinterpret_cast<float*>(w + p.l_off);
   ws.o = reinterpret_cast<float*>(w + p.o_off);
   ws.rows = p.rows;
-  ws.wgs = std::min(attn::kMaxWgs, 2 * cus);
+  const int per_cu = a.kv.cb == 1 && a.kv.dim == 256 ? attn::Ring<true, 256>::kPerCu : 2;
+  static_assert(attn::Ring<true, 64>::kPerCu == 2 && attn::Ring<true, 128>::kPerCu == 2 &&
+                    attn::Ring<false, 64>::kPerCu == 2 && attn::Ring<false, 128>::kPerCu == 2 &&
+                    attn::Ring<false, 256>::kPerCu == 2,
+                "two workgroups to a CU");
+  ws.wgs = std::min(attn::kMaxWgs, per_cu * cus);
   switch (a.kv.dim) {
     case 64: attn::launch_dim64(a, ws, dt, s); break;
     case 128: attn::launch_dim128(a, ws, dt, s); break;
