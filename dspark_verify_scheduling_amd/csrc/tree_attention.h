@@ -8,7 +8,7 @@
 namespace dspark {
 namespace attn {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / kWave;
 
 // What the split kernel leaves for the joining kernel: the schedule's prefix
@@ -24,11 +24,11 @@ struct Parts {
   int rows;       // rows of a segment, at most
 };
 
-// Tiles of 16 query rows of a segment, at most, and keys of a unit.
+// Tiles of 16 query rows of a segment, at most (one to a wave), and keys of a
+// unit.
+constexpr int kMaxTiles = kWaves;
 template <int D>
 struct Size {
-  static constexpr int kTilesPerWave = D == 256 ? 1 : 2;
-  static constexpr int kTiles = kWaves * kTilesPerWave;
   static constexpr int kKeys = D >= 128 ? 32 : 64;
 };
 
@@ -56,7 +56,7 @@ __device__ inline bool rows_of(const AttnArgs& a, int r, int total_eff, int* c0,
 
 template <int D>
 __device__ inline Shape shape_of(const AttnArgs& a, int c0, int len, int prefix) {
-  constexpr int kT = Size<D>::kTiles, kK = Size<D>::kKeys;
+  constexpr int kT = kMaxTiles, kK = Size<D>::kKeys;
   Shape s;
   s.c0 = c0;
   s.len = len;
@@ -79,7 +79,16 @@ __device__ inline int64_t units_of(const AttnArgs& a, int c0, int len, int prefi
 // Workgroups that get units: never one without.
 __device__ inline int wgs_in_use(int64_t total, int wgs) { return (int)min((int64_t)wgs, total); }
 
-// The first unit of workgroup w of n <= total.
+// Workgroups go to the eight XCDs in turn. Shares are numbered so that an XCD's
+// are consecutive: the heads of a request and the segments of a head then meet
+// in one L2, and an XCD's requests spread over the memory's channels (with share =
+// workgroup and eight heads, each XCD read one head of all pages).
+constexpr int kXcds = 8;
+__device__ inline int share_of(int wg, int wgs) {
+  return wgs % kXcds ? wg : wg % kXcds * (wgs / kXcds) + wg / kXcds;
+}
+
+// The first unit of share w of n <= total.
 __device__ inline int64_t wg_start(int64_t total, int w, int n) { return total * w / n; }
 
 template <typename T>
@@ -140,6 +149,13 @@ __device__ inline void copy4(const unsigned char* from, unsigned lane_bytes, uns
                : "v"(lane_bytes), "s"(from), "s"(__builtin_amdgcn_readfirstlane((int)lds_at))
                : "memory");
 }
+// A loaded value has arrived here. Without it, the wait for a load from before
+// a loop stands at its first use inside, and there waits for the copies of
+// every step.
+template <typename X>
+__device__ inline void settle(X& x) {
+  asm volatile("" : "+v"(x));
+}
 // All but the last `N` loads of the wave are done (they end in order).
 template <int N>
 __device__ inline void wait_copies() {
@@ -188,28 +204,25 @@ struct Ring {
   static constexpr int kRow = 2 * D;                  // bytes of a row of a tile
   static constexpr int kTile = kKeys * kRow;          // keys, or values
   static constexpr int kTiles = 2 * kTile;            // both
-  // copies of 16 rows: kWave 16-byte chunks each
+  // a wave's share of a tile: kRows keys (waves 0 to 3) or values (4 to 7), in
+  // copies of kWave 16-byte chunks
+  static constexpr int kRows = kKeys / 4;
   static constexpr int kChunks = D * CB / 16;         // of a cache row
   static constexpr int kRowsPerCopy = kWave / kChunks;
-  static constexpr int kCopies = 16 / kRowsPerCopy;
-  // a wave's share of a tile: with 64 keys the wave's 16 and their values, with
-  // 32 keys 16 of them (waves 0 and 1) or their values (2 and 3)
-  static constexpr int kParts = kGroups == 4 ? 2 : 1;
-  static constexpr int kPerWave = kParts * (kCopies + (E8 ? 1 : 0));
-  static constexpr int kPart = 16 * D + 64;           // codes, exponents; 8 bits
-  static constexpr int kPiece = kParts * kPart;
+  static constexpr int kCopies = kRows / kRowsPerCopy;
+  static_assert(kCopies * kRowsPerCopy == kRows, "whole copies");
+  static constexpr int kPerWave = kCopies + (E8 ? 1 : 0);
+  static constexpr int kPiece = kRows * D + 64;       // codes, exponents; 8 bits
   static constexpr int kRaw = 2 * kTiles;             // offset of the waves' rings
+  // (fewer where the LDS of a CU, or of half a CU, holds no more)
   static constexpr int kStages =
-      E8 ? (D == 256 ? 2 : 4) : (65536 / kTiles < 4 ? 65536 / kTiles : 4);
-  static constexpr int kFlags = E8 ? kRaw + kStages * kWaves * kPiece : kStages * kTiles;
-  // bad pages, a byte per stage and wave (8 bits: per tile and wave, after the
-  // wave's own per stage)
-  static constexpr int kOdd = kFlags + 4 * kStages + 8;  // rows with NaN or infinity, 16 bits a
-                                                         // group, two tiles
+      D == 256 ? 4 : (E8 ? 4 : (65536 / kTiles < 4 ? 65536 / kTiles : 4));
+  // rows with NaN or infinity, a bit each; of two tiles
+  static constexpr int kOdd = E8 ? kRaw + kStages * kWaves * kPiece : kStages * kTiles;
   static constexpr int kBytes = kOdd + 16;
   // workgroups to a CU, of its 160 KiB
-  static constexpr int kPerCu = kBytes <= 81920 - 256 ? 2 : 1;
-  static_assert(kBytes <= 163840 - 256, "a CU's LDS");
+  static constexpr int kPerCu = D == 256 ? 1 : 2;
+  static_assert(kBytes <= 163840 / kPerCu - 256, "a CU's LDS");
   static __device__ int swizzle(int row) {
     return D >= 128 ? row & 15 : (row >> 1) & 7;
   }
@@ -239,11 +252,14 @@ struct Cursor {
   int64_t off;   // next unit within request r
   int64_t n_r;   // units of request r, -1: not known yet
   int r, window;
+  int share;
   int begun;     // 0 before the share's first segment
   int w_c0, w_len, w_prefix;
 };
 
-__device__ inline void load_window(const AttnArgs& a, int total_eff, int first, Cursor& c) {
+__device__ inline void load_window(const AttnArgs& a, int first, Cursor& c) {
+  int total;
+  const int total_eff = rows_in_use(a.req, &total);
   const int r = first + lane_id();
   c.window = first;
   c.w_c0 = c.w_len = c.w_prefix = 0;
@@ -255,14 +271,17 @@ __device__ inline void load_window(const AttnArgs& a, int total_eff, int first, 
       c.w_prefix = prefix;
     }
   }
+  settle(c.w_c0);
+  settle(c.w_len);
+  settle(c.w_prefix);
 }
 
 template <int D>
-__device__ __forceinline__ Span next_span(const AttnArgs& a, int total_eff, Cursor& c, Job* job) {
+__device__ __forceinline__ Span next_span(const AttnArgs& a, Cursor& c, Job* job) {
   Span j;
   j.n = 0;
   while (c.left > 0) {
-    if (c.r - c.window >= kWave) load_window(a, total_eff, c.r, c);
+    if (c.r - c.window >= kWave) load_window(a, c.r, c);
     const int l = c.r - c.window;
     const int len = read_lane(c.w_len, l);
     const Shape s = shape_of<D>(a, read_lane(c.w_c0, l), len, read_lane(c.w_prefix, l));
@@ -286,7 +305,7 @@ __device__ __forceinline__ Span next_span(const AttnArgs& a, int total_eff, Curs
       job->tile0 = seg * s.per;
       job->mt = min(s.per, s.mtiles - job->tile0);
       job->whole = j.n == s.nku;
-      job->slot = 2 * blockIdx.x + c.begun;
+      job->slot = 2 * c.share + c.begun;
     }
     c.begun = 1;
     c.off += j.n;
@@ -296,110 +315,135 @@ __device__ __forceinline__ Span next_span(const AttnArgs& a, int total_eff, Curs
   return j;
 }
 
+// Where the wave's rows of 64 tiles of a segment are, a tile to a lane, so that
+// starting a tile's copies is two lane reads and no arithmetic.
+struct Places {
+  unsigned lo, hi;          // of the rows
+  unsigned s_lo, s_hi;      // of their exponents
+  unsigned long long none;  // bit l: some page of lane l's tile is none
+};
+
 // The producing side of the ring: this wave's copies of the next tile.
 template <bool E8, int D>
 struct Feeder {
   typedef Ring<E8, D> R;
   Cursor c;
-  Span j, nj;    // the segment copied from, and the one after it
-  int i;         // its next tile
-  int ids, nids; // page ids of the wave's rows, lane l: tile id_first + l
-  int id_first;
+  Span j, nj;      // the segment copied from, and the one after it
+  int t;           // its tile in lane 0 of `at`
+  int idx, end;    // next lane, lanes that hold a tile: 0 when nothing is left
+  Places at, nat;  // of j from tile t on, of nj from its first
   int stage;
+  unsigned none;   // bit per stage: some page of its tile is none
 
-  static __device__ int group_of(int wave) { return wave % R::kGroups; }
-
-  // The page ids have arrived here, and not at each of their uses: a wait for
-  // them would be one for the copies behind them too.
-  __device__ void settle() { asm volatile("" : "+v"(ids)); }
-
-  // lanes 0..63: the pages of 64 tiles from tile i on
-  __device__ int fetch(const AttnArgs& a, const Span& x, int t, int wave) const {
-    const int64_t key =
-        (int64_t)x.first + (int64_t)(t + lane_id()) * R::kKeys + group_of(wave) * 16;
-    const int p = (int)min(key, (int64_t)x.keys - 1) >> a.kv.page_shift;
-    return a.req.table[(size_t)x.r * a.req.width + p];
-  }
-
-  __device__ void start(const AttnArgs& a, int total_eff, const Cursor& at, int wave) {
-    c = at;
-    j = next_span<D>(a, total_eff, c, nullptr);
-    ids = fetch(a, j, 0, wave);
-    settle();
-    nj = next_span<D>(a, total_eff, c, nullptr);
-    nids = nj.n > 0 ? fetch(a, nj, 0, wave) : 0;
-    i = id_first = stage = 0;
-  }
-
-  // 16 rows of the cache; SWIZZLE: as rows of a tile
-  template <bool SWIZZLE>
-  static __device__ void copies(const unsigned char* from, unsigned lds_at) {
-    const int lane = lane_id();
+  static __device__ Places fetch(const AttnArgs& a, const Span& x, int t, int wave) {
+    const bool values = wave >= 4;
+    const int row0 = (wave & 3) * R::kRows;
+    Places p;
+    p.none = 0;
+    int64_t own = 0;
+    const int64_t first = (int64_t)x.first + (int64_t)(t + lane_id()) * R::kKeys;
+    int id[R::kGroups];
 #pragma unroll
-    for (int n = 0; n < R::kCopies; ++n) {
-      const int row = n * R::kRowsPerCopy + lane / R::kChunks;
-      const int chunk = SWIZZLE ? (lane % R::kChunks) ^ R::swizzle(row) : lane % R::kChunks;
-      copy16(from + n * R::kRowsPerCopy * D * R::CB,
-             (lane / R::kChunks) * D * R::CB + (unsigned)chunk * 16, lds_at + n * 1024);
+    for (int g = 0; g < R::kGroups; ++g)
+      id[g] = a.req.table[(size_t)x.r * a.req.width +
+                          ((int)min(first + g * 16, (int64_t)x.keys - 1) >> a.kv.page_shift)];
+#pragma unroll
+    for (int g = 0; g < R::kGroups; ++g) {
+      const bool none = id[g] < 0 || id[g] >= a.kv.num_blocks;
+      p.none |= __ballot(none);
+      // a page that is none: any valid one, its keys are masked
+      if (g == row0 >> 4) own = none ? 0 : id[g];
     }
+    const int64_t row = ((int64_t)x.h << a.kv.page_shift) +
+                        ((first + row0) & ((1 << a.kv.page_shift) - 1));
+    const uint64_t k =
+        (uint64_t)((values ? a.kv.v : a.kv.k) + own * a.kv.page_bytes + row * (D * R::CB));
+    p.lo = (unsigned)k;
+    p.hi = (unsigned)(k >> 32);
+    p.s_lo = p.s_hi = 0;
+    if constexpr (E8) {
+      const uint64_t e =
+          (uint64_t)((values ? a.kv.vs : a.kv.ks) + own * a.kv.scale_page_bytes + row);
+      p.s_lo = (unsigned)e;
+      p.s_hi = (unsigned)(e >> 32);
+      settle(p.s_lo);
+      settle(p.s_hi);
+    }
+    settle(p.lo);
+    settle(p.hi);
+    return p;
+  }
+
+  __device__ void start(const AttnArgs& a, const Cursor& from, int wave) {
+    c = from;
+    j = next_span<D>(a, c, nullptr);
+    at = fetch(a, j, 0, wave);
+    nj = next_span<D>(a, c, nullptr);
+    nat = at;
+    if (nj.n > 0) nat = fetch(a, nj, 0, wave);
+    t = idx = stage = 0;
+    end = min(j.n, kWave);
+    none = 0;
+  }
+
+  static __device__ const unsigned char* place(unsigned lo, unsigned hi, int lane) {
+    return (const unsigned char*)(((uint64_t)(unsigned)__builtin_amdgcn_readlane((int)hi, lane)
+                                   << 32) |
+                                  (unsigned)__builtin_amdgcn_readlane((int)lo, lane));
   }
 
   // Starts the wave's copies of the next tile.
-  __device__ void next(const AttnArgs& a, int total_eff, unsigned lds, int wave) {
-    if (j.n == 0) return;
-    const int g = group_of(wave);
-    const int key = j.first + i * R::kKeys + g * 16;
-    int id = __builtin_amdgcn_readlane(ids, i - id_first);
-    const bool bad = id < 0 || id >= a.kv.num_blocks;
-    if (bad) id = 0;  // any valid page: its keys are masked
-    const int64_t row =
-        ((int64_t)j.h << a.kv.page_shift) + (key & ((1 << a.kv.page_shift) - 1));
+  __device__ __forceinline__ void next(const AttnArgs& a, unsigned lds, int wave) {
+    if (end == 0) return;
+    const int lane = lane_id();
+    const int row0 = (wave & 3) * R::kRows;
+    const unsigned char* from = place(at.lo, at.hi, idx);
+    const unsigned to = E8 ? lds + R::kRaw + (stage * kWaves + wave) * R::kPiece
+                           : lds + stage * R::kTiles + (wave >= 4 ? R::kTile : 0) + row0 * R::kRow;
 #pragma unroll
-    for (int p = 0; p < R::kParts; ++p) {
-      const bool values = R::kParts == 2 ? p == 1 : wave >= 2;
-      const unsigned char* from = uniform((values ? a.kv.v : a.kv.k) +
-                                          (int64_t)id * a.kv.page_bytes + row * (D * R::CB));
-      if constexpr (E8) {
-        const unsigned to =
-            lds + R::kRaw + (stage * kWaves + wave) * R::kPiece + p * R::kPart;
-        copies<false>(from, to);
-        if (lane_id() < 4)
-          copy4(uniform((values ? a.kv.vs : a.kv.ks) + (int64_t)id * a.kv.scale_page_bytes + row),
-                lane_id() * 4, to + 16 * D);
-      } else {
-        copies<true>(from, lds + stage * R::kTiles + (values ? R::kTile : 0) + g * 16 * R::kRow);
-      }
+    for (int n = 0; n < R::kCopies; ++n) {
+      // 16 bits: as rows of a tile
+      const int r = row0 + n * R::kRowsPerCopy + lane / R::kChunks;
+      const int chunk = E8 ? lane % R::kChunks : (lane % R::kChunks) ^ R::swizzle(r);
+      copy16(from + n * R::kRowsPerCopy * D * R::CB,
+             (lane / R::kChunks) * D * R::CB + (unsigned)chunk * 16, to + n * 1024);
     }
-    if (lane_id() == 0)
-      lds_write<unsigned char>(lds + R::kFlags + stage * 4 + wave, bad ? 1 : 0);
+    if constexpr (E8) {
+      const unsigned char* e = place(at.s_lo, at.s_hi, idx);
+      if (lane < R::kRows / 4) copy4(e, lane * 4, to + R::kRows * D);
+    }
+    if (__builtin_expect((at.none | none) != 0, 0))
+      none = (none & ~(1u << stage)) | ((unsigned)(at.none >> idx) & 1u) << stage;
     stage = stage + 1 == R::kStages ? 0 : stage + 1;
-    if (++i == j.n) {
-      j = nj;
-      ids = nids;
-      settle();
-      i = id_first = 0;
-      if (j.n > 0) {
-        nj = next_span<D>(a, total_eff, c, nullptr);
-        nids = nj.n > 0 ? fetch(a, nj, 0, wave) : 0;
+    if (__builtin_expect(++idx == end, 0)) {
+      t += end;
+      idx = 0;
+      if (t < j.n) {
+        at = fetch(a, j, t, wave);
+      } else {
+        j = nj;
+        at = nat;
+        t = 0;
+        if (j.n > 0) {
+          nj = next_span<D>(a, c, nullptr);
+          if (nj.n > 0) nat = fetch(a, nj, 0, wave);
+        }
       }
-    } else if (i - id_first == kWave) {
-      ids = fetch(a, j, i, wave);
-      settle();
-      id_first = i;
+      end = min(j.n - t, kWave);
     }
   }
 };
 
-// A wave's part of a segment: NT of its 16-row tiles (tile w, w + 4, ..; none for
-// a wave past the last) over all its keys, which the four waves bring into LDS
-// together. The products are
+// A wave's part of a segment: its 16-row tile (ROWS false: none, the wave only
+// feeds the ring) over all its keys, which the waves bring into LDS together.
+// The products are
 //   S^T = K Q^T: keys are its rows and queries its columns, so a lane holds the
 //   scores of one query (lane & 15) for four keys of each sixteen, which are in
 //   place as the operand of  O^T = V^T P^T.
-template <typename T, bool E8, int D, int NT>
+template <typename T, bool E8, int D, bool ROWS>
 __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, const Span& span,
-                                        const Job& job, Feeder<E8, D>& feed, int total_eff,
-                                        unsigned lds, int64_t left, int& stage) {
+                                        const Job& job, Feeder<E8, D>& feed, unsigned lds,
+                                        int left, int& stage) {
   typedef Types<T> TT;
   typedef typename TT::V8 V8;
   typedef typename TT::V4 V4;
@@ -407,20 +451,22 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
   constexpr int NF = D / 32;         // operand chunks of a key
   constexpr int ND = D / 16;         // 16-column tiles of the output
   constexpr int NG = R::kGroups;     // 16-key groups of a tile
-  constexpr int NTX = NT ? NT : 1;
   const Shape& s = job.s;
   const int lane = lane_id(), qi = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int len = s.len, prefix = s.prefix;
-  const int keys = s.keys;
+  const int len = s.len, prefix = s.prefix, keys = s.keys;
   const SmallDiv by_group(a.group);
+  const int m = (job.tile0 + wave) * 16 + qi;
+  const int qrow = by_group.quo(m);  // the request's row that the lane's query belongs to
+  const bool live = ROWS && m < s.mrows;
 
-  // the step's own tree: bit l of anc, in lane l, is row l + 1 itself, with its
-  // ancestors' bits; row 0 is everybody's
-  unsigned long long anc = 0;
-  if (NT > 0 && a.req.parents) {
+  // rows of the step's own tree that the lane's query sees, bit l for row l + 1;
+  // row 0 is everybody's. Bit l of anc, in lane l, is row l + 1 itself, with its
+  // ancestors' bits.
+  unsigned long long seen = qrow >= 64 ? ~0ull : (1ull << qrow) - 1;
+  if (ROWS && a.req.parents) {
     int up = lane + 1 < len ? a.req.parents[(size_t)span.r * a.req.gamma + lane] : 0;
-    anc = 1ull << lane;
+    unsigned long long anc = 1ull << lane;
     for (int i = 0; i < 6; ++i) {
       const int from = max(up - 1, 0);
       const unsigned long long more = __shfl(anc, from, kWave);
@@ -430,6 +476,8 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
         up = next;
       }
     }
+    const unsigned long long path = __shfl(anc, max(qrow - 1, 0) & 63, kWave);
+    seen = qrow > 0 ? path : 0;
   }
   // Scores in units of log2 with a positive factor, so that a masked score stays
   // -infinity under it: the scale's sign and its zero go into the queries.
@@ -438,37 +486,26 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
   if (flat) sl = 1.0f;
   const unsigned sign = a.scale < 0.0f ? 0x80008000u : 0u;
   // queries as operands
-  V8 qf[NTX][NF];
-  f32x4 o[NTX][ND];
-  float mx[NTX], l[NTX];
-  int qrow[NTX];  // the request's row that the lane's query belongs to
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int m = (job.tile0 + wave + kWaves * t) * 16 + qi;
-    const int row = by_group.quo(m);
-    qrow[t] = row;
-    const unsigned char* src = a.q + (size_t)(s.c0 + row) * a.q_ld +
-                               (size_t)(span.h * a.group + (m - row * a.group)) * D * 2;
+  V8 qf[NF];
+  f32x4 o[ND];
+  float mx = -__builtin_inff(), l = 0.0f;
+  {
+    const unsigned char* src = a.q + (size_t)(s.c0 + qrow) * a.q_ld +
+                               ((size_t)(span.h * a.group + (m - qrow * a.group)) * D + g * 8) * 2;
+    kv_u32x4 w[NF];
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
-      const int d = f * 32 + g * 8;
-      kv_u32x4 w = (kv_u32x4){0, 0, 0, 0};
-      if (m < s.mrows && !flat) w = *reinterpret_cast<const kv_u32x4*>(src + d * 2) ^ sign;
-      qf[t][f] = __builtin_bit_cast(V8, w);
+      w[f] = (kv_u32x4){0, 0, 0, 0};
+      if (live && !flat) w[f] = *reinterpret_cast<const kv_u32x4*>(src + f * 64) ^ sign;
     }
-    mx[t] = -__builtin_inff();
-    l[t] = 0.0f;
 #pragma unroll
-    for (int d = 0; d < ND; ++d) o[t][d] = (f32x4){0, 0, 0, 0};
+    for (int f = 0; f < NF; ++f) {
+      settle(w[f]);
+      qf[f] = __builtin_bit_cast(V8, w[f]);
+    }
+#pragma unroll
+    for (int d = 0; d < ND; ++d) o[d] = (f32x4){0, 0, 0, 0};
   }
-
-  // rows of the step's own tree that the lane's query sees, bit l for row l + 1
-  auto seen_by = [&](int t) {
-    const int j = qrow[t];
-    if (!a.req.parents) return j >= 64 ? ~0ull : (1ull << j) - 1;
-    const unsigned long long path = __shfl(anc, max(j - 1, 0) & 63, kWave);
-    return j > 0 ? path : 0ull;
-  };
 
   // lane's offsets in a tile: its chunk of a key, its piece of a value row
   const int key_at = qi * R::kRow + ((g ^ R::swizzle(qi)) << 4);
@@ -478,16 +515,26 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
 
   for (int i = 0; i < span.n; ++i, --left) {
     const int key0 = span.first + i * R::kKeys;
+    // 16-key groups on a page that is none
+    unsigned missing = 0;
+    if (__builtin_expect((feed.none >> stage) & 1, 0)) {
+#pragma unroll
+      for (int b = 0; b < NG; ++b) {
+        const int p = min(key0 + 16 * b, keys - 1) >> a.kv.page_shift;
+        int id = a.req.table[(size_t)span.r * a.req.width + p];
+        settle(id);
+        if (id < 0 || id >= a.kv.num_blocks) missing |= 1u << b;
+      }
+      missing = __builtin_amdgcn_readfirstlane(missing);
+    }
     // the tile holds keys that some query does not see (the request's own rows
-    // after its root, keys past its last), or (found below) rows of a page that
-    // is none
-    bool edge = key0 + R::kKeys > prefix + 1;
-    unsigned buf, flags;
-    unsigned odd_at = lds + R::kOdd;
+    // after its root, keys past its last), or such a group
+    const bool edge = key0 + R::kKeys > prefix + 1 || missing;
+    unsigned buf, odd_at = lds + R::kOdd;
     // Values of keys that do not exist are anything: zeros in their place. NaN and
     // infinity in a row that some query does not see must not meet its zero
-    // weight: such elements are left out here and added below. Four 16-bit (8-bit
-    // codes: eight) elements at a time; returns what was left out.
+    // weight: such elements are left out here and added below. 16 bytes at a
+    // time; returns whether something was left out.
     auto clean = [&](kv_u32x4& w, bool there) {
       unsigned strange = 0;
 #pragma unroll
@@ -504,7 +551,7 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
       }
       return strange != 0 && there;
     };
-    // rows (16 bits) that a ballot over copy n's lanes names
+    // the wave's rows that a ballot over copy n's lanes names
     auto rows_in = [&](unsigned long long found, int n) {
       unsigned rows = 0;
       while (found) {
@@ -513,6 +560,17 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
       }
       return rows;
     };
+    auto put_odd = [&](unsigned rows) {
+      if (lane == 0) {
+        if constexpr (R::kRows == 8) {
+          lds_write<unsigned char>(odd_at + (wave & 3), (unsigned char)rows);
+        } else {
+          lds_write<unsigned short>(odd_at + 2 * (wave & 3), (unsigned short)rows);
+        }
+      }
+    };
+    const bool values = wave >= 4;
+    const int row0 = (wave & 3) * R::kRows;  // of the wave's keys, or values
     if constexpr (E8) {
       // the wave's piece of this tile: done when the pieces after it may not be
       if (left > R::kStages - 1) {
@@ -520,53 +578,40 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
       } else {
         wait_copies<0>();
       }
-      const int tile = (int)(left & 1);
+      const int tile = stage & 1;  // (an even number of stages)
       buf = lds + tile * R::kTiles;
       odd_at += tile * 8;
-      const int gr = Feeder<E8, D>::group_of(wave);
-      const unsigned mine = (unsigned)__builtin_amdgcn_readfirstlane(
-          (int)lds_read<unsigned char>(lds + R::kFlags + stage * 4 + wave));
+      const unsigned from = lds + R::kRaw + (stage * kWaves + wave) * R::kPiece;
+      const unsigned to = buf + (values ? R::kTile : 0);
+      unsigned strange_rows = 0;
 #pragma unroll
-      for (int p = 0; p < R::kParts; ++p) {
-        const bool values = R::kParts == 2 ? p == 1 : wave >= 2;
-        const unsigned from = lds + R::kRaw + (stage * kWaves + wave) * R::kPiece + p * R::kPart;
-        const unsigned to = buf + (values ? R::kTile : 0) + gr * 16 * R::kRow;
-        unsigned strange_rows = 0;
-#pragma unroll
-        for (int n = 0; n < R::kCopies; ++n) {
-          const int row = n * R::kRowsPerCopy + lane / R::kChunks;
-          const int c = lane % R::kChunks;
-          kv_u32x4 w = lds_read<kv_u32x4>(from + n * 1024 + lane * 16);
-          unsigned b = lds_read<unsigned char>(from + 16 * D + row);
-          if (values && (edge || mine)) {
-            const bool there = key0 + gr * 16 + row < keys && !mine;
-            strange_rows |= rows_in(__ballot(clean(w, there)), n);
-            b = there ? b : 127u;
-          }
-          const float e = __builtin_bit_cast(float, b << 23);
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            kv_u32x4 z;
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              z[2 * y] = __builtin_bit_cast(
-                  unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * x + y], e, false));
-              z[2 * y + 1] = __builtin_bit_cast(
-                  unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * x + y], e, true));
-            }
-            lds_write(to + row * R::kRow + (((2 * c + x) ^ R::swizzle(row)) << 4), z);
-          }
+      for (int n = 0; n < R::kCopies; ++n) {
+        const int r = n * R::kRowsPerCopy + lane / R::kChunks, row = row0 + r;
+        const int c = lane % R::kChunks;
+        kv_u32x4 w = lds_read<kv_u32x4>(from + n * 1024 + lane * 16);
+        unsigned b = lds_read<unsigned char>(from + R::kRows * D + r);
+        if (values && edge) {
+          const bool there = key0 + row < keys && !((missing >> (row >> 4)) & 1);
+          strange_rows |= rows_in(__ballot(clean(w, there)), n);
+          b = there ? b : 127u;
         }
-        if (values && lane == 0)
-          lds_write<unsigned short>(odd_at + gr * 2, (unsigned short)strange_rows);
+        const float e = __builtin_bit_cast(float, b << 23);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          kv_u32x4 z;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            z[2 * y] = __builtin_bit_cast(
+                unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * x + y], e, false));
+            z[2 * y + 1] = __builtin_bit_cast(
+                unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[2 * x + y], e, true));
+          }
+          lds_write(to + row * R::kRow + (((2 * c + x) ^ R::swizzle(row)) << 4), z);
+        }
       }
-      if (lane == 0)
-        lds_write<unsigned char>(lds + R::kFlags + 4 * R::kStages + tile * 4 + wave,
-                                 (unsigned char)mine);
-      feed.next(a, total_eff, lds, wave);
+      if (values && edge) put_odd(strange_rows);
+      feed.next(a, lds, wave);
       barrier();
-      flags = lds_read<unsigned>(lds + R::kFlags + 4 * R::kStages + tile * 4);
-      edge |= __builtin_amdgcn_readfirstlane((int)flags) != 0;
     } else {
       // this tile's copies are done when those of the stages after it may not be
       if (left > R::kStages - 2) {
@@ -576,46 +621,32 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
       }
       barrier();
       buf = lds + stage * R::kTiles;
-      flags = lds_read<unsigned>(lds + R::kFlags + stage * 4);
-      feed.next(a, total_eff, lds, wave);
-      edge |= __builtin_amdgcn_readfirstlane((int)flags) != 0;
+      feed.next(a, lds, wave);
       if (edge) {
-        if (wave < NG) {
+        if (values) {
           unsigned strange_rows = 0;
 #pragma unroll
           for (int n = 0; n < R::kCopies; ++n) {
-            const int row = wave * 16 + n * R::kRowsPerCopy + lane / R::kChunks;
-            const bool there = key0 + row < keys && !((flags >> (8 * wave)) & 255u);
-            const unsigned at = buf + R::kTile + wave * 16 * R::kRow + n * 1024 + lane * 16;
+            const int row = row0 + n * R::kRowsPerCopy + lane / R::kChunks;
+            const bool there = key0 + row < keys && !((missing >> (row >> 4)) & 1);
+            const unsigned at = buf + R::kTile + row0 * R::kRow + n * 1024 + lane * 16;
             kv_u32x4 w = lds_read<kv_u32x4>(at);
             strange_rows |= rows_in(__ballot(clean(w, there)), n);
             lds_write(at, w);
           }
-          if (lane == 0) lds_write<unsigned short>(odd_at + wave * 2, (unsigned short)strange_rows);
+          put_odd(strange_rows);
         }
         barrier();
       }
     }
     stage = stage + 1 == R::kStages ? 0 : stage + 1;
-    auto missing = [&](int group) { return (flags >> (8 * group)) & 255u; };
-    unsigned long long odd = 0;  // rows of the tile that hold NaN or infinity
-    if (edge) {
-      if constexpr (NG == 4) {
-        odd = read_lane(lds_read<unsigned long long>(odd_at), 0);
-      } else {
-        odd = (unsigned)read_lane((int)lds_read<unsigned>(odd_at), 0);
-      }
-    }
-    if constexpr (NT > 0) {
+    if constexpr (ROWS) {
       // Scores. Reads from LDS go out in batches, ahead of the products that use
-      // them and, for the values, of the softmax: one at a time, their latency is
-      // most of the loop.
-      f32x4 sc[NT][NG];
+      // them and, for the values, of the softmax.
+      f32x4 sc[NG];
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int b = 0; b < NG; ++b) sc[t][b] = (f32x4){0, 0, 0, 0};
-      constexpr int FB = NF < 4 ? NF : 4;
+      for (int b = 0; b < NG; ++b) sc[b] = (f32x4){0, 0, 0, 0};
+      constexpr int FB = 2;
 #pragma unroll
       for (int b = 0; b < NG; b += 2)
 #pragma unroll
@@ -631,131 +662,129 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
 #pragma unroll
           for (int f = 0; f < FB; ++f)
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-              for (int t = 0; t < NT; ++t)
-                sc[t][b + x] = TT::mfma(kf[f][x], qf[t][f0 + f], sc[t][b + x]);
+            for (int x = 0; x < 2; ++x) sc[b + x] = TT::mfma(kf[f][x], qf[f0 + f], sc[b + x]);
         }
-      V4 vl[ND][NG / 2], vh[ND][NG / 2];
+      constexpr int DB = ND / 2;
+      V4 vl[DB][NG / 2], vh[DB][NG / 2];
+      auto read_values = [&](int d0) {
 #pragma unroll
-      for (int d = 0; d < ND; ++d)
+        for (int d = 0; d < DB; ++d)
 #pragma unroll
-        for (int c = 0; c < NG / 2; ++c) {
-          const unsigned at = buf + ((val_at ^ (d << 5)) + c * 32 * R::kRow);
-          vl[d][c] = lds_columns<V4>(at);
-          vh[d][c] = lds_columns<V4>(at + 16 * R::kRow);
-        }
-      __builtin_amdgcn_sched_barrier(0);
+          for (int c = 0; c < NG / 2; ++c) {
+            const unsigned at = buf + ((val_at ^ ((d0 + d) << 5)) + c * 32 * R::kRow);
+            vl[d][c] = lds_columns<V4>(at);
+            vh[d][c] = lds_columns<V4>(at + 16 * R::kRow);
+          }
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      read_values(0);
       if (edge) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const unsigned long long seen = seen_by(t);
-#pragma unroll
-          for (int b = 0; b < NG; ++b)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int rel = key0 + b * 16 + g * 4 + e - prefix;
-              const bool own = rel < len && ((seen >> ((rel - 1) & 63)) & 1);
-              if (missing(b) || (rel > 0 && !own)) sc[t][b][e] = -__builtin_inff();
-            }
-        }
-      }
-      // weights
-      V8 pf[NT][NG / 2];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float top = sc[t][0][0];
-#pragma unroll
-        for (int b = 0; b < NG; ++b)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[t][b][e]);
-        if (__any(top * sl > mx[t] + kSlack)) {
-          const float next = fmaxf(mx[t], group_max(top * sl));
-          const float fix =
-              next == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(mx[t] - next);
-          mx[t] = next;
-          l[t] *= fix;
-#pragma unroll
-          for (int d = 0; d < ND; ++d) o[t][d] *= fix;
-        }
-        const float ref = mx[t] == -__builtin_inff() ? 0.0f : mx[t];
-#pragma unroll
         for (int b = 0; b < NG; ++b)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][b][e], sl, -ref));
-            l[t] += p;
-            pf[t][b >> 1][(b & 1) * 4 + e] = (T)p;
+            const int rel = key0 + b * 16 + g * 4 + e - prefix;
+            const bool own = rel < len && ((seen >> ((rel - 1) & 63)) & 1);
+            if (((missing >> b) & 1) || (rel > 0 && !own)) sc[b][e] = -__builtin_inff();
           }
       }
+      // weights
+      float top = sc[0][0];
+#pragma unroll
+      for (int b = 0; b < NG; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[b][e]);
+      if (__any(top * sl > mx + kSlack)) {
+        const float next = fmaxf(mx, group_max(top * sl));
+        const float fix = next == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(mx - next);
+        mx = next;
+        l *= fix;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) o[d] *= fix;
+      }
+      const float ref = mx == -__builtin_inff() ? 0.0f : mx;
+      V8 pf[NG / 2];
+#pragma unroll
+      for (int b = 0; b < NG; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][e], sl, -ref));
+          l += p;
+          pf[b >> 1][(b & 1) * 4 + e] = (T)p;
+        }
       // O^T += V^T P^T
 #pragma unroll
-      for (int c = 0; c < NG / 2; ++c)
+      for (int d0 = 0; d0 < ND; d0 += DB) {
+        if (d0) read_values(d0);
 #pragma unroll
-        for (int d = 0; d < ND; ++d) {
-          const V8 vf = __builtin_shufflevector(vl[d][c], vh[d][c], 0, 1, 2, 3, 4, 5, 6, 7);
+        for (int c = 0; c < NG / 2; ++c)
 #pragma unroll
-          for (int t = 0; t < NT; ++t) o[t][d] = TT::mfma(vf, pf[t][c], o[t][d]);
+          for (int d = 0; d < DB; ++d) {
+            const V8 vf = __builtin_shufflevector(vl[d][c], vh[d][c], 0, 1, 2, 3, 4, 5, 6, 7);
+            o[d0 + d] = TT::mfma(vf, pf[c], o[d0 + d]);
+          }
+      }
+      if (edge) {
+        unsigned long long odd = 0;  // rows of the tile that hold NaN or infinity
+        if constexpr (NG == 4) {
+          odd = read_lane(lds_read<unsigned long long>(odd_at), 0);
+        } else {
+          odd = (unsigned)read_lane((int)lds_read<unsigned>(odd_at), 0);
         }
-      while (odd) {
-        // a row with NaN or infinity: they go to the queries that see it
-        const int row = (int)__builtin_ctzll(odd);
-        odd &= odd - 1;
-        const int key = key0 + row, rel = key - prefix;
-        const int64_t id = a.req.table[(size_t)span.r * a.req.width + (key >> a.kv.page_shift)];
-        const int64_t at =
-            ((int64_t)span.h << a.kv.page_shift) + (key & ((1 << a.kv.page_shift) - 1));
-        const unsigned char* src = a.kv.v + id * a.kv.page_bytes + at * (D * R::CB);
+        while (odd) {
+          // they go to the queries that see the row
+          const int row = (int)__builtin_ctzll(odd);
+          odd &= odd - 1;
+          const int key = key0 + row, rel = key - prefix;
+          const int64_t id = a.req.table[(size_t)span.r * a.req.width + (key >> a.kv.page_shift)];
+          const int64_t at =
+              ((int64_t)span.h << a.kv.page_shift) + (key & ((1 << a.kv.page_shift) - 1));
+          const unsigned char* src = a.kv.v + id * a.kv.page_bytes + at * (D * R::CB);
+          const bool vis = rel <= 0 || ((seen >> ((rel - 1) & 63)) & 1);
 #pragma unroll
-        for (int d = 0; d < ND; ++d) {
+          for (int d = 0; d < ND; ++d) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int col = d * 16 + g * 4 + e;
-            float v;
-            if (E8) {
-              v = (src[col] & 127) == 127 ? __builtin_nanf("") : 0.0f;
-            } else {
-              v = (float)reinterpret_cast<const T*>(src)[col];
-              v = finite_f32(v) ? 0.0f : v;
+            for (int e = 0; e < 4; ++e) {
+              const int col = d * 16 + g * 4 + e;
+              float v;
+              if (E8) {
+                v = (src[col] & 127) == 127 ? __builtin_nanf("") : 0.0f;
+              } else {
+                v = (float)reinterpret_cast<const T*>(src)[col];
+                v = finite_f32(v) ? 0.0f : v;
+              }
+              settle(v);  // one at a time: no registers for a rare path
+              o[d][e] += vis ? v : 0.0f;
             }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const bool vis = rel <= 0 || ((seen_by(t) >> ((rel - 1) & 63)) & 1);
-              if (vis) o[t][d][e] += v;
-            }
-            asm volatile("" ::: "memory");  // one element at a time: no registers for a rare path
           }
         }
       }
     }
   }
 
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const float sum = group_sum(l[t]);
-    const int m = (job.tile0 + wave + kWaves * t) * 16 + qi;
-    if (m >= s.mrows) continue;
-    if (job.whole) {
-      const int head = span.h * a.group + (m - qrow[t] * a.group);
+  if constexpr (ROWS) {
+    const float sum = group_sum(l);
+    if (live && job.whole) {
+      const int head = span.h * a.group + (m - qrow * a.group);
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      T* dst = reinterpret_cast<T*>(a.out + (size_t)(s.c0 + qrow[t]) * a.out_ld) + head * D + g * 4;
+      T* dst = reinterpret_cast<T*>(a.out + (size_t)(s.c0 + qrow) * a.out_ld) + head * D + g * 4;
 #pragma unroll
       for (int d = 0; d < ND; ++d) {
         V4 z;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[e] = (T)(o[t][d][e] * inv);
+        for (int e = 0; e < 4; ++e) z[e] = (T)(o[d][e] * inv);
         *reinterpret_cast<V4*>(dst + d * 16) = z;
       }
       if (a.lse && g == 0)
-        a.lse[(size_t)(s.c0 + qrow[t]) * a.num_heads + head] =
-            sum == 0.0f ? -__builtin_inff() : (mx[t] + __builtin_amdgcn_logf(sum)) * kLn2;
-    } else {
-      const size_t at = (size_t)job.slot * ws.rows + (wave + kWaves * t) * 16 + qi;
+        a.lse[(size_t)(s.c0 + qrow) * a.num_heads + head] =
+            sum == 0.0f ? -__builtin_inff() : (mx + __builtin_amdgcn_logf(sum)) * kLn2;
+    } else if (live) {
+      const size_t at = (size_t)job.slot * ws.rows + wave * 16 + qi;
       float* dst = ws.o + at * D + g * 4;
 #pragma unroll
-      for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4*>(dst + d * 16) = o[t][d];
+      for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4*>(dst + d * 16) = o[d];
       if (g == 0) {
-        ws.m[at] = mx[t];
+        ws.m[at] = mx;
         ws.l[at] = sum;
       }
     }
@@ -767,7 +796,7 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
 // themselves and a long one is split over many workgroups. The ring of tiles
 // runs on across segments.
 template <typename T, bool E8, int D>
-__global__ __launch_bounds__(kThreads, 2) void split_kernel(AttnArgs a, Parts ws) {
+__global__ __launch_bounds__(kThreads, (2 * Ring<E8, D>::kPerCu)) void split_kernel(AttnArgs a, Parts ws) {
   typedef Ring<E8, D> R;
   __shared__ __align__(1024) unsigned char lds_mem[R::kBytes];
   __shared__ int64_t wsum[kWaves];
@@ -788,15 +817,16 @@ __global__ __launch_bounds__(kThreads, 2) void split_kernel(AttnArgs a, Parts ws
   int64_t total;
   const int wgs_all = gridDim.x;
   if (q.B <= kWave) {
-    load_window(a, total_eff, 0, cur);
+    load_window(a, 0, cur);
     const int64_t mine =
         cur.w_len ? units_of<D>(a, cur.w_c0, cur.w_len, cur.w_prefix) : 0;
     const int64_t incl = wave_incl_scan_op(mine, (int64_t)0, OpAdd{});
     total = read_lane(incl, kWave - 1);
     if (blockIdx.x == 0 && tid < q.B) ws.base[tid] = incl - mine;
     const int wgs = wgs_in_use(total, wgs_all);
-    u0 = (int)blockIdx.x < wgs ? wg_start(total, blockIdx.x, wgs) : total;
-    u1 = (int)blockIdx.x < wgs ? wg_start(total, blockIdx.x + 1, wgs) : total;
+    cur.share = share_of(blockIdx.x, wgs);
+    u0 = (int)blockIdx.x < wgs ? wg_start(total, cur.share, wgs) : total;
+    u1 = (int)blockIdx.x < wgs ? wg_start(total, cur.share + 1, wgs) : total;
     const unsigned long long past = __ballot(u0 < incl);
     cur.r = past ? (int)__builtin_ctzll(past) : 0;
     cur.off = u0 - read_lane(incl - mine, cur.r);
@@ -819,8 +849,9 @@ __global__ __launch_bounds__(kThreads, 2) void split_kernel(AttnArgs a, Parts ws
       }
     }
     const int wgs = wgs_in_use(total, wgs_all);
-    u0 = (int)blockIdx.x < wgs ? wg_start(total, blockIdx.x, wgs) : total;
-    u1 = (int)blockIdx.x < wgs ? wg_start(total, blockIdx.x + 1, wgs) : total;
+    cur.share = share_of(blockIdx.x, wgs);
+    u0 = (int)blockIdx.x < wgs ? wg_start(total, cur.share, wgs) : total;
+    u1 = (int)blockIdx.x < wgs ? wg_start(total, cur.share + 1, wgs) : total;
     if (at <= u0 && u0 < at + mine) {
       for (int r = r0; r < r1; ++r) {
         const int64_t n = units(r);
@@ -835,7 +866,7 @@ __global__ __launch_bounds__(kThreads, 2) void split_kernel(AttnArgs a, Parts ws
     __syncthreads();
     cur.r = __builtin_amdgcn_readfirstlane(start_r);
     cur.off = read_lane(start_off, 0);
-    if (u0 < u1) load_window(a, total_eff, cur.r, cur);
+    if (u0 < u1) load_window(a, cur.r, cur);
   }
   if (blockIdx.x == 0 && tid == 0) {
     ws.base[q.B] = total;
@@ -845,28 +876,28 @@ __global__ __launch_bounds__(kThreads, 2) void split_kernel(AttnArgs a, Parts ws
   if (u0 >= u1) return;
   cur.left = u1 - u0;
   Feeder<E8, D> feed;
-  feed.start(a, total_eff, cur, wave);
+  feed.start(a, cur, wave);
 #pragma unroll
-  for (int i = 0; i < (E8 ? R::kStages : R::kStages - 1); ++i) feed.next(a, total_eff, lds, wave);
+  for (int i = 0; i < (E8 ? R::kStages : R::kStages - 1); ++i) feed.next(a, lds, wave);
   int64_t left = u1 - u0;
   int stage = 0;
   for (;;) {
     Job job;
-    const Span span = next_span<D>(a, total_eff, cur, &job);
+    const Span span = next_span<D>(a, cur, &job);
     if (span.n == 0) break;
-    // tiles of this wave; none of a request whose tree is none
-    int nt = max(0, (job.mt - wave + kWaves - 1) / kWaves);
+    // the wave has a tile of it, or not; nobody has of a request whose tree is none
+    bool rows = wave < job.mt;
     if (q.parents) {
       const int lane = lane_id();
       const int up = lane + 1 < job.s.len ? q.parents[(size_t)span.r * q.gamma + lane] : 0;
-      if (__ballot(up < 0 || up > lane)) nt = 0;
+      if (__ballot(up < 0 || up > lane)) rows = false;
     }
-    if (nt == 0) {
-      segment<T, E8, D, 0>(a, ws, span, job, feed, total_eff, lds, left, stage);
-    } else if (nt == 1) {
-      segment<T, E8, D, 1>(a, ws, span, job, feed, total_eff, lds, left, stage);
-    } else if constexpr (Size<D>::kTilesPerWave > 1) {
-      segment<T, E8, D, 2>(a, ws, span, job, feed, total_eff, lds, left, stage);
+    // tiles still to come, as far as the end of the ring is concerned
+    const int near = (int)min(left, (int64_t)1 << 30);
+    if (rows) {
+      segment<T, E8, D, true>(a, ws, span, job, feed, lds, near, stage);
+    } else {
+      segment<T, E8, D, false>(a, ws, span, job, feed, lds, near, stage);
     }
     left -= span.n;
   }

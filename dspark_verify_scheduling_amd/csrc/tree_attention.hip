@@ -9,15 +9,17 @@ namespace dspark {
 namespace attn {
 namespace {
 
+constexpr int kJoinThreads = 256;
+
 // One workgroup per (request, key/value head, share of its rows): joins the
 // parts that several workgroups of the split kernel left of a segment, in order,
 // D / 8 lanes to a row with eight elements each. A part's statistics and outputs
 // are read together, so a row costs about one memory latency. The first
 // workgroup of each request also checks it and its pages.
 template <typename T, int D>
-__global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, Parts ws, int shares) {
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a, Parts ws, int shares) {
   typedef typename Types<T>::V8 V8;
-  constexpr int kLanes = D / 8, kRows = kThreads / kLanes;
+  constexpr int kLanes = D / 8, kRows = kJoinThreads / kLanes;
   const ReqView& q = a.req;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int share = blockIdx.x % shares, rh = blockIdx.x / shares;
@@ -41,7 +43,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, Parts ws, in
       bits = DSPARK_DATA_BAD_TREE;
     } else {
       const int64_t keys = (int64_t)prefix + len;
-      for (int64_t p = tid; p <= (keys - 1) >> a.kv.page_shift; p += kThreads) {
+      for (int64_t p = tid; p <= (keys - 1) >> a.kv.page_shift; p += kJoinThreads) {
         const int id = q.table[(size_t)r * q.width + p];
         if (id < 0 || id >= a.kv.num_blocks) bits = DSPARK_DATA_BAD_PAGE;
       }
@@ -132,7 +134,7 @@ struct Plan {
 Plan plan(int B, int gamma, int group, int D) {
   Plan p;
   const int mtiles = (group * (gamma + 1) + 15) / 16;
-  p.rows = 16 * std::min(D == 256 ? Size<256>::kTiles : Size<128>::kTiles, mtiles);
+  p.rows = 16 * std::min(kMaxTiles, mtiles);
   const size_t stat = align256((size_t)2 * kMaxWgs * p.rows * sizeof(float));
   p.m_off = align256((size_t)(B + 1) * sizeof(int64_t));
   p.l_off = p.m_off + stat;
@@ -145,10 +147,10 @@ template <int D>
 void launch_join(const AttnArgs& a, const Parts& ws, dspark_dtype dt, hipStream_t s) {
   // a workgroup's rows at once, and more workgroups where there are few pairs
   const int pairs = a.req.B * a.kv.hkv;
-  const int rows = a.group * (a.req.gamma + 1), at_once = kThreads / (D / 8);
+  const int rows = a.group * (a.req.gamma + 1), at_once = kJoinThreads / (D / 8);
   const int most = (rows + at_once - 1) / at_once;
   const int shares = std::max(1, std::min(most, 4096 / std::max(pairs, 1)));
-  const dim3 grid((unsigned)pairs * shares), block(kThreads);
+  const dim3 grid((unsigned)pairs * shares), block(kJoinThreads);
   if (dt == DSPARK_BF16) {
     hipLaunchKernelGGL((join_kernel<__bf16, D>), grid, block, 0, s, a, ws, shares);
   } else {
@@ -175,11 +177,7 @@ hipError_t launch_attention(const AttnArgs& a, dspark_dtype dt, hipStream_t s) {
   ws.l = reinterpret_cast<float*>(w + p.l_off);
   ws.o = reinterpret_cast<float*>(w + p.o_off);
   ws.rows = p.rows;
-  const int per_cu = a.kv.cb == 1 && a.kv.dim == 256 ? attn::Ring<true, 256>::kPerCu : 2;
-  static_assert(attn::Ring<true, 64>::kPerCu == 2 && attn::Ring<true, 128>::kPerCu == 2 &&
-                    attn::Ring<false, 64>::kPerCu == 2 && attn::Ring<false, 128>::kPerCu == 2 &&
-                    attn::Ring<false, 256>::kPerCu == 2,
-                "two workgroups to a CU");
+  const int per_cu = a.kv.dim == 256 ? attn::Ring<false, 256>::kPerCu : attn::Ring<false, 128>::kPerCu;
   ws.wgs = std::min(attn::kMaxWgs, per_cu * cus);
   switch (a.kv.dim) {
     case 64: attn::launch_dim64(a, ws, dt, s); break;
