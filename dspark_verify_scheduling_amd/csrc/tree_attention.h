@@ -219,7 +219,8 @@ struct Ring {
       D == 256 ? 4 : (E8 ? 4 : (65536 / kTiles < 4 ? 65536 / kTiles : 4));
   // rows with NaN or infinity, a bit each; of two tiles
   static constexpr int kOdd = E8 ? kRaw + kStages * kWaves * kPiece : kStages * kTiles;
-  static constexpr int kBytes = kOdd + 16;
+  static constexpr int kReqs = kOdd + 16;  // rows of up to kWave requests, 3 words each
+  static constexpr int kBytes = kReqs + 12 * kWave;
   // workgroups to a CU, of its 160 KiB
   static constexpr int kPerCu = D == 256 ? 1 : 2;
   static_assert(kBytes <= 163840 / kPerCu - 256, "a CU's LDS");
@@ -244,55 +245,43 @@ struct Job {
   bool whole;  // it covers all the request's keys
 };
 
-// Where a wave is in its workgroup's share of the units. Lane l holds the rows
-// of request `window + l` (len 0: malformed), so that most steps from request to
-// request read nothing.
+// Where a wave is in its workgroup's share of the units.
 struct Cursor {
   int64_t left;  // units of the share still to come
   int64_t off;   // next unit within request r
-  int64_t n_r;   // units of request r, -1: not known yet
-  int r, window;
+  int r;
   int share;
   int begun;     // 0 before the share's first segment
-  int w_c0, w_len, w_prefix;
 };
 
-__device__ inline void load_window(const AttnArgs& a, int first, Cursor& c) {
-  int total;
-  const int total_eff = rows_in_use(a.req, &total);
-  const int r = first + lane_id();
-  c.window = first;
-  c.w_c0 = c.w_len = c.w_prefix = 0;
-  if (r < a.req.B) {
-    int c0, len, prefix;
-    if (rows_of(a, r, total_eff, &c0, &len, &prefix)) {
-      c.w_c0 = c0;
-      c.w_len = len;
-      c.w_prefix = prefix;
-    }
-  }
-  settle(c.w_c0);
-  settle(c.w_len);
-  settle(c.w_prefix);
-}
-
+// The next segment of a share. `reqs`: the requests' rows in LDS where a wave's
+// lanes hold the batch (len 0: malformed); otherwise they are read from memory.
 template <int D>
-__device__ __forceinline__ Span next_span(const AttnArgs& a, Cursor& c, Job* job) {
+__device__ __forceinline__ Span next_span(const AttnArgs& a, unsigned reqs, Cursor& c, Job* job) {
   Span j;
   j.n = 0;
   while (c.left > 0) {
-    if (c.r - c.window >= kWave) load_window(a, c.r, c);
-    const int l = c.r - c.window;
-    const int len = read_lane(c.w_len, l);
-    const Shape s = shape_of<D>(a, read_lane(c.w_c0, l), len, read_lane(c.w_prefix, l));
-    if (c.n_r < 0) c.n_r = len ? (int64_t)a.kv.hkv * s.nseg * s.nku : 0;
-    if (c.off >= c.n_r) {
+    int c0 = 0, len = 0, prefix = 0;
+    if (a.req.B <= kWave) {
+      const unsigned at = reqs + 12 * c.r;
+      c0 = lds_read<int>(at);
+      len = lds_read<int>(at + 4);
+      prefix = lds_read<int>(at + 8);
+    } else {
+      int total;
+      const int total_eff = rows_in_use(a.req, &total);
+      if (!rows_of(a, c.r, total_eff, &c0, &len, &prefix)) len = 0;
+    }
+    c0 = __builtin_amdgcn_readfirstlane(c0);
+    len = __builtin_amdgcn_readfirstlane(len);
+    prefix = __builtin_amdgcn_readfirstlane(prefix);
+    const Shape s = shape_of<D>(a, c0, len, prefix);
+    if (c.off >= (len ? (int64_t)a.kv.hkv * s.nseg * s.nku : 0)) {
       ++c.r;
       c.off = 0;
-      c.n_r = -1;
       continue;
     }
-    const int item = (int)(c.off / s.nku);
+    const int item = __builtin_amdgcn_readfirstlane((int)(c.off / s.nku));
     const int ku0 = (int)(c.off - (int64_t)item * s.nku);
     j.r = c.r;
     j.n = (int)min((int64_t)(s.nku - ku0), c.left);
@@ -315,118 +304,100 @@ __device__ __forceinline__ Span next_span(const AttnArgs& a, Cursor& c, Job* job
   return j;
 }
 
-// Where the wave's rows of 64 tiles of a segment are, a tile to a lane, so that
-// starting a tile's copies is two lane reads and no arithmetic.
-struct Places {
-  unsigned lo, hi;          // of the rows
-  unsigned s_lo, s_hi;      // of their exponents
-  unsigned long long none;  // bit l: some page of lane l's tile is none
-};
-
-// The producing side of the ring: this wave's copies of the next tile.
+// The producing side of the ring: this wave's copies of the next tile. Few
+// registers are kept for it: a reload of a spilled one would wait for every copy
+// under way.
 template <bool E8, int D>
 struct Feeder {
   typedef Ring<E8, D> R;
+  typedef unsigned long long u64;
   Cursor c;
   Span j, nj;      // the segment copied from, and the one after it
-  int t;           // its tile in lane 0 of `at`
+  int t;           // its tile in lane 0 of `ids`
   int idx, end;    // next lane, lanes that hold a tile: 0 when nothing is left
-  Places at, nat;  // of j from tile t on, of nj from its first
+  int ids, nids;   // pages of the wave's rows: of j from tile t on, of nj from its first
+  u64 bad, nbad;   // bit l: some page of lane l's tile is none
   int stage;
   unsigned none;   // bit per stage: some page of its tile is none
 
-  static __device__ Places fetch(const AttnArgs& a, const Span& x, int t, int wave) {
-    const bool values = wave >= 4;
-    const int row0 = (wave & 3) * R::kRows;
-    Places p;
-    p.none = 0;
-    int64_t own = 0;
+  // The pages of 64 tiles from tile t on, a tile to a lane.
+  static __device__ int fetch(const AttnArgs& a, const Span& x, int t, int wave, u64* bad) {
+    const int group = ((wave & 3) * R::kRows) >> 4;
+    int own = 0;
     const int64_t first = (int64_t)x.first + (int64_t)(t + lane_id()) * R::kKeys;
     int id[R::kGroups];
 #pragma unroll
     for (int g = 0; g < R::kGroups; ++g)
       id[g] = a.req.table[(size_t)x.r * a.req.width +
                           ((int)min(first + g * 16, (int64_t)x.keys - 1) >> a.kv.page_shift)];
+    u64 b = 0;
 #pragma unroll
     for (int g = 0; g < R::kGroups; ++g) {
       const bool none = id[g] < 0 || id[g] >= a.kv.num_blocks;
-      p.none |= __ballot(none);
+      b |= __ballot(none);
       // a page that is none: any valid one, its keys are masked
-      if (g == row0 >> 4) own = none ? 0 : id[g];
+      if (g == group) own = none ? 0 : id[g];
     }
-    const int64_t row = ((int64_t)x.h << a.kv.page_shift) +
-                        ((first + row0) & ((1 << a.kv.page_shift) - 1));
-    const uint64_t k =
-        (uint64_t)((values ? a.kv.v : a.kv.k) + own * a.kv.page_bytes + row * (D * R::CB));
-    p.lo = (unsigned)k;
-    p.hi = (unsigned)(k >> 32);
-    p.s_lo = p.s_hi = 0;
-    if constexpr (E8) {
-      const uint64_t e =
-          (uint64_t)((values ? a.kv.vs : a.kv.ks) + own * a.kv.scale_page_bytes + row);
-      p.s_lo = (unsigned)e;
-      p.s_hi = (unsigned)(e >> 32);
-      settle(p.s_lo);
-      settle(p.s_hi);
-    }
-    settle(p.lo);
-    settle(p.hi);
-    return p;
+    *bad = b;
+    settle(own);
+    return own;
   }
 
-  __device__ void start(const AttnArgs& a, const Cursor& from, int wave) {
+  __device__ void start(const AttnArgs& a, unsigned lds, const Cursor& from, int wave) {
     c = from;
-    j = next_span<D>(a, c, nullptr);
-    at = fetch(a, j, 0, wave);
-    nj = next_span<D>(a, c, nullptr);
-    nat = at;
-    if (nj.n > 0) nat = fetch(a, nj, 0, wave);
+    j = next_span<D>(a, lds + R::kReqs, c, nullptr);
+    ids = fetch(a, j, 0, wave, &bad);
+    nj = next_span<D>(a, lds + R::kReqs, c, nullptr);
+    nids = 0;
+    nbad = 0;
+    if (nj.n > 0) nids = fetch(a, nj, 0, wave, &nbad);
     t = idx = stage = 0;
     end = min(j.n, kWave);
     none = 0;
-  }
-
-  static __device__ const unsigned char* place(unsigned lo, unsigned hi, int lane) {
-    return (const unsigned char*)(((uint64_t)(unsigned)__builtin_amdgcn_readlane((int)hi, lane)
-                                   << 32) |
-                                  (unsigned)__builtin_amdgcn_readlane((int)lo, lane));
   }
 
   // Starts the wave's copies of the next tile.
   __device__ __forceinline__ void next(const AttnArgs& a, unsigned lds, int wave) {
     if (end == 0) return;
     const int lane = lane_id();
+    const bool values = wave >= 4;
     const int row0 = (wave & 3) * R::kRows;
-    const unsigned char* from = place(at.lo, at.hi, idx);
+    const int id = __builtin_amdgcn_readlane(ids, idx);
+    const int key = j.first + (t + idx) * R::kKeys + row0;
+    const int64_t row =
+        ((int64_t)j.h << a.kv.page_shift) + (key & ((1 << a.kv.page_shift) - 1));
+    const unsigned char* from =
+        (values ? a.kv.v : a.kv.k) + id * a.kv.page_bytes + row * (D * R::CB);
     const unsigned to = E8 ? lds + R::kRaw + (stage * kWaves + wave) * R::kPiece
-                           : lds + stage * R::kTiles + (wave >= 4 ? R::kTile : 0) + row0 * R::kRow;
+                           : lds + stage * R::kTiles + (values ? R::kTile : 0) + row0 * R::kRow;
 #pragma unroll
     for (int n = 0; n < R::kCopies; ++n) {
       // 16 bits: as rows of a tile
       const int r = row0 + n * R::kRowsPerCopy + lane / R::kChunks;
       const int chunk = E8 ? lane % R::kChunks : (lane % R::kChunks) ^ R::swizzle(r);
-      copy16(from + n * R::kRowsPerCopy * D * R::CB,
+      copy16(uniform(from) + n * R::kRowsPerCopy * D * R::CB,
              (lane / R::kChunks) * D * R::CB + (unsigned)chunk * 16, to + n * 1024);
     }
     if constexpr (E8) {
-      const unsigned char* e = place(at.s_lo, at.s_hi, idx);
-      if (lane < R::kRows / 4) copy4(e, lane * 4, to + R::kRows * D);
+      const unsigned char* e = (values ? a.kv.vs : a.kv.ks) + id * a.kv.scale_page_bytes + row;
+      if (lane < R::kRows / 4) copy4(uniform(e), lane * 4, to + R::kRows * D);
     }
-    if (__builtin_expect((at.none | none) != 0, 0))
-      none = (none & ~(1u << stage)) | ((unsigned)(at.none >> idx) & 1u) << stage;
+    if (__builtin_expect((bad | none) != 0, 0))
+      none = (none & ~(1u << stage)) | ((unsigned)(bad >> idx) & 1u) << stage;
     stage = stage + 1 == R::kStages ? 0 : stage + 1;
     if (__builtin_expect(++idx == end, 0)) {
       t += end;
       idx = 0;
       if (t < j.n) {
-        at = fetch(a, j, t, wave);
+        ids = fetch(a, j, t, wave, &bad);
       } else {
         j = nj;
-        at = nat;
+        ids = nids;
+        bad = nbad;
         t = 0;
         if (j.n > 0) {
-          nj = next_span<D>(a, c, nullptr);
-          if (nj.n > 0) nat = fetch(a, nj, 0, wave);
+          nj = next_span<D>(a, lds + R::kReqs, c, nullptr);
+          if (nj.n > 0) nids = fetch(a, nj, 0, wave, &nbad);
         }
       }
       end = min(j.n - t, kWave);
@@ -811,15 +782,19 @@ __global__ __launch_bounds__(kThreads, (2 * Ring<E8, D>::kPerCu)) void split_ker
   // every wave finds its workgroup's share by itself where a wave's lanes hold
   // the batch; the workgroup together where they do not
   Cursor cur;
-  cur.n_r = -1;
   cur.begun = 0;
   int64_t u0, u1;
   int64_t total;
   const int wgs_all = gridDim.x;
   if (q.B <= kWave) {
-    load_window(a, 0, cur);
-    const int64_t mine =
-        cur.w_len ? units_of<D>(a, cur.w_c0, cur.w_len, cur.w_prefix) : 0;
+    int c0 = 0, len = 0, prefix = 0;
+    if (lane_id() < q.B && !rows_of(a, lane_id(), total_eff, &c0, &len, &prefix)) len = 0;
+    if (wave == 0) {
+      lds_write(lds + R::kReqs + 12 * lane_id(), c0);
+      lds_write(lds + R::kReqs + 12 * lane_id() + 4, len);
+      lds_write(lds + R::kReqs + 12 * lane_id() + 8, prefix);
+    }
+    const int64_t mine = len ? units_of<D>(a, c0, len, prefix) : 0;
     const int64_t incl = wave_incl_scan_op(mine, (int64_t)0, OpAdd{});
     total = read_lane(incl, kWave - 1);
     if (blockIdx.x == 0 && tid < q.B) ws.base[tid] = incl - mine;
@@ -830,6 +805,7 @@ __global__ __launch_bounds__(kThreads, (2 * Ring<E8, D>::kPerCu)) void split_ker
     const unsigned long long past = __ballot(u0 < incl);
     cur.r = past ? (int)__builtin_ctzll(past) : 0;
     cur.off = u0 - read_lane(incl - mine, cur.r);
+    barrier();
   } else {
     auto units = [&](int r) {
       int c0, len, prefix;
@@ -866,7 +842,6 @@ __global__ __launch_bounds__(kThreads, (2 * Ring<E8, D>::kPerCu)) void split_ker
     __syncthreads();
     cur.r = __builtin_amdgcn_readfirstlane(start_r);
     cur.off = read_lane(start_off, 0);
-    if (u0 < u1) load_window(a, cur.r, cur);
   }
   if (blockIdx.x == 0 && tid == 0) {
     ws.base[q.B] = total;
@@ -876,14 +851,14 @@ __global__ __launch_bounds__(kThreads, (2 * Ring<E8, D>::kPerCu)) void split_ker
   if (u0 >= u1) return;
   cur.left = u1 - u0;
   Feeder<E8, D> feed;
-  feed.start(a, cur, wave);
+  feed.start(a, lds, cur, wave);
 #pragma unroll
   for (int i = 0; i < (E8 ? R::kStages : R::kStages - 1); ++i) feed.next(a, lds, wave);
   int64_t left = u1 - u0;
   int stage = 0;
   for (;;) {
     Job job;
-    const Span span = next_span<D>(a, cur, &job);
+    const Span span = next_span<D>(a, lds + R::kReqs, cur, &job);
     if (span.n == 0) break;
     // the wave has a tile of it, or not; nobody has of a request whose tree is none
     bool rows = wave < job.mt;
