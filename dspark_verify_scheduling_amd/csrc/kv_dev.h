@@ -80,6 +80,7 @@ struct AttnArgs {
   ReqView req;
   KvView kv;
   int num_heads, group;
+  int waves;  // of a workgroup, and so 16-row tiles of a segment, at most
   const unsigned char* q;
   int64_t q_ld;  // bytes
   float scale;

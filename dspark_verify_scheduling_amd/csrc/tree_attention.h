@@ -8,9 +8,6 @@
 namespace dspark {
 namespace attn {
 
-constexpr int kThreads = 512;
-constexpr int kWaves = kThreads / kWave;
-
 // What the split kernel leaves for the joining kernel: the schedule's prefix
 // sums, and per partial segment the running maximum and sum of each of its rows
 // and their unnormalised outputs. Workgroup w has segments 2 w (the one its
@@ -24,9 +21,18 @@ struct Parts {
   int rows;       // rows of a segment, at most
 };
 
-// Tiles of 16 query rows of a segment, at most (one to a wave), and keys of a
-// unit.
-constexpr int kMaxTiles = kWaves;
+// Waves of a workgroup, one to each 16-row tile of a segment: the more rows meet
+// in a segment the fewer reads of its keys; with few rows in a request four
+// waves do, and feed the tiles with less work around it (32 chains of 9 rows,
+// 32 query heads on 8, 1k to 8k keys: 110 us against 125 with eight; 64 trees of
+// up to 17 rows, 64 on 8, 8-bit: 299 us against 240).
+constexpr int kMostWaves = 8, kFewWaves = 4;  // (shape_of() shifts by them)
+// (Its share of a tile has to stay within a page: 16 keys.)
+inline int waves_for(int rows, int dim) {
+  return rows <= 16 * kFewWaves && dim >= 128 ? kFewWaves : kMostWaves;
+}
+
+// Keys of a unit.
 template <int D>
 struct Size {
   static constexpr int kKeys = D >= 128 ? 32 : 64;
@@ -56,7 +62,7 @@ __device__ inline bool rows_of(const AttnArgs& a, int r, int total_eff, int* c0,
 
 template <int D>
 __device__ inline Shape shape_of(const AttnArgs& a, int c0, int len, int prefix) {
-  constexpr int kT = kMaxTiles, kK = Size<D>::kKeys;
+  constexpr int kK = Size<D>::kKeys;
   Shape s;
   s.c0 = c0;
   s.len = len;
@@ -64,7 +70,7 @@ __device__ inline Shape shape_of(const AttnArgs& a, int c0, int len, int prefix)
   s.keys = prefix + len;
   s.mrows = a.group * len;
   s.mtiles = (s.mrows + 15) >> 4;
-  s.nseg = (s.mtiles + kT - 1) / kT;
+  s.nseg = (s.mtiles + a.waves - 1) >> (a.waves == kFewWaves ? 2 : 3);
   s.per = (s.mtiles + s.nseg - 1) / s.nseg;
   s.nku = (s.keys + kK - 1) / kK;
   return s;
@@ -189,6 +195,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // log2): weights then stay below 2^kSlack, and most steps rescale nothing.
 constexpr float kSlack = 8.0f;
 
+// Workgroups to a CU, by their LDS.
+constexpr int per_cu(int dim) { return dim == 256 ? 1 : 2; }
+
 // LDS of a workgroup. A tile of keys and values in 16 bits is shared by its
 // waves; rows are unpadded (copies into LDS write densely), and 16-byte chunk c
 // of a row lies at chunk c ^ swizzle(row), so that the 16 rows which a wave reads
@@ -196,7 +205,7 @@ constexpr float kSlack = 8.0f;
 //   16-bit caches: a ring of kStages tiles, filled straight from memory.
 //   8-bit caches: each wave has a ring of kStages pieces of codes and exponents
 //   for itself, and widens its piece of the next tile into one of two tiles.
-template <bool E8, int D>
+template <bool E8, int D, int W>
 struct Ring {
   static constexpr int CB = E8 ? 1 : 2;
   static constexpr int kKeys = Size<D>::kKeys;
@@ -204,26 +213,27 @@ struct Ring {
   static constexpr int kRow = 2 * D;                  // bytes of a row of a tile
   static constexpr int kTile = kKeys * kRow;          // keys, or values
   static constexpr int kTiles = 2 * kTile;            // both
-  // a wave's share of a tile: kRows keys (waves 0 to 3) or values (4 to 7), in
-  // copies of kWave 16-byte chunks
-  static constexpr int kRows = kKeys / 4;
+  // a wave's share of a tile: kRows keys (the first half of the waves) or values
+  // (the second), in copies of kWave 16-byte chunks
+  static constexpr int kRows = kKeys / (W / 2);
   static constexpr int kChunks = D * CB / 16;         // of a cache row
   static constexpr int kRowsPerCopy = kWave / kChunks;
   static constexpr int kCopies = kRows / kRowsPerCopy;
   static_assert(kCopies * kRowsPerCopy == kRows, "whole copies");
+  static_assert(kRows <= 16, "of one page");
   static constexpr int kPerWave = kCopies + (E8 ? 1 : 0);
   static constexpr int kPiece = kRows * D + 64;       // codes, exponents; 8 bits
   static constexpr int kRaw = 2 * kTiles;             // offset of the waves' rings
-  // (fewer where the LDS of a CU, or of half a CU, holds no more)
+  // (what the LDS of a CU, or of half a CU, holds; even in an 8-bit ring)
   static constexpr int kStages =
       D == 256 ? 4 : (E8 ? 4 : (65536 / kTiles < 4 ? 65536 / kTiles : 4));
   // rows with NaN or infinity, a bit each; of two tiles
-  static constexpr int kOdd = E8 ? kRaw + kStages * kWaves * kPiece : kStages * kTiles;
+  static constexpr int kOdd = E8 ? kRaw + kStages * W * kPiece : kStages * kTiles;
   static constexpr int kReqs = kOdd + 16;  // rows of up to kWave requests, 3 words each
   static constexpr int kBytes = kReqs + 12 * kWave;
-  // workgroups to a CU, of its 160 KiB
-  static constexpr int kPerCu = D == 256 ? 1 : 2;
+  static constexpr int kPerCu = per_cu(D);
   static_assert(kBytes <= 163840 / kPerCu - 256, "a CU's LDS");
+  static_assert(!E8 || kStages % 2 == 0, "pieces go to the two tiles in turn");
   static __device__ int swizzle(int row) {
     return D >= 128 ? row & 15 : (row >> 1) & 7;
   }
@@ -307,9 +317,9 @@ __device__ __forceinline__ Span next_span(const AttnArgs& a, unsigned reqs, Curs
 // The producing side of the ring: this wave's copies of the next tile. Few
 // registers are kept for it: a reload of a spilled one would wait for every copy
 // under way.
-template <bool E8, int D>
+template <bool E8, int D, int W>
 struct Feeder {
-  typedef Ring<E8, D> R;
+  typedef Ring<E8, D, W> R;
   typedef unsigned long long u64;
   Cursor c;
   Span j, nj;      // the segment copied from, and the one after it
@@ -322,7 +332,7 @@ struct Feeder {
 
   // The pages of 64 tiles from tile t on, a tile to a lane.
   static __device__ int fetch(const AttnArgs& a, const Span& x, int t, int wave, u64* bad) {
-    const int group = ((wave & 3) * R::kRows) >> 4;
+    const int group = ((wave & (W / 2 - 1)) * R::kRows) >> 4;
     int own = 0;
     const int64_t first = (int64_t)x.first + (int64_t)(t + lane_id()) * R::kKeys;
     int id[R::kGroups];
@@ -360,15 +370,15 @@ struct Feeder {
   __device__ __forceinline__ void next(const AttnArgs& a, unsigned lds, int wave) {
     if (end == 0) return;
     const int lane = lane_id();
-    const bool values = wave >= 4;
-    const int row0 = (wave & 3) * R::kRows;
+    const bool values = wave >= W / 2;
+    const int row0 = (wave & (W / 2 - 1)) * R::kRows;
     const int id = __builtin_amdgcn_readlane(ids, idx);
     const int key = j.first + (t + idx) * R::kKeys + row0;
     const int64_t row =
         ((int64_t)j.h << a.kv.page_shift) + (key & ((1 << a.kv.page_shift) - 1));
     const unsigned char* from =
         (values ? a.kv.v : a.kv.k) + id * a.kv.page_bytes + row * (D * R::CB);
-    const unsigned to = E8 ? lds + R::kRaw + (stage * kWaves + wave) * R::kPiece
+    const unsigned to = E8 ? lds + R::kRaw + (stage * W + wave) * R::kPiece
                            : lds + stage * R::kTiles + (values ? R::kTile : 0) + row0 * R::kRow;
 #pragma unroll
     for (int n = 0; n < R::kCopies; ++n) {
@@ -411,14 +421,14 @@ struct Feeder {
 //   S^T = K Q^T: keys are its rows and queries its columns, so a lane holds the
 //   scores of one query (lane & 15) for four keys of each sixteen, which are in
 //   place as the operand of  O^T = V^T P^T.
-template <typename T, bool E8, int D, bool ROWS>
+template <typename T, bool E8, int D, int W, bool ROWS>
 __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, const Span& span,
-                                        const Job& job, Feeder<E8, D>& feed, unsigned lds,
+                                        const Job& job, Feeder<E8, D, W>& feed, unsigned lds,
                                         int left, int& stage) {
   typedef Types<T> TT;
   typedef typename TT::V8 V8;
   typedef typename TT::V4 V4;
-  typedef Ring<E8, D> R;
+  typedef Ring<E8, D, W> R;
   constexpr int NF = D / 32;         // operand chunks of a key
   constexpr int ND = D / 16;         // 16-column tiles of the output
   constexpr int NG = R::kGroups;     // 16-key groups of a tile
@@ -534,14 +544,14 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
     auto put_odd = [&](unsigned rows) {
       if (lane == 0) {
         if constexpr (R::kRows == 8) {
-          lds_write<unsigned char>(odd_at + (wave & 3), (unsigned char)rows);
+          lds_write<unsigned char>(odd_at + (wave & (W / 2 - 1)), (unsigned char)rows);
         } else {
-          lds_write<unsigned short>(odd_at + 2 * (wave & 3), (unsigned short)rows);
+          lds_write<unsigned short>(odd_at + 2 * (wave & (W / 2 - 1)), (unsigned short)rows);
         }
       }
     };
-    const bool values = wave >= 4;
-    const int row0 = (wave & 3) * R::kRows;  // of the wave's keys, or values
+    const bool values = wave >= W / 2;
+    const int row0 = (wave & (W / 2 - 1)) * R::kRows;  // of the wave's keys, or values
     if constexpr (E8) {
       // the wave's piece of this tile: done when the pieces after it may not be
       if (left > R::kStages - 1) {
@@ -552,7 +562,7 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
       const int tile = stage & 1;  // (an even number of stages)
       buf = lds + tile * R::kTiles;
       odd_at += tile * 8;
-      const unsigned from = lds + R::kRaw + (stage * kWaves + wave) * R::kPiece;
+      const unsigned from = lds + R::kRaw + (stage * W + wave) * R::kPiece;
       const unsigned to = buf + (values ? R::kTile : 0);
       unsigned strange_rows = 0;
 #pragma unroll
@@ -766,11 +776,13 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
 // order: workgroup w takes the w-th equal share, so ragged contexts balance by
 // themselves and a long one is split over many workgroups. The ring of tiles
 // runs on across segments.
-template <typename T, bool E8, int D>
-__global__ __launch_bounds__(kThreads, (2 * Ring<E8, D>::kPerCu)) void split_kernel(AttnArgs a, Parts ws) {
-  typedef Ring<E8, D> R;
+template <typename T, bool E8, int D, int W>
+__global__ __launch_bounds__(W * kWave, (Ring<E8, D, W>::kPerCu * W / 4)) void split_kernel(
+    AttnArgs a, Parts ws) {
+  constexpr int kThreads = W * kWave;
+  typedef Ring<E8, D, W> R;
   __shared__ __align__(1024) unsigned char lds_mem[R::kBytes];
-  __shared__ int64_t wsum[kWaves];
+  __shared__ int64_t wsum[W];
   __shared__ int start_r;
   __shared__ int64_t start_off;
   const ReqView& q = a.req;
@@ -850,7 +862,7 @@ __global__ __launch_bounds__(kThreads, (2 * Ring<E8, D>::kPerCu)) void split_ker
   }
   if (u0 >= u1) return;
   cur.left = u1 - u0;
-  Feeder<E8, D> feed;
+  Feeder<E8, D, W> feed;
   feed.start(a, lds, cur, wave);
 #pragma unroll
   for (int i = 0; i < (E8 ? R::kStages : R::kStages - 1); ++i) feed.next(a, lds, wave);
@@ -870,24 +882,32 @@ __global__ __launch_bounds__(kThreads, (2 * Ring<E8, D>::kPerCu)) void split_ker
     // tiles still to come, as far as the end of the ring is concerned
     const int near = (int)min(left, (int64_t)1 << 30);
     if (rows) {
-      segment<T, E8, D, true>(a, ws, span, job, feed, lds, near, stage);
+      segment<T, E8, D, W, true>(a, ws, span, job, feed, lds, near, stage);
     } else {
-      segment<T, E8, D, false>(a, ws, span, job, feed, lds, near, stage);
+      segment<T, E8, D, W, false>(a, ws, span, job, feed, lds, near, stage);
     }
     left -= span.n;
   }
 }
 
+template <int D, int W>
+void launch_waves(const AttnArgs& a, const Parts& ws, dspark_dtype dt, hipStream_t s) {
+  const dim3 grid((unsigned)ws.wgs), block(W * kWave);
+  if (a.kv.cb == 1) {
+    hipLaunchKernelGGL((split_kernel<__bf16, true, D, W>), grid, block, 0, s, a, ws);
+  } else if (dt == DSPARK_BF16) {
+    hipLaunchKernelGGL((split_kernel<__bf16, false, D, W>), grid, block, 0, s, a, ws);
+  } else {
+    hipLaunchKernelGGL((split_kernel<_Float16, false, D, W>), grid, block, 0, s, a, ws);
+  }
+}
+
 template <int D>
 void launch_dim(const AttnArgs& a, const Parts& ws, dspark_dtype dt, hipStream_t s) {
-  const dim3 grid((unsigned)ws.wgs), block(kThreads);
-  if (a.kv.cb == 1) {
-    hipLaunchKernelGGL((split_kernel<__bf16, true, D>), grid, block, 0, s, a, ws);
-  } else if (dt == DSPARK_BF16) {
-    hipLaunchKernelGGL((split_kernel<__bf16, false, D>), grid, block, 0, s, a, ws);
-  } else {
-    hipLaunchKernelGGL((split_kernel<_Float16, false, D>), grid, block, 0, s, a, ws);
+  if constexpr (D >= 128) {
+    if (a.waves == kFewWaves) return launch_waves<D, kFewWaves>(a, ws, dt, s);
   }
+  launch_waves<D, kMostWaves>(a, ws, dt, s);
 }
 
 void launch_dim64(const AttnArgs& a, const Parts& ws, dspark_dtype dt, hipStream_t s);

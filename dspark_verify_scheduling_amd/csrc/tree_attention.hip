@@ -134,7 +134,7 @@ struct Plan {
 Plan plan(int B, int gamma, int group, int D) {
   Plan p;
   const int mtiles = (group * (gamma + 1) + 15) / 16;
-  p.rows = 16 * std::min(kMaxTiles, mtiles);
+  p.rows = 16 * std::min(waves_for(group * (gamma + 1), D), mtiles);
   const size_t stat = align256((size_t)2 * kMaxWgs * p.rows * sizeof(float));
   p.m_off = align256((size_t)(B + 1) * sizeof(int64_t));
   p.l_off = p.m_off + stat;
@@ -165,7 +165,9 @@ size_t attention_workspace(int B, int gamma, int num_heads, int num_kv_heads, in
   return attn::plan(B, gamma, num_heads / num_kv_heads, head_dim).bytes;
 }
 
-hipError_t launch_attention(const AttnArgs& a, dspark_dtype dt, hipStream_t s) {
+hipError_t launch_attention(const AttnArgs& args, dspark_dtype dt, hipStream_t s) {
+  AttnArgs a = args;
+  a.waves = attn::waves_for(a.group * (a.req.gamma + 1), a.kv.dim);
   int cus = 0;
   hipError_t e = current_cu_count(&cus);
   if (e != hipSuccess) return e;
@@ -177,7 +179,7 @@ hipError_t launch_attention(const AttnArgs& a, dspark_dtype dt, hipStream_t s) {
   ws.l = reinterpret_cast<float*>(w + p.l_off);
   ws.o = reinterpret_cast<float*>(w + p.o_off);
   ws.rows = p.rows;
-  const int per_cu = a.kv.dim == 256 ? attn::Ring<false, 256>::kPerCu : attn::Ring<false, 128>::kPerCu;
+  const int per_cu = attn::per_cu(a.kv.dim);
   ws.wgs = std::min(attn::kMaxWgs, per_cu * cus);
   switch (a.kv.dim) {
     case 64: attn::launch_dim64(a, ws, dt, s); break;
