@@ -226,29 +226,57 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a) {
   const int total_eff = rows_in_use(q, &total);
   const int64_t reach = (int64_t)q.width << a.kv.page_shift;
   if (blockIdx.x == 0) {
-    // one wave per request, a lane per page
+    // sixteen lanes per request, a lane per page; kAhead requests of a lane at
+    // once, so that a batch costs two memory latencies (256 requests, one by one:
+    // 27 us)
+    constexpr int kLanes = 16, kAhead = 8;
     __shared__ int all;
     if (tid == 0) all = total != total_eff ? DSPARK_DATA_BAD_LENS : 0;
     __syncthreads();
-    for (int r = tid / kWave; r < q.B; r += kThreads / kWave) {
-      const int s = q.cu[r], e = q.cu[r + 1], st = q.prefix[r];
-      int bits = 0;
-      if (s < 0 || e < s || e > total_eff || st < 0) {
-        bits = DSPARK_DATA_BAD_LENS;
-      } else if (e > s) {
-        const int64_t hi = (int64_t)st + (e - s);
-        if (hi > reach) {
-          bits = DSPARK_DATA_BAD_PAGE;
-        } else {
-          for (int64_t p = (st >> a.kv.page_shift) + lane; p <= (hi - 1) >> a.kv.page_shift;
-               p += kWave) {
-            const int id = q.table[(size_t)r * q.width + p];
-            if (id < 0 || id >= a.kv.num_blocks) bits = DSPARK_DATA_BAD_PAGE;
+    const int l = tid % kLanes;
+    int bits = 0;
+    for (int r0 = tid / kLanes; r0 < q.B; r0 += kAhead * (kThreads / kLanes)) {
+      int s[kAhead], e[kAhead], st[kAhead], id[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int r = min(r0 + k * (kThreads / kLanes), q.B - 1);
+        s[k] = q.cu[r];
+        e[k] = q.cu[r + 1];
+        st[k] = q.prefix[r];
+      }
+      int first[kAhead], last[kAhead];  // the lane's pages
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int r = min(r0 + k * (kThreads / kLanes), q.B - 1);
+        first[k] = 0;
+        last[k] = -1;
+        if (s[k] < 0 || e[k] < s[k] || e[k] > total_eff || st[k] < 0) {
+          bits |= DSPARK_DATA_BAD_LENS;
+        } else if (e[k] > s[k]) {
+          const int64_t hi = (int64_t)st[k] + (e[k] - s[k]);
+          if (hi > reach) {
+            bits |= DSPARK_DATA_BAD_PAGE;
+          } else {
+            first[k] = (st[k] >> a.kv.page_shift) + l;
+            last[k] = (int)((hi - 1) >> a.kv.page_shift);
           }
         }
+        id[k] = 0;
+        if (first[k] <= last[k]) id[k] = q.table[(size_t)r * q.width + first[k]];
       }
-      if (bits) atomicOr(&all, bits);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int r = min(r0 + k * (kThreads / kLanes), q.B - 1);
+        if (first[k] <= last[k] && (id[k] < 0 || id[k] >= a.kv.num_blocks))
+          bits |= DSPARK_DATA_BAD_PAGE;
+#pragma unroll 4
+        for (int p = first[k] + kLanes; p <= last[k]; p += kLanes) {
+          const int x = q.table[(size_t)r * q.width + p];
+          if (x < 0 || x >= a.kv.num_blocks) bits |= DSPARK_DATA_BAD_PAGE;
+        }
+      }
     }
+    if (bits) atomicOr(&all, bits);
     __syncthreads();
     if (tid == 0) {
       a.meta[0] = total;
@@ -314,128 +342,185 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a) {
 
 // ------------------------------------------------------------------ commit
 
-constexpr int kMoveBatch = 8;
-
-// The moves of request r, by the first wave's lanes: lane l has k = l + 1.
-// Returns the status bits; *src, *dst the lane's cache indices, *src = -1 where
-// it moves nothing.
-__device__ int path_moves(const CommitArgs& a, int r, int lane, int64_t* src, int64_t* dst) {
+// The moves of N requests, L lanes to each: lane l of them has k = l + 1. `r`:
+// the request of the lane's group, -1 for none. bits: its status; *src, *dst the
+// lane's cache indices, *src = -1 where it moves nothing. N requests cost three
+// memory latencies together.
+template <int L, int N>
+__device__ inline void path_moves(const CommitArgs& a, const int (&r)[N], int lane, int (&bits)[N],
+                                  int64_t (&src)[N], int64_t (&dst)[N]) {
   const ReqView& q = a.req;
-  *src = *dst = -1;
-  const int c = a.num_correct[r], prefix = q.prefix[r];
-  if (c < 0 || c > q.gamma || prefix < 0) return DSPARK_DATA_BAD_LENS;
-  const int32_t* path = a.path + (size_t)r * (q.gamma + 1);
-  const bool on = lane < c;
-  const int here = on ? path[lane + 1] : 0, before = on ? path[lane] : 0;
-  const bool ok = path[0] == 0 && (!on || (here > before && here <= q.gamma));
-  if (__ballot(!ok)) return DSPARK_DATA_BAD_TREE;
-  if (on && here != lane + 1) {
-    *src = (int64_t)prefix + here;
-    *dst = (int64_t)prefix + lane + 1;
-  }
+  const int l = lane & (L - 1);
+  const unsigned long long group = (L == 64 ? ~0ull : (1ull << (L & 63)) - 1) << (lane - l);
   const int64_t reach = (int64_t)q.width << a.kv.page_shift;
-  bool good = true;
-  if (*src >= 0) {
-    good = *src < reach;
-    if (good) {
-      const int s = q.table[(size_t)r * q.width + (*src >> a.kv.page_shift)];
-      const int d = q.table[(size_t)r * q.width + (*dst >> a.kv.page_shift)];
-      good = s >= 0 && s < a.kv.num_blocks && d >= 0 && d < a.kv.num_blocks;
+  int c[N], prefix[N], root[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    c[n] = prefix[n] = root[n] = 0;
+    if (r[n] >= 0) {
+      c[n] = a.num_correct[r[n]];
+      prefix[n] = q.prefix[r[n]];
+      root[n] = a.path[(size_t)r[n] * (q.gamma + 1)];
     }
   }
-  if (__ballot(!good)) {
-    *src = -1;
-    return DSPARK_DATA_BAD_PAGE;
+  int here[N], before[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    bits[n] = c[n] < 0 || c[n] > q.gamma || prefix[n] < 0 ? DSPARK_DATA_BAD_LENS : 0;
+    here[n] = before[n] = 0;
+    if (!bits[n] && l < c[n]) {
+      here[n] = a.path[(size_t)r[n] * (q.gamma + 1) + l + 1];
+      before[n] = a.path[(size_t)r[n] * (q.gamma + 1) + l];
+    }
   }
-  return 0;
+  int s[N], d[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    src[n] = dst[n] = -1;
+    const bool on = !bits[n] && l < c[n];
+    const bool ok = root[n] == 0 && (!on || (here[n] > before[n] && here[n] <= q.gamma));
+    if ((__ballot(!ok) & group) && !bits[n]) bits[n] = DSPARK_DATA_BAD_TREE;
+    if (!bits[n] && on && here[n] != l + 1) {
+      src[n] = (int64_t)prefix[n] + here[n];
+      dst[n] = (int64_t)prefix[n] + l + 1;
+    }
+    s[n] = d[n] = 0;
+    if (src[n] >= reach) {
+      s[n] = -1;
+    } else if (src[n] >= 0) {
+      s[n] = q.table[(size_t)r[n] * q.width + (src[n] >> a.kv.page_shift)];
+      d[n] = q.table[(size_t)r[n] * q.width + (dst[n] >> a.kv.page_shift)];
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const bool good = s[n] >= 0 && s[n] < a.kv.num_blocks && d[n] >= 0 && d[n] < a.kv.num_blocks;
+    if (__ballot(!good) & group) {
+      src[n] = -1;
+      bits[n] = DSPARK_DATA_BAD_PAGE;
+    }
+  }
 }
 
-// One workgroup per (request, layer); a thread owns 16-byte columns of it (one
-// place of one head of the keys or of the values) and moves the path's rows of
-// that column in ascending order. Path rows ascend and path[k] >= k, so a move
-// never overwrites the source of a later one, and a batch of kMoveBatch loads
-// may run ahead of its stores: the rows it stores to, k .. k + kMoveBatch - 1,
-// lie below every later source.
+// Status and number of moves of all requests; one workgroup.
+template <int L>
+__device__ void commit_status(const CommitArgs& a) {
+  constexpr int N = 8, kGroups = kThreads / L;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  __shared__ int all, moved;
+  if (tid == 0) all = moved = 0;
+  __syncthreads();
+  int seen = 0, count = 0;
+  for (int r0 = 0; r0 < a.req.B; r0 += N * kGroups) {
+    int r[N], bits[N];
+    int64_t src[N], dst[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int x = r0 + n * kGroups + tid / L;
+      r[n] = x < a.req.B ? x : -1;
+    }
+    path_moves<L, N>(a, r, lane, bits, src, dst);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      seen |= bits[n];
+      count += src[n] >= 0;
+    }
+  }
+  if (seen) atomicOr(&all, seen);
+  if (count) atomicAdd(&moved, count);
+  __syncthreads();
+  if (tid == 0) {
+    a.meta[0] = moved;
+    a.meta[1] = all;
+  }
+}
+
+// The n moves of one column of T: up to kMoveBatch loads ahead of their stores.
+template <typename T>
+__device__ inline void move_column(unsigned char* base, int64_t page_bytes, int64_t row_bytes, int n,
+                                   const int* s_id, const int* s_off, const int* d_id,
+                                   const int* d_off) {
+  constexpr int kMoveBatch = 8;
+  for (int k0 = 0; k0 < n; k0 += kMoveBatch) {
+    T x[kMoveBatch];
+#pragma unroll
+    for (int i = 0; i < kMoveBatch; ++i) {
+      x[i] = (T){};
+      if (k0 + i < n)
+        x[i] = *reinterpret_cast<const T*>(base + s_id[k0 + i] * page_bytes +
+                                           s_off[k0 + i] * row_bytes);
+    }
+#pragma unroll
+    for (int i = 0; i < kMoveBatch; ++i) {
+      if (k0 + i < n)
+        *reinterpret_cast<T*>(base + d_id[k0 + i] * page_bytes + d_off[k0 + i] * row_bytes) = x[i];
+    }
+  }
+}
+
+// One workgroup per (request, kCommitLayers layers); a thread owns 16-byte
+// columns of them (one place of one head of a layer's keys or values) or bytes
+// of exponents, and moves the path's rows of that column in ascending order.
+// Path rows ascend and path[k] >= k, so a move never overwrites the source of a
+// later one, and a batch of loads may run ahead of its stores: the rows it
+// stores to, k .. k + kMoveBatch - 1, lie below every later source.
+constexpr int kCommitLayers = 4;
+
 __global__ __launch_bounds__(kThreads) void commit_kernel(CommitArgs a) {
   const ReqView& q = a.req;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   if (blockIdx.x == 0) {
     if (blockIdx.y != 0) return;
-    __shared__ int all, moved;
-    if (tid == 0) all = moved = 0;
-    __syncthreads();
-    for (int r = tid / kWave; r < q.B; r += kThreads / kWave) {
-      int64_t src, dst;
-      const int bits = path_moves(a, r, lane, &src, &dst);
-      const int n = __popcll(__ballot(src >= 0));
-      if (lane == 0) {
-        if (bits) atomicOr(&all, bits);
-        if (n) atomicAdd(&moved, n);
-      }
-    }
-    __syncthreads();
-    if (tid == 0) {
-      a.meta[0] = moved;
-      a.meta[1] = all;
+    if (q.gamma <= 16) {
+      commit_status<16>(a);
+    } else {
+      commit_status<kWave>(a);
     }
     return;
   }
-  const int r = blockIdx.x - 1;
   __shared__ int s_id[DSPARK_MAX_GAMMA], s_off[DSPARK_MAX_GAMMA], d_id[DSPARK_MAX_GAMMA],
       d_off[DSPARK_MAX_GAMMA];
   __shared__ int n_moves;
   if (tid < kWave) {
-    int64_t src, dst;
-    path_moves(a, r, lane, &src, &dst);
-    const unsigned long long m = __ballot(src >= 0);
-    if (src >= 0) {
+    const int r[1] = {(int)blockIdx.x - 1};
+    int bits[1];
+    int64_t src[1], dst[1];
+    path_moves<kWave, 1>(a, r, lane, bits, src, dst);
+    const unsigned long long m = __ballot(src[0] >= 0);
+    if (src[0] >= 0) {
       const int i = __popcll(m & ((1ull << lane) - 1));
       const int mask = (1 << a.kv.page_shift) - 1;
-      s_id[i] = q.table[(size_t)r * q.width + (src >> a.kv.page_shift)];
-      d_id[i] = q.table[(size_t)r * q.width + (dst >> a.kv.page_shift)];
-      s_off[i] = (int)(src & mask);
-      d_off[i] = (int)(dst & mask);
+      s_id[i] = q.table[(size_t)r[0] * q.width + (src[0] >> a.kv.page_shift)];
+      d_id[i] = q.table[(size_t)r[0] * q.width + (dst[0] >> a.kv.page_shift)];
+      s_off[i] = (int)(src[0] & mask);
+      d_off[i] = (int)(dst[0] & mask);
     }
     if (lane == 0) n_moves = __popcll(m);
   }
   __syncthreads();
   const int n = n_moves;
   if (n == 0) return;
-  const int row_vecs = a.kv.dim * a.kv.cb / 16;
-  const size_t row_bytes = (size_t)a.kv.dim * a.kv.cb;
-  const int cols = 2 * a.kv.hkv * row_vecs;
-  for (int col = tid; col < cols; col += kThreads) {
-    const int row = col / row_vecs;  // keys' heads, then values' heads
-    const int w = row >= a.kv.hkv, h = row - w * a.kv.hkv;
-    unsigned char* base = (w ? a.kv.v : a.kv.k) + (size_t)blockIdx.y * a.kv.layer_bytes +
-                          (((size_t)h << a.kv.page_shift) * row_bytes) +
-                          (size_t)(col - row * row_vecs) * 16;
-    for (int k0 = 0; k0 < n; k0 += kMoveBatch) {
-      kv_u32x4 x[kMoveBatch];
-#pragma unroll
-      for (int i = 0; i < kMoveBatch; ++i) {
-        x[i] = (kv_u32x4){0u, 0u, 0u, 0u};
-        if (k0 + i < n)
-          x[i] = *reinterpret_cast<const kv_u32x4*>(base + (size_t)s_id[k0 + i] * a.kv.page_bytes +
-                                                    s_off[k0 + i] * row_bytes);
-      }
-#pragma unroll
-      for (int i = 0; i < kMoveBatch; ++i) {
-        if (k0 + i < n)
-          *reinterpret_cast<kv_u32x4*>(base + (size_t)d_id[k0 + i] * a.kv.page_bytes +
-                                       d_off[k0 + i] * row_bytes) = x[i];
-      }
-    }
+  const int row_bytes = a.kv.dim * a.kv.cb, row_vecs = row_bytes / 16;
+  const int rows = 2 * a.kv.hkv;  // of a layer: keys' heads, then values' heads
+  const int cols = rows * row_vecs;
+  const int layer0 = blockIdx.y * kCommitLayers;
+  const int layers = min(kCommitLayers, a.kv.num_layers - layer0);
+  for (int i = tid; i < layers * cols; i += kThreads) {
+    const int layer = i / cols, col = i - layer * cols;
+    const int row = col / row_vecs, w = row >= a.kv.hkv, h = row - w * a.kv.hkv;
+    move_column<kv_u32x4>((w ? a.kv.v : a.kv.k) + (layer0 + layer) * a.kv.layer_bytes +
+                              ((int64_t)h << a.kv.page_shift) * row_bytes +
+                              (col - row * row_vecs) * 16,
+                          a.kv.page_bytes, row_bytes, n, s_id, s_off, d_id, d_off);
   }
   if (a.kv.ks) {
-    for (int row = tid; row < 2 * a.kv.hkv; row += kThreads) {
+    for (int i = tid; i < layers * rows; i += kThreads) {
+      const int layer = i / rows, row = i - layer * rows;
       const int w = row >= a.kv.hkv, h = row - w * a.kv.hkv;
-      uint8_t* base = (w ? a.kv.vs : a.kv.ks) + (size_t)blockIdx.y * a.kv.scale_layer_bytes +
-                      ((size_t)h << a.kv.page_shift);
-      for (int k = 0; k < n; ++k) {
-        base[(size_t)d_id[k] * a.kv.scale_page_bytes + d_off[k]] =
-            base[(size_t)s_id[k] * a.kv.scale_page_bytes + s_off[k]];
-      }
+      move_column<unsigned char>((w ? a.kv.vs : a.kv.ks) +
+                                     (layer0 + layer) * a.kv.scale_layer_bytes +
+                                     ((int64_t)h << a.kv.page_shift),
+                                 a.kv.scale_page_bytes, 1, n, s_id, s_off, d_id, d_off);
     }
   }
 }
@@ -494,7 +579,8 @@ hipError_t launch_read(const ReadArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_commit(const CommitArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(commit_kernel, dim3(1u + (unsigned)a.req.B, (unsigned)a.kv.num_layers),
+  hipLaunchKernelGGL(commit_kernel, dim3(1u + (unsigned)a.req.B,
+                                         ((unsigned)a.kv.num_layers + kCommitLayers - 1) / kCommitLayers),
                      dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
