@@ -68,7 +68,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a, Parts ws
     const int rows = min(s.per * 16, s.mrows - seg * s.per * 16);
     const int row = (step - seg * steps) * kRows + tid / kLanes;
     if (row < rows) {
-      constexpr int kAhead = 4;
+      constexpr int kAhead = 8;
       float top = -__builtin_inff(), sum = 0.0f;
       f32x4 y[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
       for (int p0 = 0; p0 < n; p0 += kAhead) {
@@ -149,7 +149,7 @@ void launch_join(const AttnArgs& a, const Parts& ws, dspark_dtype dt, hipStream_
   const int pairs = a.req.B * a.kv.hkv;
   const int rows = a.group * (a.req.gamma + 1), at_once = kJoinThreads / (D / 8);
   const int most = (rows + at_once - 1) / at_once;
-  const int shares = std::max(1, std::min(most, 4096 / std::max(pairs, 1)));
+  const int shares = std::max(1, std::min(most, 1024 / std::max(pairs, 1)));
   const dim3 grid((unsigned)pairs * shares), block(kJoinThreads);
   if (dt == DSPARK_BF16) {
     hipLaunchKernelGGL((join_kernel<__bf16, D>), grid, block, 0, s, a, ws, shares);
