@@ -20,30 +20,66 @@ constexpr int kThreads = 256;
 
 // ------------------------------------------------------------------ append
 
-// Status of request r, its pages and positions included; one thread.
-__device__ int append_status(const AppendArgs& a, int r, int total_eff) {
+// Status of all requests, their pages and positions included; one workgroup. L
+// lanes to a request, lane l for its row l + 1 and its l-th page, N requests of
+// a lane at once: a batch costs three memory latencies.
+template <int L>
+__device__ int append_status(const AppendArgs& a, int total_eff) {
+  constexpr int N = 4, kGroups = kThreads / L;
+  static_assert((DSPARK_MAX_GAMMA + 1) / 16 + 2 <= 16, "pages of a step to a group");
   const ReqView& q = a.req;
-  int bits = request_status(q, r, total_eff);
-  if (bits) return bits;
-  const int len = q.cu[r + 1] - q.cu[r];
-  const int64_t lo = q.prefix[r], hi = lo + len;  // cache indices [lo, hi)
-  if (hi > ((int64_t)q.width << a.kv.page_shift)) return DSPARK_DATA_BAD_PAGE;
-  for (int64_t p = lo >> a.kv.page_shift; p <= (hi - 1) >> a.kv.page_shift; ++p) {
-    const int id = q.table[(size_t)r * q.width + p];
-    if (id < 0 || id >= a.kv.num_blocks) bits |= DSPARK_DATA_BAD_PAGE;
-  }
-  if (a.rope && hi > a.rope_rows) {
-    // a tree's depths may still be small enough
-    for (int j = 0; j < len; ++j) {
-      int depth = j;
-      if (q.parents) {
-        depth = 0;
-        for (int n = j; n > 0; n = q.parents[(size_t)r * q.gamma + n - 1]) ++depth;
+  const int lane = threadIdx.x & (kWave - 1), l = lane & (L - 1);
+  const unsigned long long group = (L == 64 ? ~0ull : (1ull << (L & 63)) - 1) << (lane - l);
+  int all = 0;
+  for (int r0 = 0; r0 < q.B; r0 += N * kGroups) {
+    int r[N], c0[N], len[N], prefix[N], par[N], id[N];
+    bool ok[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      // (past the last: the last once more)
+      r[n] = min(r0 + n * kGroups + (int)threadIdx.x / L, q.B - 1);
+      ok[n] = request_rows(q, r[n], total_eff, &c0[n], &len[n]);
+      prefix[n] = q.prefix[r[n]];
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      ok[n] = ok[n] && prefix[n] >= 0;
+      if (!ok[n]) all |= DSPARK_DATA_BAD_LENS;
+      par[n] = id[n] = 0;
+      if (ok[n] && q.parents && l + 1 < len[n]) par[n] = q.parents[(size_t)r[n] * q.gamma + l];
+      const int64_t hi = (int64_t)prefix[n] + len[n];  // cache indices [prefix, hi)
+      if (ok[n]) {
+        const int64_t p = (prefix[n] >> a.kv.page_shift) + l;
+        if (hi > ((int64_t)q.width << a.kv.page_shift)) {
+          id[n] = -1;
+        } else if (p <= (hi - 1) >> a.kv.page_shift) {
+          id[n] = q.table[(size_t)r[n] * q.width + p];
+        }
       }
-      if (lo + depth >= a.rope_rows) bits |= DSPARK_DATA_BAD_POS;
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      if (__ballot(par[n] < 0 || par[n] > l) & group) {
+        all |= DSPARK_DATA_BAD_TREE;
+      } else if (ok[n]) {
+        if (id[n] < 0 || id[n] >= a.kv.num_blocks) all |= DSPARK_DATA_BAD_PAGE;
+        const int64_t hi = (int64_t)prefix[n] + len[n];
+        if (a.rope && hi > a.rope_rows && hi <= ((int64_t)q.width << a.kv.page_shift)) {
+          // a tree's depths may still be small enough
+          if (prefix[n] >= a.rope_rows) all |= DSPARK_DATA_BAD_POS;
+          if (l + 1 < len[n]) {
+            int depth = l + 1;
+            if (q.parents) {
+              depth = 0;
+              for (int m = l + 1; m > 0; m = q.parents[(size_t)r[n] * q.gamma + m - 1]) ++depth;
+            }
+            if ((int64_t)prefix[n] + depth >= a.rope_rows) all |= DSPARK_DATA_BAD_POS;
+          }
+        }
+      }
     }
   }
-  return bits;
+  return all;
 }
 
 template <typename T>
@@ -65,7 +101,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
   const int total_eff = rows_in_use(q, &total);
   if (blockIdx.x == 0) {
     int bits = total != total_eff ? DSPARK_DATA_BAD_LENS : 0;
-    for (int r = tid; r < q.B; r += kThreads) bits |= append_status(a, r, total_eff);
+    bits |= q.gamma <= 16 ? append_status<16>(a, total_eff) : append_status<kWave>(a, total_eff);
     __shared__ int all;
     if (tid == 0) all = 0;
     __syncthreads();
@@ -83,6 +119,25 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
   int c0, len;
   if (!request_rows(q, r, total_eff, &c0, &len) || j >= len) return;
   const int prefix = q.prefix[r];
+  const int li = lane & (LPH - 1);  // the lane's eight elements: 8 li ..
+  const int hq = a.num_heads, hkv = a.kv.hkv;
+  const int heads = hq + 2 * hkv;
+  const unsigned char* rows[3] = {a.q + (size_t)(c0 + j) * a.q_ld, a.k + (size_t)(c0 + j) * a.k_ld,
+                                  a.v + (size_t)(c0 + j) * a.v_ld};
+  // of the n-th head of q, k and v in turn; loaded a round ahead, the first with
+  // the reads that say where the row goes
+  auto load = [&](int h) {
+    const int hh = h < hq ? h : (h < hq + hkv ? h - hq : h - hq - hkv);
+    T8 x = {};
+    if (h < heads)
+      x = *reinterpret_cast<const T8*>((h < hq ? rows[0] : h < hq + hkv ? rows[1] : rows[2]) +
+                                       (size_t)(hh * D + 8 * li) * 2);
+    return x;
+  };
+  T8 next = load(tid / LPH);
+  T8 weight[2] = {};
+  if (a.q_weight) weight[0] = *(reinterpret_cast<const T8*>(a.q_weight) + li);
+  if (a.k_weight) weight[1] = *(reinterpret_cast<const T8*>(a.k_weight) + li);
   if (prefix < 0 || (int64_t)prefix + len > ((int64_t)q.width << a.kv.page_shift)) return;
   const int64_t slot = (int64_t)prefix + j;
   const int id = q.table[(size_t)r * q.width + (slot >> a.kv.page_shift)];
@@ -98,9 +153,6 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
   const int64_t pos = (int64_t)prefix + depth;
   if (a.rope && pos >= a.rope_rows) return;
 
-  const int li = lane & (LPH - 1);  // the lane's eight elements: 8 li ..
-  const int hq = a.num_heads, hkv = a.kv.hkv;
-  const int heads = hq + 2 * hkv;
   const int half = a.rope_dim >> 1;
   // the lane's cosines and sines, the same for every head
   float co[8], si[8];
@@ -128,29 +180,24 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
       if (turned) swap = low ? lane + half / 8 : lane - half / 8;
     }
   }
-  const unsigned char* rows[3] = {a.q + (size_t)(c0 + j) * a.q_ld, a.k + (size_t)(c0 + j) * a.k_ld,
-                                  a.v + (size_t)(c0 + j) * a.v_ld};
   const int off = (int)(slot & ((1 << a.kv.page_shift) - 1));
   for (int h0 = 0; h0 < heads; h0 += HPP) {
     const int h = h0 + tid / LPH;
     const bool live = h < heads;
     const int kind = h < hq ? 0 : (h < hq + hkv ? 1 : 2);
     const int hh = kind == 0 ? h : (kind == 1 ? h - hq : h - hq - hkv);
-    float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (live) {
-      const T8 raw = *reinterpret_cast<const T8*>(rows[kind] + (size_t)(hh * D + 8 * li) * 2);
+    float x[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = (float)raw[e];
-    }
-    const T* w = reinterpret_cast<const T*>(kind == 0 ? a.q_weight : a.k_weight);
+    for (int e = 0; e < 8; ++e) x[e] = (float)next[e];
+    next = load(h + HPP);
     if (a.q_weight || a.k_weight) {
       float ss = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(x[e], x[e], ss);
       for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor(ss, o, kWave);
-      if (live && kind < 2 && w) {
+      if (kind == 0 ? a.q_weight != nullptr : kind == 1 && a.k_weight) {
         const float rstd = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-        const T8 ww = *reinterpret_cast<const T8*>(w + 8 * li);
+        const T8 ww = kind == 0 ? weight[0] : weight[1];
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = x[e] * rstd * (float)ww[e];
       }
@@ -169,10 +216,15 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
     }
     int e8 = 0;
     float inv = 1.0f;
-    if constexpr (E8) {
+    if (E8 && __any(live && kind != 0)) {
       float amax = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) amax = finite_f32(x[e]) ? fmaxf(amax, fabsf(x[e])) : amax;
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));  // NaN apart
+      if (__any(!finite_f32(amax))) {
+        amax = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = finite_f32(x[e]) ? fmaxf(amax, fabsf(x[e])) : amax;
+      }
       for (int o = LPH / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o, kWave));
       e8 = e4m3_exponent(amax);
       inv = pow2f(-e8);
@@ -213,13 +265,15 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
 
 // ------------------------------------------------------------------ read
 
-constexpr int kReadRows = 16;  // rows per workgroup
+constexpr int kReadThreads = 512;
+constexpr int kReadRows = 8;  // rows per workgroup
 
 // One workgroup per kReadRows output rows: a thread per row finds its request
 // and page, then D / 8 lanes per (row, head) copy or widen eight elements each.
 template <bool E8, int D>
-__global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a) {
-  constexpr int LPH = D / 8, HPP = kThreads / LPH;
+__global__ __launch_bounds__(kReadThreads) void read_kernel(ReadArgs a) {
+  constexpr int EPL = E8 ? 16 : 8;  // elements of a lane, in 16 bytes
+  constexpr int LPH = D / EPL, HPP = kReadThreads / LPH;
   const ReqView& q = a.req;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   int total;
@@ -235,11 +289,11 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a) {
     __syncthreads();
     const int l = tid % kLanes;
     int bits = 0;
-    for (int r0 = tid / kLanes; r0 < q.B; r0 += kAhead * (kThreads / kLanes)) {
+    for (int r0 = tid / kLanes; r0 < q.B; r0 += kAhead * (kReadThreads / kLanes)) {
       int s[kAhead], e[kAhead], st[kAhead], id[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const int r = min(r0 + k * (kThreads / kLanes), q.B - 1);
+        const int r = min(r0 + k * (kReadThreads / kLanes), q.B - 1);
         s[k] = q.cu[r];
         e[k] = q.cu[r + 1];
         st[k] = q.prefix[r];
@@ -247,7 +301,7 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a) {
       int first[kAhead], last[kAhead];  // the lane's pages
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const int r = min(r0 + k * (kThreads / kLanes), q.B - 1);
+        const int r = min(r0 + k * (kReadThreads / kLanes), q.B - 1);
         first[k] = 0;
         last[k] = -1;
         if (s[k] < 0 || e[k] < s[k] || e[k] > total_eff || st[k] < 0) {
@@ -266,7 +320,7 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a) {
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const int r = min(r0 + k * (kThreads / kLanes), q.B - 1);
+        const int r = min(r0 + k * (kReadThreads / kLanes), q.B - 1);
         if (first[k] <= last[k] && (id[k] < 0 || id[k] >= a.kv.num_blocks))
           bits |= DSPARK_DATA_BAD_PAGE;
 #pragma unroll 4
@@ -287,55 +341,86 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a) {
   __shared__ int page_of[kReadRows], off_of[kReadRows];
   const int row0 = (blockIdx.x - 1) * kReadRows;
   if (row0 >= total_eff) return;
-  if (tid < kReadRows) {
-    const int row = row0 + tid;
-    int id = -1, off = 0;
-    if (row < total_eff) {
-      // the last request that starts at or before the row
-      int lo = 0, hi = q.B;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (q.cu[mid] <= row) lo = mid; else hi = mid;
+  {
+    // the last request that starts at or before each of the wave's rows, 64 steps
+    // of the search at once and its rows together
+    constexpr int N = kReadRows / (kReadThreads / kWave);
+    const int first = row0 + tid / kWave * N;
+    int lo[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) lo[i] = 0;
+    for (int n = q.B; n > 1;) {
+      const int step = (n + kWave - 1) / kWave;
+      int at[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int r = lo[i] + lane * step;
+        at[i] = lane * step < n && r < q.B ? q.cu[r] : 0x7FFFFFFF;
       }
-      const int s = q.cu[lo], e = q.cu[lo + 1], st = q.prefix[lo];
-      if (s >= 0 && s <= row && row < e && e <= total_eff && st >= 0 &&
-          (int64_t)st + (e - s) <= reach) {
-        const int64_t slot = (int64_t)st + (row - s);
-        id = q.table[(size_t)lo * q.width + (slot >> a.kv.page_shift)];
-        if (id >= a.kv.num_blocks) id = -1;
-        off = (int)(slot & ((1 << a.kv.page_shift) - 1));
-      }
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        lo[i] += max(__popcll(__ballot(at[i] <= first + i)) - 1, 0) * step;
+      n = step;
     }
-    page_of[tid] = id;
-    off_of[tid] = off;
+    // one row to a lane from here
+    int r = lo[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) r = lane == i ? lo[i] : r;
+    const int row = first + lane;
+    if (lane < N) {
+      int id = -1, off = 0;
+      if (row < total_eff) {
+        const int s = q.cu[r], e = q.cu[r + 1], st = q.prefix[r];
+        if (s >= 0 && s <= row && row < e && e <= total_eff && st >= 0 &&
+            (int64_t)st + (e - s) <= reach) {
+          const int64_t slot = (int64_t)st + (row - s);
+          id = q.table[(size_t)r * q.width + (slot >> a.kv.page_shift)];
+          if (id >= a.kv.num_blocks) id = -1;
+          off = (int)(slot & ((1 << a.kv.page_shift) - 1));
+        }
+      }
+      page_of[row - row0] = id;
+      off_of[row - row0] = off;
+    }
   }
   __syncthreads();
   const int li = lane & (LPH - 1);
-  for (int n = tid / LPH; n < kReadRows * a.kv.hkv; n += HPP) {
+  const int items = kReadRows * a.kv.hkv;
+  // streamed: nothing comes back to either side
+#pragma unroll 4
+  for (int n = tid / LPH; n < items; n += HPP) {
     const int i = n / a.kv.hkv, h = n - i * a.kv.hkv;
     const int id = page_of[i];
-    if (id < 0) continue;
+    const bool live = id >= 0;
+    const size_t page = (size_t)(live ? id : 0);
     const size_t at = ((size_t)h << a.kv.page_shift) + off_of[i];
-    const size_t dst = (size_t)(row0 + i) * a.out_ld + (size_t)(h * D + 8 * li) * 2;
+    const size_t dst = (size_t)(row0 + i) * a.out_ld + (size_t)(h * D + EPL * li) * 2;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      const unsigned char* src = (w ? a.kv.v : a.kv.k) + (size_t)id * a.kv.page_bytes;
-      kv_u32x4 o;
+      const unsigned char* src = (w ? a.kv.v : a.kv.k) + page * a.kv.page_bytes;
+      unsigned char* to = (w ? a.v_out : a.k_out) + dst;
       if constexpr (E8) {
-        const kv_u32x2 c = *reinterpret_cast<const kv_u32x2*>(src + at * D + 8 * li);
+        const kv_u32x4 c = __builtin_nontemporal_load(
+            reinterpret_cast<const kv_u32x4*>(src + at * D + EPL * li));
         const float sc =
-            pow2f((int)(w ? a.kv.vs : a.kv.ks)[(size_t)id * a.kv.scale_page_bytes + at] - 127);
+            pow2f((int)(w ? a.kv.vs : a.kv.ks)[page * a.kv.scale_page_bytes + at] - 127);
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          o[2 * g] = __builtin_bit_cast(
-              unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[g], sc, false));
-          o[2 * g + 1] = __builtin_bit_cast(
-              unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[g], sc, true));
+        for (int x = 0; x < 2; ++x) {
+          kv_u32x4 o;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            o[2 * g] = __builtin_bit_cast(
+                unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * x + g], sc, false));
+            o[2 * g + 1] = __builtin_bit_cast(
+                unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * x + g], sc, true));
+          }
+          if (live) __builtin_nontemporal_store(o, reinterpret_cast<kv_u32x4*>(to + 16 * x));
         }
       } else {
-        o = *reinterpret_cast<const kv_u32x4*>(src + (at * D + 8 * li) * 2);
+        const kv_u32x4 o = __builtin_nontemporal_load(
+            reinterpret_cast<const kv_u32x4*>(src + (at * D + EPL * li) * 2));
+        if (live) __builtin_nontemporal_store(o, reinterpret_cast<kv_u32x4*>(to));
       }
-      *reinterpret_cast<kv_u32x4*>((w ? a.v_out : a.k_out) + dst) = o;
     }
   }
 }
@@ -543,13 +628,13 @@ template <bool E8>
 void read_by_dim(const ReadArgs& a, unsigned grid, hipStream_t s) {
   switch (a.kv.dim) {
     case 64:
-      hipLaunchKernelGGL((read_kernel<E8, 64>), dim3(grid), dim3(kThreads), 0, s, a);
+      hipLaunchKernelGGL((read_kernel<E8, 64>), dim3(grid), dim3(kReadThreads), 0, s, a);
       break;
     case 128:
-      hipLaunchKernelGGL((read_kernel<E8, 128>), dim3(grid), dim3(kThreads), 0, s, a);
+      hipLaunchKernelGGL((read_kernel<E8, 128>), dim3(grid), dim3(kReadThreads), 0, s, a);
       break;
     default:
-      hipLaunchKernelGGL((read_kernel<E8, 256>), dim3(grid), dim3(kThreads), 0, s, a);
+      hipLaunchKernelGGL((read_kernel<E8, 256>), dim3(grid), dim3(kReadThreads), 0, s, a);
   }
 }
 
