@@ -552,6 +552,7 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
     };
     const bool values = wave >= W / 2;
     const int row0 = (wave & (W / 2 - 1)) * R::kRows;  // of the wave's keys, or values
+    __builtin_amdgcn_s_setprio(0);
     if constexpr (E8) {
       // the wave's piece of this tile: done when the pieces after it may not be
       if (left > R::kStages - 1) {
@@ -621,6 +622,8 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
       }
     }
     stage = stage + 1 == R::kStages ? 0 : stage + 1;
+    // products before other waves' copies (64 trees, 8-bit: 243 -> 233 us)
+    __builtin_amdgcn_s_setprio(2);
     if constexpr (ROWS) {
       // Scores. Reads from LDS go out in batches, ahead of the products that use
       // them and, for the values, of the softmax.
