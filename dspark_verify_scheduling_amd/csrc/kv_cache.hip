@@ -12,6 +12,8 @@
 // bad requests or rows out.
 #include "kv_dev.h"
 
+#include <algorithm>
+
 namespace dspark {
 
 namespace {
@@ -266,11 +268,14 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
 // ------------------------------------------------------------------ read
 
 constexpr int kReadThreads = 512;
-constexpr int kReadRows = 8;  // rows per workgroup
+// Rows of a workgroup: few, so that a small call is many workgroups; more where a
+// row gives its threads nothing to do (one head of 128: 230 MB in 98 us with 8
+// rows, 48 us with 64).
+constexpr int kReadFew = 8, kReadMany = 64;
 
-// One workgroup per kReadRows output rows: a thread per row finds its request
+// One workgroup per kReadRows rows: a thread per row finds its request
 // and page, then D / 8 lanes per (row, head) copy or widen eight elements each.
-template <bool E8, int D>
+template <bool E8, int D, int kReadRows>
 __global__ __launch_bounds__(kReadThreads) void read_kernel(ReadArgs a) {
   constexpr int EPL = E8 ? 16 : 8;  // elements of a lane, in 16 bytes
   constexpr int LPH = D / EPL, HPP = kReadThreads / LPH;
@@ -543,15 +548,13 @@ __device__ inline void move_column(unsigned char* base, int64_t page_bytes, int6
   }
 }
 
-// One workgroup per (request, kCommitLayers layers); a thread owns 16-byte
-// columns of them (one place of one head of a layer's keys or values) or bytes
+// `parts` workgroups per (request, `per` layers), part blockIdx.y % parts; a thread
+// owns 16-byte columns of them (one place of one head of a layer's keys or values) or bytes
 // of exponents, and moves the path's rows of that column in ascending order.
 // Path rows ascend and path[k] >= k, so a move never overwrites the source of a
 // later one, and a batch of loads may run ahead of its stores: the rows it
 // stores to, k .. k + kMoveBatch - 1, lie below every later source.
-constexpr int kCommitLayers = 4;
-
-__global__ __launch_bounds__(kThreads) void commit_kernel(CommitArgs a) {
+__global__ __launch_bounds__(kThreads) void commit_kernel(CommitArgs a, int per, int parts) {
   const ReqView& q = a.req;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   if (blockIdx.x == 0) {
@@ -588,9 +591,10 @@ __global__ __launch_bounds__(kThreads) void commit_kernel(CommitArgs a) {
   const int row_bytes = a.kv.dim * a.kv.cb, row_vecs = row_bytes / 16;
   const int rows = 2 * a.kv.hkv;  // of a layer: keys' heads, then values' heads
   const int cols = rows * row_vecs;
-  const int layer0 = blockIdx.y * kCommitLayers;
-  const int layers = min(kCommitLayers, a.kv.num_layers - layer0);
-  for (int i = tid; i < layers * cols; i += kThreads) {
+  const int group = blockIdx.y / parts, first = (blockIdx.y - group * parts) * kThreads + tid;
+  const int layer0 = group * per;
+  const int layers = min(per, a.kv.num_layers - layer0);
+  for (int i = first; i < layers * cols; i += parts * kThreads) {
     const int layer = i / cols, col = i - layer * cols;
     const int row = col / row_vecs, w = row >= a.kv.hkv, h = row - w * a.kv.hkv;
     move_column<kv_u32x4>((w ? a.kv.v : a.kv.k) + (layer0 + layer) * a.kv.layer_bytes +
@@ -599,7 +603,7 @@ __global__ __launch_bounds__(kThreads) void commit_kernel(CommitArgs a) {
                           a.kv.page_bytes, row_bytes, n, s_id, s_off, d_id, d_off);
   }
   if (a.kv.ks) {
-    for (int i = tid; i < layers * rows; i += kThreads) {
+    for (int i = first; i < layers * rows; i += parts * kThreads) {
       const int layer = i / rows, row = i - layer * rows;
       const int w = row >= a.kv.hkv, h = row - w * a.kv.hkv;
       move_column<unsigned char>((w ? a.kv.vs : a.kv.ks) +
@@ -624,17 +628,27 @@ void append_by_dim(const AppendArgs& a, unsigned grid, hipStream_t s) {
   }
 }
 
+template <bool E8, int D>
+void read_by_rows(const ReadArgs& a, hipStream_t s) {
+  const int64_t rows = a.req.B > 0 ? a.req.max_rows : 0;
+  const int at_once = kReadFew * a.kv.hkv * (D * a.kv.cb / 16);  // threads with a vector
+  if (at_once < kReadThreads) {
+    hipLaunchKernelGGL((read_kernel<E8, D, kReadMany>),
+                       dim3(1u + (unsigned)((rows + kReadMany - 1) / kReadMany)),
+                       dim3(kReadThreads), 0, s, a);
+  } else {
+    hipLaunchKernelGGL((read_kernel<E8, D, kReadFew>),
+                       dim3(1u + (unsigned)((rows + kReadFew - 1) / kReadFew)),
+                       dim3(kReadThreads), 0, s, a);
+  }
+}
+
 template <bool E8>
-void read_by_dim(const ReadArgs& a, unsigned grid, hipStream_t s) {
+void read_by_dim(const ReadArgs& a, hipStream_t s) {
   switch (a.kv.dim) {
-    case 64:
-      hipLaunchKernelGGL((read_kernel<E8, 64>), dim3(grid), dim3(kReadThreads), 0, s, a);
-      break;
-    case 128:
-      hipLaunchKernelGGL((read_kernel<E8, 128>), dim3(grid), dim3(kReadThreads), 0, s, a);
-      break;
-    default:
-      hipLaunchKernelGGL((read_kernel<E8, 256>), dim3(grid), dim3(kReadThreads), 0, s, a);
+    case 64: return read_by_rows<E8, 64>(a, s);
+    case 128: return read_by_rows<E8, 128>(a, s);
+    default: read_by_rows<E8, 256>(a, s);
   }
 }
 
@@ -653,20 +667,28 @@ hipError_t launch_append(const AppendArgs& a, dspark_dtype dt, hipStream_t s) {
 }
 
 hipError_t launch_read(const ReadArgs& a, hipStream_t s) {
-  const int rows = a.req.B > 0 ? a.req.max_rows : 0;
-  const unsigned grid = 1u + (unsigned)((rows + (int64_t)kReadRows - 1) / kReadRows);
   if (a.kv.cb == 1) {
-    read_by_dim<true>(a, grid, s);
+    read_by_dim<true>(a, s);
   } else {
-    read_by_dim<false>(a, grid, s);
+    read_by_dim<false>(a, s);
   }
   return hipGetLastError();
 }
 
 hipError_t launch_commit(const CommitArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(commit_kernel, dim3(1u + (unsigned)a.req.B,
-                                         ((unsigned)a.kv.num_layers + kCommitLayers - 1) / kCommitLayers),
-                     dim3(kThreads), 0, s, a);
+  // up to four layers to a workgroup, whose moves are then looked up once; where
+  // that leaves few workgroups, fewer layers, and a layer to several (6 requests,
+  // 14 layers of 8 heads of 256: 24 workgroups took 29 us, 672 take 8.7)
+  constexpr int64_t kEnough = 1024;
+  const int64_t pairs = (int64_t)a.req.B * a.kv.num_layers;
+  const int per = (int)std::max<int64_t>(1, std::min<int64_t>(4, pairs / kEnough));
+  const int groups = (a.kv.num_layers + per - 1) / per;
+  const int cols = per * 2 * a.kv.hkv * (a.kv.dim * a.kv.cb / 16);
+  const int64_t wgs = std::max<int64_t>(1, (int64_t)a.req.B * groups);
+  const int parts = (int)std::max<int64_t>(
+      1, std::min<int64_t>((cols + kThreads - 1) / kThreads, kEnough / wgs));
+  hipLaunchKernelGGL(commit_kernel, dim3(1u + (unsigned)a.req.B, (unsigned)(groups * parts)),
+                     dim3(kThreads), 0, s, a, per, parts);
   return hipGetLastError();
 }
 
