@@ -25,7 +25,7 @@ struct Parts {
 // in a segment the fewer reads of its keys; with few rows in a request four
 // waves do, and feed the tiles with less work around it (32 chains of 9 rows,
 // 32 query heads on 8, 1k to 8k keys: 110 us against 125 with eight; 64 trees of
-// up to 17 rows, 64 on 8, 8-bit: 299 us against 240).
+// up to 17 rows, 64 on 8, 8-bit: 245 us against 233).
 constexpr int kMostWaves = 8, kFewWaves = 4;  // (shape_of() shifts by them)
 // (Its share of a tile has to stay within a page: 16 keys.)
 inline int waves_for(int rows, int dim) {
@@ -195,8 +195,13 @@ constexpr float kLn2 = 0.6931471805599453f;
 // log2): weights then stay below 2^kSlack, and most steps rescale nothing.
 constexpr float kSlack = 8.0f;
 
-// Workgroups to a CU, by their LDS.
-constexpr int per_cu(int dim) { return dim == 256 ? 1 : 2; }
+// Workgroups to a CU, by their LDS. Small ones over an 8-bit cache have fewer
+// pieces under way and are three instead: the widening is latency (64 single
+// tokens, 64 query heads on 8, up to 4k keys: 87 us against 113; over 16 bits, 112
+// against 110).
+constexpr int per_cu(int dim, bool e8, int waves) {
+  return dim == 256 ? 1 : (e8 && waves == kFewWaves ? 3 : 2);
+}
 
 // LDS of a workgroup. A tile of keys and values in 16 bits is shared by its
 // waves; rows are unpadded (copies into LDS write densely), and 16-byte chunk c
@@ -226,12 +231,12 @@ struct Ring {
   static constexpr int kRaw = 2 * kTiles;             // offset of the waves' rings
   // (what the LDS of a CU, or of half a CU, holds; even in an 8-bit ring)
   static constexpr int kStages =
-      D == 256 ? 4 : (E8 ? 4 : (65536 / kTiles < 4 ? 65536 / kTiles : 4));
+      D == 256 ? 4 : (E8 ? (W == kFewWaves ? 2 : 4) : (65536 / kTiles < 4 ? 65536 / kTiles : 4));
   // rows with NaN or infinity, a bit each; of two tiles
   static constexpr int kOdd = E8 ? kRaw + kStages * W * kPiece : kStages * kTiles;
   static constexpr int kReqs = kOdd + 16;  // rows of up to kWave requests, 3 words each
   static constexpr int kBytes = kReqs + 12 * kWave;
-  static constexpr int kPerCu = per_cu(D);
+  static constexpr int kPerCu = per_cu(D, E8, W);
   static_assert(kBytes <= 163840 / kPerCu - 256, "a CU's LDS");
   static_assert(!E8 || kStages % 2 == 0, "pieces go to the two tiles in turn");
   static __device__ int swizzle(int row) {

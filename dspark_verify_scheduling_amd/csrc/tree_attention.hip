@@ -123,8 +123,8 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a, Parts ws
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Workgroups of the split kernel, at most: two to a CU (their LDS rings).
-constexpr int kMaxWgs = 512;
+// Workgroups of the split kernel, at most: three to a CU (their LDS rings).
+constexpr int kMaxWgs = 768;
 
 struct Plan {
   int rows;
@@ -179,7 +179,7 @@ hipError_t launch_attention(const AttnArgs& args, dspark_dtype dt, hipStream_t s
   ws.l = reinterpret_cast<float*>(w + p.l_off);
   ws.o = reinterpret_cast<float*>(w + p.o_off);
   ws.rows = p.rows;
-  const int per_cu = attn::per_cu(a.kv.dim);
+  const int per_cu = attn::per_cu(a.kv.dim, a.kv.cb == 1, a.waves);
   ws.wgs = std::min(attn::kMaxWgs, per_cu * cus);
   switch (a.kv.dim) {
     case 64: attn::launch_dim64(a, ws, dt, s); break;
