@@ -44,7 +44,8 @@
 // the present row), one ballot over the children that match it and a bit
 // scan, at most gamma of them; rows come after their parents, so the walk
 // ascends and ends. It is bound by the two dependent read rounds before it,
-// like the chain's finalize.
+// like the chain's finalize: 2.4 us for 8 requests, 4.6 for 256 after an argmax
+// pass of 44 to 46 us (298 MB of 129280-word rows, 6.6 TB/s).
 //
 // The partials are fully rewritten by every call, so the workspace needs no
 // initialization and holds no state between calls.

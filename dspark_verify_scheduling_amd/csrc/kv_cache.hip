@@ -92,7 +92,13 @@ template <>
 struct Vec8<_Float16> { typedef f16x8 type; };
 
 // One workgroup per (request, row): LPH lanes per head take the heads of q, k
-// and v in turn.
+// and v in turn. y = x * (mean(x^2) + eps)^(-1/2) * w, then (a, b) -> (a c - b s,
+// b c + a s), in float32; 8-bit rows scale by the power of two of their largest
+// magnitude. Every row is read and written once. 256 requests of up to 9 rows, 32
+// query heads on 8 of 128, into 8 bits: 13 us (27 MB, 2.1 TB/s; 6 us at a copy's
+// rate): the arithmetic of a row (about 250 instructions a wave and round) and
+// the reads that say where it goes, in one round of workgroups. 128 threads took
+// 15.6 us, 512 14.9. A few rows: 3.4 us, latency.
 template <typename T, bool E8, int D>
 __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
   typedef typename Vec8<T>::type T8;
@@ -273,8 +279,11 @@ constexpr int kReadThreads = 512;
 // rows, 48 us with 64).
 constexpr int kReadFew = 8, kReadMany = 64;
 
-// One workgroup per kReadRows rows: a thread per row finds its request
-// and page, then D / 8 lanes per (row, head) copy or widen eight elements each.
+// One workgroup per kReadRows rows: a wave finds its rows' requests and pages,
+// then 16-byte vectors of (row, head) are copied or widened. Bound by HBM: 437 MB
+// (a third of it read) of 16 contexts of an 8-bit cache, 8 heads of 128, in 96 us,
+// 4.5 TB/s; a copy of 2 GiB reaches 4.9. Nontemporal both ways (104 us without).
+// A few short spans: 4 us.
 template <bool E8, int D, int kReadRows>
 __global__ __launch_bounds__(kReadThreads) void read_kernel(ReadArgs a) {
   constexpr int EPL = E8 ? 16 : 8;  // elements of a lane, in 16 bytes
@@ -553,7 +562,9 @@ __device__ inline void move_column(unsigned char* base, int64_t page_bytes, int6
 // of exponents, and moves the path's rows of that column in ascending order.
 // Path rows ascend and path[k] >= k, so a move never overwrites the source of a
 // later one, and a batch of loads may run ahead of its stores: the rows it
-// stores to, k .. k + kMoveBatch - 1, lie below every later source.
+// stores to, k .. k + kMoveBatch - 1, lie below every later source. Bound by HBM:
+// 178 MB read and written of 256 requests, 32 layers of 8 heads of 128 in 8 bits,
+// in 34 us, 5.2 TB/s. A few requests and layers: 4 us.
 __global__ __launch_bounds__(kThreads) void commit_kernel(CommitArgs a, int per, int parts) {
   const ReqView& q = a.req;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);

@@ -780,10 +780,30 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
   }
 }
 
+// out = sum_k e^(s_k - m) v_k / sum_k e^(s_k - m) in one pass over the keys: running
+// maximum m, sum and outputs in float32 registers, m moved only when a score
+// passes it by kSlack. Parts of a row join by (m, sum, outputs) in join_kernel.
+//
 // Persistent over the units of all (request, key/value head, row segment)s in
 // order: workgroup w takes the w-th equal share, so ragged contexts balance by
 // themselves and a long one is split over many workgroups. The ring of tiles
 // runs on across segments.
+//
+// Bound. Few rows to a head: the stream of keys and values. 32 chains of up to 9
+// rows, 32 query heads on 8 of 128, bf16, 1k to 8k keys: 607 MB, 105 us and 5 for
+// the join (5.8 TB/s of the 7.0 that a plain read reaches; without the products
+// 104). Many rows over 8 bits: the latency of one tile's widening, products and
+// barrier, with four waves to a SIMD to cover it. 64 trees of up to 17 rows, 64 on
+// 8: 580 MB and 76 GFLOP, 231 us and 12 (2.5 TB/s, 328 TFLOP/s; the copies alone
+// 120). Two trees of 65 rows over 131k keys, 16 on 2 of 64, f16: 103 MB and
+// 27 GFLOP, 62 to 80 us and 14 (the product of 8192 x 8192 matrices of the vendor's
+// library reaches 1207 TFLOP/s here). One token over 700 keys: 8 us and 4, all of it
+// the chain of dependent reads (lengths, pages, queries, keys).
+//
+// Tried and not kept: keys and values straight into registers, a wave to 32 keys
+// (846 us the 64 trees, and spills); 64 keys to a step of 8-bit tiles (252 to 313);
+// five stages (240); exponents copied for four tiles at once (251); two row tiles to
+// each of four waves (263).
 template <typename T, bool E8, int D, int W>
 __global__ __launch_bounds__(W * kWave, (Ring<E8, D, W>::kPerCu * W / 4)) void split_kernel(
     AttnArgs a, Parts ws) {
