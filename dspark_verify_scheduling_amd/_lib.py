@@ -135,7 +135,8 @@ def lib() -> ctypes.CDLL:
 
 
 def hostcheck() -> ctypes.CDLL:
-    """Host-only build of the device sigmoid (CPU tests of its logic)."""
+    """Host-only build of the device sigmoid and of the cache read's search
+    (CPU tests of their logic)."""
     global _hostcheck
     if _hostcheck is None:
         if not HOSTCHECK_PATH.exists():
@@ -143,6 +144,9 @@ def hostcheck() -> ctypes.CDLL:
         handle = ctypes.CDLL(str(HOSTCHECK_PATH))
         handle.dspark_hostcheck_sigmoid.restype = None
         handle.dspark_hostcheck_sigmoid.argtypes = [c_void_p, c_void_p, c_void_p, c_int64, c_int]
+        handle.dspark_hostcheck_request_search.restype = None
+        handle.dspark_hostcheck_request_search.argtypes = [c_void_p, c_int32, c_void_p, c_void_p,
+                                                           c_int64]
         _hostcheck = handle
     return _hostcheck
 

@@ -3,7 +3,8 @@
 ``python -m dspark_verify_scheduling_amd.build`` or ``build()`` compiles every
 HIP source under ``csrc/`` with hipcc for gfx950. A second, host-only library,
 ``libdspark_hostcheck.so``, exposes the device sigmoid compiled for the CPU so
-that its rarely taken exact path can be tested without a GPU.
+that its rarely taken exact path can be tested without a GPU, and the cache
+read's search for its indexes on malformed lengths.
 """
 
 from __future__ import annotations

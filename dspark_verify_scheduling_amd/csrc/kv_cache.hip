@@ -11,6 +11,7 @@
 // writes the status; the others repeat the checks of what they touch and leave
 // bad requests or rows out.
 #include "kv_dev.h"
+#include "request_search.h"
 
 #include <algorithm>
 
@@ -373,7 +374,7 @@ __global__ __launch_bounds__(kReadThreads) void read_kernel(ReadArgs a) {
       }
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        lo[i] += max(__popcll(__ballot(at[i] <= first + i)) - 1, 0) * step;
+        lo[i] += search_skip(__ballot(at[i] <= first + i), step);
       n = step;
     }
     // one row to a lane from here
