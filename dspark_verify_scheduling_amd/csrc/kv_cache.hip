@@ -382,18 +382,39 @@ __global__ __launch_bounds__(kReadThreads) void read_kernel(ReadArgs a) {
 #pragma unroll
     for (int i = 1; i < N; ++i) r = lane == i ? lo[i] : r;
     const int row = first + lane;
-    if (lane < N) {
-      int id = -1, off = 0;
-      if (row < total_eff) {
-        const int s = q.cu[r], e = q.cu[r + 1], st = q.prefix[r];
-        if (s >= 0 && s <= row && row < e && e <= total_eff && st >= 0 &&
-            (int64_t)st + (e - s) <= reach) {
-          const int64_t slot = (int64_t)st + (row - s);
-          id = q.table[(size_t)r * q.width + (slot >> a.kv.page_shift)];
-          if (id >= a.kv.num_blocks) id = -1;
-          off = (int)(slot & ((1 << a.kv.page_shift) - 1));
+    // the cache index of packed row x as one of request c's; -1 where it is none of
+    // them, or the request is malformed
+    auto slot_of = [&](int c, int x) -> int64_t {
+      const int s = q.cu[c], e = q.cu[c + 1], st = q.prefix[c];
+      const bool ok = s >= 0 && s <= x && x < e && e <= total_eff && st >= 0 &&
+                      (int64_t)st + (e - s) <= reach;
+      return ok ? (int64_t)st + (x - s) : -1;
+    };
+    const bool mine = lane < N && row < total_eff;
+    int64_t slot = mine ? slot_of(r, row) : -1;
+    // Lengths out of order mislead the search: rows that it does not find are
+    // looked for in every request, 64 at once, and go to the first that holds them.
+    // (Rows of none are too: those of a malformed request, or before the first.)
+    unsigned long long lost = __ballot(mine && slot < 0);
+    while (lost) {
+      const int i = (int)__builtin_ctzll(lost);
+      lost &= lost - 1;
+      for (int r0 = 0; r0 < q.B; r0 += kWave) {
+        const unsigned long long h =
+            __ballot(r0 + lane < q.B && slot_of(r0 + lane, first + i) >= 0);
+        if (!h) continue;
+        if (lane == i) {
+          r = r0 + (int)__builtin_ctzll(h);
+          slot = slot_of(r, row);
         }
+        break;
       }
+    }
+    if (lane < N) {
+      int id = -1;
+      if (slot >= 0) id = q.table[(size_t)r * q.width + (slot >> a.kv.page_shift)];
+      if (id >= a.kv.num_blocks) id = -1;
+      const int off = (int)(slot & ((1 << a.kv.page_shift) - 1));
       page_of[row - row0] = id;
       off_of[row - row0] = off;
     }

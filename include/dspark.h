@@ -750,9 +750,10 @@ dspark_status dspark_kv_append(int32_t B, int32_t gamma, int32_t num_heads, dspa
  * Data errors: a request whose rows lie outside [0, min(cu_seqlens[B],
  *   max_rows)), or that starts below 0, sets DSPARK_DATA_BAD_LENS; one that
  *   ends beyond its table row DSPARK_DATA_BAD_PAGE; none of its rows is
- *   written, and where cu_seqlens is out of order rows of other requests may
- *   be left out too. A row on a page id outside [0, num_blocks) sets
- *   DSPARK_DATA_BAD_PAGE and is left out alone.
+ *   written. Where cu_seqlens is out of order, a row that two well-formed
+ *   requests claim gets the value of one of them, the same in every call. A row
+ *   on a page id outside [0, num_blocks) sets DSPARK_DATA_BAD_PAGE and is left
+ *   out alone.
  */
 dspark_status dspark_kv_read(int32_t B, int32_t max_rows, const int32_t* cu_seqlens,
                              const int32_t* starts, const int32_t* block_table,

@@ -12,7 +12,7 @@ import torch
 import dspark_verify_scheduling_amd as dv
 import oracle
 from _gpu import DEV, say
-from test_gpu_target import Batch, i32, make_cache
+from test_gpu_target import Batch, bits, i32, make_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +72,66 @@ def test_read_stays_inside_its_arrays_where_lengths_are_out_of_order(B):
             bad = any(s < 0 or e < s or e > total for s, e in zip(cu[:-1], cu[1:]))
             assert meta[0] == total and bool(meta[1] & oracle.DATA_BAD_LENS) == bad, (at, value)
             assert bool((rd.k_out[total:] == -7).all())
+
+
+@pytest.mark.parametrize("kind,hkv,D,B", [("bf16", 1, 64, 4), ("e4m3", 8, 128, 70), ("f16", 2, 64, 300)])
+def test_read_leaves_other_requests_alone_where_lengths_are_out_of_order(kind, hkv, D, B):
+    """Every row that one well-formed request claims comes back, whatever the other
+    lengths are; a row that none claims is not written, and one that several claim
+    is a row of one of them."""
+    say(f"read beside malformed lengths {kind} hkv={hkv} D={D} B={B}")
+    rng = np.random.default_rng(B)
+    lens = rng.integers(1, 5, B).tolist()
+    b = Batch(2, lens, rng.integers(0, 40, B).tolist(), 4, 16, False)
+    cache = make_cache(kind, b.nb, hkv, 16, D)
+    x = torch.randn(b.rows, hkv, D, device=DEV).to(cache.row_dtype)
+    ap = dv.alloc_append_outputs(b.rows, hkv, cache)
+    dv.dspark_kv_append(B, 4, x, x, x, b.rows, *b.args(), cache, ap)
+    total, reach = int(b.cu[-1]), b.width * b.page
+    per_slot = {}  # what the cache holds at (page, offset), as bits
+    pages = bits(cache.k).cpu()
+    scales = None if cache.k_scale is None else cache.k_scale.cpu()
+    ctx = np.array(b.ctx)
+
+    def want(r, j):
+        i = int(ctx[r]) + j
+        pg, of = int(b.table[r, i // 16]), i % 16
+        if pg < 0:
+            return None
+        if (pg, of) not in per_slot:
+            v = pages[pg, :, of]
+            if scales is not None:
+                e = scales[pg, :, of].double() - 127
+                v = v.view(torch.float8_e4m3fn).double() * torch.exp2(e)[:, None]
+            per_slot[pg, of] = v.to(cache.row_dtype)
+        return per_slot[pg, of]
+
+    shuffled = rng.permutation(b.cu[:-1])
+    trials = [(at, w) for at in (B // 3, B // 2) for w in (10 ** 6, -5, total, 0)] + [(None, None)]
+    alone = 0
+    for at, w in trials:
+        cu = b.cu.copy()
+        if at is None:
+            cu[:-1] = shuffled
+        else:
+            cu[at] = w
+        claims = {}
+        for r in range(B):
+            s, e = int(cu[r]), int(cu[r + 1])
+            if 0 <= s <= e <= total and ctx[r] + e - s <= reach:
+                for row in range(s, e):
+                    claims.setdefault(row, []).append(want(r, row - s))
+        outs = []
+        for _ in range(2):
+            rd = dv.alloc_kv_read_outputs(b.rows, cache)
+            rd.k_out.fill_(-7)
+            dv.dspark_kv_read(B, b.rows, i32(cu), i32(ctx), i32(b.table), cache, rd)
+            torch.cuda.synchronize()
+            outs.append(rd.k_out.cpu())
+        assert torch.equal(outs[0].view(torch.int16), outs[1].view(torch.int16))
+        for row in range(b.rows):
+            got = outs[0][row]
+            may = [torch.full_like(got, -7) if v is None else v for v in claims.get(row, [None])]
+            assert any(torch.equal(got.nan_to_num(9), v.nan_to_num(9)) for v in may), (at, w, row)
+            alone += len(claims.get(row, [])) == 1
+    assert alone >= total // 2

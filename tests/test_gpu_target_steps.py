@@ -339,9 +339,6 @@ def test_commit_of_many_layers():
             assert torch.equal(t.view(torch.uint8), w)
 
 
-@pytest.mark.skip(reason="read looks a row's request up by a search that lengths out of order "
-                         "mislead; a version that then looked through every request ended in an "
-                         "illegal access at B = 300 whose cause is not shown, and was taken out")
 @pytest.mark.parametrize("B", [4, 300])
 def test_read_beside_requests_out_of_order(B):
     """Malformed lengths leave the rows of the well-formed requests as they are."""
