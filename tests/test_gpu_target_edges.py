@@ -12,7 +12,7 @@ import torch
 import dspark_verify_scheduling_amd as dv
 import oracle
 from _gpu import DEV, say
-from test_gpu_target import Batch, bits, i32, make_cache
+from test_gpu_target import TYPES, W, Batch, bits, f64, get, i32, make_cache, put, within
 
 pytestmark = pytest.mark.gpu
 
@@ -135,3 +135,73 @@ def test_read_leaves_other_requests_alone_where_lengths_are_out_of_order(kind, h
             assert any(torch.equal(got.nan_to_num(9), v.nan_to_num(9)) for v in may), (at, w, row)
             alone += len(claims.get(row, [])) == 1
     assert alone >= total // 2
+
+
+# ------------------------------------------------------------------ scores at the ends of their range
+
+@pytest.mark.parametrize("kind,D,size", [
+    ("bf16", 128, 3e4), ("bf16", 64, 1e9), ("f16", 64, 9e3), ("f16", 256, 3e4), ("e4m3", 128, 3e4)])
+def test_equal_scores_of_any_size_give_the_mean(kind, D, size):
+    """Keys all alike: the weights are equal however large the scores are, and the
+    output is the mean of the values. Equal scores have equal weights p, so sum p v
+    / sum p errs by the rounding of p, of n float32 additions each and of the
+    output; the scores' own errors cancel."""
+    say(f"equal scores of size {size:g}^2 {kind} D={D}")
+    code, dt, u = TYPES[kind]
+    b = Batch(1, [3, 1], [500, 40], 4, 16, False)
+    cache = make_cache(kind, b.nb, 1, 16, D)
+    rng = np.random.default_rng(0)
+    key = (rng.uniform(0.5, 1, (1, 1, D)) * size).astype(np.float32)
+    vals = []
+    for r in range(2):
+        T = b.ctx[r] + b.lens[r]
+        vals.append(rng.normal(1, 1, (T, 1, D)).astype(np.float32))
+        put(cache, b.slots(r, 0, T), np.repeat(key, T, 0), vals[r])
+    q = torch.full((b.rows, 4, D), size, device=DEV).to(dt)
+    q[:, 1] *= -1
+    o = dv.alloc_attention_outputs(2, 4, b.rows, 4, cache, lse=True)
+    dv.dspark_tree_attention(2, 4, q, b.rows, *b.args(), cache, D ** -0.5, o)
+    torch.cuda.synchronize()
+    assert o.attention_meta.tolist() == [4, 0]
+    got, lse = f64(o.out), f64(o.lse)
+    assert np.isfinite(lse[:4]).all()
+    for r in range(2):
+        v = get(cache, b.slots(r, 0, b.ctx[r] + b.lens[r]), "v")[:, 0]
+        for j in range(b.lens[r]):
+            n = b.ctx[r] + j + 1
+            mean, size_v = v[:n].mean(0), np.abs(v[:n]).mean(0)
+            within(got[b.cu[r] + j], np.broadcast_to(mean, (4, D)),
+                   u * np.abs(mean) + (u + 2 * (n + 32) * W) * size_v, (r, j))
+
+
+@pytest.mark.parametrize("kind,size", [("bf16", 3e4), ("f16", 9e3), ("e4m3", 3e4)])
+def test_a_key_far_above_the_others_takes_everything(kind, size):
+    """Scores that rise by thousands of their float32 steps from key to key: all of
+    the weight is the last key's, whichever part of the keys holds it."""
+    say(f"rising scores {kind}")
+    code, dt, u = TYPES[kind]
+    D, T = 64, 900
+    b = Batch(1, [1], [T - 1], 1, 16, False)
+    cache = make_cache(kind, b.nb, 1, 16, D)
+    rng = np.random.default_rng(0)
+    k = np.zeros((T, 1, D), np.float32)
+    # element i holds a digit of the key's number: exact in every type
+    for i in range(2):
+        k[:, 0, i] = (np.arange(T) // 30 ** i % 30)
+    v = rng.normal(0, 1, (T, 1, D)).astype(np.float32)
+    if kind == "e4m3":
+        k = np.minimum(k, 16)  # integers up to 16 are codes
+    put(cache, b.slots(0, 0, T), k, v)
+    q = torch.zeros(b.rows, 2, D, device=DEV, dtype=dt)
+    q[:, :, 0] = size
+    q[:, :, 1] = size
+    o = dv.alloc_attention_outputs(1, 1, b.rows, 2, cache)
+    for scale in (size, -size):
+        dv.dspark_tree_attention(1, 1, q, b.rows, *b.args(), cache, scale, o)
+        torch.cuda.synchronize()
+        kk, vv = get(cache, b.slots(0, 0, T), "k")[:, 0], get(cache, b.slots(0, 0, T), "v")[:, 0]
+        s = (kk[:, 0] + kk[:, 1]) * np.sign(scale)
+        top = vv[s == s.max()]
+        mean = top.mean(0)
+        within(f64(o.out[0]), np.broadcast_to(mean, (2, D)),
+               u * np.abs(mean) + (u + 2 * (len(top) + 32) * W) * np.abs(top).mean(0), scale)
