@@ -9,8 +9,8 @@ namespace dspark {
 namespace attn {
 
 // What the split kernel leaves for the joining kernel: the schedule's prefix
-// sums, and per partial segment the running maximum and sum of each of its rows
-// and their unnormalised outputs. Workgroup w has segments 2 w (the one its
+// sums, and per partial segment the running maximum (less Types::kAbove) and sum of
+// each of its rows and their unnormalised outputs. Workgroup w has segments 2 w (the one its
 // range starts with) and 2 w + 1 (a later one that its range ends in).
 struct Parts {
   int64_t* base;  // [B + 1] first unit of each request, then the total
@@ -97,10 +97,18 @@ __device__ inline int share_of(int wg, int wgs) {
 // The first unit of share w of n <= total.
 __device__ inline int64_t wg_start(int64_t total, int w, int n) { return total * w / n; }
 
+// The weights of a row are 2^(score - m), m its running maximum (in log2) less
+// kAbove. m follows the scores only when they pass it by kAbove + kSlack, so most
+// steps rescale nothing, and the weights stay below 2^(kAbove + kSlack).
+// bfloat16 has float32's exponents and needs no kAbove. float16 holds 2^15 to
+// 2^-24: with kAbove a weight counts down to 2^-36 of the largest, 25 below it in
+// e; with the largest at 1 it would end at 2^-25, and the tail of a long context
+// under one large weight with it.
 template <typename T>
 struct Types;
 template <>
 struct Types<__bf16> {
+  static constexpr float kSlack = 8.0f, kAbove = 0.0f;
   typedef bf16x8 V8;
   typedef bf16x4 V4;
   static constexpr unsigned kExpMask = 0x7F80u;
@@ -110,6 +118,7 @@ struct Types<__bf16> {
 };
 template <>
 struct Types<_Float16> {
+  static constexpr float kSlack = 4.0f, kAbove = 11.0f;
   typedef f16x8 V8;
   typedef f16x4 V4;
   static constexpr unsigned kExpMask = 0x7C00u;
@@ -191,9 +200,6 @@ __device__ inline float group_sum(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// A row's maximum follows its scores only when they pass it by this much (in
-// log2): weights then stay below 2^kSlack, and most steps rescale nothing.
-constexpr float kSlack = 8.0f;
 
 // Workgroups to a CU, by their LDS. Small ones over an 8-bit cache have fewer
 // pieces under way and are three instead: the widening is latency (64 single
@@ -687,8 +693,14 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
 #pragma unroll
         for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[b][e]);
       // (a difference: mx + kSlack would round by such a step too)
-      if (__any(top * sl - mx > kSlack)) {
-        const float next = fmaxf(mx, group_max(top * sl));
+      if (__any(top * sl - mx > TT::kAbove + TT::kSlack)) {
+        float next = group_max(top * sl);
+        if constexpr (TT::kAbove > 0.0f) {
+          // (not where kAbove rounds up to more than a weight may be)
+          const float less = next - TT::kAbove;
+          next = next - less > TT::kAbove + TT::kSlack ? next : less;
+        }
+        next = fmaxf(mx, next);
         const float fix = next == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(mx - next);
         mx = next;
         l *= fix;

@@ -770,8 +770,10 @@ dspark_status dspark_kv_read(int32_t B, int32_t max_rows, const int32_t* cu_seql
  *   lse = log sum_k exp(s_k)
  * over the indices seen. Scores, maxima, sums and the accumulated output are
  * float32; the weights exp(s_k - max) round to the query type before their
- * product with v (float32 accumulation), and the output rounds once. A value
- * that a row does not see adds nothing to it, whatever it holds.
+ * product with v (float32 accumulation), and the output rounds once. In float16
+ * the weights are scaled by a power of two first, so that they count down to
+ * 2^-36 of the row's largest. A value that a row does not see adds nothing to it,
+ * whatever it holds.
  *
  * Arguments:
  *   B, gamma, num_heads, dt   as for dspark_kv_append

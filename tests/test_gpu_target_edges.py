@@ -205,3 +205,37 @@ def test_a_key_far_above_the_others_takes_everything(kind, size):
         mean = top.mean(0)
         within(f64(o.out[0]), np.broadcast_to(mean, (2, D)),
                u * np.abs(mean) + (u + 2 * (len(top) + 32) * W) * np.abs(top).mean(0), scale)
+
+
+@pytest.mark.parametrize("below", [12.0, 18.0, 22.0])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_the_tail_under_large_weights_counts(D, below):
+    """One key in a hundred, whose value is zero, and keys of e^-below of its weight
+    between them (every share of the keys has some of both): what the small ones
+    add up to is the output. In float16 a weight is off by half of 2^-24 where the
+    largest are 2^11 at least, so by 2^-36 of one of those, besides u, and the
+    output by half of 2^-24 where it is small."""
+    say(f"a long tail, e^-{below:g} each, D={D}")
+    code, dt, u = TYPES["f16"]
+    T, page, every = 20_000, 64, 100
+    b = Batch(1, [1], [T - 1], 1, page, False)
+    cache = make_cache("f16", b.nb, 1, page, D)
+    rng = np.random.default_rng(0)
+    k = np.zeros((T, 1, D), np.float32)
+    k[:, 0, 0] = -below / 2
+    k[::every, 0, 0] = 0
+    v = rng.normal(1000, 500, (T, 1, D)).astype(np.float32)
+    v[::every] = 0
+    put(cache, b.slots(0, 0, T), k, v)
+    q = torch.zeros(b.rows, 2, D, device=DEV, dtype=dt)
+    q[:, :, 0] = 2
+    o = dv.alloc_attention_outputs(1, 1, b.rows, 2, cache, lse=True)
+    dv.dspark_tree_attention(1, 1, q, b.rows, *b.args(), cache, 1.0, o)
+    torch.cuda.synchronize()
+    kk, vv = (get(cache, b.slots(0, 0, T), n).transpose(1, 0, 2) for n in "kv")
+    ref, rl, mean_abs, top = oracle.tree_attention(f64(q[:1]), kk, vv, T - 1, None, 1.0)
+    t = (D + 16) * W * top[..., None] + 2 * W
+    bound = (u * np.abs(ref) + (u + 2 * t + (T + 32) * W) * mean_abs +
+             every * 2.0 ** -36 * np.abs(vv).max() + 2.0 ** -25)
+    within(f64(o.out[:1]), ref, bound, "out")
+    within(f64(o.lse[:1]), rl, t[..., 0] + (T + 32) * W + 4 * W * np.abs(rl), "lse")
