@@ -586,7 +586,9 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
         if (values && edge) {
           const bool there = key0 + row < keys && !((missing >> (row >> 4)) & 1);
           strange_rows |= rows_in(__ballot(clean(w, there)), n);
-          b = there ? b : 127u;
+          // (no row that append writes has more than 246; a code may pass every finite
+          // number under it, and rows that do not see the row must not)
+          b = there ? min(b, 246u) : 127u;
         }
         const float e = __builtin_bit_cast(float, b << 23);
 #pragma unroll

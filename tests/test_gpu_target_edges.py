@@ -239,3 +239,34 @@ def test_the_tail_under_large_weights_counts(D, below):
              every * 2.0 ** -36 * np.abs(vv).max() + 2.0 ** -25)
     within(f64(o.out[:1]), ref, bound, "out")
     within(f64(o.lse[:1]), rl, t[..., 0] + (T + 32) * W + 4 * W * np.abs(rl), "lse")
+
+
+# ------------------------------------------------------------------ bytes of a row that is not there
+
+@pytest.mark.parametrize("D,hq", [(64, 4), (128, 4), (128, 32), (256, 4), (256, 32)])
+def test_exponent_bytes_of_an_unseen_row_do_not_matter(D, hq):
+    """A row of the step that append left out (its page holds whatever was there) has
+    any codes and exponent bytes: the rows that do not see it keep their outputs to
+    the bit."""
+    say(f"any exponent byte in a sibling's row D={D} hq={hq}")
+    b = Batch(3, [5, 1], [61, 30], 6, 16, True)
+    b.parents[0, :4] = [0, 0, 1, 2]  # 0-1-3, 0-2-4
+    cache = make_cache("e4m3", b.nb, 2, 16, D)
+    rng = np.random.default_rng(1)
+    for r in range(2):
+        T = b.ctx[r] + b.lens[r]
+        put(cache, b.slots(r, 0, T), *rng.normal(0, 1, (2, T, 2, D)).astype(np.float32))
+    q = torch.from_numpy(rng.normal(0, 1, (b.rows, hq, D)).astype(np.float32)).bfloat16().to(DEV)
+    o = dv.alloc_attention_outputs(2, 6, b.rows, hq, cache)
+    args, par = b.args(), b.par()
+    pg, of = b.slots(0, 62, 63)[0]  # row 1: rows 1 and 3 see it
+    want = None
+    for byte in (120, 0, 246, 247, 254, 255):
+        for t in (cache.k_scale, cache.v_scale):
+            t[pg, :, of] = byte
+        o.out.fill_(-7)
+        dv.dspark_tree_attention(2, 6, q, b.rows, *args, cache, 0.1, o, tree_parents=par)
+        torch.cuda.synchronize()
+        got = o.out[[0, 2, 4, 5]].clone()
+        want = got if want is None else want
+        assert torch.isfinite(got.float()).all() and torch.equal(got, want), byte
