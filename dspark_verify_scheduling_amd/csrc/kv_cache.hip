@@ -279,6 +279,10 @@ constexpr int kReadThreads = 512;
 // row gives its threads nothing to do (one head of 128: 230 MB in 98 us with 8
 // rows, 48 us with 64).
 constexpr int kReadFew = 8, kReadMany = 64;
+// Workgroups of a launch that have rows, at most: a grid of 2^32 threads or more is
+// cut off without an error. More rows are more launches (all in one, a loop over
+// its rows in each workgroup, took 108 us for the 437 MB below).
+constexpr int64_t kReadWgs = 1 << 20;
 
 // One workgroup per kReadRows rows: a wave finds its rows' requests and pages,
 // then 16-byte vectors of (row, head) are copied or widened. Bound by HBM: 437 MB
@@ -295,6 +299,7 @@ __global__ __launch_bounds__(kReadThreads) void read_kernel(ReadArgs a) {
   const int total_eff = rows_in_use(q, &total);
   const int64_t reach = (int64_t)q.width << a.kv.page_shift;
   if (blockIdx.x == 0) {
+    if (a.first_row) return;
     // sixteen lanes per request, a lane per page; kAhead requests of a lane at
     // once, so that a batch costs two memory latencies (256 requests, one by one:
     // 27 us)
@@ -354,7 +359,7 @@ __global__ __launch_bounds__(kReadThreads) void read_kernel(ReadArgs a) {
     return;
   }
   __shared__ int page_of[kReadRows], off_of[kReadRows];
-  const int row0 = (blockIdx.x - 1) * kReadRows;
+  const int row0 = a.first_row + (blockIdx.x - 1) * kReadRows;
   if (row0 >= total_eff) return;
   {
     // the last request that starts at or before each of the wave's rows, 64 steps
@@ -665,15 +670,20 @@ template <bool E8, int D>
 void read_by_rows(const ReadArgs& a, hipStream_t s) {
   const int64_t rows = a.req.B > 0 ? a.req.max_rows : 0;
   const int at_once = kReadFew * a.kv.hkv * (D * a.kv.cb / 16);  // threads with a vector
-  if (at_once < kReadThreads) {
-    hipLaunchKernelGGL((read_kernel<E8, D, kReadMany>),
-                       dim3(1u + (unsigned)((rows + kReadMany - 1) / kReadMany)),
-                       dim3(kReadThreads), 0, s, a);
-  } else {
-    hipLaunchKernelGGL((read_kernel<E8, D, kReadFew>),
-                       dim3(1u + (unsigned)((rows + kReadFew - 1) / kReadFew)),
-                       dim3(kReadThreads), 0, s, a);
-  }
+  const int per = at_once < kReadThreads ? kReadMany : kReadFew;
+  ReadArgs part = a;
+  int64_t first = 0;
+  do {
+    part.first_row = (int)first;
+    const int64_t wgs = std::min<int64_t>((rows - first + per - 1) / per, kReadWgs);
+    const dim3 grid(1u + (unsigned)wgs), block(kReadThreads);
+    if (per == kReadMany) {
+      hipLaunchKernelGGL((read_kernel<E8, D, kReadMany>), grid, block, 0, s, part);
+    } else {
+      hipLaunchKernelGGL((read_kernel<E8, D, kReadFew>), grid, block, 0, s, part);
+    }
+    first += wgs * per;
+  } while (first < rows);
 }
 
 template <bool E8>

@@ -63,6 +63,7 @@ struct ReadArgs {
   unsigned char* k_out;
   unsigned char* v_out;
   int64_t out_ld;  // bytes
+  int first_row;   // of a launch
   int32_t* meta;
 };
 hipError_t launch_read(const ReadArgs& a, hipStream_t s);

@@ -270,3 +270,58 @@ def test_exponent_bytes_of_an_unseen_row_do_not_matter(D, hq):
         got = o.out[[0, 2, 4, 5]].clone()
         want = got if want is None else want
         assert torch.isfinite(got.float()).all() and torch.equal(got, want), byte
+
+
+# ------------------------------------------------------------------ large reads
+
+@pytest.mark.parametrize("rows", [8 * 2 ** 20 + 777, 8 * 2 ** 23 + 4096])
+def test_read_of_more_rows_than_a_launch_holds(rows):
+    """8.4 and 67 million rows, the latter with more than 2^32 threads' work (137 GB
+    of outputs): the first and the last rows, and those around every 2^23, are
+    those of the cache."""
+    say(f"read of {rows} rows")
+    hkv, D, page = 2, 256, 256
+    if torch.cuda.mem_get_info()[0] < 2.2 * rows * hkv * D * 2:
+        pytest.skip("needs more memory")
+    cache = dv.alloc_kv_cache(5, hkv, page, D, dv.BF16, DEV)
+    cache.k.normal_()
+    cache.v.normal_()
+    ids = (torch.arange(rows // page + 1, device=DEV, dtype=torch.int32) * 3 % 5).view(1, -1)
+    rd = dv.alloc_kv_read_outputs(rows + 100, cache)
+    spans = [(0, 4096), (rows - 8192, rows)]
+    spans += [(x - 2048, x + 2048) for x in range(2 ** 23, rows - 2048, 2 ** 23)]
+    for t in rd[:2]:
+        t[rows:] = -7
+        for lo, hi in spans:
+            t[lo:hi] = -7
+    dv.dspark_kv_read(1, rows + 100, i32([0, rows]), i32([0]), ids, cache, rd)
+    torch.cuda.synchronize()
+    assert rd.read_meta.tolist() == [rows, 0]
+    for t, pool in ((rd.k_out, cache.k), (rd.v_out, cache.v)):
+        assert bool((t[rows:] == -7).all())
+        for lo, hi in spans:
+            i = torch.arange(lo, hi, device=DEV)
+            assert torch.equal(t[lo:hi], pool[i // page * 3 % 5, :, i % page]), lo
+    del rd
+    torch.cuda.empty_cache()
+
+
+def test_read_into_buffers_of_any_number_of_rows():
+    """The launch does not grow with the rows that the buffers are said to hold."""
+    say("read with max_rows 2^31 - 1")
+    b, cache, rows = filled(6)
+    total = int(b.cu[-1])
+    rd = dv.alloc_kv_read_outputs(b.rows, cache)
+    for t in rd[:2]:
+        t.fill_(-7)
+    cu, pre, table = b.args()
+    for most in (80_000_000, 2 ** 31 - 1):
+        st = dv._lib.lib().dspark_kv_read(
+            b.B, most, cu.data_ptr(), pre.data_ptr(), table.data_ptr(), b.width, cache._ref,
+            rd.k_out.data_ptr(), rd.v_out.data_ptr(), 64, rd.read_meta.data_ptr(),
+            torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert st == dv._lib.OK
+        assert rd.read_meta.tolist() == [total, 0]
+        for t in rd[:2]:
+            assert torch.equal(t[:total], rows[:total]) and bool((t[total:] == -7).all())
