@@ -76,6 +76,15 @@ def _device(cache: "KvCache") -> int:
 
 # ------------------------------------------------------------------ cache
 
+def _strides(t: torch.Tensor) -> tuple:
+    """Strides in which a dimension of one has its dense one: it has none of its own."""
+    out, dense = [], 1
+    for n, s in zip(reversed(t.shape), reversed(t.stride())):
+        out.append(s if n != 1 else dense)
+        dense = out[-1] * n
+    return tuple(reversed(out))
+
+
 class KvCache:
     """A paged cache: ``k`` and ``v`` [num_blocks, num_kv_heads, block_size,
     head_dim] in bfloat16, float16 or float8_e4m3fn, or with a leading layer
@@ -97,16 +106,19 @@ class KvCache:
             raise ValueError(f"the cache must be on a CUDA device, got {k.device}")
         heads, size, dim = k.shape[-3:]
         dense = (size * dim, dim, 1)
-        if k.stride() != v.stride() or tuple(k.stride()[-3:]) != dense:
+        ks = _strides(k)
+        if ks != _strides(v) or ks[-3:] != dense:
             raise ValueError("k and v need the same strides, dense in their last three dimensions")
         e8 = k.dtype == torch.float8_e4m3fn
+        ss = None
         if e8:
             for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
                 if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8:
                     raise TypeError(f"{name} must be a uint8 tensor")
                 if t.shape != k.shape[:-1] or t.device != k.device:
                     raise ValueError(f"{name} must be {tuple(k.shape[:-1])} on {k.device}")
-                if tuple(t.stride()[-2:]) != (size, 1) or t.stride() != k_scale.stride():
+                ss = ss or _strides(t)
+                if ss[-2:] != (size, 1) or _strides(t) != ss:
                     raise ValueError("k_scale and v_scale need the same strides, dense in their "
                                      "last two dimensions")
         elif k_scale is not None or v_scale is not None:
@@ -119,13 +131,10 @@ class KvCache:
         self.row_dtype = torch.bfloat16 if e8 else k.dtype
         self.device = k.device
         self.device_index = k.get_device()
-        ks, ss = k.stride(), (k_scale.stride() if e8 else None)
         self._desc = _lib.KvCacheDesc(
             k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if e8 else None,
             v_scale.data_ptr() if e8 else None,
-            # a dimension of one has no stride of its own
-            ks[-4] if self.num_blocks > 1 else heads * size * dim,
-            (ss[-3] if self.num_blocks > 1 else heads * size) if e8 else 0,
+            ks[-4], ss[-3] if e8 else 0,
             ks[0] if k.dim() == 5 else 0, ss[0] if e8 and k.dim() == 5 else 0,
             self.num_layers, self.num_blocks, heads, size, dim, self.dtype)
         self._ref = ctypes.cast(ctypes.pointer(self._desc), ctypes.c_void_p)

@@ -325,3 +325,54 @@ def test_read_into_buffers_of_any_number_of_rows():
         assert rd.read_meta.tolist() == [total, 0]
         for t in rd[:2]:
             assert torch.equal(t[:total], rows[:total]) and bool((t[total:] == -7).all())
+
+
+# ------------------------------------------------------------------ views of a pool
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_caches_whose_dimensions_of_one_have_any_stride(kind):
+    """One head stored as [page][1][dim], and a single page cut from two pools of
+    different page strides: the strides of dimensions of one do not matter."""
+    say(f"cache views {kind}")
+    D, page = 64, 16
+    el = torch.float8_e4m3fn if kind == "e4m3" else torch.bfloat16
+    e8 = kind == "e4m3"
+
+    def pool(*shape, dtype=el):
+        return torch.zeros(shape, device=DEV).to(dtype)
+
+    token_major = [pool(3, page, 1, D).transpose(1, 2) for _ in range(2)]
+    scales = [pool(3, page, 1, dtype=torch.uint8).transpose(1, 2) for _ in range(2)] if e8 else []
+    one_page = [pool(4, 2, 1, page, D)[1:2, 0], pool(4, 1, page, D)[2:3]]
+    one_scale = [pool(4, 2, 1, page, dtype=torch.uint8)[1:2, 0],
+                 pool(4, 1, page, dtype=torch.uint8)[2:3]] if e8 else []
+    one_layer = [pool(2, 5, 1, page, D)[:1], pool(1, 5, 1, page, D)]
+    layer_scale = [pool(2, 5, 1, page, dtype=torch.uint8)[:1],
+                   pool(1, 5, 1, page, dtype=torch.uint8)] if e8 else []
+    x = torch.randn(5, 1, D, device=DEV).bfloat16()
+    if e8:
+        x = x.to(el).to(torch.bfloat16)  # codes: exact in 8 bits under an exponent of 0
+        x[:, :, 0] = 448
+    for k_v, sc in ((token_major, scales), (one_page, one_scale), (one_layer, layer_scale)):
+        cache = dv.KvCache(*k_v, *sc)
+        lay = cache.layer(0) if k_v[0].dim() == 5 else cache
+        ap = dv.alloc_append_outputs(5, 1, lay)
+        rd = dv.alloc_kv_read_outputs(5, lay)
+        args = i32([0, 5]), i32([3]), i32([[0]])
+        dv.dspark_kv_append(1, 4, x, x, x, 5, *args, lay, ap)
+        dv.dspark_kv_read(1, 5, *args, lay, rd)
+        cm = torch.empty(2, dtype=torch.int32, device=DEV)
+        dv.dspark_kv_commit(1, 4, i32([[0, 2, 4, -1, -1]]), i32([2]), i32([3]), i32([[0]]), cache, cm)
+        torch.cuda.synchronize()
+        assert ap.append_meta.tolist() == rd.read_meta.tolist() == [5, 0] and cm.tolist() == [2, 0]
+        assert torch.equal(rd.k_out, x) and torch.equal(rd.v_out, x)
+        for t in k_v:
+            t = t[0] if t.dim() == 5 else t
+            assert torch.equal(t[0, 0, 3:8].float(), x[[0, 2, 4, 3, 4], 0].float())
+    # what is not dense is refused as before
+    with pytest.raises(ValueError, match="dense"):
+        dv.KvCache(*[pool(3, page, 2, D).transpose(1, 2) for _ in range(2)],
+                   *[pool(3, 2, page, dtype=torch.uint8) for _ in sc])
+    with pytest.raises(ValueError, match="strides"):
+        dv.KvCache(pool(4, 2, 1, page, D)[:, 0], pool(4, 1, page, D),
+                   *[pool(4, 1, page, dtype=torch.uint8) for _ in sc])
