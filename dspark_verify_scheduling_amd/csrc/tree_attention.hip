@@ -126,23 +126,24 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a, Parts ws
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Workgroups of the split kernel, at most: three to a CU (their LDS rings).
-constexpr int kMaxWgs = 768;
+constexpr int kCus = 256;  // of the card
 
 struct Plan {
   int rows;
+  int wgs;  // workgroups of the split kernel, at most: what its LDS rings leave room for
   size_t m_off, l_off, o_off, bytes;
 };
 
 Plan plan(int B, int gamma, int group, int D) {
   Plan p;
-  const int mtiles = (group * (gamma + 1) + 15) / 16;
-  p.rows = 16 * std::min(waves_for(group * (gamma + 1), D), mtiles);
-  const size_t stat = align256((size_t)2 * kMaxWgs * p.rows * sizeof(float));
+  const int mtiles = (group * (gamma + 1) + 15) / 16, waves = waves_for(group * (gamma + 1), D);
+  p.rows = 16 * std::min(waves, mtiles);
+  p.wgs = kCus * per_cu(D, true, waves);  // (8 bits: the most)
+  const size_t stat = align256((size_t)2 * p.wgs * p.rows * sizeof(float));
   p.m_off = align256((size_t)(B + 1) * sizeof(int64_t));
   p.l_off = p.m_off + stat;
   p.o_off = p.l_off + stat;
-  p.bytes = p.o_off + align256((size_t)2 * kMaxWgs * p.rows * D * sizeof(float));
+  p.bytes = p.o_off + align256((size_t)2 * p.wgs * p.rows * D * sizeof(float));
   return p;
 }
 
@@ -182,8 +183,7 @@ hipError_t launch_attention(const AttnArgs& args, dspark_dtype dt, hipStream_t s
   ws.l = reinterpret_cast<float*>(w + p.l_off);
   ws.o = reinterpret_cast<float*>(w + p.o_off);
   ws.rows = p.rows;
-  const int per_cu = attn::per_cu(a.kv.dim, a.kv.cb == 1, a.waves);
-  ws.wgs = std::min(attn::kMaxWgs, per_cu * cus);
+  ws.wgs = std::min(attn::kCus, cus) * attn::per_cu(a.kv.dim, a.kv.cb == 1, a.waves);
   switch (a.kv.dim) {
     case 64: attn::launch_dim64(a, ws, dt, s); break;
     case 128: attn::launch_dim128(a, ws, dt, s); break;

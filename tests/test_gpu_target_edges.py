@@ -13,6 +13,7 @@ import dspark_verify_scheduling_amd as dv
 import oracle
 from _gpu import DEV, say
 from test_gpu_target import TYPES, W, Batch, bits, f64, get, i32, make_cache, put, within
+from test_gpu_target_steps import ref_long
 
 pytestmark = pytest.mark.gpu
 
@@ -376,3 +377,44 @@ def test_caches_whose_dimensions_of_one_have_any_stride(kind):
     with pytest.raises(ValueError, match="strides"):
         dv.KvCache(pool(4, 2, 1, page, D)[:, 0], pool(4, 1, page, D),
                    *[pool(4, 1, page, dtype=torch.uint8) for _ in sc])
+
+
+# ------------------------------------------------------------------ workspace
+
+@pytest.mark.parametrize("kind,gamma,hq,hkv,D", [
+    ("bf16", 3, 4, 2, 64), ("e4m3", 3, 4, 2, 128), ("f16", 31, 16, 2, 128), ("e4m3", 31, 16, 2, 256),
+    ("bf16", 3, 4, 1, 256)])
+def test_attention_keeps_to_its_workspace(kind, gamma, hq, hkv, D):
+    """Contexts that every workgroup has a part of, in a workspace of just the size
+    asked for: the bytes behind it stay, the rows are right."""
+    say(f"workspace {kind} gamma={gamma} hq={hq} hkv={hkv} D={D}")
+    _, dt, u = TYPES[kind]
+    b = Batch(1, [gamma + 1, 2], [30_000, 9_000], gamma, 64, False)
+    cache = make_cache(kind, b.nb, hkv, 64, D)
+    torch.manual_seed(0)
+    for t in (cache.k, cache.v):
+        t.copy_(torch.randn(t.shape, device=DEV).to(t.dtype))
+    if kind == "e4m3":
+        cache.k_scale.fill_(127)
+        cache.v_scale.fill_(127)
+    q = torch.randn(b.rows, hq, D, device=DEV).to(dt)
+    o = dv.alloc_attention_outputs(b.B, gamma, b.rows, hq, cache)
+    size = dv.dspark_tree_attention_workspace_size(b.B, gamma, hq, hkv, D)
+    buf = torch.full((size + 2 ** 20,), 0xA5, dtype=torch.uint8, device=DEV)
+    o = o._replace(workspace=buf[:size])
+    dv.dspark_tree_attention(b.B, gamma, q, b.rows, *b.args(), cache, D ** -0.5, o)
+    torch.cuda.synchronize()
+    assert o.attention_meta.tolist() == [int(b.cu[-1]), 0]
+    assert bool((buf[size:] == 0xA5).all())
+    for r in range(2):
+        T = b.ctx[r] + b.lens[r]
+        pages = torch.tensor(b.table[r][:-(-T // 64)].tolist(), device=DEV)
+        k, v = (t[pages].to(torch.float32).transpose(0, 1).reshape(hkv, -1, D)[:, :T]
+                .repeat_interleave(hq // hkv, 0) for t in (cache.k, cache.v))
+        c0, c1 = int(b.cu[r]), int(b.cu[r + 1])
+        ref, mean_abs, top = ref_long(q[c0:c1], k, v, b.ctx[r], D ** -0.5)
+        t = (D + 16) * W * top[..., None] + 2 * W
+        bound = u * np.abs(ref) + (u + 2 * t + (T + 32) * W) * mean_abs
+        if kind == "f16":
+            bound = bound + T * 2.0 ** -36 * float(v.abs().max()) + 2.0 ** -25
+        within(f64(o.out[c0:c1]), ref, bound, f"request {r}")
