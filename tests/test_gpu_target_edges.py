@@ -12,7 +12,8 @@ import torch
 import dspark_verify_scheduling_amd as dv
 import oracle
 from _gpu import DEV, say
-from test_gpu_target import TYPES, W, Batch, bits, f64, get, i32, make_cache, put, within
+from test_gpu_target import (TYPES, W, Batch, attention_check, bits, f64, get, i32, make_cache, put,
+                             within)
 from test_gpu_target_steps import ref_long
 
 pytestmark = pytest.mark.gpu
@@ -418,3 +419,114 @@ def test_attention_keeps_to_its_workspace(kind, gamma, hq, hkv, D):
         if kind == "f16":
             bound = bound + T * 2.0 ** -36 * float(v.abs().max()) + 2.0 ** -25
         within(f64(o.out[c0:c1]), ref, bound, f"request {r}")
+
+
+# ------------------------------------------------------------------ every kernel of the attention
+
+@pytest.mark.parametrize("kind,lens,ctx,gamma,hq,hkv,D,page,tree,joint", [
+    # eight waves at heads of 256, 8 and 16 bits: a wave's share of a tile is two copies
+    ("e4m3", [17, 3, 17], [63, 5, 400], 16, 10, 2, 256, 32, True, False),
+    ("e4m3", [65, 1, 33], [1000, 2000, 0], 64, 16, 2, 256, 16, True, True),
+    ("e4m3", [17], [9000], 16, 8, 1, 256, 256, False, False),
+    ("f16", [17, 3, 17], [63, 5, 400], 16, 10, 2, 256, 32, True, False),
+    ("f16", [65, 20], [5000, 31], 64, 8, 4, 256, 64, True, True),
+    # 8 bits in batches beyond a wave's lanes, few rows and many, each head size
+    ("e4m3", [3] * 90, [7 * i for i in range(90)], 2, 8, 2, 128, 16, True, False),
+    ("e4m3", [1 + i % 17 for i in range(70)], [11 * i for i in range(70)], 16, 16, 2, 128, 32, True, True),
+    ("e4m3", [1 + i % 5 for i in range(300)], [i % 97 for i in range(300)], 4, 3, 1, 64, 16, True, False),
+    ("e4m3", [2] * 65, [301] * 65, 1, 4, 2, 256, 64, False, False),
+    ("e4m3", [1 + i % 33 for i in range(66)], [200 - i for i in range(66)], 32, 4, 1, 256, 16, True, False),
+])
+def test_attention_kernels(kind, lens, ctx, gamma, hq, hkv, D, page, tree, joint):
+    say(f"attention {kind} B={len(lens)} lens={lens[:4]} hq={hq} hkv={hkv} D={D}")
+    b = Batch(len(lens) + D, lens, ctx, gamma, page, tree)
+    attention_check(b, kind, hq, hkv, D, D ** -0.5, seed=D, joint=joint, repeat=2)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_rows_ignore_what_they_do_not_see(kind, D):
+    """A tree of 33 rows, eight query heads to each of two key/value heads (more than
+    64 rows to a head): NaN and infinities of two siblings' rows, in keys, in
+    values, in both, reach the rows that see them and no other."""
+    say(f"non-finite rows of a large tree {kind} D={D}")
+    _, dt, u = TYPES[kind]
+    n, hq, hkv, page = 33, 16, 2, 16
+    b = Batch(3, [n, 2], [61, 30], n - 1, page, True)
+    rng = b.rng
+    cache = make_cache(kind, b.nb, hkv, page, D)
+    T = b.ctx[0] + n
+    paths = oracle.tree_paths(b.parents[0], n)
+    k, v = rng.normal(0, 1, (2, T, hkv, D)).astype(np.float32)
+    inf = np.nan if kind == "e4m3" else np.inf
+    leaves = [j for j in range(1, n) if j not in set(b.parents[0, :n - 1].tolist())]
+    k[61 + leaves[0], 0, 3] = np.nan
+    v[61 + leaves[1], 1, D - 1] = inf
+    v[61 + 5, :, 0] = np.nan
+    v[61 + 5, :, D // 2] = inf
+    put(cache, b.slots(0, 0, T), k, v)
+    put(cache, b.slots(1, 0, 32), *rng.normal(0, 1, (2, 32, hkv, D)).astype(np.float32))
+    q = torch.from_numpy(rng.normal(0, 1, (b.rows, hq, D)).astype(np.float32)).to(dt).to(DEV)
+    o = dv.alloc_attention_outputs(2, n - 1, b.rows, hq, cache)
+    dv.dspark_tree_attention(2, n - 1, q, b.rows, *b.args(), cache, 0.1, o, tree_parents=b.par())
+    torch.cuda.synchronize()
+    assert o.attention_meta.tolist() == [n + 2, 0]
+    got = o.out[:n + 2].float().cpu().numpy()
+    for j in range(n):
+        bad = np.zeros((hq, D), bool)
+        if leaves[0] in paths[j]:
+            bad[:8] = True  # a NaN score: the whole row of that head's queries
+        if leaves[1] in paths[j]:
+            bad[8:, D - 1] = True
+        if 5 in paths[j]:
+            bad[:, [0, D // 2]] = True
+        assert np.array_equal(~np.isfinite(got[j]), bad), j
+    assert np.isfinite(got[n:]).all()
+
+
+# ------------------------------------------------------------------ lengths out of order
+
+@pytest.mark.parametrize("B", [6, 80])
+def test_attention_and_append_beside_lengths_out_of_order(B):
+    """A word out of place leaves out the two requests that it bounds, or makes them
+    others; every request that it does not touch has the rows that it has without."""
+    say(f"attention and append beside malformed lengths B={B}")
+    b, cache, rows = filled(B)
+    rng = np.random.default_rng(B)
+    for r in range(B):
+        put(cache, b.slots(r, 0, b.ctx[r] + b.lens[r]),
+            *rng.normal(0, 1, (2, b.ctx[r] + b.lens[r], 1, 64)).astype(np.float32))
+    q = torch.randn(b.rows, 2, 64, device=DEV).bfloat16()
+    o = dv.alloc_attention_outputs(B, 4, b.rows, 2, cache)
+    dv.dspark_tree_attention(B, 4, q, b.rows, *b.args(), cache, 0.125, o)
+    torch.cuda.synchronize()
+    want, total, at = o.out.clone(), int(b.cu[-1]), B // 2
+    # the shares of the keys differ: each side is within 2.1 u mean |v|, and |v| < 5
+    tol = 2 * 2.1 * 2.0 ** -8 * 5
+    other = make_cache("bf16", b.nb, 1, 16, 64)
+    for value in (10 ** 6, -5, total, 0):
+        cu = b.cu.copy()
+        cu[at] = value
+        o.out.fill_(-7)
+        dv.dspark_tree_attention(B, 4, q, b.rows, i32(cu), i32(b.ctx), i32(b.table), cache, 0.125, o)
+        ap = dv.alloc_append_outputs(b.rows, 1, other)
+        ap.q_out.fill_(-7)
+        dv.dspark_kv_append(B, 4, rows, rows, rows, b.rows, i32(cu), i32(b.ctx), i32(b.table), other, ap)
+        torch.cuda.synchronize()
+        for meta in (o.attention_meta, ap.append_meta):
+            assert meta.tolist() == [total, oracle.DATA_BAD_LENS], value
+        taken = set()  # rows of the request that the word makes out of others'
+        for r in (at - 1, at):
+            s, e = int(cu[r]), int(cu[r + 1])
+            if 0 <= s < e <= total and e - s <= 5:
+                taken |= set(range(s, e))
+        for r in range(B):
+            c = range(int(b.cu[r]), int(b.cu[r + 1]))
+            if taken & set(c):
+                continue
+            c = slice(c.start, c.stop)
+            if r in (at - 1, at):
+                assert bool((o.out[c] == -7).all()) and bool((ap.q_out[c] == -7).all())
+            else:
+                assert float((o.out[c].float() - want[c].float()).abs().max()) <= tol
+                assert torch.equal(ap.q_out[c], rows[c])
