@@ -710,6 +710,11 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
         for (int d = 0; d < ND; ++d) o[d] *= fix;
       }
       const float ref = mx == -__builtin_inff() ? 0.0f : mx;
+      // The product takes weights of the query type, each off by up to half its step;
+      // their sum takes them as they are. The outputs' error against 64 bits is 0.0023
+      // of their size for it in bfloat16 and 0.00028 in float16, where weights in
+      // float32 leave 0.0017 and 0.00021. Split in two halves with a product each they
+      // nearly would: 329 us the 64 8-bit trees against 243, 112 the chains against 110.
       V8 pf[NG / 2];
 #pragma unroll
       for (int b = 0; b < NG; ++b)
@@ -800,7 +805,7 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
 
 // out = sum_k e^(s_k - m) v_k / sum_k e^(s_k - m) in one pass over the keys: running
 // maximum m, sum and outputs in float32 registers, m moved only when a score
-// passes it by kSlack. Parts of a row join by (m, sum, outputs) in join_kernel.
+// passes it by Types::kSlack. Parts of a row join by (m, sum, outputs) in join_kernel.
 //
 // Persistent over the units of all (request, key/value head, row segment)s in
 // order: workgroup w takes the w-th equal share, so ragged contexts balance by
@@ -812,9 +817,10 @@ __device__ __forceinline__ void segment(const AttnArgs& a, const Parts& ws, cons
 // the join (5.8 TB/s of the 7.0 that a plain read reaches; without the products
 // 104). Many rows over 8 bits: the latency of one tile's widening, products and
 // barrier, with four waves to a SIMD to cover it. 64 trees of up to 17 rows, 64 on
-// 8: 580 MB and 76 GFLOP, 231 us and 12 (2.5 TB/s, 328 TFLOP/s; the copies alone
-// 120). Two trees of 65 rows over 131k keys, 16 on 2 of 64, f16: 103 MB and
-// 27 GFLOP, 62 to 80 us and 14 (the product of 8192 x 8192 matrices of the vendor's
+// 8: 580 MB and 76 GFLOP, 243 us and 12 (2.4 TB/s, 313 TFLOP/s; the copies alone
+// 120). A tree of 65 rows and a single row over 70k and 131k keys, 16 on 2 of 64,
+// f16: 103 MB; 88 us and 16.5 with the tree over the 131k (35 GFLOP), 67 and 13.5
+// over the 70k (19 GFLOP; the product of 8192 x 8192 matrices of the vendor's
 // library reaches 1207 TFLOP/s here). One token over 700 keys: 8 us and 4, all of it
 // the chain of dependent reads (lengths, pages, queries, keys).
 //
