@@ -38,6 +38,11 @@ __all__ = [
     "dspark_kv_append", "alloc_append_outputs", "dspark_kv_read", "alloc_kv_read_outputs",
     "dspark_tree_attention", "dspark_tree_attention_workspace_size", "alloc_attention_outputs",
     "dspark_tree_accept", "alloc_tree_accept_outputs", "dspark_kv_commit",
+    "dspark_kv_append_axes", "LatentCache", "alloc_latent_cache", "dspark_latent_append",
+    "alloc_latent_append_outputs", "dspark_latent_read", "alloc_latent_read_outputs",
+    "dspark_latent_commit", "dspark_latent_attention", "dspark_latent_attention_workspace_size",
+    "alloc_latent_attention_outputs", "dspark_latent_prefill",
+    "dspark_latent_prefill_workspace_size", "alloc_latent_prefill_outputs",
 ]
 
 
@@ -605,6 +610,14 @@ def dspark_tv_accept(B: int, gamma: int, V: int, dt: int, draft_logits: torch.Te
 from .target import (  # noqa: E402
     AppendOutputs, AttentionOutputs, KvCache, KvReadOutputs, TreeAcceptOutputs,
     alloc_append_outputs, alloc_attention_outputs, alloc_kv_cache, alloc_kv_read_outputs,
-    alloc_tree_accept_outputs, dspark_kv_append, dspark_kv_commit, dspark_kv_read,
-    dspark_tree_accept, dspark_tree_attention, dspark_tree_attention_workspace_size,
+    alloc_tree_accept_outputs, dspark_kv_append, dspark_kv_append_axes, dspark_kv_commit,
+    dspark_kv_read, dspark_tree_accept, dspark_tree_attention,
+    dspark_tree_attention_workspace_size,
+)
+from .latent import (  # noqa: E402
+    LatentAppendOutputs, LatentCache, LatentReadOutputs, alloc_latent_append_outputs,
+    alloc_latent_attention_outputs, alloc_latent_cache, alloc_latent_prefill_outputs,
+    alloc_latent_read_outputs, dspark_latent_append, dspark_latent_attention,
+    dspark_latent_attention_workspace_size, dspark_latent_commit, dspark_latent_prefill,
+    dspark_latent_prefill_workspace_size, dspark_latent_read,
 )

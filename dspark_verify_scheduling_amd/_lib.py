@@ -25,6 +25,8 @@ MAX_SPS_PROBES = 512
 STS_MAX_GRID, STS_MAX_BINS, STS_MAX_RECORDS = 128, 64, 4194304
 COST_ADDITIVE, COST_SPS1D = 0, 1
 MAX_HEADS, MAX_GROUP, MAX_LAYERS = 256, 64, 1024
+MAX_AXES, LATENT_MAX_HEADS, LATENT_ROPE, LATENT_GROUP = 4, 128, 64, 128
+LATENT_MAX_KEYS = 134217728
 
 
 class PlanOptions(ctypes.Structure):
@@ -40,6 +42,16 @@ class KvCacheDesc(ctypes.Structure):
                 ("layer_stride", c_int64), ("scale_layer_stride", c_int64),
                 ("num_layers", c_int32), ("num_blocks", c_int32), ("num_kv_heads", c_int32),
                 ("block_size", c_int32), ("head_dim", c_int32), ("dtype", c_int)]
+
+
+class LatentCacheDesc(ctypes.Structure):
+    """dspark_latent_cache of include/dspark.h."""
+    _fields_ = [("latent", c_void_p), ("rope", c_void_p), ("scale", c_void_p),
+                ("block_stride", c_int64), ("rope_block_stride", c_int64),
+                ("scale_block_stride", c_int64), ("layer_stride", c_int64),
+                ("rope_layer_stride", c_int64), ("scale_layer_stride", c_int64),
+                ("num_layers", c_int32), ("num_blocks", c_int32), ("block_size", c_int32),
+                ("latent_dim", c_int32), ("dtype", c_int)]
 
 
 # name -> (restype, argtypes), mirroring include/dspark.h
@@ -109,6 +121,32 @@ SIGNATURES = {
     "dspark_kv_commit": (c_int, [
         c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p,
         c_void_p]),
+    "dspark_kv_append_axes": (c_int, [
+        c_int32, c_int32, c_int, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int32,
+        c_void_p, c_void_p, c_void_p, c_int64, c_int32, c_void_p, c_void_p, c_int32, c_void_p,
+        c_void_p, c_float, c_void_p, c_int32, c_int32, c_int32, c_void_p, c_int64, c_void_p,
+        c_void_p, c_void_p]),
+    "dspark_latent_append": (c_int, [
+        c_int32, c_int32, c_int32, c_int, c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int32,
+        c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_float, c_void_p, c_int32,
+        c_int32, c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_void_p]),
+    "dspark_latent_read": (c_int, [
+        c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int64,
+        c_void_p, c_int64, c_void_p, c_void_p]),
+    "dspark_latent_commit": (c_int, [
+        c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p,
+        c_void_p]),
+    "dspark_latent_attention": (c_int, [
+        c_int32, c_int32, c_int32, c_int, c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int64,
+        c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_float, c_void_p,
+        c_int64, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "dspark_latent_attention_workspace_size": (c_size_t, [c_int32, c_int32, c_int32, c_int32]),
+    "dspark_latent_prefill": (c_int, [
+        c_int32, c_int32, c_int32, c_int, c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_int32,
+        c_int32, c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_float, c_void_p, c_int64,
+        c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "dspark_latent_prefill_workspace_size": (c_size_t, [
+        c_int32, c_int32, c_int32, c_int32, c_int32, c_int32]),
     "dspark_status_str": (ctypes.c_char_p, [c_int]),
     "dspark_last_error": (ctypes.c_char_p, []),
     "dspark_version": (c_int32, []),

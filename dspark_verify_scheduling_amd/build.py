@@ -26,10 +26,13 @@ ARCH = "gfx950"
 
 LIB_SOURCES = ["api.hip", "plan.hip", "pack.hip", "accept.hip", "tv.hip", "scatter.hip", "sts.hip", "sampling.hip",
                "api_target.hip", "kv_cache.hip", "tree_attention.hip",
-               "tree_attention_d64.hip", "tree_attention_d128.hip", "tree_attention_d256.hip"]
+               "tree_attention_d64.hip", "tree_attention_d128.hip", "tree_attention_d256.hip",
+               "api_latent.hip", "kv_append_axes.hip", "latent_cache.hip", "latent_attention.hip",
+               "latent_attention_d256.hip", "latent_attention_d512.hip", "latent_prefill.hip"]
 # sources whose generated code is checked for other uses of M0
 M0_SOURCES = ["tv.hip", "tree_attention_d64.hip", "tree_attention_d128.hip",
-              "tree_attention_d256.hip"]
+              "tree_attention_d256.hip", "latent_attention_d256.hip", "latent_attention_d512.hip",
+              "latent_prefill.hip"]
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}",
@@ -39,7 +42,7 @@ COMMON_FLAGS = [
     "-shared",
     "-Wall",
     "-Wno-unused-function",
-    "-parallel-jobs=4",
+    "-parallel-jobs=8",
     # no packed fp32 instructions: plain scalar fp32 code only
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     # no contraction of a product and a sum into one rounding anywhere, also

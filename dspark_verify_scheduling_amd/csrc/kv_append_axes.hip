@@ -1,0 +1,136 @@
+// Cache append of rows whose rotation takes a position on several axes.
+#include "append_row.h"
+#include "latent.h"
+
+#include <algorithm>
+
+namespace dspark {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// Positions of all packed rows on all axes, a share to each thread.
+__device__ int position_status(const AppendAxesArgs& a, int total_eff) {
+  int bits = 0;
+  if (a.base.req.B == 0) return bits;
+  for (int x = 0; x < a.num_axes; ++x) {
+    const int32_t* p = a.positions + x * a.positions_ld;
+#pragma unroll 8
+    for (int n = threadIdx.x; n < total_eff; n += kThreads)
+      if (p[n] < 0 || p[n] >= a.base.rope_rows) bits = DSPARK_DATA_BAD_POS;
+  }
+  return bits;
+}
+
+// One workgroup per packed row: its waves find the row's request and page each by
+// itself, and take its heads in turn. Pair i turns by row positions[axis of i] of
+// the table, so a lane gathers its eight cosines and sines from up to num_axes
+// table rows, once for all heads.
+template <typename T, bool E8, int D>
+__global__ __launch_bounds__(kThreads) void append_axes_kernel(AppendAxesArgs a) {
+  constexpr int LPH = D / 8;
+  const AppendArgs& b = a.base;
+  const ReqView& q = b.req;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  int total;
+  const int total_eff = rows_in_use(q, &total);
+  if (blockIdx.x == 0) {
+    if (a.first_row) return;
+    __shared__ int all;
+    int bits = total != total_eff ? DSPARK_DATA_BAD_LENS : 0;
+    bits |= spans_status<kThreads>(q, b.kv.page_shift, b.kv.num_blocks, total_eff, 0x7FFFFFFF);
+    bits |= position_status(a, total_eff);
+    write_meta(b.meta, total, bits, &all);
+    return;
+  }
+  const int64_t packed = a.first_row + blockIdx.x - 1;
+  if (packed >= total_eff) return;
+  const int n = (int)packed;
+  RowAppend<T, E8, D, kThreads> row(b, n);
+  int pos[DSPARK_MAX_AXES];
+  bool bad = false;
+#pragma unroll
+  for (int x = 0; x < DSPARK_MAX_AXES; ++x) {
+    pos[x] = a.positions[min(x, a.num_axes - 1) * a.positions_ld + n];
+    bad |= pos[x] < 0 || pos[x] >= b.rope_rows;
+  }
+  int r, j;
+  rows_requests<1>(q, n, total_eff, (int64_t)q.width << b.kv.page_shift, 0x7FFFFFFF, &r, &j);
+  r = __builtin_amdgcn_readfirstlane(r);
+  j = __builtin_amdgcn_readfirstlane(j);
+  if (j < 0 || bad) return;
+  const int64_t slot = (int64_t)q.prefix[r] + j;
+  const int id = q.table[(size_t)r * q.width + (slot >> b.kv.page_shift)];
+  if (id < 0 || id >= b.kv.num_blocks) return;
+
+  const int li = lane & (LPH - 1), half = b.rope_dim >> 1;
+  const bool turned = 8 * li < b.rope_dim;
+  int swap = lane;  // lane that holds the other elements of the pairs
+  // the table's entry of a pair
+  auto turn = [&](int i, float* c, float* s) {
+    const int x = (int)(a.axis[i >> 5] >> (2 * (i & 31))) & 3;
+    const int p = x < 2 ? (x == 0 ? pos[0] : pos[1]) : (x == 2 ? pos[2] : pos[3]);
+    const float* cs = b.rope + (size_t)p * b.rope_dim;
+    *c = cs[i];
+    *s = cs[half + i];
+  };
+  float co[8], si[8];
+  if (b.rope_interleaved) {
+    const int i0 = turned ? 4 * li : 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      turn(i0 + e, &co[2 * e], &si[2 * e + 1]);
+      co[2 * e + 1] = co[2 * e];
+      si[2 * e] = -si[2 * e + 1];
+    }
+  } else {
+    const bool low = 8 * li < half;
+    const int i0 = turned ? (low ? 8 * li : 8 * li - half) : 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      turn(i0 + e, &co[e], &si[e]);
+      si[e] = low ? -si[e] : si[e];
+    }
+    if (turned) swap = low ? lane + half / 8 : lane - half / 8;
+  }
+  row.finish(id, (int)(slot & ((1 << b.kv.page_shift) - 1)), co, si, turned, swap);
+}
+
+template <typename T, bool E8>
+void by_dim(const AppendAxesArgs& a, unsigned grid, hipStream_t s) {
+  switch (a.base.kv.dim) {
+    case 64:
+      hipLaunchKernelGGL((append_axes_kernel<T, E8, 64>), dim3(grid), dim3(kThreads), 0, s, a);
+      break;
+    case 128:
+      hipLaunchKernelGGL((append_axes_kernel<T, E8, 128>), dim3(grid), dim3(kThreads), 0, s, a);
+      break;
+    default:
+      hipLaunchKernelGGL((append_axes_kernel<T, E8, 256>), dim3(grid), dim3(kThreads), 0, s, a);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_append_axes(const AppendAxesArgs& a, dspark_dtype dt, hipStream_t s) {
+  // a grid of 2^32 threads or more is cut off without an error
+  constexpr int64_t kMostRows = 1 << 20;
+  const int64_t rows = a.base.req.B > 0 ? a.base.req.max_rows : 0;
+  AppendAxesArgs part = a;
+  part.first_row = 0;
+  do {
+    const unsigned grid = 1u + (unsigned)std::min<int64_t>(rows - part.first_row, kMostRows);
+    if (a.base.kv.cb == 1) {
+      by_dim<__bf16, true>(part, grid, s);
+    } else if (dt == DSPARK_BF16) {
+      by_dim<__bf16, false>(part, grid, s);
+    } else {
+      by_dim<_Float16, false>(part, grid, s);
+    }
+    part.first_row += kMostRows;
+  } while (part.first_row < rows);
+  return hipGetLastError();
+}
+
+}  // namespace dspark

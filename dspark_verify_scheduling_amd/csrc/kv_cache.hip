@@ -10,7 +10,8 @@
 // Status words: workgroup 0 of each launch checks every request by itself and
 // writes the status; the others repeat the checks of what they touch and leave
 // bad requests or rows out.
-#include "kv_dev.h"
+#include "append_row.h"
+#include "kv_moves.h"
 #include "request_search.h"
 
 #include <algorithm>
@@ -85,25 +86,15 @@ __device__ int append_status(const AppendArgs& a, int total_eff) {
   return all;
 }
 
-template <typename T>
-struct Vec8;
-template <>
-struct Vec8<__bf16> { typedef bf16x8 type; };
-template <>
-struct Vec8<_Float16> { typedef f16x8 type; };
-
 // One workgroup per (request, row): LPH lanes per head take the heads of q, k
-// and v in turn. y = x * (mean(x^2) + eps)^(-1/2) * w, then (a, b) -> (a c - b s,
-// b c + a s), in float32; 8-bit rows scale by the power of two of their largest
-// magnitude. Every row is read and written once. 256 requests of up to 9 rows, 32
+// and v in turn (append_row.h). Every row is read and written once. 256 requests of up to 9 rows, 32
 // query heads on 8 of 128, into 8 bits: 13 us (27 MB, 2.1 TB/s; 6 us at a copy's
 // rate): the arithmetic of a row (about 250 instructions a wave and round) and
 // the reads that say where it goes, in one round of workgroups. 128 threads took
 // 15.6 us, 512 14.9. A few rows: 3.4 us, latency.
 template <typename T, bool E8, int D>
 __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
-  typedef typename Vec8<T>::type T8;
-  constexpr int LPH = D / 8, HPP = kThreads / LPH;
+  constexpr int LPH = D / 8;
   const ReqView& q = a.req;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   int total;
@@ -129,24 +120,8 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
   if (!request_rows(q, r, total_eff, &c0, &len) || j >= len) return;
   const int prefix = q.prefix[r];
   const int li = lane & (LPH - 1);  // the lane's eight elements: 8 li ..
-  const int hq = a.num_heads, hkv = a.kv.hkv;
-  const int heads = hq + 2 * hkv;
-  const unsigned char* rows[3] = {a.q + (size_t)(c0 + j) * a.q_ld, a.k + (size_t)(c0 + j) * a.k_ld,
-                                  a.v + (size_t)(c0 + j) * a.v_ld};
-  // of the n-th head of q, k and v in turn; loaded a round ahead, the first with
-  // the reads that say where the row goes
-  auto load = [&](int h) {
-    const int hh = h < hq ? h : (h < hq + hkv ? h - hq : h - hq - hkv);
-    T8 x = {};
-    if (h < heads)
-      x = *reinterpret_cast<const T8*>((h < hq ? rows[0] : h < hq + hkv ? rows[1] : rows[2]) +
-                                       (size_t)(hh * D + 8 * li) * 2);
-    return x;
-  };
-  T8 next = load(tid / LPH);
-  T8 weight[2] = {};
-  if (a.q_weight) weight[0] = *(reinterpret_cast<const T8*>(a.q_weight) + li);
-  if (a.k_weight) weight[1] = *(reinterpret_cast<const T8*>(a.k_weight) + li);
+  // its first heads are loaded with the reads that say where it goes
+  RowAppend<T, E8, D, kThreads> row(a, c0 + j);
   if (prefix < 0 || (int64_t)prefix + len > ((int64_t)q.width << a.kv.page_shift)) return;
   const int64_t slot = (int64_t)prefix + j;
   const int id = q.table[(size_t)r * q.width + (slot >> a.kv.page_shift)];
@@ -190,86 +165,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
     }
   }
   const int off = (int)(slot & ((1 << a.kv.page_shift) - 1));
-  for (int h0 = 0; h0 < heads; h0 += HPP) {
-    const int h = h0 + tid / LPH;
-    const bool live = h < heads;
-    const int kind = h < hq ? 0 : (h < hq + hkv ? 1 : 2);
-    const int hh = kind == 0 ? h : (kind == 1 ? h - hq : h - hq - hkv);
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = (float)next[e];
-    next = load(h + HPP);
-    if (a.q_weight || a.k_weight) {
-      float ss = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(x[e], x[e], ss);
-      for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor(ss, o, kWave);
-      if (kind == 0 ? a.q_weight != nullptr : kind == 1 && a.k_weight) {
-        const float rstd = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-        const T8 ww = kind == 0 ? weight[0] : weight[1];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * rstd * (float)ww[e];
-      }
-    }
-    if (a.rope) {
-      float y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        // the pair's other element: a neighbour, or the same place of another lane
-        y[e] = a.rope_interleaved ? x[e ^ 1] : __shfl(x[e], swap, kWave);
-      }
-      if (turned && kind < 2) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = __builtin_fmaf(x[e], co[e], y[e] * si[e]);
-      }
-    }
-    int e8 = 0;
-    float inv = 1.0f;
-    if (E8 && __any(live && kind != 0)) {
-      float amax = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));  // NaN apart
-      if (__any(!finite_f32(amax))) {
-        amax = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) amax = finite_f32(x[e]) ? fmaxf(amax, fabsf(x[e])) : amax;
-      }
-      for (int o = LPH / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o, kWave));
-      e8 = e4m3_exponent(amax);
-      inv = pow2f(-e8);
-    }
-    if (!live) continue;
-    if (kind == 0 || !E8) {
-      T8 o;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = (T)x[e];
-      unsigned char* dst;
-      if (kind == 0) {
-        dst = a.q_out + (size_t)(c0 + j) * a.q_out_ld + (size_t)(hh * D + 8 * li) * 2;
-      } else {
-        dst = (kind == 1 ? a.kv.k : a.kv.v) + (size_t)id * a.kv.page_bytes +
-              ((((size_t)hh << a.kv.page_shift) + off) * D + 8 * li) * 2;
-      }
-      *reinterpret_cast<T8*>(dst) = o;
-    } else {
-      kv_u32x2 c;
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        int wd = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_operand(x[4 * g], inv),
-                                                 e4m3_operand(x[4 * g + 1], inv), 0, false);
-        wd = __builtin_amdgcn_cvt_pk_fp8_f32(e4m3_operand(x[4 * g + 2], inv),
-                                             e4m3_operand(x[4 * g + 3], inv), wd, true);
-        c[g] = (unsigned)wd;
-      }
-      const size_t row = ((size_t)hh << a.kv.page_shift) + off;
-      *reinterpret_cast<kv_u32x2*>((kind == 1 ? a.kv.k : a.kv.v) + (size_t)id * a.kv.page_bytes +
-                                   row * D + 8 * li) = c;
-      if (li == 0) {
-        (kind == 1 ? a.kv.ks : a.kv.vs)[(size_t)id * a.kv.scale_page_bytes + row] =
-            (uint8_t)(e8 + 127);
-      }
-    }
-  }
+  row.finish(id, off, co, si, turned, swap);
 }
 
 // ------------------------------------------------------------------ read
@@ -468,122 +364,6 @@ __global__ __launch_bounds__(kReadThreads) void read_kernel(ReadArgs a) {
 
 // ------------------------------------------------------------------ commit
 
-// The moves of N requests, L lanes to each: lane l of them has k = l + 1. `r`:
-// the request of the lane's group, -1 for none. bits: its status; *src, *dst the
-// lane's cache indices, *src = -1 where it moves nothing. N requests cost three
-// memory latencies together.
-template <int L, int N>
-__device__ inline void path_moves(const CommitArgs& a, const int (&r)[N], int lane, int (&bits)[N],
-                                  int64_t (&src)[N], int64_t (&dst)[N]) {
-  const ReqView& q = a.req;
-  const int l = lane & (L - 1);
-  const unsigned long long group = (L == 64 ? ~0ull : (1ull << (L & 63)) - 1) << (lane - l);
-  const int64_t reach = (int64_t)q.width << a.kv.page_shift;
-  int c[N], prefix[N], root[N];
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    c[n] = prefix[n] = root[n] = 0;
-    if (r[n] >= 0) {
-      c[n] = a.num_correct[r[n]];
-      prefix[n] = q.prefix[r[n]];
-      root[n] = a.path[(size_t)r[n] * (q.gamma + 1)];
-    }
-  }
-  int here[N], before[N];
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    bits[n] = c[n] < 0 || c[n] > q.gamma || prefix[n] < 0 ? DSPARK_DATA_BAD_LENS : 0;
-    here[n] = before[n] = 0;
-    if (!bits[n] && l < c[n]) {
-      here[n] = a.path[(size_t)r[n] * (q.gamma + 1) + l + 1];
-      before[n] = a.path[(size_t)r[n] * (q.gamma + 1) + l];
-    }
-  }
-  int s[N], d[N];
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    src[n] = dst[n] = -1;
-    const bool on = !bits[n] && l < c[n];
-    const bool ok = root[n] == 0 && (!on || (here[n] > before[n] && here[n] <= q.gamma));
-    if ((__ballot(!ok) & group) && !bits[n]) bits[n] = DSPARK_DATA_BAD_TREE;
-    if (!bits[n] && on && here[n] != l + 1) {
-      src[n] = (int64_t)prefix[n] + here[n];
-      dst[n] = (int64_t)prefix[n] + l + 1;
-    }
-    s[n] = d[n] = 0;
-    if (src[n] >= reach) {
-      s[n] = -1;
-    } else if (src[n] >= 0) {
-      s[n] = q.table[(size_t)r[n] * q.width + (src[n] >> a.kv.page_shift)];
-      d[n] = q.table[(size_t)r[n] * q.width + (dst[n] >> a.kv.page_shift)];
-    }
-  }
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const bool good = s[n] >= 0 && s[n] < a.kv.num_blocks && d[n] >= 0 && d[n] < a.kv.num_blocks;
-    if (__ballot(!good) & group) {
-      src[n] = -1;
-      bits[n] = DSPARK_DATA_BAD_PAGE;
-    }
-  }
-}
-
-// Status and number of moves of all requests; one workgroup.
-template <int L>
-__device__ void commit_status(const CommitArgs& a) {
-  constexpr int N = 8, kGroups = kThreads / L;
-  const int tid = threadIdx.x, lane = tid & (kWave - 1);
-  __shared__ int all, moved;
-  if (tid == 0) all = moved = 0;
-  __syncthreads();
-  int seen = 0, count = 0;
-  for (int r0 = 0; r0 < a.req.B; r0 += N * kGroups) {
-    int r[N], bits[N];
-    int64_t src[N], dst[N];
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int x = r0 + n * kGroups + tid / L;
-      r[n] = x < a.req.B ? x : -1;
-    }
-    path_moves<L, N>(a, r, lane, bits, src, dst);
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      seen |= bits[n];
-      count += src[n] >= 0;
-    }
-  }
-  if (seen) atomicOr(&all, seen);
-  if (count) atomicAdd(&moved, count);
-  __syncthreads();
-  if (tid == 0) {
-    a.meta[0] = moved;
-    a.meta[1] = all;
-  }
-}
-
-// The n moves of one column of T: up to kMoveBatch loads ahead of their stores.
-template <typename T>
-__device__ inline void move_column(unsigned char* base, int64_t page_bytes, int64_t row_bytes, int n,
-                                   const int* s_id, const int* s_off, const int* d_id,
-                                   const int* d_off) {
-  constexpr int kMoveBatch = 8;
-  for (int k0 = 0; k0 < n; k0 += kMoveBatch) {
-    T x[kMoveBatch];
-#pragma unroll
-    for (int i = 0; i < kMoveBatch; ++i) {
-      x[i] = (T){};
-      if (k0 + i < n)
-        x[i] = *reinterpret_cast<const T*>(base + s_id[k0 + i] * page_bytes +
-                                           s_off[k0 + i] * row_bytes);
-    }
-#pragma unroll
-    for (int i = 0; i < kMoveBatch; ++i) {
-      if (k0 + i < n)
-        *reinterpret_cast<T*>(base + d_id[k0 + i] * page_bytes + d_off[k0 + i] * row_bytes) = x[i];
-    }
-  }
-}
-
 // `parts` workgroups per (request, `per` layers), part blockIdx.y % parts; a thread
 // owns 16-byte columns of them (one place of one head of a layer's keys or values) or bytes
 // of exponents, and moves the path's rows of that column in ascending order.
@@ -592,7 +372,7 @@ __device__ inline void move_column(unsigned char* base, int64_t page_bytes, int6
 // stores to, k .. k + kMoveBatch - 1, lie below every later source. Bound by HBM:
 // 178 MB read and written of 256 requests, 32 layers of 8 heads of 128 in 8 bits,
 // in 34 us, 5.2 TB/s. A few requests and layers: 4 us.
-__global__ __launch_bounds__(kThreads) void commit_kernel(CommitArgs a, int per, int parts) {
+__global__ __launch_bounds__(kCommitThreads) void commit_kernel(CommitArgs a, int per, int parts) {
   const ReqView& q = a.req;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   if (blockIdx.x == 0) {
@@ -629,10 +409,10 @@ __global__ __launch_bounds__(kThreads) void commit_kernel(CommitArgs a, int per,
   const int row_bytes = a.kv.dim * a.kv.cb, row_vecs = row_bytes / 16;
   const int rows = 2 * a.kv.hkv;  // of a layer: keys' heads, then values' heads
   const int cols = rows * row_vecs;
-  const int group = blockIdx.y / parts, first = (blockIdx.y - group * parts) * kThreads + tid;
+  const int group = blockIdx.y / parts, first = (blockIdx.y - group * parts) * kCommitThreads + tid;
   const int layer0 = group * per;
   const int layers = min(per, a.kv.num_layers - layer0);
-  for (int i = first; i < layers * cols; i += parts * kThreads) {
+  for (int i = first; i < layers * cols; i += parts * kCommitThreads) {
     const int layer = i / cols, col = i - layer * cols;
     const int row = col / row_vecs, w = row >= a.kv.hkv, h = row - w * a.kv.hkv;
     move_column<kv_u32x4>((w ? a.kv.v : a.kv.k) + (layer0 + layer) * a.kv.layer_bytes +
@@ -641,7 +421,7 @@ __global__ __launch_bounds__(kThreads) void commit_kernel(CommitArgs a, int per,
                           a.kv.page_bytes, row_bytes, n, s_id, s_off, d_id, d_off);
   }
   if (a.kv.ks) {
-    for (int i = first; i < layers * rows; i += parts * kThreads) {
+    for (int i = first; i < layers * rows; i += parts * kCommitThreads) {
       const int layer = i / rows, row = i - layer * rows;
       const int w = row >= a.kv.hkv, h = row - w * a.kv.hkv;
       move_column<unsigned char>((w ? a.kv.vs : a.kv.ks) +
@@ -729,9 +509,9 @@ hipError_t launch_commit(const CommitArgs& a, hipStream_t s) {
   const int cols = per * 2 * a.kv.hkv * (a.kv.dim * a.kv.cb / 16);
   const int64_t wgs = std::max<int64_t>(1, (int64_t)a.req.B * groups);
   const int parts = (int)std::max<int64_t>(
-      1, std::min<int64_t>((cols + kThreads - 1) / kThreads, kEnough / wgs));
+      1, std::min<int64_t>((cols + kCommitThreads - 1) / kCommitThreads, kEnough / wgs));
   hipLaunchKernelGGL(commit_kernel, dim3(1u + (unsigned)a.req.B, (unsigned)(groups * parts)),
-                     dim3(kThreads), 0, s, a, per, parts);
+                     dim3(kCommitThreads), 0, s, a, per, parts);
   return hipGetLastError();
 }
 

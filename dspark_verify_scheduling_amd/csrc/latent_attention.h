@@ -1,0 +1,928 @@
+// Attention of packed verify rows (a chain or tree of drafts per request) over the
+// latents of a paged cache: the split kernel's templates, one translation unit per
+// latent size, and the schedule it shares with the joining kernel.
+#pragma once
+
+#include "latent.h"
+#include "lds_dev.h"
+
+namespace dspark {
+namespace lattn {
+
+using attn::barrier;
+using attn::copy16_shared;
+using attn::copy4;
+using attn::f32x16;
+using attn::kLn2;
+using attn::kLog2e;
+using attn::lds_columns;
+using attn::lds_read;
+using attn::lds_u8;
+using attn::lds_write;
+using attn::settle;
+using attn::Types;
+using attn::uniform;
+using attn::wait_copies;
+
+// Row tiles of a workgroup: what its registers hold. A wave keeps the queries of
+// one tile (2.25 KB a row of 512 and 64) and the outputs of all of them for its
+// share of the columns.
+constexpr int row_tiles(int dim) { return dim == 512 ? 2 : 4; }
+constexpr int waves(int dim) { return 2 * row_tiles(dim); }
+constexpr int kRowTile = 32;
+constexpr int kKeys = 64;  // keys of a unit
+
+// What the split kernel leaves for the joining kernel: the schedule's prefix
+// sums, and per partial segment the running maximum (less Types::kAbove) and sum
+// of each of its rows and their unnormalised outputs. Workgroup w has segments 2 w
+// (the one its range starts with) and 2 w + 1 (a later one that its range ends in).
+struct Parts {
+  int64_t* base;  // [B + 1] first unit of each request, then the total
+  float* m;       // [2 * wgs][rows]
+  float* l;
+  float* o;       // [2 * wgs][rows][L]
+  int wgs;        // workgroups of the split kernel
+  int rows;       // rows of a segment, at most
+};
+
+// Rows of a request: m = j * heads + h for row j and head h, in tiles of kRowTile,
+// up to row_tiles(L) tiles to a segment.
+struct Shape {
+  int len, prefix, c0;
+  int mrows, mtiles;
+  int nseg, per;  // segments side by side, tiles of each
+  int keys;
+  int nku;        // units along the keys
+};
+
+// Whether a request's rows are well formed (its tree and pages apart); their
+// place and its prefix.
+__device__ inline bool rows_of(const ReqView& q, int page_shift, int r, int total_eff, int* c0,
+                               int* len, int* prefix) {
+  const bool ok = request_rows(q, r, total_eff, c0, len);
+  *prefix = q.prefix[r];
+  const int64_t keys = (int64_t)*prefix + *len;
+  // (cache indices in 32 bits, a unit beyond included)
+  return ok && *prefix >= 0 && keys <= ((int64_t)q.width << page_shift) && keys <= 0x7FFFFF00LL;
+}
+
+template <int L>
+__device__ inline Shape shape_of(int heads, int c0, int len, int prefix) {
+  Shape s;
+  s.c0 = c0;
+  s.len = len;
+  s.prefix = prefix;
+  s.keys = prefix + len;
+  s.mrows = heads * len;
+  s.mtiles = (s.mrows + kRowTile - 1) / kRowTile;
+  s.nseg = (s.mtiles + row_tiles(L) - 1) / row_tiles(L);
+  s.per = (s.mtiles + s.nseg - 1) / s.nseg;
+  s.nku = (s.keys + kKeys - 1) / kKeys;
+  return s;
+}
+
+template <int L>
+__device__ inline int64_t units_of(int heads, int c0, int len, int prefix) {
+  const Shape s = shape_of<L>(heads, c0, len, prefix);
+  return (int64_t)s.nseg * s.nku;
+}
+
+// Workgroups that get units: a share is kLeast of them or more, since every part
+// of a segment costs its rows' outputs twice through memory.
+constexpr int kLeast = 2;
+__device__ inline int wgs_in_use(int64_t total, int wgs) {
+  return (int)min((int64_t)wgs, (total + kLeast - 1) / kLeast);
+}
+
+// Workgroups go to the eight XCDs in turn. Shares are numbered so that an XCD's
+// are consecutive: the segments of a request then meet in one L2.
+constexpr int kXcds = 8;
+__device__ inline int share_of(int wg, int wgs) {
+  return wgs % kXcds ? wg : wg % kXcds * (wgs / kXcds) + wg / kXcds;
+}
+
+// The first unit of share w of n <= total.
+__device__ inline int64_t wg_start(int64_t total, int w, int n) { return total * w / n; }
+
+// LDS of a workgroup. A tile is kKeys latents in 16 bits and their rotated parts,
+// unpadded; 16-byte chunk c of latent row r lies at chunk c ^ swizzle(r), so that
+// the rows which a wave reads at one column, and the eight rows whose columns it
+// reads transposed, spread over all banks.
+//   16-bit caches: a ring of kStages tiles, filled straight from memory.
+//   8-bit caches: a ring of codes, exponents and rotated parts; each wave widens
+//   its rows of the next tile's latents into one tile.
+template <bool E8, int L>
+struct Ring {
+  static constexpr int CB = E8 ? 1 : 2;
+  static constexpr int W = waves(L);
+  static constexpr int kOwn = kKeys / W;  // keys of a tile that a wave copies
+  static constexpr int kMaxRows = row_tiles(L) * kRowTile;
+  static constexpr int kRow = 2 * L;
+  static constexpr int kLat = kKeys * kRow;
+  static constexpr int kTurned = kKeys * kRope * 2;
+  static constexpr int kChunks = L * CB / 16;  // of a cache row
+  static constexpr int kRowsPerCopy = kWave / kChunks;
+  static constexpr int kCopies = kOwn / kRowsPerCopy;
+  static constexpr int kTurnedCopies = kOwn / 8;
+  static_assert(kCopies * kRowsPerCopy == kOwn && kOwn <= 16, "whole copies of one page");
+  static constexpr int kPerWave = kCopies + kTurnedCopies + (E8 ? 1 : 0);
+  static constexpr int kPiece = kOwn * L + 64;  // codes, exponents; 8 bits
+  static constexpr int kTurnedAt = E8 ? W * kPiece : kLat;  // in a stage
+  static constexpr int kStage = kTurnedAt + kTurned;
+  static constexpr int kStages = L == 512 ? 2 : 3;
+  static constexpr int kRing = E8 ? kLat : 0;  // offset of the ring
+  // weights in 16 bits: [row][kKeys], 16-byte chunks c of row r at c ^ (r >> 1 & 7)
+  static constexpr int kWeights = kRing + kStages * kStage;
+  // of the waves' rows: largest score, or sum, of each half of the keys
+  static constexpr int kHalves = kWeights + kMaxRows * kKeys * 2;
+  static constexpr int kFix = kHalves + 2 * kMaxRows * 4;  // and what their outputs shrink by
+  static constexpr int kFlag = kFix + kMaxRows * 4;        // some maximum moves; of two tiles
+  // rows with NaN or infinity, kOwn bits for each wave
+  static constexpr int kOdd = kFlag + 8;
+  static constexpr int kReqs = kOdd + 8;  // rows of up to kWave requests, 3 words each
+  static constexpr int kBytes = kReqs + 12 * kWave;
+  static_assert(kBytes <= 163840 - 256, "a CU's LDS");
+  static __device__ int swizzle(int row) { return (row & 7) << 1 | ((row >> 3) & 1); }
+  static __device__ int turned_swizzle(int row) { return (row >> 1) & 7; }
+};
+
+// One segment: the queries of several row tiles of one request over some units of
+// its keys. What the copies need of it,
+struct Span {
+  int r;
+  int first;  // its first key
+  int n;      // units; 0: there is no such segment
+  int keys;   // of the request
+};
+// and the rest.
+struct Job {
+  Shape s;
+  int tile0, mt;
+  int slot;    // its place among the parts
+  bool whole;  // it covers all the request's keys
+};
+
+// Where a wave is in its workgroup's share of the units.
+struct Cursor {
+  int64_t left;  // units of the share still to come
+  int64_t off;   // next unit within request r
+  int r;
+  int share;
+  int begun;     // 0 before the share's first segment
+};
+
+// The next segment of a share. `reqs`: the requests' rows in LDS where a wave's
+// lanes hold the batch (len 0: malformed); otherwise they are read from memory.
+template <int L>
+__device__ __forceinline__ Span next_span(const LatentAttnArgs& a, unsigned reqs, Cursor& c,
+                                          Job* job) {
+  Span j;
+  j.n = 0;
+  while (c.left > 0) {
+    int c0 = 0, len = 0, prefix = 0;
+    if (a.req.B <= kWave) {
+      const unsigned at = reqs + 12 * c.r;
+      c0 = lds_read<int>(at);
+      len = lds_read<int>(at + 4);
+      prefix = lds_read<int>(at + 8);
+    } else {
+      int total;
+      const int total_eff = rows_in_use(a.req, &total);
+      if (!rows_of(a.req, a.kv.page_shift, c.r, total_eff, &c0, &len, &prefix)) len = 0;
+    }
+    c0 = __builtin_amdgcn_readfirstlane(c0);
+    len = __builtin_amdgcn_readfirstlane(len);
+    prefix = __builtin_amdgcn_readfirstlane(prefix);
+    const Shape s = shape_of<L>(a.num_heads, c0, len, prefix);
+    if (c.off >= (len ? (int64_t)s.nseg * s.nku : 0)) {
+      ++c.r;
+      c.off = 0;
+      continue;
+    }
+    const int seg = __builtin_amdgcn_readfirstlane((int)(c.off / s.nku));
+    const int ku0 = (int)(c.off - (int64_t)seg * s.nku);
+    j.r = c.r;
+    j.n = (int)min((int64_t)(s.nku - ku0), c.left);
+    j.first = ku0 * kKeys;
+    j.keys = s.keys;
+    if (job) {
+      job->s = s;
+      job->tile0 = seg * s.per;
+      job->mt = min(s.per, s.mtiles - job->tile0);
+      job->whole = j.n == s.nku;
+      job->slot = 2 * c.share + c.begun;
+    }
+    c.begun = 1;
+    c.off += j.n;
+    c.left -= j.n;
+    break;
+  }
+  return j;
+}
+
+// The producing side of the ring: this wave's copies of the next tile.
+template <bool E8, int L>
+struct Feeder {
+  typedef Ring<E8, L> R;
+  typedef unsigned long long u64;
+  Cursor c;
+  Span j, nj;      // the segment copied from, and the one after it
+  int t;           // its tile in lane 0 of `ids`
+  int idx, end;    // next lane, lanes that hold a tile: 0 when nothing is left
+  int ids, nids;   // pages of the wave's rows: of j from tile t on, of nj from its first
+  u64 bad, nbad;   // bit l: some page of lane l's tile is none
+  int stage;
+  unsigned none;   // bit per stage: some page of its tile is none
+
+  // The pages of 64 tiles from tile t on, a tile to a lane.
+  static __device__ int fetch(const LatentAttnArgs& a, const Span& x, int t, int wave, u64* bad) {
+    int own = 0;
+    const int64_t first = (int64_t)x.first + (int64_t)(t + lane_id()) * kKeys;
+    int id[kKeys / 16];
+#pragma unroll
+    for (int g = 0; g < kKeys / 16; ++g)
+      id[g] = a.req.table[(size_t)x.r * a.req.width +
+                          ((int)min(first + g * 16, (int64_t)x.keys - 1) >> a.kv.page_shift)];
+    u64 b = 0;
+#pragma unroll
+    for (int g = 0; g < kKeys / 16; ++g) {
+      const bool none = id[g] < 0 || id[g] >= a.kv.num_blocks;
+      b |= __ballot(none);
+      // a page that is none: any valid one, its keys are masked
+      if (g == wave * R::kOwn / 16) own = none ? 0 : id[g];
+    }
+    *bad = b;
+    settle(own);
+    return own;
+  }
+
+  __device__ void start(const LatentAttnArgs& a, unsigned lds, const Cursor& from, int wave) {
+    c = from;
+    j = next_span<L>(a, lds + R::kReqs, c, nullptr);
+    ids = fetch(a, j, 0, wave, &bad);
+    nj = next_span<L>(a, lds + R::kReqs, c, nullptr);
+    nids = 0;
+    nbad = 0;
+    if (nj.n > 0) nids = fetch(a, nj, 0, wave, &nbad);
+    t = idx = stage = 0;
+    end = min(j.n, kWave);
+    none = 0;
+  }
+
+  // Starts the wave's copies of the next tile.
+  __device__ __forceinline__ void next(const LatentAttnArgs& a, unsigned lds, int wave) {
+    if (end == 0) return;
+    const int lane = lane_id();
+    const int row0 = wave * R::kOwn;
+    const int64_t id = __builtin_amdgcn_readlane(ids, idx);
+    const int key = j.first + (t + idx) * kKeys + row0;
+    const int off = key & ((1 << a.kv.page_shift) - 1);
+    const unsigned at = lds + R::kRing + stage * R::kStage;
+    const unsigned char* from = a.kv.latent + id * a.kv.page_bytes + off * (L * R::CB);
+    const unsigned to = at + (E8 ? wave * R::kPiece : row0 * R::kRow);
+#pragma unroll
+    for (int n = 0; n < R::kCopies; ++n) {
+      const int r = n * R::kRowsPerCopy + lane / R::kChunks;
+      const int chunk = E8 ? lane % R::kChunks : (lane % R::kChunks) ^ R::swizzle(row0 + r);
+      copy16_shared(uniform(from) + n * R::kRowsPerCopy * L * R::CB,
+                    (lane / R::kChunks) * L * R::CB + (unsigned)chunk * 16, to + n * 1024);
+    }
+    if constexpr (E8) {
+      constexpr int kBytes = R::kOwn * (L / kLatGroup);
+      const unsigned char* e =
+          a.kv.scale + id * a.kv.scale_page_bytes + off * (L / kLatGroup);
+      if (lane < kBytes / 4) copy4(uniform(e), lane * 4, to + R::kOwn * L);
+    }
+    const unsigned char* turned = a.kv.rope + id * a.kv.rope_page_bytes + off * (kRope * 2);
+#pragma unroll
+    for (int n = 0; n < R::kTurnedCopies; ++n) {
+      const int r = n * 8 + (lane >> 3);
+      copy16_shared(uniform(turned) + n * 1024,
+                    (lane & ~7) * 16 + (((lane & 7) ^ R::turned_swizzle(row0 + r)) << 4),
+                    at + R::kTurnedAt + row0 * (kRope * 2) + n * 1024);
+    }
+    if (__builtin_expect((bad | none) != 0, 0))
+      none = (none & ~(1u << stage)) | ((unsigned)(bad >> idx) & 1u) << stage;
+    stage = stage + 1 == R::kStages ? 0 : stage + 1;
+    if (__builtin_expect(++idx == end, 0)) {
+      t += end;
+      idx = 0;
+      if (t < j.n) {
+        ids = fetch(a, j, t, wave, &bad);
+      } else {
+        j = nj;
+        ids = nids;
+        bad = nbad;
+        t = 0;
+        if (j.n > 0) {
+          nj = next_span<L>(a, lds + R::kReqs, c, nullptr);
+          if (nj.n > 0) nids = fetch(a, nj, 0, wave, &nbad);
+        }
+      }
+      end = min(j.n - t, kWave);
+    }
+  }
+};
+
+// A segment: `mt` row tiles over some units of the keys, which the waves bring into
+// LDS together. Wave (t, half) = (wave / 2, wave % 2) has row tile t and half the
+// keys of a tile for the scores, and a share of the columns for the outputs:
+//   S^T = K Q^T: keys are its rows and queries its columns, so a lane holds the
+//   scores of one query (lane & 31) for sixteen keys, four in a row each. Its
+//   weights go to LDS as the operand of
+//   O^T = C^T P^T, whose C^T (the same latents) comes transposed out of LDS in that
+//   order of keys. Every wave reads all rows' weights and its columns of the tile.
+// The rows' running maximum is kept by both waves of a row tile. It moves when some
+// score passes it by Types::kSlack: a wave that sees one raises a flag, and then the
+// halves' maxima meet in LDS, the weights are taken again and the outputs shrink.
+template <typename T, bool E8, int L>
+__device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws, const Span& span,
+                                        const Job& job, int mt, Feeder<E8, L>& feed, unsigned lds,
+                                        int left, int& stage, int& tick) {
+  typedef Types<T> TT;
+  typedef typename TT::V8 V8;
+  typedef typename TT::V4 V4;
+  typedef Ring<E8, L> R;
+  constexpr int NL = L / 16, NF = NL + kRope / 16;  // operand chunks of a latent, of a key
+  constexpr int NT = row_tiles(L);
+  constexpr int ND = L / 32 / R::W;                 // 32-column tiles of a wave's outputs
+  constexpr int kOwn = R::kOwn;
+  const Shape& s = job.s;
+  const int lane = lane_id(), qi = lane & 31, hi = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int tile = wave >> 1, half = wave & 1;
+  const int len = s.len, prefix = s.prefix, keys = s.keys;
+  const int m = (job.tile0 + tile) * kRowTile + qi;
+  const int qrow = m / a.num_heads;  // the request's row that the lane's query belongs to
+  const bool live = tile < mt && m < s.mrows;
+
+  // rows of the step's own tree that the lane's query sees, bit l for row l + 1;
+  // row 0 is everybody's. Bit l of anc, in lane l, is row l + 1 itself, with its
+  // ancestors' bits.
+  unsigned long long seen = qrow >= 64 ? ~0ull : (1ull << qrow) - 1;
+  if (a.req.parents && mt > 0) {
+    int up = lane + 1 < len ? a.req.parents[(size_t)span.r * a.req.gamma + lane] : 0;
+    unsigned long long anc = 1ull << lane;
+    for (int i = 0; i < 6; ++i) {
+      const int from = max(up - 1, 0);
+      const unsigned long long more = __shfl(anc, from, kWave);
+      const int next = __shfl(up, from, kWave);
+      if (up > 0) {
+        anc |= more;
+        up = next;
+      }
+    }
+    const unsigned long long path = __shfl(anc, max(qrow - 1, 0) & 63, kWave);
+    seen = qrow > 0 ? path : 0;
+  }
+  // Scores in units of log2 with a positive factor, so that a masked score stays
+  // -infinity under it: the scale's sign and its zero go into the queries.
+  float sl = fminf(fabsf(a.scale) * kLog2e, 3.4028235e38f);
+  const bool flat = sl == 0.0f;
+  if (flat) sl = 1.0f;
+  const unsigned sign = a.scale < 0.0f ? 0x80008000u : 0u;
+  // queries as operands
+  V8 qf[NF];
+  f32x16 o[NT][ND];
+  float mx = -__builtin_inff(), l = 0.0f;
+  {
+    const int head = m - qrow * a.num_heads;
+    const size_t row = (size_t)(s.c0 + qrow);
+    const unsigned char* ql = a.ql + row * a.ql_ld + head * a.ql_head_ld + hi * 16;
+    const unsigned char* qr = a.qr + row * a.qr_ld + head * a.qr_head_ld + hi * 16;
+    kv_u32x4 w[NF];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      w[f] = (kv_u32x4){0, 0, 0, 0};
+      if (live && !flat)
+        w[f] = *reinterpret_cast<const kv_u32x4*>(f < NL ? ql + f * 32 : qr + (f - NL) * 32) ^ sign;
+    }
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      settle(w[f]);
+      qf[f] = __builtin_bit_cast(V8, w[f]);
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[t][d][e] = 0.0f;
+  }
+
+  // lane's offsets in a tile: its chunk of a latent and of a rotated part (of its
+  // wave's half of the keys), its piece of a row that is read for its columns
+  const int key_row = half * 32 + qi;
+  const int lat_at = key_row * R::kRow + ((hi ^ R::swizzle(key_row)) << 4);
+  const int turned_at = key_row * (kRope * 2) + ((hi ^ R::turned_swizzle(key_row)) << 4);
+  const int t4 = lane & 15, vrow = hi * 4 + (t4 >> 2);
+  // (a swizzle changes bits 4 to 7 of an address: what lies above is a sum)
+  const int val_at =
+      vrow * R::kRow +
+      (((((lane >> 4) & 1) * 2 + ((t4 >> 1) & 1) + (wave * ND & 3) * 4) ^ R::swizzle(vrow)) << 4) +
+      (t4 & 1) * 8 + (wave * ND >> 2) * 256;
+  // its chunk of the weights of row lane & 31 of a row tile
+  const unsigned weight_at = lds + R::kWeights + qi * (kKeys * 2) + ((hi ^ ((qi >> 1) & 7)) << 4);
+  // a word of its row in the row statistics
+  const unsigned row_at = (tile * kRowTile + qi) * 4;
+
+  for (int i = 0; i < span.n; ++i, --left) {
+    const int key0 = span.first + i * kKeys;
+    // 16-key groups on a page that is none
+    unsigned missing = 0;
+    if (__builtin_expect((feed.none >> stage) & 1, 0)) {
+#pragma unroll
+      for (int b = 0; b < kKeys / 16; ++b) {
+        const int p = min(key0 + 16 * b, keys - 1) >> a.kv.page_shift;
+        int id = a.req.table[(size_t)span.r * a.req.width + p];
+        settle(id);
+        if (id < 0 || id >= a.kv.num_blocks) missing |= 1u << b;
+      }
+      missing = __builtin_amdgcn_readfirstlane(missing);
+    }
+    // the tile holds keys that some query does not see (the request's own rows
+    // after its root, keys past its last), or such a group
+    const bool edge = key0 + kKeys > prefix + 1 || missing;
+    const unsigned raw = lds + R::kRing + stage * R::kStage;
+    const unsigned turned = raw + R::kTurnedAt;
+    const int row0 = wave * kOwn;  // of the wave's keys
+    // The wave's rows that hold nothing for some query, as bits: keys that do not
+    // exist (anything may be there), and rows with a NaN or infinite element, which
+    // must not meet a zero weight. They become zeros; queries that see one of the
+    // latter get a NaN score below instead. `strange`: rows with such elements.
+    auto hide = [&](unsigned strange) {
+      unsigned there = 0;
+#pragma unroll
+      for (int x = 0; x < kOwn; ++x)
+        if (key0 + row0 + x < keys && !((missing >> ((row0 + x) >> 4)) & 1)) there |= 1u << x;
+      if (lane == 0) {
+        if constexpr (kOwn == 8) {
+          lds_write<unsigned char>(lds + R::kOdd + wave, (unsigned char)(strange & there));
+        } else {
+          lds_write<unsigned short>(lds + R::kOdd + 2 * wave, (unsigned short)(strange & there));
+        }
+      }
+      return strange | (~there & ((1u << kOwn) - 1));
+    };
+    // rows that a ballot over lanes names, `chunks` lanes a row
+    auto rows_in = [&](unsigned long long found, int chunks, int first) {
+      unsigned rows = 0;
+      while (found) {
+        rows |= 1u << (first + (int)__builtin_ctzll(found) / chunks);
+        found &= found - 1;
+      }
+      return rows;
+    };
+    auto strange16 = [&](const kv_u32x4& w) {
+      bool bad = false;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        bad |= (w[x] & TT::kExpMask) == TT::kExpMask ||
+               (w[x] >> 16 & TT::kExpMask) == TT::kExpMask;
+      return bad;
+    };
+    const unsigned own_turned = turned + row0 * (kRope * 2) + lane * 16;
+    auto strange_turned = [&]() {
+      unsigned rows = 0;
+#pragma unroll
+      for (int n = 0; n < R::kTurnedCopies; ++n)
+        rows |= rows_in(__ballot(strange16(lds_read<kv_u32x4>(own_turned + n * 1024))), 8, n * 8);
+      return rows;
+    };
+    auto hide_turned = [&](unsigned hidden) {
+#pragma unroll
+      for (int n = 0; n < R::kTurnedCopies; ++n)
+        if ((hidden >> (n * 8 + (lane >> 3))) & 1)
+          lds_write(own_turned + n * 1024, (kv_u32x4){0, 0, 0, 0});
+    };
+    // this tile's copies are done when those of the stages after it may not be
+    if (R::kStages > 2 && left > R::kStages - 2) {
+      wait_copies<(R::kStages - 2) * R::kPerWave>();
+    } else {
+      wait_copies<0>();
+    }
+    unsigned buf;
+    if constexpr (E8) {
+      buf = lds;
+      const unsigned from = raw + wave * R::kPiece;
+      unsigned hidden = 0;
+      if (edge) {
+        unsigned strange = strange_turned();
+#pragma unroll
+        for (int n = 0; n < R::kCopies; ++n) {
+          const int r = n * R::kRowsPerCopy + lane / R::kChunks, c = lane % R::kChunks;
+          const kv_u32x4 w = lds_read<kv_u32x4>(from + n * 1024 + lane * 16);
+          // (no row that append writes has an exponent byte above 246; a code may
+          // pass every finite number under it)
+          bool bad = lds_read<unsigned char>(from + kOwn * L + r * (L / kLatGroup) +
+                                             c / (kLatGroup / 16)) > 246;
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int y = 0; y < 32; y += 8) bad |= ((w[x] >> y) & 0x7Fu) == 0x7Fu;
+          strange |= rows_in(__ballot(bad), R::kChunks, n * R::kRowsPerCopy);
+        }
+        hidden = strange;
+        hidden = hide(strange);
+        hide_turned(hidden);
+      }
+      // everybody is done with the tile before
+      barrier();
+#pragma unroll
+      for (int n = 0; n < R::kCopies; ++n) {
+        const int r = n * R::kRowsPerCopy + lane / R::kChunks, c = lane % R::kChunks;
+        const kv_u32x4 w = lds_read<kv_u32x4>(from + n * 1024 + lane * 16);
+        const unsigned ex = lds_read<unsigned char>(from + kOwn * L + r * (L / kLatGroup) +
+                                                    c / (kLatGroup / 16));
+        const bool gone = (hidden >> r) & 1;
+        const float e = __builtin_bit_cast(float, (gone ? 127u : ex) << 23);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          kv_u32x4 z;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const unsigned v = gone ? 0u : w[2 * x + y];
+            z[2 * y] = __builtin_bit_cast(
+                unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, e, false));
+            z[2 * y + 1] = __builtin_bit_cast(
+                unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, e, true));
+          }
+          lds_write(buf + (row0 + r) * R::kRow + (((2 * c + x) ^ R::swizzle(row0 + r)) << 4), z);
+        }
+      }
+    } else {
+      buf = raw;
+      if (edge) {
+        const unsigned own = buf + row0 * R::kRow + lane * 16;
+        unsigned strange = strange_turned();
+#pragma unroll
+        for (int n = 0; n < R::kCopies; ++n)
+          strange |= rows_in(__ballot(strange16(lds_read<kv_u32x4>(own + n * 1024))), R::kChunks,
+                             n * R::kRowsPerCopy);
+        const unsigned hidden = hide(strange);
+        hide_turned(hidden);
+#pragma unroll
+        for (int n = 0; n < R::kCopies; ++n)
+          if ((hidden >> (n * R::kRowsPerCopy + lane / R::kChunks)) & 1)
+            lds_write(own + n * 1024, (kv_u32x4){0, 0, 0, 0});
+      }
+    }
+    barrier();
+    feed.next(a, lds, wave);
+    stage = stage + 1 == R::kStages ? 0 : stage + 1;
+    const unsigned flag = lds + R::kFlag + tick * 4, other_flag = lds + R::kFlag + (tick ^ 1) * 4;
+    tick ^= 1;
+    if (mt == 0) {
+      barrier();  // (the tile may go)
+      continue;
+    }
+    if (wave == 0 && lane == 0) lds_write<unsigned>(other_flag, 0u);
+
+    // Scores. Reads from LDS go out a batch ahead of the products that use them.
+    f32x16 sc;
+    float top = -__builtin_inff();
+    V8 pf[2];
+    // The product takes weights of the query type, each off by up to half its step;
+    // their sum takes them as they are.
+    auto weigh = [&](float* sum) {
+      const float ref = mx == -__builtin_inff() ? 0.0f : mx;
+      *sum = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float p = __builtin_amdgcn_exp2f(sc[e] * sl - ref);
+        *sum += p;
+        pf[e >> 3][e & 7] = (T)p;
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        lds_write((weight_at ^ ((half * 2 + c) << 5)) + tile * (kRowTile * kKeys * 2), pf[c]);
+    };
+    float sum = 0.0f;
+    if (tile < mt) {
+      f32x16 s2;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sc[e] = s2[e] = 0.0f;
+      constexpr int FB = 4;
+      static_assert(NF % FB == 0, "whole batches");
+      V8 kf[2][FB];
+      unsigned ka[8], ta = turned + turned_at;
+      {
+        unsigned at = buf + lat_at;
+        settle(at);
+#pragma unroll
+        for (int f = 0; f < 8; ++f) ka[f] = at ^ (f << 5);
+        settle(ta);
+      }
+      auto read_keys = [&](int f0, V8 (&k)[FB]) {
+#pragma unroll
+        for (int f = 0; f < FB; ++f)
+          k[f] = f0 + f < NL ? lds_read<V8>(ka[(f0 + f) & 7] + ((f0 + f) >> 3) * 256)
+                             : lds_read<V8>(ta ^ ((f0 + f - NL) << 5));
+      };
+      read_keys(0, kf[0]);
+#pragma unroll
+      for (int f0 = 0; f0 < NF; f0 += FB) {
+        if (f0 + FB < NF) read_keys(f0 + FB, kf[(f0 / FB + 1) & 1]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int f = 0; f < FB; f += 2) {
+          sc = TT::mfma32(kf[(f0 / FB) & 1][f], qf[f0 + f], sc);
+          s2 = TT::mfma32(kf[(f0 / FB) & 1][f + 1], qf[f0 + f + 1], s2);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sc[e] += s2[e];
+      if (edge) {
+        const unsigned odd = lds_read<unsigned>(lds + R::kOdd + half * 4);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int k = 8 * (e >> 2) + 4 * hi + (e & 3);
+          const int rel = key0 + half * 32 + k - prefix;
+          const bool own = rel < len && ((seen >> ((rel - 1) & 63)) & 1);
+          if (((missing >> (half * 2 + (e >> 3))) & 1) || (rel > 0 && !own)) {
+            sc[e] = -__builtin_inff();
+          } else if ((odd >> k) & 1) {
+            sc[e] = __builtin_nanf("");
+          }
+        }
+      }
+      // Weights. The product with the scale rounds before the maximum is taken off,
+      // so that the largest weight is 1 whatever the size of its score.
+      top = sc[0];
+#pragma unroll
+      for (int e = 1; e < 16; ++e) top = fmaxf(top, sc[e]);
+      top *= sl;
+      if (__any(top - mx > TT::kAbove + TT::kSlack)) {
+        if (lane == 0) lds_write<unsigned>(flag, 1u);
+      } else {
+        weigh(&sum);
+      }
+    }
+    // columns of the tile: of 16 keys, the wave's share
+    V4 vl[2][ND], vh[2][ND];
+    V8 pw[2][NT];
+    unsigned va[ND], wa = weight_at;
+    {
+      unsigned at = buf + val_at;
+      settle(at);
+#pragma unroll
+      for (int d = 0; d < ND; ++d) va[d] = at ^ (d << 6);
+      settle(wa);
+    }
+    auto read_values = [&](int c, int into) {
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        vl[into][d] = lds_columns<V4>(va[d] + c * 16 * R::kRow);
+        vh[into][d] = lds_columns<V4>((va[d] ^ 16) + (c * 16 + 8) * R::kRow);
+      }
+    };
+    auto read_weights = [&](int c, int into) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        pw[into][t] = lds_read<V8>((wa ^ (c << 5)) + t * (kRowTile * kKeys * 2));
+    };
+    read_values(0, 0);
+    barrier();
+    if (__builtin_expect(lds_read<unsigned>(flag) != 0, 0)) {
+      top = fmaxf(top, __shfl_xor(top, 32, kWave));
+      if (hi == 0 && tile < mt)
+        lds_write<float>(lds + R::kHalves + half * (R::kMaxRows * 4) + row_at, top);
+      barrier();
+      if (tile < mt) {
+        float next = fmaxf(top, lds_read<float>(lds + R::kHalves + (half ^ 1) * (R::kMaxRows * 4) +
+                                                row_at));
+        if (next - mx > TT::kAbove + TT::kSlack) {
+          if constexpr (TT::kAbove > 0.0f) {
+            // (not where kAbove rounds up to more than a weight may be)
+            const float less = next - TT::kAbove;
+            next = next - less > TT::kAbove + TT::kSlack ? next : less;
+          }
+          next = fmaxf(mx, next);
+        } else {
+          next = mx;
+        }
+        const float fix = next == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(mx - next);
+        mx = next;
+        l *= fix;
+        if (hi == 0 && half == 0) lds_write<float>(lds + R::kFix + row_at, fix);
+        weigh(&sum);
+      }
+      barrier();
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        if (t < mt) {
+          const float fix = lds_read<float>(lds + R::kFix + (t * kRowTile + qi) * 4);
+#pragma unroll
+          for (int d = 0; d < ND; ++d) o[t][d] *= fix;
+        }
+    }
+    l += sum;
+    // O^T += C^T P^T
+    read_weights(0, 0);
+#pragma unroll
+    for (int c = 0; c < kKeys / 16; ++c) {
+      if (c + 1 < kKeys / 16) {
+        read_values(c + 1, (c + 1) & 1);
+        read_weights(c + 1, (c + 1) & 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        if (t < mt) {
+#pragma unroll
+          for (int d = 0; d < ND; ++d) {
+            const V8 vf = __builtin_shufflevector(vl[c & 1][d], vh[c & 1][d], 0, 1, 2, 3, 4, 5, 6, 7);
+            o[t][d] = TT::mfma32(vf, pw[c & 1][t], o[t][d]);
+          }
+        }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // (the next tile's first barrier comes before anything here is overwritten:
+    // the weights, the statistics and, in 8 bits, the tile)
+  }
+
+  if (mt == 0) return;
+  // the halves' sums meet
+  l += __shfl_xor(l, 32, kWave);
+  barrier();
+  if (hi == 0 && tile < mt) lds_write<float>(lds + R::kHalves + half * (R::kMaxRows * 4) + row_at, l);
+  barrier();
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int mm = (job.tile0 + t) * kRowTile + qi;
+    if (t >= mt || mm >= s.mrows) continue;
+    const unsigned at = lds + R::kHalves + (t * kRowTile + qi) * 4;
+    const float sum = lds_read<float>(at) + lds_read<float>(at + R::kMaxRows * 4);
+    const int row = mm / a.num_heads, head = mm - row * a.num_heads;
+    if (job.whole) {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      T* dst = reinterpret_cast<T*>(a.out + (size_t)(s.c0 + row) * a.out_ld) + head * L +
+               wave * (ND * 32) + hi * 4;
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          V4 z;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[e] = (T)(o[t][d][4 * x + e] * inv);
+          *reinterpret_cast<V4*>(dst + d * 32 + x * 8) = z;
+        }
+      if (a.lse && hi == 0 && wave == 2 * t)
+        a.lse[(size_t)(s.c0 + row) * a.num_heads + head] =
+            sum == 0.0f ? -__builtin_inff() : (mx + __builtin_amdgcn_logf(sum)) * kLn2;
+    } else {
+      const size_t part = (size_t)job.slot * ws.rows + t * kRowTile + qi;
+      float* dst = ws.o + part * L + wave * (ND * 32) + hi * 4;
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          *reinterpret_cast<f32x4*>(dst + d * 32 + x * 8) =
+              (f32x4){o[t][d][4 * x], o[t][d][4 * x + 1], o[t][d][4 * x + 2], o[t][d][4 * x + 3]};
+      if (hi == 0 && wave == 2 * t) {
+        ws.m[part] = mx;
+        ws.l[part] = sum;
+      }
+    }
+  }
+}
+
+// out = sum_k e^(s_k - m) c_k / sum_k e^(s_k - m) in one pass over the cached rows,
+// which are keys and values at once: running maximum m, sum and outputs in float32
+// registers, m moved only when a score passes it by Types::kSlack. Parts of a row
+// join by (m, sum, outputs) in join_kernel.
+//
+// Persistent over the units of all (request, row segment)s in order: workgroup w
+// takes the w-th equal share, so ragged contexts balance by themselves and a long
+// one is split over many workgroups. The ring of tiles runs on across segments.
+template <typename T, bool E8, int L>
+__global__ __launch_bounds__(waves(L) * kWave, waves(L) / 4) void split_kernel(LatentAttnArgs a,
+                                                                               Parts ws) {
+  constexpr int kThreads = waves(L) * kWave;
+  typedef Ring<E8, L> R;
+  __shared__ __align__(1024) unsigned char lds_mem[R::kBytes];
+  __shared__ int64_t wsum[waves(L)];
+  __shared__ int start_r;
+  __shared__ int64_t start_off;
+  const ReqView& q = a.req;
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const unsigned lds = (unsigned)(uintptr_t)(lds_u8*)lds_mem;
+  int rows_total;
+  const int total_eff = rows_in_use(q, &rows_total);
+  const int shift = a.kv.page_shift;
+  // every wave finds its workgroup's share by itself where a wave's lanes hold
+  // the batch; the workgroup together where they do not
+  Cursor cur;
+  cur.begun = 0;
+  int64_t u0, u1;
+  int64_t total;
+  const int wgs_all = gridDim.x;
+  if (q.B <= kWave) {
+    int c0 = 0, len = 0, prefix = 0;
+    if (lane_id() < q.B && !rows_of(q, shift, lane_id(), total_eff, &c0, &len, &prefix)) len = 0;
+    if (wave == 0) {
+      lds_write(lds + R::kReqs + 12 * lane_id(), c0);
+      lds_write(lds + R::kReqs + 12 * lane_id() + 4, len);
+      lds_write(lds + R::kReqs + 12 * lane_id() + 8, prefix);
+    }
+    const int64_t mine = len ? units_of<L>(a.num_heads, c0, len, prefix) : 0;
+    const int64_t incl = wave_incl_scan_op(mine, (int64_t)0, OpAdd{});
+    total = read_lane(incl, kWave - 1);
+    if (blockIdx.x == 0 && tid < q.B) ws.base[tid] = incl - mine;
+    const int wgs = wgs_in_use(total, wgs_all);
+    cur.share = share_of(blockIdx.x, wgs);
+    u0 = (int)blockIdx.x < wgs ? wg_start(total, cur.share, wgs) : total;
+    u1 = (int)blockIdx.x < wgs ? wg_start(total, cur.share + 1, wgs) : total;
+    const unsigned long long past = __ballot(u0 < incl);
+    cur.r = past ? (int)__builtin_ctzll(past) : 0;
+    cur.off = u0 - read_lane(incl - mine, cur.r);
+    barrier();
+  } else {
+    auto units = [&](int r) {
+      int c0, len, prefix;
+      return rows_of(q, shift, r, total_eff, &c0, &len, &prefix)
+                 ? units_of<L>(a.num_heads, c0, len, prefix)
+                 : (int64_t)0;
+    };
+    const int per = (q.B + kThreads - 1) / kThreads;
+    const int r0 = min(tid * per, q.B), r1 = min(r0 + per, q.B);
+    int64_t mine = 0;
+    for (int r = r0; r < r1; ++r) mine += units(r);
+    int64_t at = block_excl_scan<int64_t, kThreads>(mine, wsum, &total);
+    if (blockIdx.x == 0) {
+      int64_t b = at;
+      for (int r = r0; r < r1; ++r) {
+        ws.base[r] = b;
+        b += units(r);
+      }
+    }
+    const int wgs = wgs_in_use(total, wgs_all);
+    cur.share = share_of(blockIdx.x, wgs);
+    u0 = (int)blockIdx.x < wgs ? wg_start(total, cur.share, wgs) : total;
+    u1 = (int)blockIdx.x < wgs ? wg_start(total, cur.share + 1, wgs) : total;
+    if (at <= u0 && u0 < at + mine) {
+      for (int r = r0; r < r1; ++r) {
+        const int64_t n = units(r);
+        if (u0 < at + n) {
+          start_r = r;
+          start_off = u0 - at;
+          break;
+        }
+        at += n;
+      }
+    }
+    __syncthreads();
+    cur.r = __builtin_amdgcn_readfirstlane(start_r);
+    cur.off = read_lane(start_off, 0);
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    ws.base[q.B] = total;
+    a.meta[0] = rows_total;
+    a.meta[1] = rows_total != total_eff ? DSPARK_DATA_BAD_LENS : 0;
+  }
+  if (u0 >= u1) return;
+  cur.left = u1 - u0;
+  Feeder<E8, L> feed;
+  feed.start(a, lds, cur, wave);
+#pragma unroll
+  for (int i = 0; i < R::kStages - 1; ++i) feed.next(a, lds, wave);
+  int64_t left = u1 - u0;
+  int stage = 0, tick = 0;
+  if (tid == 0) lds_write<unsigned>(lds + R::kFlag, 0u);
+  for (;;) {
+    Job job;
+    const Span span = next_span<L>(a, lds + R::kReqs, cur, &job);
+    if (span.n == 0) break;
+    // row tiles: none of a request whose tree is none
+    int mt = job.mt;
+    if (q.parents) {
+      const int lane = lane_id();
+      const int up = lane + 1 < job.s.len ? q.parents[(size_t)span.r * q.gamma + lane] : 0;
+      if (__ballot(up < 0 || up > lane)) mt = 0;
+    }
+    // tiles still to come, as far as the end of the ring is concerned
+    const int near = (int)min(left, (int64_t)1 << 30);
+    segment<T, E8, L>(a, ws, span, job, mt, feed, lds, near, stage, tick);
+    left -= span.n;
+  }
+}
+
+template <int L>
+void launch_split(const LatentAttnArgs& a, const Parts& ws, dspark_dtype dt, hipStream_t s) {
+  const dim3 grid((unsigned)ws.wgs), block(waves(L) * kWave);
+  if (a.kv.cb == 1) {
+    hipLaunchKernelGGL((split_kernel<__bf16, true, L>), grid, block, 0, s, a, ws);
+  } else if (dt == DSPARK_BF16) {
+    hipLaunchKernelGGL((split_kernel<__bf16, false, L>), grid, block, 0, s, a, ws);
+  } else {
+    hipLaunchKernelGGL((split_kernel<_Float16, false, L>), grid, block, 0, s, a, ws);
+  }
+}
+
+void launch_dim256(const LatentAttnArgs& a, const Parts& ws, dspark_dtype dt, hipStream_t s);
+void launch_dim512(const LatentAttnArgs& a, const Parts& ws, dspark_dtype dt, hipStream_t s);
+
+}  // namespace lattn
+}  // namespace dspark

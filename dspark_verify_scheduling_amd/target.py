@@ -10,7 +10,7 @@ the current device. ``KvCache`` describes a cache once; calls of a layer take
 from __future__ import annotations
 
 import ctypes
-from typing import NamedTuple, Optional
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
@@ -220,6 +220,59 @@ def dspark_kv_append(B: int, gamma: int, q: torch.Tensor, k: torch.Tensor, v: to
         _stream(stream),
     )
     _lib.check("dspark_kv_append", _lib.lib().dspark_kv_append(*args))
+    return out
+
+
+def dspark_kv_append_axes(B: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, max_rows: int,
+                          cu_seqlens: torch.Tensor, prefix_lens: torch.Tensor,
+                          positions: torch.Tensor, pair_axis: Sequence[int],
+                          block_table: torch.Tensor, cache: KvCache, out: AppendOutputs,
+                          rope: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                          k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                          rope_interleaved: bool = False, stream=None) -> AppendOutputs:
+    """dspark_kv_append for rows whose pairs turn by positions on several axes:
+    pair i by ``positions[pair_axis[i]]`` (``positions``: [axes, >= max_rows]
+    int32, rows dense; ``pair_axis``: rope_dim / 2 whole numbers). Requests have
+    any number of rows."""
+    dev = _device(cache)
+    dt, D, hkv = cache.row_dtype, cache.head_dim, cache.num_kv_heads
+    hq = q.shape[1] if q.dim() == 3 else 0
+    table, width = _table(block_table, B, dev)
+    if rope is None or rope.dim() != 2:
+        raise ValueError("rope must be [positions, rope_dim]")
+    rope_rows, rope_dim = rope.shape
+    pair_axis = [int(x) for x in pair_axis]
+    if len(pair_axis) != rope_dim // 2:
+        raise ValueError(f"pair_axis holds {len(pair_axis)} axes, needs {rope_dim // 2}")
+    if not isinstance(positions, torch.Tensor) or positions.dtype != _I32:
+        raise TypeError("positions must be an int32 tensor")
+    if positions.get_device() != dev:
+        raise ValueError(f"positions must be on the current device cuda:{dev}, got {positions.device}")
+    if positions.dim() != 2 or positions.shape[1] < max_rows:
+        raise ValueError(f"positions must be [axes, >= {max_rows}], got {tuple(positions.shape)}")
+    ld = positions.stride(0) if positions.shape[0] > 1 else max(max_rows, positions.shape[1])
+    if positions.shape[1] > 1 and positions.stride(1) != 1:
+        raise ValueError("the rows of positions must be dense")
+    axes = (ctypes.c_int32 * max(len(pair_axis), 1))(*pair_axis)
+    args = (
+        B, hq, _CODE[dt],
+        *_rows(q, "q", dt, max_rows, hq, D, dev),
+        *_rows(k, "k", dt, max_rows, hkv, D, dev),
+        *_rows(v, "v", dt, max_rows, hkv, D, dev), max_rows,
+        _on(cu_seqlens, "cu_seqlens", _I32, B + 1, dev),
+        _on(prefix_lens, "prefix_lens", _I32, B, dev),
+        positions.data_ptr(), ld, positions.shape[0], ctypes.cast(axes, ctypes.c_void_p),
+        table, width,
+        _on(q_weight, "q_weight", dt, D, dev, required=False),
+        _on(k_weight, "k_weight", dt, D, dev, required=False), eps,
+        _on(rope, "rope", torch.float32, 1, dev), rope_rows, rope_dim,
+        1 if rope_interleaved else 0,
+        *_rows(out.q_out, "q_out", dt, max_rows, hq, D, dev),
+        cache._one_layer(),
+        _on(out.append_meta, "append_meta", _I32, 2, dev),
+        _stream(stream),
+    )
+    _lib.check("dspark_kv_append_axes", _lib.lib().dspark_kv_append_axes(*args))
     return out
 
 

@@ -36,6 +36,17 @@
  *   dspark_tree_attention  attention of the packed rows over the cache
  *   dspark_tree_accept     greedy accept along a draft tree
  *   dspark_kv_commit the accepted path's cache rows moved to consecutive slots
+ *   dspark_kv_append_axes  the append of rows whose rotation takes a position
+ *                    on several axes (time, height, width)
+ *
+ * and the same over a cache of one latent vector and one rotated part a token,
+ * from which all heads' keys and values come:
+ *
+ *   dspark_latent_append, dspark_latent_read, dspark_latent_commit
+ *   dspark_latent_attention  attention of the packed rows over the latents
+ *                    themselves (absorbed form)
+ *   dspark_latent_prefill    attention of prompt rows over keys and values
+ *                    expanded from the latents (expanded form)
  *
  * Page references used below:
  *   [Budget] akiyangdev, "DSpark 自适应 Verify 怎样分配候选预算"
@@ -122,6 +133,11 @@ typedef enum dspark_input {
 #define DSPARK_MAX_HEADS 256           /* query heads of the target-pass calls */
 #define DSPARK_MAX_GROUP 64            /* query heads per key/value head */
 #define DSPARK_MAX_LAYERS 1024         /* layers of one dspark_kv_commit */
+#define DSPARK_MAX_AXES 4              /* axes of a position */
+#define DSPARK_LATENT_MAX_HEADS 128    /* query heads over a latent cache */
+#define DSPARK_LATENT_ROPE 64          /* elements of its rotated part */
+#define DSPARK_LATENT_MAX_KEYS 134217728 /* cached indices of one dspark_latent_prefill */
+#define DSPARK_LATENT_GROUP 128        /* elements of an E4M3 latent to an exponent */
 
 /* How the planner prices a budget (see dspark_plan_pack_ex). */
 typedef enum dspark_cost_mode {
@@ -860,6 +876,236 @@ dspark_status dspark_kv_commit(int32_t B, int32_t gamma, const int32_t* path_row
                                const int32_t* num_correct, const int32_t* prefix_lens,
                                const int32_t* block_table, int32_t table_width,
                                const dspark_kv_cache* cache, int32_t* commit_meta, void* stream);
+
+/*
+ * dspark_kv_append_axes - the append of rows with positions on several axes.
+ *
+ * dspark_kv_append for prompts and drafts of models that rotate by a position
+ * in time, height and width: the norms, the rotation of pair i by (c_i, s_i)
+ * of table row positions[pair_axis[i]][row], and the cache write at index
+ * prefix + j, which is no position here. Requests have any number of rows, also
+ * none.
+ *
+ * Arguments as for dspark_kv_append unless stated:
+ *   positions          [num_axes, positions_ld] int32: row n's position on axis a at
+ *                      a * positions_ld + n
+ *   positions_ld       >= max_rows
+ *   num_axes           1..DSPARK_MAX_AXES
+ *   pair_axis_host     HOST [rope_dim / 2] int32: each pair's axis, 0..num_axes-1
+ *   rope               [rope_rows, rope_dim] as for dspark_kv_append; required
+ * Data errors: a request whose rows lie outside [0, min(cu_seqlens[B],
+ *   max_rows)), or whose prefix is negative, sets DSPARK_DATA_BAD_LENS, one that
+ *   ends beyond its table row DSPARK_DATA_BAD_PAGE; none of its rows is written.
+ *   A row on a page id outside [0, num_blocks) (DSPARK_DATA_BAD_PAGE), or with a
+ *   position outside [0, rope_rows) on any of the num_axes axes
+ *   (DSPARK_DATA_BAD_POS), is left out alone. Where cu_seqlens is out of order, a
+ *   row that two well-formed requests claim goes to one of them, the same in
+ *   every call.
+ */
+dspark_status dspark_kv_append_axes(int32_t B, int32_t num_heads, dspark_dtype dt, const void* q,
+                                    int64_t q_ld, const void* k, int64_t k_ld, const void* v,
+                                    int64_t v_ld, int32_t max_rows, const int32_t* cu_seqlens,
+                                    const int32_t* prefix_lens, const int32_t* positions,
+                                    int64_t positions_ld, int32_t num_axes,
+                                    const int32_t* pair_axis_host, const int32_t* block_table,
+                                    int32_t table_width, const void* q_weight,
+                                    const void* k_weight, float eps, const float* rope,
+                                    int32_t rope_rows, int32_t rope_dim, int32_t rope_interleaved,
+                                    void* q_out, int64_t q_out_ld, const dspark_kv_cache* cache,
+                                    int32_t* append_meta, void* stream);
+
+/*
+ * ---- The target pass over a latent cache ---------------------------------
+ *
+ * Models of this kind cache one vector c of latent_dim elements and one rotated
+ * part r of DSPARK_LATENT_ROPE elements a token. Head h's key is (W_k[h] c, r)
+ * and its value W_v[h] c. Absorbed, the score q . W_k[h] c is taken as (W_k[h]^T
+ * q) . c and W_v[h] is applied to the weighted mean of the latents, so that all
+ * heads read the same cached rows (dspark_latent_attention: few rows a request).
+ * Expanded, keys and values are made from the cached rows first
+ * (dspark_latent_prefill: prompts). Both are the same function.
+ *
+ * Rows, trees, requests, pages and status bits are those of the target pass
+ * above. Page p of a layer holds latents as [block_size][latent_dim] at latent
+ * + p * block_stride elements, rotated parts as [block_size]
+ * [DSPARK_LATENT_ROPE] at rope + p * rope_block_stride. With dtype E4M3 the latent
+ * is stored as codes with an exponent byte (as for dspark_kv_cache) for each
+ * DSPARK_LATENT_GROUP elements, at [block_size][latent_dim /
+ * DSPARK_LATENT_GROUP] from scale + p * scale_block_stride; the rotated part is
+ * BF16 then.
+ */
+typedef struct dspark_latent_cache {
+  void* latent;      /* device, 16-byte aligned */
+  void* rope;        /* device, 16-byte aligned */
+  uint8_t* scale;    /* device, 16-byte aligned; E4M3 only, otherwise ignored */
+  int64_t block_stride;       /* elements from page to page, a multiple of 16 bytes */
+  int64_t rope_block_stride;  /* elements, a multiple of 8 */
+  int64_t scale_block_stride; /* bytes, a multiple of 16 */
+  int64_t layer_stride;       /* elements from layer to layer; dspark_latent_commit */
+  int64_t rope_layer_stride;
+  int64_t scale_layer_stride;
+  int32_t num_layers;         /* dspark_latent_commit; the other calls use layer 0 */
+  int32_t num_blocks;         /* pages of each layer, >= 1 */
+  int32_t block_size;         /* 16, 32, 64, 128 or 256 */
+  int32_t latent_dim;         /* 256 or 512 */
+  dspark_dtype dtype;         /* of the latents: BF16, F16 or E4M3 */
+} dspark_latent_cache;
+
+/*
+ * dspark_latent_append - norm, rotation and cache write of the packed rows.
+ *
+ * For every packed row n, in float32 and rounded once at the end: the first
+ * latent_dim elements x of kv row n become x * (mean(x^2) + eps)^(-1/2) * weight
+ * (as they are where weight is NULL); the DSPARK_LATENT_ROPE elements behind
+ * them, and those of each head of q_rope, turn by the row's position as in
+ * dspark_kv_append with rope_dim = DSPARK_LATENT_ROPE (as they are where rope is
+ * NULL). q_rope_out = the turned queries; the cache gets latent and rotated part at
+ * index prefix + j.
+ *
+ * Arguments:
+ *   B                  requests, 0..DSPARK_MAX_BATCH
+ *   gamma              0: requests have any number of rows, also none, in a chain;
+ *                      1..DSPARK_MAX_GAMMA: up to gamma + 1 rows
+ *   tree_parents       [B, gamma] int32 or NULL (chain); NULL if gamma is 0. The
+ *                      position of row j is prefix + depth(j)
+ *   num_heads          of q_rope, 1..DSPARK_LATENT_MAX_HEADS, or 0 for no queries
+ *   dt                 type of kv, weight and q_rope: BF16 or F16; the cache
+ *                      holds the same type, or E4M3 with BF16
+ *   kv, kv_ld          rows of latent_dim + DSPARK_LATENT_ROPE elements
+ *   q_rope             row n, head h at q_rope + n * q_ld + h * q_head_ld
+ *   q_rope_out         rows as q_rope; q_rope itself (with its strides) is allowed
+ *   All rows 16-byte aligned, strides multiples of 8 elements.
+ *   weight             [latent_dim] or NULL, 16-byte aligned
+ *   rope               [rope_rows, DSPARK_LATENT_ROPE] float32 or NULL
+ *   append_meta        out [2] int32: cu_seqlens[B], status bits
+ * Data errors: as for dspark_kv_append; where cu_seqlens is out of order as for
+ *   dspark_kv_append_axes.
+ */
+dspark_status dspark_latent_append(int32_t B, int32_t gamma, int32_t num_heads, dspark_dtype dt,
+                                   const void* kv, int64_t kv_ld, const void* q_rope,
+                                   int64_t q_ld, int64_t q_head_ld, int32_t max_rows,
+                                   const int32_t* cu_seqlens, const int32_t* prefix_lens,
+                                   const int32_t* tree_parents, const int32_t* block_table,
+                                   int32_t table_width, const void* weight, float eps,
+                                   const float* rope, int32_t rope_rows, int32_t rope_interleaved,
+                                   void* q_rope_out, int64_t q_out_ld, int64_t q_out_head_ld,
+                                   const dspark_latent_cache* cache, int32_t* append_meta,
+                                   void* stream);
+
+/*
+ * dspark_latent_read - cache rows back as dense rows.
+ *
+ *   latent_out[cu[r] + j], rope_out[cu[r] + j] = what the cache holds at index
+ *   starts[r] + j for j < cu[r+1] - cu[r]
+ * in the cache's type (BF16 for E4M3: exact), out_ld and rope_out_ld elements
+ * apart. Arguments, limits and data errors as for dspark_kv_read.
+ */
+dspark_status dspark_latent_read(int32_t B, int32_t max_rows, const int32_t* cu_seqlens,
+                                 const int32_t* starts, const int32_t* block_table,
+                                 int32_t table_width, const dspark_latent_cache* cache,
+                                 void* latent_out, int64_t out_ld, void* rope_out,
+                                 int64_t rope_out_ld, int32_t* read_meta, void* stream);
+
+/*
+ * dspark_latent_commit - the accepted path's cache rows moved to consecutive
+ * slots: dspark_kv_commit for a latent cache.
+ */
+dspark_status dspark_latent_commit(int32_t B, int32_t gamma, const int32_t* path_rows,
+                                   const int32_t* num_correct, const int32_t* prefix_lens,
+                                   const int32_t* block_table, int32_t table_width,
+                                   const dspark_latent_cache* cache, int32_t* commit_meta,
+                                   void* stream);
+
+/*
+ * dspark_latent_attention - attention of the packed rows over the latents.
+ *
+ * Row j of request r sees the cache indices 0..prefix-1 and prefix + i for i in
+ * anc(j), itself included:
+ *   s_k = scale * (q_latent . c_k + q_rope . r_k),
+ *   out = sum_k exp(s_k) c_k / sum_k exp(s_k),  lse = log sum_k exp(s_k)
+ * over the indices seen, for every head, in the precision of
+ * dspark_tree_attention. A cached row that a row does not see adds nothing to it,
+ * whatever it holds; one with a NaN or infinite element leaves the outputs of
+ * the rows that see it without meaning.
+ *
+ * Arguments:
+ *   B, gamma           as for dspark_tree_attention
+ *   num_heads          1..DSPARK_LATENT_MAX_HEADS
+ *   dt                 BF16 or F16; the cache holds the same type, or E4M3 with BF16
+ *   q_latent           row n, head h at q_latent + n * ql_ld + h * ql_head_ld:
+ *                      latent_dim elements; q_rope alike (DSPARK_LATENT_ROPE)
+ *   out                row n at out + n * out_ld: num_heads dense heads of latent_dim
+ *   All 16-byte aligned, strides multiples of 8 elements.
+ *   scale              finite
+ *   lse                [max_rows, num_heads] float32 or NULL
+ *   attention_meta     out [2] int32: cu_seqlens[B], status bits
+ *   workspace          dspark_latent_attention_workspace_size() bytes, 256-byte
+ *                      aligned; contents irrelevant, no state between calls;
+ *                      calls that share it must not overlap in time
+ * Data errors: as for dspark_tree_attention.
+ */
+dspark_status dspark_latent_attention(int32_t B, int32_t gamma, int32_t num_heads,
+                                      dspark_dtype dt, const void* q_latent, int64_t ql_ld,
+                                      int64_t ql_head_ld, const void* q_rope, int64_t qr_ld,
+                                      int64_t qr_head_ld, int32_t max_rows,
+                                      const int32_t* cu_seqlens, const int32_t* prefix_lens,
+                                      const int32_t* tree_parents, const int32_t* block_table,
+                                      int32_t table_width, const dspark_latent_cache* cache,
+                                      float scale, void* out, int64_t out_ld, float* lse,
+                                      int32_t* attention_meta, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace dspark_latent_attention needs (0 for invalid sizes). */
+size_t dspark_latent_attention_workspace_size(int32_t B, int32_t gamma, int32_t num_heads,
+                                              int32_t latent_dim);
+
+/*
+ * dspark_latent_prefill - causal attention of prompt rows, expanded form.
+ *
+ * Row j of request r, of any number of rows (also none), sees the cache indices
+ * 0..prefix+j, which must hold them (dspark_latent_append). For every head h:
+ *   k = W_k[h] c, v = W_v[h] c for the cached latents, rounded to dt once;
+ *   s = scale * (q[0 : nope] . k + q[nope :] . r),  out = softmax(s) v
+ * with the products' sums, scores, maxima, sums and outputs in float32, and the
+ * softmax's weights rounded as in dspark_tree_attention. Cached rows that a row
+ * does not see, or that hold NaN or infinity, as for dspark_latent_attention.
+ *
+ * Arguments:
+ *   B                  requests, 0..DSPARK_MAX_BATCH
+ *   num_heads, dt      as for dspark_latent_attention
+ *   nope               elements of a head's unrotated part and of its values: 64 or
+ *                      128
+ *   q, q_ld            row n at q + n * q_ld: num_heads dense heads of nope +
+ *                      DSPARK_LATENT_ROPE elements, turned (the rotated part of
+ *                      a row may be dspark_latent_append's q_rope_out)
+ *   w_k, w_v           head h at w_k + h * w_head_ld: [nope][latent_dim] dense, of type
+ *                      dt; w_v alike
+ *   max_keys           cached indices of all requests together (sum of prefix +
+ *                      rows) that the workspace has room for, up to
+ *                      DSPARK_LATENT_MAX_KEYS
+ *   out, out_ld        row n at out + n * out_ld: num_heads dense heads of nope
+ *   All 16-byte aligned, strides multiples of 8 elements.
+ *   lse, prefill_meta, workspace  as for dspark_latent_attention, with
+ *                      dspark_latent_prefill_workspace_size()
+ * Data errors: a request whose rows lie outside [0, min(cu_seqlens[B],
+ *   max_rows)), whose prefix is negative, or whose keys with those of the requests
+ *   before it pass max_keys, sets DSPARK_DATA_BAD_LENS; one that ends beyond its
+ *   table row or has a page id outside [0, num_blocks) DSPARK_DATA_BAD_PAGE. None
+ *   of such a request's rows is written.
+ */
+dspark_status dspark_latent_prefill(int32_t B, int32_t num_heads, int32_t nope, dspark_dtype dt,
+                                    const void* q, int64_t q_ld, const void* w_k,
+                                    const void* w_v, int64_t w_head_ld, int32_t max_rows,
+                                    int32_t max_keys, const int32_t* cu_seqlens,
+                                    const int32_t* prefix_lens, const int32_t* block_table,
+                                    int32_t table_width, const dspark_latent_cache* cache,
+                                    float scale, void* out, int64_t out_ld, float* lse,
+                                    int32_t* prefill_meta, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace dspark_latent_prefill needs (0 for invalid sizes). */
+size_t dspark_latent_prefill_workspace_size(int32_t B, int32_t max_rows, int32_t max_keys,
+                                            int32_t num_heads, int32_t nope, int32_t latent_dim);
 
 /* Name of a status code (static string). */
 const char* dspark_status_str(dspark_status s);
