@@ -24,9 +24,8 @@ using attn::Types;
 using attn::uniform;
 using attn::wait_copies;
 
-// Row tiles of a workgroup: what its registers hold. A wave keeps the queries of
-// one tile (2.25 KB a row of 512 and 64) and the outputs of all of them for its
-// share of the columns.
+// Row tiles of a workgroup, at most: what its registers hold. A wave keeps the
+// queries of one tile and the outputs of all of them for its share of the columns.
 constexpr int row_tiles(int dim) { return dim == 512 ? 2 : 4; }
 constexpr int waves(int dim) { return 2 * row_tiles(dim); }
 constexpr int kRowTile = 32;
@@ -324,8 +323,9 @@ struct Feeder {
   }
 };
 
-// A segment: `mt` row tiles over some units of the keys, which the waves bring into
-// LDS together. Wave (t, half) = (wave / 2, wave % 2) has row tile t and half the
+// A segment: some row tiles over some units of the keys, which the waves bring into
+// LDS together. (Tiles without rows, and those of a request whose tree is none, are
+// computed with zeros for queries and not written.) Wave (t, half) = (wave / 2, wave % 2) has row tile t and half the
 // keys of a tile for the scores, and a share of the columns for the outputs:
 //   S^T = K Q^T: keys are its rows and queries its columns, so a lane holds the
 //   scores of one query (lane & 31) for sixteen keys, four in a row each. Its
@@ -337,7 +337,7 @@ struct Feeder {
 // halves' maxima meet in LDS, the weights are taken again and the outputs shrink.
 template <typename T, bool E8, int L>
 __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws, const Span& span,
-                                        const Job& job, int mt, Feeder<E8, L>& feed, unsigned lds,
+                                        const Job& job, bool good, Feeder<E8, L>& feed, unsigned lds,
                                         int left, int& stage, int& tick) {
   typedef Types<T> TT;
   typedef typename TT::V8 V8;
@@ -354,13 +354,13 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
   const int len = s.len, prefix = s.prefix, keys = s.keys;
   const int m = (job.tile0 + tile) * kRowTile + qi;
   const int qrow = m / a.num_heads;  // the request's row that the lane's query belongs to
-  const bool live = tile < mt && m < s.mrows;
+  const bool live = good && tile < job.mt && m < s.mrows;
 
   // rows of the step's own tree that the lane's query sees, bit l for row l + 1;
   // row 0 is everybody's. Bit l of anc, in lane l, is row l + 1 itself, with its
   // ancestors' bits.
   unsigned long long seen = qrow >= 64 ? ~0ull : (1ull << qrow) - 1;
-  if (a.req.parents && mt > 0) {
+  if (a.req.parents) {
     int up = lane + 1 < len ? a.req.parents[(size_t)span.r * a.req.gamma + lane] : 0;
     unsigned long long anc = 1ull << lane;
     for (int i = 0; i < 6; ++i) {
@@ -572,10 +572,6 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
     stage = stage + 1 == R::kStages ? 0 : stage + 1;
     const unsigned flag = lds + R::kFlag + tick * 4, other_flag = lds + R::kFlag + (tick ^ 1) * 4;
     tick ^= 1;
-    if (mt == 0) {
-      barrier();  // (the tile may go)
-      continue;
-    }
     if (wave == 0 && lane == 0) lds_write<unsigned>(other_flag, 0u);
 
     // Scores. Reads from LDS go out a batch ahead of the products that use them.
@@ -598,11 +594,10 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
         lds_write((weight_at ^ ((half * 2 + c) << 5)) + tile * (kRowTile * kKeys * 2), pf[c]);
     };
     float sum = 0.0f;
-    if (tile < mt) {
-      f32x16 s2;
+    {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) sc[e] = s2[e] = 0.0f;
-      constexpr int FB = 4;
+      for (int e = 0; e < 16; ++e) sc[e] = 0.0f;
+      constexpr int FB = L == 512 ? 4 : 2;
       static_assert(NF % FB == 0, "whole batches");
       V8 kf[2][FB];
       unsigned ka[8], ta = turned + turned_at;
@@ -625,26 +620,18 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
         if (f0 + FB < NF) read_keys(f0 + FB, kf[(f0 / FB + 1) & 1]);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int f = 0; f < FB; f += 2) {
-          sc = TT::mfma32(kf[(f0 / FB) & 1][f], qf[f0 + f], sc);
-          s2 = TT::mfma32(kf[(f0 / FB) & 1][f + 1], qf[f0 + f + 1], s2);
-        }
+        for (int f = 0; f < FB; ++f) sc = TT::mfma32(kf[(f0 / FB) & 1][f], qf[f0 + f], sc);
         __builtin_amdgcn_sched_barrier(0);
       }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) sc[e] += s2[e];
       if (edge) {
         const unsigned odd = lds_read<unsigned>(lds + R::kOdd + half * 4);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int k = 8 * (e >> 2) + 4 * hi + (e & 3);
           const int rel = key0 + half * 32 + k - prefix;
-          const bool own = rel < len && ((seen >> ((rel - 1) & 63)) & 1);
-          if (((missing >> (half * 2 + (e >> 3))) & 1) || (rel > 0 && !own)) {
-            sc[e] = -__builtin_inff();
-          } else if ((odd >> k) & 1) {
-            sc[e] = __builtin_nanf("");
-          }
+          const bool own = (rel < len) & ((int)(seen >> ((rel - 1) & 63)) & 1);
+          const bool gone = ((missing >> (half * 2 + (e >> 3))) & 1) | ((rel > 0) & !own);
+          sc[e] = gone ? -__builtin_inff() : ((odd >> k) & 1 ? __builtin_nanf("") : sc[e]);
         }
       }
       // Weights. The product with the scale rounds before the maximum is taken off,
@@ -686,10 +673,10 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
     barrier();
     if (__builtin_expect(lds_read<unsigned>(flag) != 0, 0)) {
       top = fmaxf(top, __shfl_xor(top, 32, kWave));
-      if (hi == 0 && tile < mt)
+      if (hi == 0)
         lds_write<float>(lds + R::kHalves + half * (R::kMaxRows * 4) + row_at, top);
       barrier();
-      if (tile < mt) {
+      {
         float next = fmaxf(top, lds_read<float>(lds + R::kHalves + (half ^ 1) * (R::kMaxRows * 4) +
                                                 row_at));
         if (next - mx > TT::kAbove + TT::kSlack) {
@@ -710,12 +697,11 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
       }
       barrier();
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-        if (t < mt) {
-          const float fix = lds_read<float>(lds + R::kFix + (t * kRowTile + qi) * 4);
+      for (int t = 0; t < NT; ++t) {
+        const float fix = lds_read<float>(lds + R::kFix + (t * kRowTile + qi) * 4);
 #pragma unroll
-          for (int d = 0; d < ND; ++d) o[t][d] *= fix;
-        }
+        for (int d = 0; d < ND; ++d) o[t][d] *= fix;
+      }
     }
     l += sum;
     // O^T += C^T P^T
@@ -728,30 +714,26 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
       }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-        if (t < mt) {
+      for (int d = 0; d < ND; ++d) {
+        const V8 vf = __builtin_shufflevector(vl[c & 1][d], vh[c & 1][d], 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
-          for (int d = 0; d < ND; ++d) {
-            const V8 vf = __builtin_shufflevector(vl[c & 1][d], vh[c & 1][d], 0, 1, 2, 3, 4, 5, 6, 7);
-            o[t][d] = TT::mfma32(vf, pw[c & 1][t], o[t][d]);
-          }
-        }
+        for (int t = 0; t < NT; ++t) o[t][d] = TT::mfma32(vf, pw[c & 1][t], o[t][d]);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
     // (the next tile's first barrier comes before anything here is overwritten:
     // the weights, the statistics and, in 8 bits, the tile)
   }
 
-  if (mt == 0) return;
   // the halves' sums meet
   l += __shfl_xor(l, 32, kWave);
   barrier();
-  if (hi == 0 && tile < mt) lds_write<float>(lds + R::kHalves + half * (R::kMaxRows * 4) + row_at, l);
+  if (hi == 0) lds_write<float>(lds + R::kHalves + half * (R::kMaxRows * 4) + row_at, l);
   barrier();
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int mm = (job.tile0 + t) * kRowTile + qi;
-    if (t >= mt || mm >= s.mrows) continue;
+    if (!good || t >= job.mt || mm >= s.mrows) continue;
     const unsigned at = lds + R::kHalves + (t * kRowTile + qi) * 4;
     const float sum = lds_read<float>(at) + lds_read<float>(at + R::kMaxRows * 4);
     const int row = mm / a.num_heads, head = mm - row * a.num_heads;
@@ -895,16 +877,15 @@ __global__ __launch_bounds__(waves(L) * kWave, waves(L) / 4) void split_kernel(L
     Job job;
     const Span span = next_span<L>(a, lds + R::kReqs, cur, &job);
     if (span.n == 0) break;
-    // row tiles: none of a request whose tree is none
-    int mt = job.mt;
+    bool good = true;  // its tree is one
     if (q.parents) {
       const int lane = lane_id();
       const int up = lane + 1 < job.s.len ? q.parents[(size_t)span.r * q.gamma + lane] : 0;
-      if (__ballot(up < 0 || up > lane)) mt = 0;
+      good = __ballot(up < 0 || up > lane) == 0;
     }
     // tiles still to come, as far as the end of the ring is concerned
     const int near = (int)min(left, (int64_t)1 << 30);
-    segment<T, E8, L>(a, ws, span, job, mt, feed, lds, near, stage, tick);
+    segment<T, E8, L>(a, ws, span, job, good, feed, lds, near, stage, tick);
     left -= span.n;
   }
 }
