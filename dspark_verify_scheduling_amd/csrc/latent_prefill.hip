@@ -574,12 +574,14 @@ __global__ __launch_bounds__(kAttendWaves * kWave, 2) void attend_kernel(LatentP
     top *= sl;
     if (__any(top - mx > TT::kAbove + TT::kSlack)) {
       float next = fmaxf(top, __shfl_xor(top, 32, kWave));
+      // (rows for themselves: what one sees moves no other's weights)
+      const bool moves = next - mx > TT::kAbove + TT::kSlack;
       if constexpr (TT::kAbove > 0.0f) {
         // (not where kAbove rounds up to more than a weight may be)
         const float less = next - TT::kAbove;
         next = next - less > TT::kAbove + TT::kSlack ? next : less;
       }
-      next = fmaxf(mx, next);
+      next = moves ? fmaxf(mx, next) : mx;
       const float fix = next == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(mx - next);
       mx = next;
       l *= fix;

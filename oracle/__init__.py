@@ -47,6 +47,7 @@ from .target import (
     DATA_BAD_PAGE, DATA_BAD_POS, DATA_BAD_TREE, commit_moves, e4m3_exponent, e4m3_round,
     e4m3_values, norm_rope, tree_accept, tree_attention, tree_ok, tree_paths,
 )
+from .latent import axes_turn, latent_attention, latent_e4m3, latent_prefill
 
 __all__ = [
     "sigmoid32", "survival", "plan", "pack", "accept", "row_argmax", "tv_accept",
@@ -55,4 +56,5 @@ __all__ = [
     "DATA_BAD_COST", "DATA_BAD_CONF", "DATA_BAD_LENS", "FX_SHIFT",
     "DATA_BAD_TREE", "DATA_BAD_PAGE", "DATA_BAD_POS", "commit_moves", "e4m3_exponent", "e4m3_round",
     "e4m3_values", "norm_rope", "tree_accept", "tree_attention", "tree_ok", "tree_paths",
+    "axes_turn", "latent_attention", "latent_e4m3", "latent_prefill",
 ]
