@@ -268,38 +268,46 @@ struct Feeder {
     none = 0;
   }
 
-  // Starts the wave's copies of the next tile.
-  __device__ __forceinline__ void next(const LatentAttnArgs& a, unsigned lds, int wave) {
+  // The wave's copies of the next tile: begin(), each of the kPerWave copies once, so
+  // that they can go out between products, and end(). Where no tile is left, the
+  // last one's go out once more, into a stage that nobody reads.
+  const unsigned char *from, *turned, *exps;
+  unsigned at;
+  __device__ __forceinline__ void begin(const LatentAttnArgs& a, unsigned lds, int wave) {
+    at = lds + R::kRing + stage * R::kStage;
     if (end == 0) return;
-    const int lane = lane_id();
-    const int row0 = wave * R::kOwn;
     const int64_t id = __builtin_amdgcn_readlane(ids, idx);
-    const int key = j.first + (t + idx) * kKeys + row0;
+    const int key = j.first + (t + idx) * kKeys + wave * R::kOwn;
     const int off = key & ((1 << a.kv.page_shift) - 1);
-    const unsigned at = lds + R::kRing + stage * R::kStage;
-    const unsigned char* from = a.kv.latent + id * a.kv.page_bytes + off * (L * R::CB);
-    const unsigned to = at + (E8 ? wave * R::kPiece : row0 * R::kRow);
-#pragma unroll
-    for (int n = 0; n < R::kCopies; ++n) {
-      const int r = n * R::kRowsPerCopy + lane / R::kChunks;
+    from = uniform(a.kv.latent + id * a.kv.page_bytes + off * (L * R::CB));
+    turned = uniform(a.kv.rope + id * a.kv.rope_page_bytes + off * (kRope * 2));
+    if constexpr (E8)
+      exps = uniform(a.kv.scale + id * a.kv.scale_page_bytes + off * (L / kLatGroup));
+  }
+
+  template <int N>
+  __device__ __forceinline__ void copy(int wave) {
+    const int lane = lane_id(), row0 = wave * R::kOwn;
+    if constexpr (N < R::kCopies) {
+      const int r = N * R::kRowsPerCopy + lane / R::kChunks;
       const int chunk = E8 ? lane % R::kChunks : (lane % R::kChunks) ^ R::swizzle(row0 + r);
-      copy16_shared(uniform(from) + n * R::kRowsPerCopy * L * R::CB,
-                    (lane / R::kChunks) * L * R::CB + (unsigned)chunk * 16, to + n * 1024);
-    }
-    if constexpr (E8) {
-      constexpr int kBytes = R::kOwn * (L / kLatGroup);
-      const unsigned char* e =
-          a.kv.scale + id * a.kv.scale_page_bytes + off * (L / kLatGroup);
-      if (lane < kBytes / 4) copy4(uniform(e), lane * 4, to + R::kOwn * L);
-    }
-    const unsigned char* turned = a.kv.rope + id * a.kv.rope_page_bytes + off * (kRope * 2);
-#pragma unroll
-    for (int n = 0; n < R::kTurnedCopies; ++n) {
-      const int r = n * 8 + (lane >> 3);
-      copy16_shared(uniform(turned) + n * 1024,
-                    (lane & ~7) * 16 + (((lane & 7) ^ R::turned_swizzle(row0 + r)) << 4),
+      copy16_shared(from + N * R::kRowsPerCopy * L * R::CB,
+                    (lane / R::kChunks) * L * R::CB + (unsigned)chunk * 16,
+                    at + (E8 ? wave * R::kPiece : row0 * R::kRow) + N * 1024);
+    } else if constexpr (N < R::kCopies + R::kTurnedCopies) {
+      constexpr int n = N - R::kCopies;
+      copy16_shared(turned + n * 1024,
+                    (lane & ~7) * 16 +
+                        (((lane & 7) ^ R::turned_swizzle(row0 + n * 8 + (lane >> 3))) << 4),
                     at + R::kTurnedAt + row0 * (kRope * 2) + n * 1024);
+    } else {
+      constexpr int kBytes = R::kOwn * (L / kLatGroup);
+      if (lane < kBytes / 4) copy4(exps, lane * 4, at + wave * R::kPiece + R::kOwn * L);
     }
+  }
+
+  __device__ __forceinline__ void end_tile(const LatentAttnArgs& a, unsigned lds, int wave) {
+    if (end == 0) return;
     if (__builtin_expect((bad | none) != 0, 0))
       none = (none & ~(1u << stage)) | ((unsigned)(bad >> idx) & 1u) << stage;
     stage = stage + 1 == R::kStages ? 0 : stage + 1;
@@ -321,6 +329,35 @@ struct Feeder {
       end = min(j.n - t, kWave);
     }
   }
+
+  template <int N = 0>
+  __device__ __forceinline__ void copies(int wave) {
+    copy<N>(wave);
+    if constexpr (N + 1 < R::kPerWave) copies<N + 1>(wave);
+  }
+};
+
+// o *= fix for outputs that stay in the accumulation registers. As plain code the
+// product would come out in other registers, and every step of the loop would move
+// all outputs between the two (1 KB a lane, and spills). No product that writes o
+// is under way here: the scores' products, which are later ones, have been read.
+// The waits are those between a write of a register and its read as an operand.
+__device__ inline void shrink(f32x16& o, float fix) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    float x = o[e], y;
+    asm volatile(
+        "v_accvgpr_read_b32 %1, %0\n\ts_nop 1\n\tv_mul_f32 %1, %1, %2\n\ts_nop 1\n\t"
+        "v_accvgpr_write_b32 %0, %1\n\ts_nop 1"
+        : "+a"(x), "=&v"(y)
+        : "v"(fix));
+    o[e] = x;
+  }
+}
+
+template <int N>
+struct Index {
+  static constexpr int value = N;
 };
 
 // A segment: some row tiles over some units of the keys, which the waves bring into
@@ -338,7 +375,7 @@ struct Feeder {
 template <typename T, bool E8, int L>
 __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws, const Span& span,
                                         const Job& job, bool good, Feeder<E8, L>& feed, unsigned lds,
-                                        int left, int& stage, int& tick) {
+                                        int& stage, int& tick) {
   typedef Types<T> TT;
   typedef typename TT::V8 V8;
   typedef typename TT::V4 V4;
@@ -426,7 +463,7 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
   // a word of its row in the row statistics
   const unsigned row_at = (tile * kRowTile + qi) * 4;
 
-  for (int i = 0; i < span.n; ++i, --left) {
+  for (int i = 0; i < span.n; ++i) {
     const int key0 = span.first + i * kKeys;
     // 16-key groups on a page that is none
     unsigned missing = 0;
@@ -496,56 +533,56 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
           lds_write(own_turned + n * 1024, (kv_u32x4){0, 0, 0, 0});
     };
     // this tile's copies are done when those of the stages after it may not be
-    if (R::kStages > 2 && left > R::kStages - 2) {
-      wait_copies<(R::kStages - 2) * R::kPerWave>();
-    } else {
-      wait_copies<0>();
-    }
+    wait_copies<(R::kStages - 2) * R::kPerWave>();
     unsigned buf;
     if constexpr (E8) {
       buf = lds;
       const unsigned from = raw + wave * R::kPiece;
-      unsigned hidden = 0;
+      kv_u32x4 w[R::kCopies];
+      unsigned ex[R::kCopies];
+#pragma unroll
+      for (int n = 0; n < R::kCopies; ++n) {
+        const int r = n * R::kRowsPerCopy + lane / R::kChunks, c = lane % R::kChunks;
+        w[n] = lds_read<kv_u32x4>(from + n * 1024 + lane * 16);
+        ex[n] = lds_read<unsigned char>(from + kOwn * L + r * (L / kLatGroup) + c / (kLatGroup / 16));
+      }
       if (edge) {
         unsigned strange = strange_turned();
 #pragma unroll
         for (int n = 0; n < R::kCopies; ++n) {
-          const int r = n * R::kRowsPerCopy + lane / R::kChunks, c = lane % R::kChunks;
-          const kv_u32x4 w = lds_read<kv_u32x4>(from + n * 1024 + lane * 16);
           // (no row that append writes has an exponent byte above 246; a code may
           // pass every finite number under it)
-          bool bad = lds_read<unsigned char>(from + kOwn * L + r * (L / kLatGroup) +
-                                             c / (kLatGroup / 16)) > 246;
+          bool bad = ex[n] > 246;
 #pragma unroll
           for (int x = 0; x < 4; ++x)
 #pragma unroll
-            for (int y = 0; y < 32; y += 8) bad |= ((w[x] >> y) & 0x7Fu) == 0x7Fu;
+            for (int y = 0; y < 32; y += 8) bad |= ((w[n][x] >> y) & 0x7Fu) == 0x7Fu;
           strange |= rows_in(__ballot(bad), R::kChunks, n * R::kRowsPerCopy);
         }
-        hidden = strange;
-        hidden = hide(strange);
+        const unsigned hidden = hide(strange);
         hide_turned(hidden);
+#pragma unroll
+        for (int n = 0; n < R::kCopies; ++n)
+          if ((hidden >> (n * R::kRowsPerCopy + lane / R::kChunks)) & 1) {
+            w[n] = (kv_u32x4){0, 0, 0, 0};
+            ex[n] = 127;
+          }
       }
       // everybody is done with the tile before
       barrier();
 #pragma unroll
       for (int n = 0; n < R::kCopies; ++n) {
         const int r = n * R::kRowsPerCopy + lane / R::kChunks, c = lane % R::kChunks;
-        const kv_u32x4 w = lds_read<kv_u32x4>(from + n * 1024 + lane * 16);
-        const unsigned ex = lds_read<unsigned char>(from + kOwn * L + r * (L / kLatGroup) +
-                                                    c / (kLatGroup / 16));
-        const bool gone = (hidden >> r) & 1;
-        const float e = __builtin_bit_cast(float, (gone ? 127u : ex) << 23);
+        const float e = __builtin_bit_cast(float, ex[n] << 23);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           kv_u32x4 z;
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const unsigned v = gone ? 0u : w[2 * x + y];
             z[2 * y] = __builtin_bit_cast(
-                unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, e, false));
+                unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[n][2 * x + y], e, false));
             z[2 * y + 1] = __builtin_bit_cast(
-                unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, e, true));
+                unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[n][2 * x + y], e, true));
           }
           lds_write(buf + (row0 + r) * R::kRow + (((2 * c + x) ^ R::swizzle(row0 + r)) << 4), z);
         }
@@ -568,13 +605,12 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
       }
     }
     barrier();
-    feed.next(a, lds, wave);
+    feed.begin(a, lds, wave);
     stage = stage + 1 == R::kStages ? 0 : stage + 1;
     const unsigned flag = lds + R::kFlag + tick * 4, other_flag = lds + R::kFlag + (tick ^ 1) * 4;
     tick ^= 1;
     if (wave == 0 && lane == 0) lds_write<unsigned>(other_flag, 0u);
 
-    // Scores. Reads from LDS go out a batch ahead of the products that use them.
     f32x16 sc;
     float top = -__builtin_inff();
     V8 pf[2];
@@ -595,11 +631,13 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
     };
     float sum = 0.0f;
     {
+      // Scores, in two sums by turns: a product waits for the one before it in its own
+      // sum (36 in one sum: 44 cycles each, in two 32). Between the products go the
+      // reads of operands kAhead products later and the copies of the next tile.
+      f32x16 s2;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) sc[e] = 0.0f;
-      constexpr int FB = L == 512 ? 4 : 2;
-      static_assert(NF % FB == 0, "whole batches");
-      V8 kf[2][FB];
+      for (int e = 0; e < 16; ++e) sc[e] = s2[e] = 0.0f;
+      constexpr int kAhead = 6;
       unsigned ka[8], ta = turned + turned_at;
       {
         unsigned at = buf + lat_at;
@@ -608,21 +646,33 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
         for (int f = 0; f < 8; ++f) ka[f] = at ^ (f << 5);
         settle(ta);
       }
-      auto read_keys = [&](int f0, V8 (&k)[FB]) {
-#pragma unroll
-        for (int f = 0; f < FB; ++f)
-          k[f] = f0 + f < NL ? lds_read<V8>(ka[(f0 + f) & 7] + ((f0 + f) >> 3) * 256)
-                             : lds_read<V8>(ta ^ ((f0 + f - NL) << 5));
+      V8 kf[kAhead + 1];
+      auto read_key = [&](int f) {
+        kf[f % (kAhead + 1)] = f < NL ? lds_read<V8>(ka[f & 7] + (f >> 3) * 256)
+                                      : lds_read<V8>(ta ^ ((f - NL) << 5));
       };
-      read_keys(0, kf[0]);
 #pragma unroll
-      for (int f0 = 0; f0 < NF; f0 += FB) {
-        if (f0 + FB < NF) read_keys(f0 + FB, kf[(f0 / FB + 1) & 1]);
+      for (int f = 0; f < kAhead; ++f) read_key(f);
+      auto step = [&](auto self, auto at) {
+        constexpr int f = decltype(at)::value;
+        if constexpr (f + kAhead < NF) read_key(f + kAhead);
         __builtin_amdgcn_sched_barrier(0);
+        if constexpr (f & 1) {
+          s2 = TT::mfma32(kf[f % (kAhead + 1)], qf[f], s2);
+        } else {
+          sc = TT::mfma32(kf[f % (kAhead + 1)], qf[f], sc);
+        }
+        // copy n goes out behind product n * NF / kPerWave
+        constexpr int n0 = (f * R::kPerWave + NF - 1) / NF, n1 = ((f + 1) * R::kPerWave + NF - 1) / NF;
+        if constexpr (n0 < n1) feed.template copy<n0>(wave);
+        static_assert(n1 - n0 <= 1, "a copy to a product");
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (f + 1 < NF) self(self, Index<f + 1>{});
+      };
+      step(step, Index<0>{});
+      feed.end_tile(a, lds, wave);
 #pragma unroll
-        for (int f = 0; f < FB; ++f) sc = TT::mfma32(kf[(f0 / FB) & 1][f], qf[f0 + f], sc);
-        __builtin_amdgcn_sched_barrier(0);
-      }
+      for (int e = 0; e < 16; ++e) sc[e] += s2[e];
       if (edge) {
         const unsigned odd = lds_read<unsigned>(lds + R::kOdd + half * 4);
 #pragma unroll
@@ -646,9 +696,9 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
         weigh(&sum);
       }
     }
-    // columns of the tile: of 16 keys, the wave's share
-    V4 vl[2][ND], vh[2][ND];
-    V8 pw[2][NT];
+    // columns of the tile, the wave's share: operand k is 16 keys' (k / ND) of 32
+    // columns
+    constexpr int NV = kKeys / 16 * ND, kVAhead = 3;
     unsigned va[ND], wa = weight_at;
     {
       unsigned at = buf + val_at;
@@ -657,21 +707,23 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
       for (int d = 0; d < ND; ++d) va[d] = at ^ (d << 6);
       settle(wa);
     }
-    auto read_values = [&](int c, int into) {
-#pragma unroll
-      for (int d = 0; d < ND; ++d) {
-        vl[into][d] = lds_columns<V4>(va[d] + c * 16 * R::kRow);
-        vh[into][d] = lds_columns<V4>((va[d] ^ 16) + (c * 16 + 8) * R::kRow);
-      }
+    V4 vl[kVAhead + 1], vh[kVAhead + 1];
+    V8 pw[2][NT];
+    auto read_value = [&](int k) {
+      const int c = k / ND, d = k % ND;
+      vl[k % (kVAhead + 1)] = lds_columns<V4>(va[d] + c * 16 * R::kRow);
+      vh[k % (kVAhead + 1)] = lds_columns<V4>((va[d] ^ 16) + (c * 16 + 8) * R::kRow);
     };
-    auto read_weights = [&](int c, int into) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        pw[into][t] = lds_read<V8>((wa ^ (c << 5)) + t * (kRowTile * kKeys * 2));
+    auto read_weight = [&](int c, int t) {
+      pw[c & 1][t] = lds_read<V8>((wa ^ (c << 5)) + t * (kRowTile * kKeys * 2));
     };
-    read_values(0, 0);
+#pragma unroll
+    for (int k = 0; k < kVAhead; ++k) read_value(k);
     barrier();
-    if (__builtin_expect(lds_read<unsigned>(flag) != 0, 0)) {
+    const unsigned moved = lds_read<unsigned>(flag);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) read_weight(0, t);
+    if (__builtin_expect(moved != 0, 0)) {
       top = fmaxf(top, __shfl_xor(top, 32, kWave));
       if (hi == 0)
         lds_write<float>(lds + R::kHalves + half * (R::kMaxRows * 4) + row_at, top);
@@ -700,25 +752,35 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
       for (int t = 0; t < NT; ++t) {
         const float fix = lds_read<float>(lds + R::kFix + (t * kRowTile + qi) * 4);
 #pragma unroll
-        for (int d = 0; d < ND; ++d) o[t][d] *= fix;
+        for (int d = 0; d < ND; ++d) {
+          if constexpr (L == 512) {
+            shrink(o[t][d], fix);
+          } else {
+            o[t][d] *= fix;
+          }
+        }
+        read_weight(0, t);
       }
     }
     l += sum;
-    // O^T += C^T P^T
-    read_weights(0, 0);
+    // O^T += C^T P^T, the reads of operands kVAhead later between the products
 #pragma unroll
-    for (int c = 0; c < kKeys / 16; ++c) {
+    for (int k = 0; k < NV; ++k) {
+      const int c = k / ND, d = k % ND;
+      if (k + kVAhead < NV) read_value(k + kVAhead);
       if (c + 1 < kKeys / 16) {
-        read_values(c + 1, (c + 1) & 1);
-        read_weights(c + 1, (c + 1) & 1);
+        if (ND == 1) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) read_weight(c + 1, t);
+        } else if (d < NT) {
+          read_weight(c + 1, d);
+        }
       }
+      const V8 vf = __builtin_shufflevector(vl[k % (kVAhead + 1)], vh[k % (kVAhead + 1)], 0, 1, 2, 3,
+                                            4, 5, 6, 7);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int d = 0; d < ND; ++d) {
-        const V8 vf = __builtin_shufflevector(vl[c & 1][d], vh[c & 1][d], 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) o[t][d] = TT::mfma32(vf, pw[c & 1][t], o[t][d]);
-      }
+      for (int t = 0; t < NT; ++t) o[t][d] = TT::mfma32(vf, pw[c & 1][t], o[t][d]);
       __builtin_amdgcn_sched_barrier(0);
     }
     // (the next tile's first barrier comes before anything here is overwritten:
@@ -869,8 +931,11 @@ __global__ __launch_bounds__(waves(L) * kWave, waves(L) / 4) void split_kernel(L
   Feeder<E8, L> feed;
   feed.start(a, lds, cur, wave);
 #pragma unroll
-  for (int i = 0; i < R::kStages - 1; ++i) feed.next(a, lds, wave);
-  int64_t left = u1 - u0;
+  for (int i = 0; i < R::kStages - 1; ++i) {
+    feed.begin(a, lds, wave);
+    feed.copies(wave);
+    feed.end_tile(a, lds, wave);
+  }
   int stage = 0, tick = 0;
   if (tid == 0) lds_write<unsigned>(lds + R::kFlag, 0u);
   for (;;) {
@@ -883,11 +948,9 @@ __global__ __launch_bounds__(waves(L) * kWave, waves(L) / 4) void split_kernel(L
       const int up = lane + 1 < job.s.len ? q.parents[(size_t)span.r * q.gamma + lane] : 0;
       good = __ballot(up < 0 || up > lane) == 0;
     }
-    // tiles still to come, as far as the end of the ring is concerned
-    const int near = (int)min(left, (int64_t)1 << 30);
-    segment<T, E8, L>(a, ws, span, job, good, feed, lds, near, stage, tick);
-    left -= span.n;
+    segment<T, E8, L>(a, ws, span, job, good, feed, lds, stage, tick);
   }
+  wait_copies<0>();
 }
 
 template <int L>
