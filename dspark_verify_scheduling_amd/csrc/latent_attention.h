@@ -35,11 +35,13 @@ constexpr int kKeys = 64;  // keys of a unit
 // sums, and per partial segment the running maximum (less Types::kAbove) and sum
 // of each of its rows and their unnormalised outputs. Workgroup w has segments 2 w
 // (the one its range starts with) and 2 w + 1 (a later one that its range ends in).
+// The outputs lie as the lanes hold them, so that both kernels' accesses are whole
+// lines: 32 columns of a row tile are a block of four times 64 lanes' four floats.
 struct Parts {
   int64_t* base;  // [B + 1] first unit of each request, then the total
   float* m;       // [2 * wgs][rows]
   float* l;
-  float* o;       // [2 * wgs][rows][L]
+  float* o;       // [2 * wgs][rows / kRowTile][L / 32][4][kWave][4]
   int wgs;        // workgroups of the split kernel
   int rows;       // rows of a segment, at most
 };
@@ -352,6 +354,26 @@ __device__ inline void shrink(f32x16& o, float fix) {
         : "+a"(x), "=&v"(y)
         : "v"(fix));
     o[e] = x;
+  }
+}
+
+// Four times four columns of a row, 8 apart, less those that lane ^ 32 has, to memory:
+// the two lanes swap halves, so that each stores eight in a row.
+template <typename T>
+__device__ inline void store_columns(T* row, const float (&y)[16]) {
+  typedef typename Types<T>::V8 V8;
+  const int hi = lane_id() >> 5;
+#pragma unroll
+  for (int x = 0; x < 4; x += 2) {
+    V8 z;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float mine = hi ? y[4 * x + 4 + e] : y[4 * x + e];
+      const float other = __shfl_xor(hi ? y[4 * x + e] : y[4 * x + 4 + e], 32, kWave);
+      z[e] = (T)(hi ? other : mine);
+      z[4 + e] = (T)(hi ? mine : other);
+    }
+    *reinterpret_cast<V8*>(row + (x + hi) * 8) = z;
   }
 }
 
@@ -749,17 +771,20 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
       }
       barrier();
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const float fix = lds_read<float>(lds + R::kFix + (t * kRowTile + qi) * 4);
+      for (int t = 0; t < NT; ++t) read_weight(0, t);
+      if (i > 0) {  // (zeros before)
 #pragma unroll
-        for (int d = 0; d < ND; ++d) {
-          if constexpr (L == 512) {
-            shrink(o[t][d], fix);
-          } else {
-            o[t][d] *= fix;
+        for (int t = 0; t < NT; ++t) {
+          const float fix = lds_read<float>(lds + R::kFix + (t * kRowTile + qi) * 4);
+#pragma unroll
+          for (int d = 0; d < ND; ++d) {
+            if constexpr (L == 512) {
+              shrink(o[t][d], fix);
+            } else {
+              o[t][d] *= fix;
+            }
           }
         }
-        read_weight(0, t);
       }
     }
     l += sum;
@@ -794,39 +819,38 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
   barrier();
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
+    if (!good || t >= job.mt) continue;
     const int mm = (job.tile0 + t) * kRowTile + qi;
-    if (!good || t >= job.mt || mm >= s.mrows) continue;
+    const bool there = mm < s.mrows;
     const unsigned at = lds + R::kHalves + (t * kRowTile + qi) * 4;
     const float sum = lds_read<float>(at) + lds_read<float>(at + R::kMaxRows * 4);
-    const int row = mm / a.num_heads, head = mm - row * a.num_heads;
     if (job.whole) {
+      const int row = mm / a.num_heads, head = mm - row * a.num_heads;
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
       T* dst = reinterpret_cast<T*>(a.out + (size_t)(s.c0 + row) * a.out_ld) + head * L +
-               wave * (ND * 32) + hi * 4;
+               wave * (ND * 32);
 #pragma unroll
-      for (int d = 0; d < ND; ++d)
+      for (int d = 0; d < ND; ++d) {
+        float y[16];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          V4 z;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) z[e] = (T)(o[t][d][4 * x + e] * inv);
-          *reinterpret_cast<V4*>(dst + d * 32 + x * 8) = z;
-        }
-      if (a.lse && hi == 0 && wave == 2 * t)
+        for (int e = 0; e < 16; ++e) y[e] = o[t][d][e] * inv;
+        if (there) store_columns(dst + d * 32, y);
+      }
+      if (a.lse && there && hi == 0 && wave == 2 * t)
         a.lse[(size_t)(s.c0 + row) * a.num_heads + head] =
             sum == 0.0f ? -__builtin_inff() : (mx + __builtin_amdgcn_logf(sum)) * kLn2;
     } else {
-      const size_t part = (size_t)job.slot * ws.rows + t * kRowTile + qi;
-      float* dst = ws.o + part * L + wave * (ND * 32) + hi * 4;
+      const size_t part = (size_t)job.slot * ws.rows + t * kRowTile;
+      float* dst = ws.o + part * L + wave * (ND * 32 * kRowTile) + lane * 4;
 #pragma unroll
       for (int d = 0; d < ND; ++d)
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-          *reinterpret_cast<f32x4*>(dst + d * 32 + x * 8) =
+          *reinterpret_cast<f32x4*>(dst + (d * 4 + x) * (kWave * 4)) =
               (f32x4){o[t][d][4 * x], o[t][d][4 * x + 1], o[t][d][4 * x + 2], o[t][d][4 * x + 3]};
       if (hi == 0 && wave == 2 * t) {
-        ws.m[part] = mx;
-        ws.l[part] = sum;
+        ws.m[part + qi] = mx;
+        ws.l[part + qi] = sum;
       }
     }
   }

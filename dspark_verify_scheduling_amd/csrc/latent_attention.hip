@@ -11,16 +11,14 @@ namespace {
 
 constexpr int kJoinThreads = 256;
 
-// One workgroup per (request, share of its rows): joins the parts that several
-// workgroups of the split kernel left of a segment, in order, L / 8 lanes to a row
-// with eight elements each. A part's statistics and outputs are read together, so
-// a row costs about one memory latency. The first workgroup of each request also
-// checks it and its pages.
+// One workgroup per (request, share of its blocks of 32 rows by 32 columns), a wave
+// to a block: joins the parts that several workgroups of the split kernel left of a
+// segment, in order. A part's statistics and outputs are read together, several parts
+// at once. The first workgroup of each request also checks it and its pages.
 template <typename T, int L>
 __global__ __launch_bounds__(kJoinThreads) void join_kernel(LatentAttnArgs a, Parts ws,
                                                             int shares) {
-  typedef typename Types<T>::V8 V8;
-  constexpr int kLanes = L / 8, kRows = kJoinThreads / kLanes;
+  constexpr int kBlocks = L / 32, kJoinWaves = kJoinThreads / kWave;
   const ReqView& q = a.req;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int share = blockIdx.x % shares, r = blockIdx.x / shares;
@@ -53,66 +51,69 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(LatentAttnArgs a, Pa
   if (!good || !tree) return;
   const Shape s = shape_of<L>(a.num_heads, c0, len, prefix);
   const int wgs = wgs_in_use(units, ws.wgs);
-  const int col = (tid % kLanes) * 8;
-  // rows in order over the segments, kRows of one at a time
-  const int steps = (s.per * kRowTile + kRows - 1) / kRows;
-  for (int step = share; step < s.nseg * steps; step += shares) {
-    const int seg = step / steps;
+  const int qi = lane & 31;
+  // blocks in order over the segments and their row tiles
+  for (int n = share * kJoinWaves + tid / kWave; n < s.mtiles * kBlocks; n += shares * kJoinWaves) {
+    const int mtile = n / kBlocks, block = n - mtile * kBlocks;
+    const int seg = mtile / s.per;
     const int64_t u0 = base + (int64_t)seg * s.nku, u1 = u0 + s.nku;
     // workgroups of the first and the last unit
     const int wa = (int)(((u0 + 1) * wgs - 1) / units), wb = (int)((u1 * wgs - 1) / units);
     if (wa == wb) continue;
     const int slot0 = 2 * wa + (wg_start(units, wa, wgs) == u0 ? 0 : 1);
-    const int n = wb - wa + 1;
-    const int rows = min(s.per * kRowTile, s.mrows - seg * s.per * kRowTile);
-    const int row = (step - seg * steps) * kRows + tid / kLanes;
-    if (row < rows) {
-      constexpr int kAhead = 8;
-      float top = -__builtin_inff(), sum = 0.0f;
-      f32x4 y[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-      for (int p0 = 0; p0 < n; p0 += kAhead) {
-        float m[kAhead], l[kAhead];
-        f32x4 x[kAhead][2];
+    const int parts = wb - wa + 1;
+    const int tile = mtile - seg * s.per;
+    constexpr int kAhead = 4;
+    float top = -__builtin_inff(), sum = 0.0f;
+    f32x4 y[4];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          const int p = p0 + k;
-          m[k] = -__builtin_inff();
-          l[k] = 0.0f;
-          x[k][0] = x[k][1] = (f32x4){0, 0, 0, 0};
-          if (p < n) {
-            const size_t at = (size_t)(p ? 2 * (wa + p) : slot0) * ws.rows + row;
-            m[k] = ws.m[at];
-            l[k] = ws.l[at];
-            x[k][0] = *reinterpret_cast<const f32x4*>(ws.o + at * L + col);
-            x[k][1] = *reinterpret_cast<const f32x4*>(ws.o + at * L + col + 4);
-          }
+    for (int x = 0; x < 4; ++x) y[x] = (f32x4){0, 0, 0, 0};
+    for (int p0 = 0; p0 < parts; p0 += kAhead) {
+      float m[kAhead], l[kAhead];
+      f32x4 v[kAhead][4];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int p = p0 + k;
+        m[k] = -__builtin_inff();
+        l[k] = 0.0f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) v[k][x] = (f32x4){0, 0, 0, 0};
+        if (p < parts) {
+          const size_t at = (size_t)(p ? 2 * (wa + p) : slot0) * ws.rows + tile * kRowTile;
+          m[k] = ws.m[at + qi];
+          l[k] = ws.l[at + qi];
+          const float* src = ws.o + at * L + block * (32 * kRowTile) + lane * 4;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) v[k][x] = *reinterpret_cast<const f32x4*>(src + x * (kWave * 4));
         }
-        float next = top;
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) next = fmaxf(next, m[k]);
-        const bool none = next == -__builtin_inff();  // nothing seen, or NaN scores only
-        const float fix = none ? 1.0f : __builtin_amdgcn_exp2f(top - next);
-        sum *= fix;
-        y[0] *= fix;
-        y[1] *= fix;
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          const float f = none ? 1.0f : __builtin_amdgcn_exp2f(m[k] - next);
-          sum += l[k] * f;
-          y[0] += x[k][0] * f;
-          y[1] += x[k][1] * f;
-        }
-        top = next;
       }
-      const int mm = seg * s.per * kRowTile + row;
-      const int j = mm / a.num_heads, head = mm - j * a.num_heads;
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      V8 z;
+      float next = top;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = (T)(y[e >> 2][e & 3] * inv);
-      *reinterpret_cast<V8*>(reinterpret_cast<T*>(a.out + (size_t)(c0 + j) * a.out_ld) + head * L +
-                             col) = z;
-      if (a.lse && col == 0)
+      for (int k = 0; k < kAhead; ++k) next = fmaxf(next, m[k]);
+      const bool none = next == -__builtin_inff();  // nothing seen, or NaN scores only
+      const float fix = none ? 1.0f : __builtin_amdgcn_exp2f(top - next);
+      sum *= fix;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) y[x] *= fix;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const float f = none ? 1.0f : __builtin_amdgcn_exp2f(m[k] - next);
+        sum += l[k] * f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) y[x] += v[k][x] * f;
+      }
+      top = next;
+    }
+    const int mm = mtile * kRowTile + qi;
+    const int j = mm / a.num_heads, head = mm - j * a.num_heads;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    float z[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) z[e] = y[e >> 2][e & 3] * inv;
+    if (mm < s.mrows) {
+      store_columns(reinterpret_cast<T*>(a.out + (size_t)(c0 + j) * a.out_ld) + head * L + block * 32,
+                    z);
+      if (a.lse && block == 0 && lane < 32)
         a.lse[(size_t)(c0 + j) * a.num_heads + head] =
             sum == 0.0f ? -__builtin_inff() : (top + __builtin_amdgcn_logf(sum)) * kLn2;
     }
@@ -143,9 +144,9 @@ Plan plan(int B, int gamma, int num_heads, int L) {
 
 template <int L>
 void launch_join(const LatentAttnArgs& a, const Parts& ws, dspark_dtype dt, hipStream_t s) {
-  // a workgroup's rows at once, and more workgroups where there are few requests
-  const int rows = a.num_heads * (a.req.gamma + 1), at_once = kJoinThreads / (L / 8);
-  const int most = (rows + at_once - 1) / at_once;
+  // a workgroup's blocks at once, and more workgroups where there are few requests
+  const int tiles = (a.num_heads * (a.req.gamma + 1) + kRowTile - 1) / kRowTile;
+  const int most = tiles * (L / 32) / (kJoinThreads / kWave);
   const int shares = std::max(1, std::min(most, 2048 / std::max(a.req.B, 1)));
   const dim3 grid((unsigned)a.req.B * shares), block(kJoinThreads);
   if (dt == DSPARK_BF16) {
