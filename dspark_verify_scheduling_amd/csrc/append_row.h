@@ -12,7 +12,7 @@ struct Vec8<__bf16> { typedef bf16x8 type; };
 template <>
 struct Vec8<_Float16> { typedef f16x8 type; };
 
-// A workgroup's row: LPH lanes per head take the heads of q, k and v in turn, a
+// A row of THREADS threads, a workgroup or a wave: LPH lanes per head take the heads of q, k and v in turn, a
 // round of heads loaded ahead. y = x * (mean(x^2) + eps)^(-1/2) * w, then (a, b) ->
 // (a c - b s, b c + a s), in float32; 8-bit rows scale by the power of two of their
 // largest magnitude.
@@ -22,7 +22,7 @@ struct RowAppend {
   static constexpr int LPH = D / 8, HPP = THREADS / LPH;
   const AppendArgs& a;
   const size_t packed;
-  const int tid, li;  // the lane's eight elements: 8 li ..
+  const int tid, li;  // of the row; the lane's eight elements: 8 li ..
   const int hq, hkv, heads;
   const unsigned char* rows[3];
   T8 next, weight[2];
@@ -38,7 +38,7 @@ struct RowAppend {
   }
 
   __device__ __forceinline__ RowAppend(const AppendArgs& args, int packed_row)
-      : a(args), packed((size_t)packed_row), tid(threadIdx.x), li(threadIdx.x & (LPH - 1)),
+      : a(args), packed((size_t)packed_row), tid(threadIdx.x % THREADS), li(threadIdx.x & (LPH - 1)),
         hq(args.num_heads), hkv(args.kv.hkv), heads(args.num_heads + 2 * args.kv.hkv),
         rows{args.q + (size_t)packed_row * args.q_ld, args.k + (size_t)packed_row * args.k_ld,
              args.v + (size_t)packed_row * args.v_ld} {

@@ -23,13 +23,13 @@ __device__ int position_status(const AppendAxesArgs& a, int total_eff) {
   return bits;
 }
 
-// One workgroup per packed row: its waves find the row's request and page each by
-// itself, and take its heads in turn. Pair i turns by row positions[axis of i] of
-// the table, so a lane gathers its eight cosines and sines from up to num_axes
-// table rows, once for all heads.
-template <typename T, bool E8, int D>
+// ROWS packed rows to a workgroup, its waves split between them: a wave finds its
+// row's request and page by itself, and a row's waves take its heads in turn. Pair i
+// turns by row positions[axis of i] of the table, so a lane gathers its eight
+// cosines and sines from up to num_axes table rows, once for all heads.
+template <typename T, bool E8, int D, int ROWS>
 __global__ __launch_bounds__(kThreads) void append_axes_kernel(AppendAxesArgs a) {
-  constexpr int LPH = D / 8;
+  constexpr int LPH = D / 8, kRowThreads = kThreads / ROWS;
   const AppendArgs& b = a.base;
   const ReqView& q = b.req;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
@@ -44,10 +44,11 @@ __global__ __launch_bounds__(kThreads) void append_axes_kernel(AppendAxesArgs a)
     write_meta(b.meta, total, bits, &all);
     return;
   }
-  const int64_t packed = a.first_row + blockIdx.x - 1;
+  const int64_t packed = a.first_row + (int64_t)(blockIdx.x - 1) * ROWS +
+                         __builtin_amdgcn_readfirstlane(tid / kRowThreads);
   if (packed >= total_eff) return;
   const int n = (int)packed;
-  RowAppend<T, E8, D, kThreads> row(b, n);
+  RowAppend<T, E8, D, kRowThreads> row(b, n);
   int pos[DSPARK_MAX_AXES];
   bool bad = false;
 #pragma unroll
@@ -97,17 +98,29 @@ __global__ __launch_bounds__(kThreads) void append_axes_kernel(AppendAxesArgs a)
   row.finish(id, (int)(slot & ((1 << b.kv.page_shift) - 1)), co, si, turned, swap);
 }
 
-template <typename T, bool E8>
+template <typename T, bool E8, int ROWS>
 void by_dim(const AppendAxesArgs& a, unsigned grid, hipStream_t s) {
   switch (a.base.kv.dim) {
     case 64:
-      hipLaunchKernelGGL((append_axes_kernel<T, E8, 64>), dim3(grid), dim3(kThreads), 0, s, a);
+      hipLaunchKernelGGL((append_axes_kernel<T, E8, 64, ROWS>), dim3(grid), dim3(kThreads), 0, s, a);
       break;
     case 128:
-      hipLaunchKernelGGL((append_axes_kernel<T, E8, 128>), dim3(grid), dim3(kThreads), 0, s, a);
+      hipLaunchKernelGGL((append_axes_kernel<T, E8, 128, ROWS>), dim3(grid), dim3(kThreads), 0, s, a);
       break;
     default:
-      hipLaunchKernelGGL((append_axes_kernel<T, E8, 256>), dim3(grid), dim3(kThreads), 0, s, a);
+      hipLaunchKernelGGL((append_axes_kernel<T, E8, 256, ROWS>), dim3(grid), dim3(kThreads), 0, s, a);
+  }
+}
+
+template <int ROWS>
+void by_type(const AppendAxesArgs& a, dspark_dtype dt, unsigned rows, hipStream_t s) {
+  const unsigned grid = 1u + (rows + ROWS - 1) / ROWS;
+  if (a.base.kv.cb == 1) {
+    by_dim<__bf16, true, ROWS>(a, grid, s);
+  } else if (dt == DSPARK_BF16) {
+    by_dim<__bf16, false, ROWS>(a, grid, s);
+  } else {
+    by_dim<_Float16, false, ROWS>(a, grid, s);
   }
 }
 
@@ -120,13 +133,12 @@ hipError_t launch_append_axes(const AppendAxesArgs& a, dspark_dtype dt, hipStrea
   AppendAxesArgs part = a;
   part.first_row = 0;
   do {
-    const unsigned grid = 1u + (unsigned)std::min<int64_t>(rows - part.first_row, kMostRows);
-    if (a.base.kv.cb == 1) {
-      by_dim<__bf16, true>(part, grid, s);
-    } else if (dt == DSPARK_BF16) {
-      by_dim<__bf16, false>(part, grid, s);
+    const unsigned n = (unsigned)std::min<int64_t>(rows - part.first_row, kMostRows);
+    // few rows: all waves to one
+    if (rows <= 1024) {
+      by_type<1>(part, dt, n, s);
     } else {
-      by_dim<_Float16, false>(part, grid, s);
+      by_type<kThreads / kWave>(part, dt, n, s);
     }
     part.first_row += kMostRows;
   } while (part.first_row < rows);

@@ -31,8 +31,21 @@ constexpr int waves(int dim) { return 2 * row_tiles(dim); }
 constexpr int kRowTile = 32;
 constexpr int kKeys = 64;  // keys of a unit
 
+// A row's weights are 2^(score - m), m its running maximum (in log2) less kAbove,
+// which follows the scores when they pass it by kAbove + kSlack (see attn::Types).
+// Moving one row's here stops its workgroup, so that float16 gives two of its bits
+// for fewer moves: a weight counts down to 2^-34 of the largest, 23 below it in e.
+template <typename T>
+struct Soft {
+  static constexpr float kSlack = 8.0f, kAbove = 0.0f;
+};
+template <>
+struct Soft<_Float16> {
+  static constexpr float kSlack = 6.0f, kAbove = 9.0f;
+};
+
 // What the split kernel leaves for the joining kernel: the schedule's prefix
-// sums, and per partial segment the running maximum (less Types::kAbove) and sum
+// sums, and per partial segment the running maximum (less Soft::kAbove) and sum
 // of each of its rows and their unnormalised outputs. Workgroup w has segments 2 w
 // (the one its range starts with) and 2 w + 1 (a later one that its range ends in).
 // The outputs lie as the lanes hold them, so that both kernels' accesses are whole
@@ -261,13 +274,16 @@ struct Feeder {
     c = from;
     j = next_span<L>(a, lds + R::kReqs, c, nullptr);
     ids = fetch(a, j, 0, wave, &bad);
+    t = idx = stage = 0;
+    end = min(j.n, kWave);
+    none = 0;
+  }
+  // The segment after the first: once the first's copies have started.
+  __device__ void look_ahead(const LatentAttnArgs& a, unsigned lds, int wave) {
     nj = next_span<L>(a, lds + R::kReqs, c, nullptr);
     nids = 0;
     nbad = 0;
     if (nj.n > 0) nids = fetch(a, nj, 0, wave, &nbad);
-    t = idx = stage = 0;
-    end = min(j.n, kWave);
-    none = 0;
   }
 
   // The wave's copies of the next tile: begin(), each of the kPerWave copies once, so
@@ -392,7 +408,7 @@ struct Index {
 //   O^T = C^T P^T, whose C^T (the same latents) comes transposed out of LDS in that
 //   order of keys. Every wave reads all rows' weights and its columns of the tile.
 // The rows' running maximum is kept by both waves of a row tile. It moves when some
-// score passes it by Types::kSlack: a wave that sees one raises a flag, and then the
+// score passes it by Soft::kSlack: a wave that sees one raises a flag, and then the
 // halves' maxima meet in LDS, the weights are taken again and the outputs shrink.
 template <typename T, bool E8, int L>
 __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws, const Span& span,
@@ -413,7 +429,6 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
   const int len = s.len, prefix = s.prefix, keys = s.keys;
   const int m = (job.tile0 + tile) * kRowTile + qi;
   const int qrow = m / a.num_heads;  // the request's row that the lane's query belongs to
-  const bool live = good && tile < job.mt && m < s.mrows;
 
   // rows of the step's own tree that the lane's query sees, bit l for row l + 1;
   // row 0 is everybody's. Bit l of anc, in lane l, is row l + 1 itself, with its
@@ -445,21 +460,42 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
   f32x16 o[NT][ND];
   float mx = -__builtin_inff(), l = 0.0f;
   {
-    const int head = m - qrow * a.num_heads;
-    const size_t row = (size_t)(s.c0 + qrow);
-    const unsigned char* ql = a.ql + row * a.ql_ld + head * a.ql_head_ld + hi * 16;
-    const unsigned char* qr = a.qr + row * a.qr_ld + head * a.qr_head_ld + hi * 16;
+    // Loaded with four lanes to 64 bytes of a row, so that a line is asked for once
+    // (a lane per row and 16 bytes: 6.5 us instead of 2 for a segment), and turned
+    // through the wave's part of the weights' place. LDS keeps the order of a wave's
+    // accesses.
     kv_u32x4 w[NF];
+    const int row4 = lane >> 2, chunk = lane & 3;
 #pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      w[f] = (kv_u32x4){0, 0, 0, 0};
-      if (live && !flat)
-        w[f] = *reinterpret_cast<const kv_u32x4*>(f < NL ? ql + f * 32 : qr + (f - NL) * 32) ^ sign;
+    for (int i = 0; i < 2; ++i) {
+      const int mm = (job.tile0 + tile) * kRowTile + row4 + 16 * i;
+      const int r = mm / a.num_heads, head = mm - r * a.num_heads;
+      const bool there = good && tile < job.mt && mm < s.mrows && !flat;
+      const size_t row = (size_t)(s.c0 + r);
+      const unsigned char* ql = a.ql + row * a.ql_ld + head * a.ql_head_ld + chunk * 16;
+      const unsigned char* qr = a.qr + row * a.qr_ld + head * a.qr_head_ld + chunk * 16;
+      // (one branch for all: a use of a value in it would wait for each load)
+#pragma unroll
+      for (int f = i; f < NF; f += 2) w[f] = (kv_u32x4){0, 0, 0, 0};
+      if (there) {
+#pragma unroll
+        for (int f = i; f < NF; f += 2)
+          w[f] = *reinterpret_cast<const kv_u32x4*>(f < NL ? ql + (f - i) * 32
+                                                           : qr + (f - i - NL) * 32);
+      }
     }
+    const unsigned own = lds + R::kWeights + wave * 2048;
 #pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      settle(w[f]);
-      qf[f] = __builtin_bit_cast(V8, w[f]);
+    for (int f = 0; f < NF; f += 2) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        settle(w[f + i]);
+        const int r = row4 + 16 * i;
+        lds_write(own + r * 64 + ((chunk ^ ((r >> 2) & 3)) << 4), w[f + i] ^ sign);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        qf[f + i] = lds_read<V8>(own + qi * 64 + (((2 * i + hi) ^ ((qi >> 2) & 3)) << 4));
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -712,7 +748,7 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
 #pragma unroll
       for (int e = 1; e < 16; ++e) top = fmaxf(top, sc[e]);
       top *= sl;
-      if (__any(top - mx > TT::kAbove + TT::kSlack)) {
+      if (__any(top - mx > Soft<T>::kAbove + Soft<T>::kSlack)) {
         if (lane == 0) lds_write<unsigned>(flag, 1u);
       } else {
         weigh(&sum);
@@ -753,11 +789,11 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
       {
         float next = fmaxf(top, lds_read<float>(lds + R::kHalves + (half ^ 1) * (R::kMaxRows * 4) +
                                                 row_at));
-        if (next - mx > TT::kAbove + TT::kSlack) {
-          if constexpr (TT::kAbove > 0.0f) {
+        if (next - mx > Soft<T>::kAbove + Soft<T>::kSlack) {
+          if constexpr (Soft<T>::kAbove > 0.0f) {
             // (not where kAbove rounds up to more than a weight may be)
-            const float less = next - TT::kAbove;
-            next = next - less > TT::kAbove + TT::kSlack ? next : less;
+            const float less = next - Soft<T>::kAbove;
+            next = next - less > Soft<T>::kAbove + Soft<T>::kSlack ? next : less;
           }
           next = fmaxf(mx, next);
         } else {
@@ -858,7 +894,7 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
 
 // out = sum_k e^(s_k - m) c_k / sum_k e^(s_k - m) in one pass over the cached rows,
 // which are keys and values at once: running maximum m, sum and outputs in float32
-// registers, m moved only when a score passes it by Types::kSlack. Parts of a row
+// registers, m moved only when a score passes it by Soft::kSlack. Parts of a row
 // join by (m, sum, outputs) in join_kernel.
 //
 // Persistent over the units of all (request, row segment)s in order: workgroup w
@@ -958,6 +994,7 @@ __global__ __launch_bounds__(waves(L) * kWave, waves(L) / 4) void split_kernel(L
   for (int i = 0; i < R::kStages - 1; ++i) {
     feed.begin(a, lds, wave);
     feed.copies(wave);
+    if (i == 0) feed.look_ahead(a, lds, wave);
     feed.end_tile(a, lds, wave);
   }
   int stage = 0, tick = 0;

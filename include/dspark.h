@@ -1024,7 +1024,8 @@ dspark_status dspark_latent_commit(int32_t B, int32_t gamma, const int32_t* path
  *   s_k = scale * (q_latent . c_k + q_rope . r_k),
  *   out = sum_k exp(s_k) c_k / sum_k exp(s_k),  lse = log sum_k exp(s_k)
  * over the indices seen, for every head, in the precision of
- * dspark_tree_attention. A cached row that a row does not see adds nothing to it,
+ * dspark_tree_attention (float16 weights count down to 2^-34 of the row's largest).
+ * A cached row that a row does not see adds nothing to it,
  * whatever it holds; one with a NaN or infinite element leaves the outputs of
  * the rows that see it without meaning.
  *
