@@ -28,9 +28,9 @@ using attn::uniform;
 using attn::wait_copies;
 
 constexpr int kPlanThreads = 1024;
-constexpr int kKeyTile = 64;    // keys of a step of the attention; a request's are padded to it
+constexpr int kKeyTile = 64;    // a request's keys are padded to it
 constexpr int kDenseTile = 128; // keys of a workgroup of the expansion
-constexpr int kRowTile = 256;   // rows of a workgroup of the attention
+constexpr int kRowTile = 128;   // rows of a workgroup of the attention
 constexpr int kXcds = 8;
 
 // A request as the plan leaves it; len 0 where it has no rows or is left out.
@@ -355,13 +355,15 @@ __global__ __launch_bounds__(kExpandThreads, 1) void expand_kernel(LatentPrefill
 
 // ------------------------------------------------------------------ attend
 
-constexpr int kAttendWaves = 8;
+constexpr int kAttendWaves = 4;
+constexpr int kStepKeys = 32;  // keys of a step
+constexpr int kHalves = kStepKeys / 32;
 
 template <int N>
 struct Ring {
   static constexpr int kRow = 2 * N;                     // bytes of a key, or of a value
-  static constexpr int kPart = kKeyTile * kRow;          // keys, or values
-  static constexpr int kTurned = kKeyTile * kRope * 2;
+  static constexpr int kPart = kStepKeys * kRow;          // keys, or values
+  static constexpr int kTurned = kStepKeys * kRope * 2;
   static constexpr int kStage = 2 * kPart + kTurned;
   static constexpr int kStages = 3;
   static constexpr int kCopies = kPart / 1024 / kAttendWaves;  // of keys, and of values
@@ -369,7 +371,7 @@ struct Ring {
   static constexpr int kOdd = kStages * kStage;          // values with NaN or infinity, a bit each
   static constexpr int kBytes = kOdd + 16;
   static_assert(kCopies >= 1, "a copy for every wave");
-  static_assert(kBytes <= 163840 - 256, "a CU's LDS");
+  static_assert(kBytes <= 163840 / 2 - 256, "a CU's LDS");
 };
 
 // A tile of kRowTile prompt rows of one head, 32 to a wave, over the head's keys up
@@ -406,7 +408,7 @@ __global__ __launch_bounds__(kAttendWaves * kWave, 2) void attend_kernel(LatentP
   // a request's last tiles, which have the most keys, come first
   const int mine = w.tile0[r + 1] - 1 - tile;
   const int j0 = mine * kRowTile, rows = min(kRowTile, req.len - j0);
-  const int n_tiles = (req.prefix + j0 + rows + kKeyTile - 1) / kKeyTile;
+  const int n_tiles = (req.prefix + j0 + rows + kStepKeys - 1) / kStepKeys;
   const unsigned char* kv = w.kv + ((int64_t)h * w.dense + w.key0[r]) * (4 * N);
   const unsigned char* turned = w.turned + (int64_t)w.key0[r] * (kRope * 2);
   auto fill = [&](int t, int stage) {
@@ -415,11 +417,11 @@ __global__ __launch_bounds__(kAttendWaves * kWave, 2) void attend_kernel(LatentP
 #pragma unroll
     for (int n = 0; n < R::kCopies; ++n) {
       const int x = (wave * R::kCopies + n) * kRows;
-      const unsigned char* from = kv + (int64_t)(t * kKeyTile + x) * (4 * N);
+      const unsigned char* from = kv + (int64_t)(t * kStepKeys + x) * (4 * N);
       copy_rows<R::kRow>(from, 4 * N, x, at + x * R::kRow);
       copy_rows<R::kRow>(from + 2 * N, 4 * N, x, at + R::kPart + x * R::kRow);
     }
-    copy_rows<kRope * 2>(turned + (int64_t)(t * kKeyTile + wave * 8) * (kRope * 2), kRope * 2,
+    copy_rows<kRope * 2>(turned + (int64_t)(t * kStepKeys + wave * 8) * (kRope * 2), kRope * 2,
                          wave * 8, at + 2 * R::kPart + wave * 1024);
   };
   fill(0, 0);
@@ -467,14 +469,14 @@ __global__ __launch_bounds__(kAttendWaves * kWave, 2) void attend_kernel(LatentP
 
   int stage = 0;
   for (int t = 0; t < n_tiles; ++t) {
-    const int key0 = t * kKeyTile;
+    const int key0 = t * kStepKeys;
     if (t + 1 < n_tiles) {
       wait_copies<R::kPerWave>();
     } else {
       wait_copies<0>();
     }
     // some row of the workgroup does not see all of the tile
-    const bool edge = key0 + kKeyTile > req.prefix + j0 + 1;
+    const bool edge = key0 + kStepKeys > req.prefix + j0 + 1;
     const unsigned buf = lds + stage * R::kStage;
     if (edge) {
       // NaN and infinity in a value must not meet the zero weight of a row that does
@@ -501,29 +503,29 @@ __global__ __launch_bounds__(kAttendWaves * kWave, 2) void attend_kernel(LatentP
         if ((here >> (n * (kWave / kLanes) + lane / kLanes)) & 1)
           lds_write(at + n * 1024, (kv_u32x4){0, 0, 0, 0});
       }
-      if (lane == 0) lds_write<unsigned char>(lds + R::kOdd + (t & 1) * 8 + wave, (unsigned char)found);
+      if (lane == 0) lds_write<unsigned char>(lds + R::kOdd + (t & 1) * 4 + wave, (unsigned char)found);
     }
     barrier();
     if (t + 2 < n_tiles) fill(t + 2, stage + 2 >= R::kStages ? stage + 2 - R::kStages : stage + 2);
     stage = stage + 1 == R::kStages ? 0 : stage + 1;
     if (!rows_here || key0 > wave_last) continue;
-    // Scores, the two halves of the keys
-    f32x16 sc[2];
+    // Scores
+    f32x16 sc[kHalves];
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < kHalves; ++b)
 #pragma unroll
       for (int e = 0; e < 16; ++e) sc[b][e] = 0.0f;
     unsigned ka = buf + key_at, ta = buf + turned_at, va = buf + val_at;
     settle(ka);
     settle(ta);
     settle(va);
-    constexpr int FB = 2;
-    V8 kf[2][FB][2];
+    constexpr int FB = 4 / kHalves;
+    V8 kf[2][FB][kHalves];
     auto read_keys = [&](int f0, int into) {
 #pragma unroll
       for (int f = 0; f < FB; ++f)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < kHalves; ++b)
           kf[into][f][b] = f0 + f < NK
                                ? lds_read<V8>((ka ^ ((f0 + f) << 5)) + b * 32 * R::kRow)
                                : lds_read<V8>((ta ^ ((f0 + f - NK) << 5)) + b * 32 * (kRope * 2));
@@ -536,7 +538,7 @@ __global__ __launch_bounds__(kAttendWaves * kWave, 2) void attend_kernel(LatentP
 #pragma unroll
       for (int f = 0; f < FB; ++f)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < kHalves; ++b)
           sc[b] = TT::mfma32(kf[(f0 / FB) & 1][f][b], qf[f0 + f], sc[b]);
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -550,10 +552,9 @@ __global__ __launch_bounds__(kAttendWaves * kWave, 2) void attend_kernel(LatentP
     };
     read_values(0, 0);
     if (edge) {
-      const unsigned long long odd =
-          lds_read<unsigned long long>(lds + R::kOdd + (t & 1) * 8);
+      const unsigned odd = lds_read<unsigned>(lds + R::kOdd + (t & 1) * 4);
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+      for (int b = 0; b < kHalves; ++b)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int k = b * 32 + 8 * (e >> 2) + 4 * hi + (e & 3);
@@ -568,7 +569,7 @@ __global__ __launch_bounds__(kAttendWaves * kWave, 2) void attend_kernel(LatentP
     // that the largest weight is 1 whatever the size of its score.
     float top = sc[0][0];
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < kHalves; ++b)
 #pragma unroll
       for (int e = 0; e < 16; ++e) top = fmaxf(top, sc[b][e]);
     top *= sl;
@@ -591,9 +592,9 @@ __global__ __launch_bounds__(kAttendWaves * kWave, 2) void attend_kernel(LatentP
     const float ref = mx == -__builtin_inff() ? 0.0f : mx;
     // The product takes weights of the query type, each off by up to half its step;
     // their sum takes them as they are.
-    V8 pf[4];
+    V8 pf[2 * kHalves];
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < kHalves; ++b)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const float p = __builtin_amdgcn_exp2f(sc[b][e] * sl - ref);
@@ -601,8 +602,8 @@ __global__ __launch_bounds__(kAttendWaves * kWave, 2) void attend_kernel(LatentP
         pf[2 * b + (e >> 3)][e & 7] = (T)p;
       }
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (c + 1 < 4) read_values(c + 1, (c + 1) & 1);
+    for (int c = 0; c < 2 * kHalves; ++c) {
+      if (c + 1 < 2 * kHalves) read_values(c + 1, (c + 1) & 1);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int d = 0; d < ND; ++d) {
