@@ -252,29 +252,35 @@ constexpr int kExpandThreads = 256;
 
 // kDenseTile keys of one head: D = W X^T with the weights' rows (keys' part, then
 // values') as rows and the dense rows as columns, so that a lane's results are
-// four elements in a row of one key. 64 of the L products to a step, through a ring
-// of three stages.
+// four elements in a row of one key; they are turned through LDS into whole lines.
+// 32 of the L products to a step, through a ring of three stages, so that two
+// workgroups share a CU and one's first loads and last stores run beside the other's
+// products.
 template <typename T, int L, int N>
-__global__ __launch_bounds__(kExpandThreads, 1) void expand_kernel(LatentPrefillArgs a, Space w,
+__global__ __launch_bounds__(kExpandThreads, 2) void expand_kernel(LatentPrefillArgs a, Space w,
                                                                    int tiles) {
   typedef Types<T> TT;
   typedef typename TT::V8 V8;
   typedef typename TT::V4 V4;
-  constexpr int kW = 4, kStages = 3, kStep = 64, kRowBytes = kStep * 2;
+  constexpr int kW = 4, kStages = 3, kStep = 32, kRowBytes = kStep * 2;
   constexpr int kX = kDenseTile * kRowBytes, kY = 2 * N * kRowBytes, kStage = kX + kY;
-  constexpr int kXCopies = kDenseTile / 8 / kW, kYCopies = 2 * N / 8 / kW;
+  constexpr int kRows = 1024 / kRowBytes;  // of a copy
+  constexpr int kXCopies = kDenseTile / kRows / kW, kYCopies = 2 * N / kRows / kW;
   constexpr int NY = N / 32;  // 32-row tiles of a wave: half of the weights' rows
-  __shared__ __align__(1024) unsigned char mem[kStages * kStage];
+  constexpr int kOut = 64 * N * 2;  // bytes of a wave's results
+  __shared__ __align__(1024) unsigned char
+      mem[kStages * kStage > kW * kOut ? kStages * kStage : kW * kOut];
+  static_assert(sizeof(mem) <= 163840 / 2 - 256, "two workgroups to a CU");
   const unsigned lds = (unsigned)(uintptr_t)(lds_u8*)mem;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int qi = lane & 31, hi = lane >> 5;
-  // an XCD has all tiles of a head where there are enough of them, so that its
-  // weights stay in its L2
+  // where there are heads for all XCDs, each has its share of them: their weights
+  // stay in its L2, and the heads of a tile of rows meet there
   int h, tile;
   if (a.num_heads % kXcds == 0) {
-    const int b = blockIdx.x / kXcds;
-    h = blockIdx.x % kXcds + b / tiles * kXcds;
-    tile = b % tiles;
+    const int own = a.num_heads / kXcds, b = blockIdx.x / kXcds;
+    h = blockIdx.x % kXcds + b % own * kXcds;
+    tile = b / own;
   } else {
     h = blockIdx.x % a.num_heads;
     tile = blockIdx.x / a.num_heads;
@@ -284,19 +290,23 @@ __global__ __launch_bounds__(kExpandThreads, 1) void expand_kernel(LatentPrefill
   const unsigned char* x = w.lat + d0 * (L * 2);
   const unsigned char* wk = a.wk + h * a.w_head_ld;
   const unsigned char* wv = a.wv + h * a.w_head_ld;
+  // (rows of 64 bytes: chunk c of row r at c ^ (r >> 2 & 3))
+  auto copy = [&](const unsigned char* from, unsigned to) {
+    const int r = lane >> 2;
+    copy16_shared(uniform(from), (unsigned)(r * (L * 2)) + (((lane & 3) ^ ((r >> 2) & 3)) << 4), to);
+  };
   auto fill = [&](int step) {
     const unsigned at = lds + step % kStages * kStage;
 #pragma unroll
     for (int n = 0; n < kXCopies; ++n) {
-      const int r = (wave * kXCopies + n) * 8;
-      copy_rows<kRowBytes>(x + (size_t)r * (L * 2) + step * kRowBytes, L * 2, r,
-                           at + r * kRowBytes);
+      const int r = (wave * kXCopies + n) * kRows;
+      copy(x + (size_t)r * (L * 2) + step * kRowBytes, at + r * kRowBytes);
     }
 #pragma unroll
     for (int n = 0; n < kYCopies; ++n) {
-      const int r = (wave * kYCopies + n) * 8;
+      const int r = (wave * kYCopies + n) * kRows;
       const unsigned char* from = r < N ? wk + (size_t)r * (L * 2) : wv + (size_t)(r - N) * (L * 2);
-      copy_rows<kRowBytes>(from + step * kRowBytes, L * 2, r, at + kX + r * kRowBytes);
+      copy(from + step * kRowBytes, at + kX + r * kRowBytes);
     }
   };
   f32x16 o[NY][2];
@@ -307,8 +317,9 @@ __global__ __launch_bounds__(kExpandThreads, 1) void expand_kernel(LatentPrefill
 #pragma unroll
       for (int e = 0; e < 16; ++e) o[y][c][e] = 0.0f;
   const int half_y = wave & 1, half_x = wave >> 1;
-  const int x_at = (half_x * 64 + qi) * kRowBytes + ((hi ^ swizzle<kRowBytes>(qi)) << 4);
-  const int y_at = kX + (half_y * N + qi) * kRowBytes + ((hi ^ swizzle<kRowBytes>(qi)) << 4);
+  const int turn = (hi ^ ((qi >> 2) & 3)) << 4;
+  const int x_at = (half_x * 64 + qi) * kRowBytes + turn;
+  const int y_at = kX + (half_y * N + qi) * kRowBytes + turn;
   constexpr int kSteps = L / kStep;
   fill(0);
   fill(1);
@@ -337,10 +348,12 @@ __global__ __launch_bounds__(kExpandThreads, 1) void expand_kernel(LatentPrefill
         for (int c = 0; c < 2; ++c) o[y][c] = TT::mfma32(yf[y], xf[c], o[y][c]);
     }
   }
+  // the wave's 64 keys by N elements, to LDS and out
+  barrier();
+  const unsigned own = lds + wave * kOut;
+  constexpr int kChunks = N * 2 / 16;  // of a key
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    T* dst = reinterpret_cast<T*>(w.kv) +
-             ((int64_t)h * w.dense + d0 + half_x * 64 + c * 32 + qi) * (2 * N) + half_y * N + hi * 4;
+  for (int c = 0; c < 2; ++c)
 #pragma unroll
     for (int y = 0; y < NY; ++y)
 #pragma unroll
@@ -348,8 +361,17 @@ __global__ __launch_bounds__(kExpandThreads, 1) void expand_kernel(LatentPrefill
         V4 z;
 #pragma unroll
         for (int e = 0; e < 4; ++e) z[e] = (T)o[y][c][4 * g + e];
-        *reinterpret_cast<V4*>(dst + y * 32 + g * 8) = z;
+        const int key = c * 32 + qi, chunk = (y * 4 + g) ^ (key & (kChunks - 1));
+        lds_write(own + key * (N * 2) + chunk * 16 + hi * 8, z);
       }
+  unsigned char* dst =
+      w.kv + (((int64_t)h * w.dense + d0 + half_x * 64) * (2 * N) + half_y * N) * 2;
+#pragma unroll
+  for (int n = 0; n < kOut / 1024; ++n) {
+    const int key = n * (kWave / kChunks) + lane / kChunks, c = lane % kChunks;
+    const kv_u32x4 z =
+        lds_read<kv_u32x4>(own + key * (N * 2) + ((c ^ (key & (kChunks - 1))) << 4));
+    *reinterpret_cast<kv_u32x4*>(dst + (int64_t)key * (4 * N) + c * 16) = z;
   }
 }
 
