@@ -156,7 +156,7 @@ struct Ring {
   static constexpr int kReqs = kOdd + 8;  // rows of up to kWave requests, 3 words each
   static constexpr int kBytes = kReqs + 12 * kWave;
   static_assert(kBytes <= 163840 - 256, "a CU's LDS");
-  static __device__ int swizzle(int row) { return (row & 7) << 1 | ((row >> 3) & 1); }
+  static __device__ int swizzle(int row) { return (row & 3) << 2 | ((row >> 2) & 3); }
   static __device__ int turned_swizzle(int row) { return (row >> 1) & 7; }
 };
 
@@ -770,7 +770,7 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
     auto read_value = [&](int k) {
       const int c = k / ND, d = k % ND;
       vl[k % (kVAhead + 1)] = lds_columns<V4>(va[d] + c * 16 * R::kRow);
-      vh[k % (kVAhead + 1)] = lds_columns<V4>((va[d] ^ 16) + (c * 16 + 8) * R::kRow);
+      vh[k % (kVAhead + 1)] = lds_columns<V4>((va[d] ^ 32) + (c * 16 + 8) * R::kRow);
     };
     auto read_weight = [&](int c, int t) {
       pw[c & 1][t] = lds_read<V8>((wa ^ (c << 5)) + t * (kRowTile * kKeys * 2));

@@ -233,7 +233,7 @@ __global__ __launch_bounds__(kGatherThreads) void gather_kernel(LatentPrefillArg
 // whose columns it reads transposed, spread over all banks.
 template <int BYTES>
 __device__ inline int swizzle(int r) {
-  return BYTES >= 256 ? (r & 7) << 1 | ((r >> 3) & 1) : ((r >> 1) & 3) << 1 | ((r >> 3) & 1);
+  return BYTES >= 256 ? (r & 3) << 2 | ((r >> 2) & 3) : ((r >> 1) & 1) << 2 | ((r >> 2) & 3);
 }
 
 // One copy of 1024 bytes: rows of BYTES from row r0 of a tile on, `stride` apart in
@@ -569,7 +569,7 @@ __global__ __launch_bounds__(kAttendWaves * kWave, 2) void attend_kernel(LatentP
 #pragma unroll
       for (int d = 0; d < ND; ++d) {
         vl[into][d] = lds_columns<V4>((va ^ (d << 6)) + c * 16 * R::kRow);
-        vh[into][d] = lds_columns<V4>((va ^ (d << 6) ^ 16) + (c * 16 + 8) * R::kRow);
+        vh[into][d] = lds_columns<V4>((va ^ (d << 6) ^ 32) + (c * 16 + 8) * R::kRow);
       }
     };
     read_values(0, 0);
@@ -587,8 +587,6 @@ __global__ __launch_bounds__(kAttendWaves * kWave, 2) void attend_kernel(LatentP
           }
         }
     }
-    // Weights: the product with the scale rounds before the maximum is taken off, so
-    // that the largest weight is 1 whatever the size of its score.
     float top = sc[0][0];
 #pragma unroll
     for (int b = 0; b < kHalves; ++b)
@@ -612,17 +610,28 @@ __global__ __launch_bounds__(kAttendWaves * kWave, 2) void attend_kernel(LatentP
       for (int d = 0; d < ND; ++d) o[d] *= fix;
     }
     const float ref = mx == -__builtin_inff() ? 0.0f : mx;
+    // The product with the scale and the maximum in one rounding: the largest weight is
+    // then 2^d, d up to half a step of its score. Where that could matter (2^-8 at a
+    // score of 2^16), the product rounds first and the largest weight is 1.
+    const bool large = __any(fabsf(ref) > 65536.0f);
     // The product takes weights of the query type, each off by up to half its step;
     // their sum takes them as they are.
     V8 pf[2 * kHalves];
+    auto weigh = [&](auto exponent) {
 #pragma unroll
-    for (int b = 0; b < kHalves; ++b)
+      for (int b = 0; b < kHalves; ++b)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float p = __builtin_amdgcn_exp2f(sc[b][e] * sl - ref);
-        l += p;
-        pf[2 * b + (e >> 3)][e & 7] = (T)p;
-      }
+        for (int e = 0; e < 16; ++e) {
+          const float p = __builtin_amdgcn_exp2f(exponent(sc[b][e]));
+          l += p;
+          pf[2 * b + (e >> 3)][e & 7] = (T)p;
+        }
+    };
+    if (__builtin_expect(large, 0)) {
+      weigh([&](float x) { return x * sl - ref; });
+    } else {
+      weigh([&](float x) { return __builtin_fmaf(x, sl, -ref); });
+    }
 #pragma unroll
     for (int c = 0; c < 2 * kHalves; ++c) {
       if (c + 1 < 2 * kHalves) read_values(c + 1, (c + 1) & 1);
