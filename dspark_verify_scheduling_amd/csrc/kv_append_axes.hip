@@ -14,11 +14,15 @@ constexpr int kThreads = 256;
 __device__ int position_status(const AppendAxesArgs& a, int total_eff) {
   int bits = 0;
   if (a.base.req.B == 0) return bits;
-  for (int x = 0; x < a.num_axes; ++x) {
-    const int32_t* p = a.positions + x * a.positions_ld;
-#pragma unroll 8
-    for (int n = threadIdx.x; n < total_eff; n += kThreads)
-      if (p[n] < 0 || p[n] >= a.base.rope_rows) bits = DSPARK_DATA_BAD_POS;
+#pragma unroll 4
+  for (int n = threadIdx.x; n < total_eff; n += kThreads) {
+    int p[DSPARK_MAX_AXES];  // all axes' loads before the first is looked at
+#pragma unroll
+    for (int x = 0; x < DSPARK_MAX_AXES; ++x)
+      p[x] = a.positions[min(x, a.num_axes - 1) * a.positions_ld + n];
+#pragma unroll
+    for (int x = 0; x < DSPARK_MAX_AXES; ++x)
+      if (p[x] < 0 || p[x] >= a.base.rope_rows) bits = DSPARK_DATA_BAD_POS;
   }
   return bits;
 }
@@ -48,7 +52,7 @@ __global__ __launch_bounds__(kThreads) void append_axes_kernel(AppendAxesArgs a)
                          __builtin_amdgcn_readfirstlane(tid / kRowThreads);
   if (packed >= total_eff) return;
   const int n = (int)packed;
-  RowAppend<T, E8, D, kRowThreads> row(b, n);
+  RowAppend<T, E8, D, kRowThreads, ROWS == 1 ? 1 : 2> row(b, n);
   int pos[DSPARK_MAX_AXES];
   bool bad = false;
 #pragma unroll
@@ -56,45 +60,47 @@ __global__ __launch_bounds__(kThreads) void append_axes_kernel(AppendAxesArgs a)
     pos[x] = a.positions[min(x, a.num_axes - 1) * a.positions_ld + n];
     bad |= pos[x] < 0 || pos[x] >= b.rope_rows;
   }
-  int r, j;
-  rows_requests<1>(q, n, total_eff, (int64_t)q.width << b.kv.page_shift, 0x7FFFFFFF, &r, &j);
+  const int li = lane & (LPH - 1), half = b.rope_dim >> 1;
+  const bool turned = 8 * li < b.rope_dim;
+  const bool low = b.rope_interleaved || 8 * li < half;
+  // the lane's first pair; its pairs' axes stand in one word
+  const int i0 = !turned ? 0 : b.rope_interleaved ? 4 * li : (low ? 8 * li : 8 * li - half);
+  const uint64_t axes = a.axis[i0 >> 5] >> (2 * (i0 & 31));
+  int swap = lane;  // lane that holds the other elements of the pairs
+  if (turned && !b.rope_interleaved) swap = low ? lane + half / 8 : lane - half / 8;
+  int r, j, prefix;
+  rows_requests<1>(q, n, total_eff, (int64_t)q.width << b.kv.page_shift, 0x7FFFFFFF, &r, &j, &prefix);
   r = __builtin_amdgcn_readfirstlane(r);
   j = __builtin_amdgcn_readfirstlane(j);
   if (j < 0 || bad) return;
-  const int64_t slot = (int64_t)q.prefix[r] + j;
+  const int64_t slot = (int64_t)__builtin_amdgcn_readfirstlane(prefix) + j;
   const int id = q.table[(size_t)r * q.width + (slot >> b.kv.page_shift)];
-  if (id < 0 || id >= b.kv.num_blocks) return;
 
-  const int li = lane & (LPH - 1), half = b.rope_dim >> 1;
-  const bool turned = 8 * li < b.rope_dim;
-  int swap = lane;  // lane that holds the other elements of the pairs
   // the table's entry of a pair
-  auto turn = [&](int i, float* c, float* s) {
-    const int x = (int)(a.axis[i >> 5] >> (2 * (i & 31))) & 3;
+  auto turn = [&](int e, float* c, float* s) {
+    const int x = (int)(axes >> (2 * e)) & 3;
     const int p = x < 2 ? (x == 0 ? pos[0] : pos[1]) : (x == 2 ? pos[2] : pos[3]);
-    const float* cs = b.rope + (size_t)p * b.rope_dim;
-    *c = cs[i];
-    *s = cs[half + i];
+    const float* cs = b.rope + (size_t)p * b.rope_dim + i0 + e;
+    *c = cs[0];
+    *s = cs[half];
   };
   float co[8], si[8];
   if (b.rope_interleaved) {
-    const int i0 = turned ? 4 * li : 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      turn(i0 + e, &co[2 * e], &si[2 * e + 1]);
+      turn(e, &co[2 * e], &si[2 * e + 1]);
       co[2 * e + 1] = co[2 * e];
       si[2 * e] = -si[2 * e + 1];
     }
   } else {
-    const bool low = 8 * li < half;
-    const int i0 = turned ? (low ? 8 * li : 8 * li - half) : 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      turn(i0 + e, &co[e], &si[e]);
+      turn(e, &co[e], &si[e]);
       si[e] = low ? -si[e] : si[e];
     }
-    if (turned) swap = low ? lane + half / 8 : lane - half / 8;
   }
+  // after the gather, which then waits along with the table's entry
+  if (id < 0 || id >= b.kv.num_blocks) return;
   row.finish(id, (int)(slot & ((1 << b.kv.page_shift) - 1)), co, si, turned, swap);
 }
 

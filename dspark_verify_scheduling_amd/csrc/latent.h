@@ -111,12 +111,12 @@ __device__ inline bool span_of(const ReqView& q, int c, int total_eff, int64_t r
 
 // The requests of the packed rows first .. first + N - 1, lane i of the wave for
 // row first + i: *r the request, *j the row's index in it, -1 where the row
-// belongs to no well-formed one. All lanes of the wave call it together. 64
+// belongs to no well-formed one, *prefix the request's. All lanes of the wave call it together. 64
 // steps of the search at once and its rows together, so that a batch of up to
 // 64 requests costs two memory latencies.
 template <int N>
 __device__ inline void rows_requests(const ReqView& q, int first, int total_eff, int64_t reach,
-                                     int64_t most, int* r, int* j) {
+                                     int64_t most, int* r, int* j, int* prefix) {
   const int lane = lane_id();
   int lo[N];
 #pragma unroll
@@ -137,12 +137,13 @@ __device__ inline void rows_requests(const ReqView& q, int first, int total_eff,
 #pragma unroll
   for (int i = 1; i < N; ++i) req = lane == i ? lo[i] : req;
   const int row = first + lane;
-  auto index_in = [&](int c, int x) {
-    int s, e, prefix;
-    return span_of(q, c, total_eff, reach, most, &s, &e, &prefix) && s <= x && x < e ? x - s : -1;
+  auto index_in = [&](int c, int x, int* before) {
+    int s, e;
+    return span_of(q, c, total_eff, reach, most, &s, &e, before) && s <= x && x < e ? x - s : -1;
   };
+  *prefix = 0;
   const bool mine = lane < N && row < total_eff;
-  int at = mine ? index_in(req, row) : -1;
+  int at = mine ? index_in(req, row, prefix) : -1, other;
   // Words out of order mislead the search: rows that it does not find are looked
   // for in every request and go to the first that holds them. (Rows of none are
   // too: those of a malformed request, or before the first.)
@@ -152,11 +153,11 @@ __device__ inline void rows_requests(const ReqView& q, int first, int total_eff,
     lost &= lost - 1;
     for (int c0 = 0; c0 < q.B; c0 += kWave) {
       const unsigned long long h =
-          __ballot(c0 + lane < q.B && index_in(c0 + lane, first + i) >= 0);
+          __ballot(c0 + lane < q.B && index_in(c0 + lane, first + i, &other) >= 0);
       if (!h) continue;
       if (lane == i) {
         req = c0 + (int)__builtin_ctzll(h);
-        at = index_in(req, row);
+        at = index_in(req, row, prefix);
       }
       break;
     }

@@ -56,7 +56,7 @@ __device__ int tree_status(const LatentAppendArgs& a, int total_eff, int64_t mos
 struct Turn {
   float co[8], si[8];
   int swap;
-  __device__ __forceinline__ Turn(const float* cs, bool interleaved, int lane) {
+  __device__ __forceinline__ void load(const float* cs, bool interleaved, int lane) {
     const int li = lane & 7;
     swap = lane;
     if (interleaved) {
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(kThreads) void latent_append_kernel(LatentAppendArg
   const unsigned char* x = a.x + (size_t)packed * a.x_ld;
   const unsigned char* heads = a.q + (size_t)packed * a.q_ld;
   // loaded with the reads that say where the row goes
-  T8 lat = {}, weight = {}, next = {};
+  T8 lat = {}, weight = {}, next[2];
   if (sub == 0 && lane < kLanes) {
     lat = *(reinterpret_cast<const T8*>(x) + lane);
     if (a.weight) weight = *(reinterpret_cast<const T8*>(a.weight) + lane);
@@ -144,13 +144,14 @@ __global__ __launch_bounds__(kThreads) void latent_append_kernel(LatentAppendArg
     return v;
   };
   int h = sub * 8 + (lane >> 3) - 1;
-  next = load(h);
-  int r, j;
-  rows_requests<1>(q, (int)packed, total_eff, reach, most, &r, &j);
+  next[0] = load(h);
+  next[1] = load(h + 8 * split);
+  int r, j, prefix;
+  rows_requests<1>(q, (int)packed, total_eff, reach, most, &r, &j, &prefix);
   r = __builtin_amdgcn_readfirstlane(r);
   j = __builtin_amdgcn_readfirstlane(j);
+  prefix = __builtin_amdgcn_readfirstlane(prefix);
   if (j < 0) return;
-  const int prefix = q.prefix[r];
   const int64_t slot = (int64_t)prefix + j;
   const int id = q.table[(size_t)r * q.width + (slot >> a.kv.page_shift)];
   int depth = j;
@@ -160,9 +161,12 @@ __global__ __launch_bounds__(kThreads) void latent_append_kernel(LatentAppendArg
     depth = 0;
     for (int n = j; n > 0; n = __builtin_amdgcn_readlane(par, n - 1)) ++depth;
   }
-  if (id < 0 || id >= a.kv.num_blocks) return;
   const int64_t pos = (int64_t)prefix + depth;
   if (a.rope && pos >= a.rope_rows) return;
+  Turn turn;
+  if (a.rope) turn.load(a.rope + (size_t)pos * kRope, a.rope_interleaved, lane);
+  // after the table's rotations, which then wait along with the page's id
+  if (id < 0 || id >= a.kv.num_blocks) return;
   const int off = (int)(slot & ((1 << a.kv.page_shift) - 1));
 
   if (sub == 0) {
@@ -215,18 +219,14 @@ __global__ __launch_bounds__(kThreads) void latent_append_kernel(LatentAppendArg
     if (to < a.num_heads)
       *(reinterpret_cast<T8*>(to < 0 ? own : out + to * a.q_out_head_ld) + (lane & 7)) = v;
   };
-  if (a.rope) {
-    const Turn turn(a.rope + (size_t)pos * kRope, a.rope_interleaved, lane);
-    for (; h - (lane >> 3) < a.num_heads; h += 8 * split) {
-      const T8 v = next;
-      next = load(h + 8 * split);
-      store(h, turn.template of<T>(v, a.rope_interleaved));
-    }
-  } else {
-    for (; h - (lane >> 3) < a.num_heads; h += 8 * split) {
-      const T8 v = next;
-      next = load(h + 8 * split);
-      store(h, v);
+  // two loads under way, each in registers of its own
+  for (; h - (lane >> 3) < a.num_heads; h += 16 * split) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int to = h + 8 * split * i;
+      const T8 v = next[i];
+      next[i] = load(to + 16 * split);
+      store(to, a.rope ? turn.template of<T>(v, a.rope_interleaved) : v);
     }
   }
 }
@@ -257,11 +257,11 @@ __global__ __launch_bounds__(kThreads) void latent_read_kernel(LatentReadArgs a)
   }
   const int64_t row0 = a.first_row + ((int64_t)(blockIdx.x - 1) * kWaves + wave) * kReadRows;
   if (row0 >= total_eff) return;
-  int r, j, id = -1, off = 0;
+  int r, j, prefix, id = -1, off = 0;
   rows_requests<kReadRows>(q, (int)row0, total_eff, (int64_t)q.width << a.kv.page_shift,
-                           0x7FFFFFFF, &r, &j);
+                           0x7FFFFFFF, &r, &j, &prefix);
   if (j >= 0) {
-    const int64_t slot = (int64_t)q.prefix[r] + j;
+    const int64_t slot = (int64_t)prefix + j;
     id = q.table[(size_t)r * q.width + (slot >> a.kv.page_shift)];
     if (id >= a.kv.num_blocks) id = -1;
     off = (int)(slot & ((1 << a.kv.page_shift) - 1));
