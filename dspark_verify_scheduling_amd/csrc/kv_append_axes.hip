@@ -34,6 +34,7 @@ __device__ int position_status(const AppendAxesArgs& a, int total_eff) {
 template <typename T, bool E8, int D, int ROWS>
 __global__ __launch_bounds__(kThreads) void append_axes_kernel(AppendAxesArgs a) {
   constexpr int LPH = D / 8, kRowThreads = kThreads / ROWS;
+  fetch_args<sizeof(a)>();
   const AppendArgs& b = a.base;
   const ReqView& q = b.req;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);

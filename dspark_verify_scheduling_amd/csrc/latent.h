@@ -98,6 +98,21 @@ hipError_t launch_latent_prefill(const LatentPrefillArgs& a, dspark_dtype dt, hi
 size_t latent_prefill_workspace(int B, int max_rows, int max_keys, int num_heads, int nope,
                                 int latent_dim);
 
+// The lines of a kernel's first `BYTES` of arguments, read together. The compiler
+// reads an argument where it is first used, and each new line is then a round trip
+// to where the launch left it, one after the other.
+template <size_t BYTES>
+__device__ __forceinline__ void fetch_args() {
+  typedef __attribute__((address_space(4))) const unsigned u32;
+  const u32* p = (const u32*)__builtin_amdgcn_kernarg_segment_ptr();
+  constexpr int kLines = (BYTES + 63) / 64;
+  unsigned x[kLines];
+#pragma unroll
+  for (int i = 0; i < kLines; ++i) x[i] = p[i * 16];
+#pragma unroll
+  for (int i = 0; i < kLines; ++i) asm volatile("" ::"s"(x[i]));
+}
+
 // Whether request c's rows are well formed as far as its words say (its tree and
 // page ids apart), and where they are. Rows in all: `most`.
 __device__ inline bool span_of(const ReqView& q, int c, int total_eff, int64_t reach, int64_t most,

@@ -16,6 +16,8 @@ using attn::f32x16;
 using attn::kLn2;
 using attn::kLog2e;
 using attn::lds_columns;
+using attn::lds_columns8;
+using attn::lds_i32x2;
 using attn::lds_read;
 using attn::lds_u8;
 using attn::lds_write;
@@ -59,6 +61,12 @@ struct Parts {
   int rows;       // rows of a segment, at most
 };
 
+// Units that a segment counts for before its first: its start and end (queries in,
+// outputs out) take as long as some tiles do. In equal shares of the units alone, the
+// workgroups with two segments were last, by 13 us (16 trees of up to 17 rows, 32
+// heads, 8 bits: 144 us; with 2, 4, 6, 8 units a segment 126, 121, 114, 120).
+constexpr int kSetup = 6;
+
 // Rows of a request: m = j * heads + h for row j and head h, in tiles of kRowTile,
 // up to row_tiles(L) tiles to a segment.
 struct Shape {
@@ -67,6 +75,7 @@ struct Shape {
   int nseg, per;  // segments side by side, tiles of each
   int keys;
   int nku;        // units along the keys
+  __device__ int64_t units() const { return (int64_t)nseg * (nku + kSetup); }
 };
 
 // Whether a request's rows are well formed (its tree and pages apart); their
@@ -97,16 +106,12 @@ __device__ inline Shape shape_of(int heads, int c0, int len, int prefix) {
 
 template <int L>
 __device__ inline int64_t units_of(int heads, int c0, int len, int prefix) {
-  const Shape s = shape_of<L>(heads, c0, len, prefix);
-  return (int64_t)s.nseg * s.nku;
+  return shape_of<L>(heads, c0, len, prefix).units();
 }
 
-// Workgroups that get units: a share is kLeast of them or more, since every part
-// of a segment costs its rows' outputs twice through memory.
-constexpr int kLeast = 2;
-__device__ inline int wgs_in_use(int64_t total, int wgs) {
-  return (int)min((int64_t)wgs, (total + kLeast - 1) / kLeast);
-}
+// Workgroups that get units. A unit each where there are few: the launch is then one
+// tile's latency (a context of 1500 at 32 heads: 18.2 us; two units each, 19.5).
+__device__ inline int wgs_in_use(int64_t total, int wgs) { return (int)min((int64_t)wgs, total); }
 
 // Workgroups go to the eight XCDs in turn. Shares are numbered so that an XCD's
 // are consecutive: the segments of a request then meet in one L2.
@@ -115,24 +120,31 @@ __device__ inline int share_of(int wg, int wgs) {
   return wgs % kXcds ? wg : wg % kXcds * (wgs / kXcds) + wg / kXcds;
 }
 
-// The first unit of share w of n <= total.
-__device__ inline int64_t wg_start(int64_t total, int w, int n) { return total * w / n; }
+// The first unit of share w of n <= total. (A division in 64 bits is a hundred
+// instructions, which a workgroup's start would fetch.)
+__device__ inline int64_t wg_start(int64_t total, int w, int n) {
+  const int64_t x = total * w;
+  return x >> 32 ? x / n : (int64_t)((unsigned)x / (unsigned)n);
+}
 
 // LDS of a workgroup. A tile is kKeys latents in 16 bits and their rotated parts,
 // unpadded; 16-byte chunk c of latent row r lies at chunk c ^ swizzle(r), so that
 // the rows which a wave reads at one column, and the eight rows whose columns it
 // reads transposed, spread over all banks.
 //   16-bit caches: a ring of kStages tiles, filled straight from memory.
-//   8-bit caches: a ring of codes, exponents and rotated parts; each wave widens
-//   its rows of the next tile's latents into one tile.
+//   8-bit caches: the same ring of codes, with the rows' exponents; a code becomes a
+//   16-bit operand between the products that read it (four conversions to a product
+//   take no time of their own: 34 cycles instead of 32). Widened into a tile of its
+//   own first, 16 trees of up to 17 rows took 160 us instead of 144.
 template <bool E8, int L>
 struct Ring {
   static constexpr int CB = E8 ? 1 : 2;
   static constexpr int W = waves(L);
   static constexpr int kOwn = kKeys / W;  // keys of a tile that a wave copies
   static constexpr int kMaxRows = row_tiles(L) * kRowTile;
-  static constexpr int kRow = 2 * L;
+  static constexpr int kRow = CB * L;
   static constexpr int kLat = kKeys * kRow;
+  static constexpr int kGroups = L / kLatGroup;  // exponents of a row
   static constexpr int kTurned = kKeys * kRope * 2;
   static constexpr int kChunks = L * CB / 16;  // of a cache row
   static constexpr int kRowsPerCopy = kWave / kChunks;
@@ -140,11 +152,11 @@ struct Ring {
   static constexpr int kTurnedCopies = kOwn / 8;
   static_assert(kCopies * kRowsPerCopy == kOwn && kOwn <= 16, "whole copies of one page");
   static constexpr int kPerWave = kCopies + kTurnedCopies + (E8 ? 1 : 0);
-  static constexpr int kPiece = kOwn * L + 64;  // codes, exponents; 8 bits
-  static constexpr int kTurnedAt = E8 ? W * kPiece : kLat;  // in a stage
+  static constexpr int kPowers = kLat;  // in a stage: exponents, 64 bytes a wave; 8 bits
+  static constexpr int kTurnedAt = kLat + (E8 ? W * 64 : 0);
   static constexpr int kStage = kTurnedAt + kTurned;
-  static constexpr int kStages = L == 512 ? 2 : 3;
-  static constexpr int kRing = E8 ? kLat : 0;  // offset of the ring
+  static constexpr int kStages = L == 512 && !E8 ? 2 : 3;
+  static constexpr int kRing = 0;  // offset of the ring
   // weights in 16 bits: [row][kKeys], 16-byte chunks c of row r at c ^ (r >> 1 & 7)
   static constexpr int kWeights = kRing + kStages * kStage;
   // of the waves' rows: largest score, or sum, of each half of the keys
@@ -154,9 +166,15 @@ struct Ring {
   // rows with NaN or infinity, kOwn bits for each wave
   static constexpr int kOdd = kFlag + 8;
   static constexpr int kReqs = kOdd + 8;  // rows of up to kWave requests, 3 words each
-  static constexpr int kBytes = kReqs + 12 * kWave;
+  // what a key's weights lose in exponent, 16 bits a key for each wave; 8 bits
+  static constexpr int kDown = kReqs + 12 * kWave;
+  static constexpr int kBytes = kDown + (E8 ? W * kKeys * 2 : 0);
+  static_assert(kStage % 256 == 0 && kDown % 16 == 0, "a swizzle is an exclusive or of addresses");
   static_assert(kBytes <= 163840 - 256, "a CU's LDS");
-  static __device__ int swizzle(int row) { return (row & 3) << 2 | ((row >> 2) & 3); }
+  static __device__ int swizzle(int row) {
+    return E8 ? (row & 3) << 1 | (row & 8) | ((row >> 2) & 1)
+              : (row & 3) << 2 | ((row >> 2) & 3);
+  }
   static __device__ int turned_swizzle(int row) { return (row >> 1) & 7; }
 };
 
@@ -208,15 +226,27 @@ __device__ __forceinline__ Span next_span(const LatentAttnArgs& a, unsigned reqs
     len = __builtin_amdgcn_readfirstlane(len);
     prefix = __builtin_amdgcn_readfirstlane(prefix);
     const Shape s = shape_of<L>(a.num_heads, c0, len, prefix);
-    if (c.off >= (len ? (int64_t)s.nseg * s.nku : 0)) {
+    if (c.off >= (len ? s.units() : 0)) {
       ++c.r;
       c.off = 0;
       continue;
     }
-    const int seg = __builtin_amdgcn_readfirstlane((int)(c.off / s.nku));
-    const int ku0 = (int)(c.off - (int64_t)seg * s.nku);
+    // (off < 2^9 segments of less than 2^26: the estimate is one off at most)
+    const int stride = s.nku + kSetup;
+    int seg = (int)((float)c.off * __builtin_amdgcn_rcpf((float)stride));
+    seg += (int64_t)(seg + 1) * stride <= c.off ? 1 : 0;
+    seg = __builtin_amdgcn_readfirstlane(seg - ((int64_t)seg * stride > c.off ? 1 : 0));
+    const int within = (int)(c.off - (int64_t)seg * stride);
+    const int n = __builtin_amdgcn_readfirstlane((int)min((int64_t)(stride - within), c.left));
+    c.off += n;
+    c.left -= n;
+    const int ku0 = max(within - kSetup, 0);
+    j.n = n - max(kSetup - within, 0);
+    if (j.n <= 0) {
+      j.n = 0;
+      continue;
+    }
     j.r = c.r;
-    j.n = (int)min((int64_t)(s.nku - ku0), c.left);
     j.first = ku0 * kKeys;
     j.keys = s.keys;
     if (job) {
@@ -227,8 +257,6 @@ __device__ __forceinline__ Span next_span(const LatentAttnArgs& a, unsigned reqs
       job->slot = 2 * c.share + c.begun;
     }
     c.begun = 1;
-    c.off += j.n;
-    c.left -= j.n;
     break;
   }
   return j;
@@ -248,42 +276,57 @@ struct Feeder {
   int stage;
   unsigned none;   // bit per stage: some page of its tile is none
 
-  // The pages of 64 tiles from tile t on, a tile to a lane.
-  static __device__ int fetch(const LatentAttnArgs& a, const Span& x, int t, int wave, u64* bad) {
-    int own = 0;
-    const int64_t first = (int64_t)x.first + (int64_t)(t + lane_id()) * kKeys;
+  // The pages of 64 tiles of x from tile t on, a tile to a lane: the loads,
+  struct Pages {
     int id[kKeys / 16];
+  };
+  static __device__ __forceinline__ Pages ask(const LatentAttnArgs& a, const Span& x, int t) {
+    Pages p;
+    const int64_t first = (int64_t)x.first + (int64_t)(t + lane_id()) * kKeys;
 #pragma unroll
     for (int g = 0; g < kKeys / 16; ++g)
-      id[g] = a.req.table[(size_t)x.r * a.req.width +
-                          ((int)min(first + g * 16, (int64_t)x.keys - 1) >> a.kv.page_shift)];
+      p.id[g] = a.req.table[(size_t)x.r * a.req.width +
+                            ((int)min(first + g * 16, (int64_t)x.keys - 1) >> a.kv.page_shift)];
+    return p;
+  }
+  // and what the wave keeps of them.
+  static __device__ __forceinline__ int take(const LatentAttnArgs& a, const Pages& p, int wave,
+                                             u64* bad) {
+    int own = 0;
     u64 b = 0;
 #pragma unroll
     for (int g = 0; g < kKeys / 16; ++g) {
-      const bool none = id[g] < 0 || id[g] >= a.kv.num_blocks;
+      const bool none = p.id[g] < 0 || p.id[g] >= a.kv.num_blocks;
       b |= __ballot(none);
       // a page that is none: any valid one, its keys are masked
-      if (g == wave * R::kOwn / 16) own = none ? 0 : id[g];
+      if (g == wave * R::kOwn / 16) own = none ? 0 : p.id[g];
     }
     *bad = b;
     settle(own);
     return own;
   }
 
-  __device__ void start(const LatentAttnArgs& a, unsigned lds, const Cursor& from, int wave) {
-    c = from;
-    j = next_span<L>(a, lds + R::kReqs, c, nullptr);
-    ids = fetch(a, j, 0, wave, &bad);
+  // Of the share's first segment, at whose end `after` is.
+  __device__ __forceinline__ void start(const LatentAttnArgs& a, const Span& first,
+                                        const Cursor& after, const Pages& p, int wave) {
+    c = after;
+    j = first;
+    ids = take(a, p, wave, &bad);
     t = idx = stage = 0;
-    end = min(j.n, kWave);
+    end = __builtin_amdgcn_readfirstlane(min(j.n, kWave));
     none = 0;
-  }
-  // The segment after the first: once the first's copies have started.
-  __device__ void look_ahead(const LatentAttnArgs& a, unsigned lds, int wave) {
-    nj = next_span<L>(a, lds + R::kReqs, c, nullptr);
+    nj.n = 0;
     nids = 0;
     nbad = 0;
-    if (nj.n > 0) nids = fetch(a, nj, 0, wave, &nbad);
+  }
+  // The segment after it: its pages are asked for, and taken later.
+  __device__ __forceinline__ Pages look_ahead(const LatentAttnArgs& a, unsigned lds) {
+    nj = next_span<L>(a, lds + R::kReqs, c, nullptr);
+    Pages p;
+#pragma unroll
+    for (int g = 0; g < kKeys / 16; ++g) p.id[g] = 0;
+    if (nj.n > 0) p = ask(a, nj, 0);
+    return p;
   }
 
   // The wave's copies of the next tile: begin(), each of the kPerWave copies once, so
@@ -308,10 +351,10 @@ struct Feeder {
     const int lane = lane_id(), row0 = wave * R::kOwn;
     if constexpr (N < R::kCopies) {
       const int r = N * R::kRowsPerCopy + lane / R::kChunks;
-      const int chunk = E8 ? lane % R::kChunks : (lane % R::kChunks) ^ R::swizzle(row0 + r);
+      const int chunk = (lane % R::kChunks) ^ R::swizzle(row0 + r);
       copy16_shared(from + N * R::kRowsPerCopy * L * R::CB,
                     (lane / R::kChunks) * L * R::CB + (unsigned)chunk * 16,
-                    at + (E8 ? wave * R::kPiece : row0 * R::kRow) + N * 1024);
+                    at + row0 * R::kRow + N * 1024);
     } else if constexpr (N < R::kCopies + R::kTurnedCopies) {
       constexpr int n = N - R::kCopies;
       copy16_shared(turned + n * 1024,
@@ -320,10 +363,16 @@ struct Feeder {
                     at + R::kTurnedAt + row0 * (kRope * 2) + n * 1024);
     } else {
       constexpr int kBytes = R::kOwn * (L / kLatGroup);
-      if (lane < kBytes / 4) copy4(exps, lane * 4, at + wave * R::kPiece + R::kOwn * L);
+      if (lane < kBytes / 4) copy4(exps, lane * 4, at + R::kPowers + wave * 64);
     }
   }
 
+  // end_tile() before the segment's last tile, and before any page is known to be none
+  __device__ __forceinline__ void end_tile_within() {
+    none = (none & ~(1u << stage)) | ((unsigned)(bad >> idx) & 1u) << stage;
+    stage = stage + 1 == R::kStages ? 0 : stage + 1;
+    ++idx;
+  }
   __device__ __forceinline__ void end_tile(const LatentAttnArgs& a, unsigned lds, int wave) {
     if (end == 0) return;
     if (__builtin_expect((bad | none) != 0, 0))
@@ -332,19 +381,28 @@ struct Feeder {
     if (__builtin_expect(++idx == end, 0)) {
       t += end;
       idx = 0;
-      if (t < j.n) {
-        ids = fetch(a, j, t, wave, &bad);
-      } else {
+      const bool more = t < j.n;
+      if (!more) {
         j = nj;
         ids = nids;
         bad = nbad;
         t = 0;
-        if (j.n > 0) {
-          nj = next_span<L>(a, lds + R::kReqs, c, nullptr);
-          if (nj.n > 0) nids = fetch(a, nj, 0, wave, &nbad);
+        if (j.n > 0) nj = next_span<L>(a, lds + R::kReqs, c, nullptr);
+      }
+      Span x = nj;
+      if (more) x = j;
+      if (more || (j.n > 0 && nj.n > 0)) {
+        u64 b;
+        const int got = take(a, ask(a, x, t), wave, &b);
+        if (more) {
+          ids = got;
+          bad = b;
+        } else {
+          nids = got;
+          nbad = b;
         }
       }
-      end = min(j.n - t, kWave);
+      end = __builtin_amdgcn_readfirstlane(min(j.n - t, kWave));
     }
   }
 
@@ -393,6 +451,26 @@ __device__ inline void store_columns(T* row, const float (&y)[16]) {
   }
 }
 
+// Eight codes of a row or column and their exponent's power of two as an operand.
+template <typename V8>
+__device__ __forceinline__ V8 widen(unsigned x, unsigned y, float power) {
+  kv_u32x4 z;
+  z[0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, power, false));
+  z[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, power, true));
+  z[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(y, power, false));
+  z[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(y, power, true));
+  return __builtin_bit_cast(V8, z);
+}
+
+// What lane l meets in step N of six that bring a maximum of all lanes into the last:
+// neighbours in a pair and in a quad, mirrors of 8 and 16 lanes, the row and the half
+// before.
+template <int N>
+__device__ __forceinline__ int across(int x) {
+  constexpr int kSteps[6] = {0xB1, 0x4E, 0x141, 0x140, 0x142, 0x143};
+  return __builtin_amdgcn_update_dpp(x, x, kSteps[N], 0xF, 0xF, false);
+}
+
 template <int N>
 struct Index {
   static constexpr int value = N;
@@ -400,8 +478,8 @@ struct Index {
 
 // A segment: some row tiles over some units of the keys, which the waves bring into
 // LDS together. (Tiles without rows, and those of a request whose tree is none, are
-// computed with zeros for queries and not written.) Wave (t, half) = (wave / 2, wave % 2) has row tile t and half the
-// keys of a tile for the scores, and a share of the columns for the outputs:
+// computed and not written.) Wave (t, half) = (wave / 2, wave % 2) has row tile t and
+// half the keys of a tile for the scores, and a share of the columns for the outputs:
 //   S^T = K Q^T: keys are its rows and queries its columns, so a lane holds the
 //   scores of one query (lane & 31) for sixteen keys, four in a row each. Its
 //   weights go to LDS as the operand of
@@ -412,8 +490,8 @@ struct Index {
 // halves' maxima meet in LDS, the weights are taken again and the outputs shrink.
 template <typename T, bool E8, int L>
 __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws, const Span& span,
-                                        const Job& job, bool good, Feeder<E8, L>& feed, unsigned lds,
-                                        int& stage, int& tick) {
+                                        const Job& job, bool first, Cursor after, Feeder<E8, L>& feed,
+                                        unsigned lds, int& stage, int& tick) {
   typedef Types<T> TT;
   typedef typename TT::V8 V8;
   typedef typename TT::V4 V4;
@@ -430,25 +508,14 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
   const int m = (job.tile0 + tile) * kRowTile + qi;
   const int qrow = m / a.num_heads;  // the request's row that the lane's query belongs to
 
-  // rows of the step's own tree that the lane's query sees, bit l for row l + 1;
-  // row 0 is everybody's. Bit l of anc, in lane l, is row l + 1 itself, with its
-  // ancestors' bits.
-  unsigned long long seen = qrow >= 64 ? ~0ull : (1ull << qrow) - 1;
-  if (a.req.parents) {
-    int up = lane + 1 < len ? a.req.parents[(size_t)span.r * a.req.gamma + lane] : 0;
-    unsigned long long anc = 1ull << lane;
-    for (int i = 0; i < 6; ++i) {
-      const int from = max(up - 1, 0);
-      const unsigned long long more = __shfl(anc, from, kWave);
-      const int next = __shfl(up, from, kWave);
-      if (up > 0) {
-        anc |= more;
-        up = next;
-      }
-    }
-    const unsigned long long path = __shfl(anc, max(qrow - 1, 0) & 63, kWave);
-    seen = qrow > 0 ? path : 0;
-  }
+  // A share's first segment starts the ring. What it reads is asked for in one go:
+  // its pages, its rows' parents, its queries; then the first tiles; then the next
+  // segment's pages.
+  typename Feeder<E8, L>::Pages pages;
+  if (first) pages = feed.ask(a, span, 0);
+  int up = 0;
+  if (a.req.parents && lane + 1 < len)
+    up = a.req.parents[(size_t)span.r * a.req.gamma + lane];
   // Scores in units of log2 with a positive factor, so that a masked score stays
   // -infinity under it: the scale's sign and its zero go into the queries.
   float sl = fminf(fabsf(a.scale) * kLog2e, 3.4028235e38f);
@@ -470,7 +537,7 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
     for (int i = 0; i < 2; ++i) {
       const int mm = (job.tile0 + tile) * kRowTile + row4 + 16 * i;
       const int r = mm / a.num_heads, head = mm - r * a.num_heads;
-      const bool there = good && tile < job.mt && mm < s.mrows && !flat;
+      const bool there = tile < job.mt && mm < s.mrows && !flat;
       const size_t row = (size_t)(s.c0 + r);
       const unsigned char* ql = a.ql + row * a.ql_ld + head * a.ql_head_ld + chunk * 16;
       const unsigned char* qr = a.qr + row * a.qr_ld + head * a.qr_head_ld + chunk * 16;
@@ -484,6 +551,20 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
                                                            : qr + (f - i - NL) * 32);
       }
     }
+    bool second = false;
+    if (first) {
+      feed.start(a, span, after, pages, wave);
+      feed.begin(a, lds, wave);
+      feed.copies(wave);
+      pages = feed.look_ahead(a, lds);
+      second = R::kStages > 2 && span.n > 1;
+      if (second) {
+        feed.end_tile_within();
+        feed.begin(a, lds, wave);
+        feed.copies(wave);
+      }
+    }
+    // (a key's codes are read sixteen to a lane, for two products)
     const unsigned own = lds + R::kWeights + wave * 2048;
 #pragma unroll
     for (int f = 0; f < NF; f += 2) {
@@ -495,7 +576,9 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        qf[f + i] = lds_read<V8>(own + qi * 64 + (((2 * i + hi) ^ ((qi >> 2) & 3)) << 4));
+        qf[f + i] = lds_read<V8>(
+            own + qi * 64 +
+            (((E8 && f < NL ? 2 * hi + i : 2 * i + hi) ^ ((qi >> 2) & 3)) << 4));
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -503,6 +586,36 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
       for (int d = 0; d < ND; ++d)
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[t][d][e] = 0.0f;
+    if (first) {
+      if (feed.nj.n > 0) feed.nids = feed.take(a, pages, wave, &feed.nbad);
+      feed.end_tile(a, lds, wave);
+      if (R::kStages > 2 && !second) {
+        feed.begin(a, lds, wave);
+        feed.copies(wave);
+        feed.end_tile(a, lds, wave);
+      }
+    }
+  }
+  // rows of the step's own tree that the lane's query sees, bit l for row l + 1;
+  // row 0 is everybody's. Bit l of anc, in lane l, is row l + 1 itself, with its
+  // ancestors' bits.
+  unsigned long long seen = qrow >= 64 ? ~0ull : (1ull << qrow) - 1;
+  bool good = true;  // the parents are a tree's
+  if (a.req.parents) {
+    settle(up);
+    good = __ballot(up < 0 || up > lane) == 0;
+    unsigned long long anc = 1ull << lane;
+    for (int i = 0; i < 6; ++i) {
+      const int from = max(up - 1, 0);
+      const unsigned long long more = __shfl(anc, from, kWave);
+      const int next = __shfl(up, from, kWave);
+      if (up > 0) {
+        anc |= more;
+        up = next;
+      }
+    }
+    const unsigned long long path = __shfl(anc, max(qrow - 1, 0) & 63, kWave);
+    seen = qrow > 0 ? path : 0;
   }
 
   // lane's offsets in a tile: its chunk of a latent and of a rotated part (of its
@@ -510,16 +623,33 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
   const int key_row = half * 32 + qi;
   const int lat_at = key_row * R::kRow + ((hi ^ R::swizzle(key_row)) << 4);
   const int turned_at = key_row * (kRope * 2) + ((hi ^ R::turned_swizzle(key_row)) << 4);
-  const int t4 = lane & 15, vrow = hi * 4 + (t4 >> 2);
+  const int t4 = lane & 15;
   // (a swizzle changes bits 4 to 7 of an address: what lies above is a sum)
-  const int val_at =
-      vrow * R::kRow +
-      (((((lane >> 4) & 1) * 2 + ((t4 >> 1) & 1) + (wave * ND & 3) * 4) ^ R::swizzle(vrow)) << 4) +
-      (t4 & 1) * 8 + (wave * ND >> 2) * 256;
+  int val_at;
+  if constexpr (E8) {
+    const int vrow = (t4 >> 3) * 8 + hi * 4 + ((t4 >> 1) & 3);
+    val_at = vrow * R::kRow +
+             ((((lane >> 4) & 1) + (wave * ND * 2 & 15)) ^ R::swizzle(vrow)) * 16 + (t4 & 1) * 8 +
+             (wave * ND * 2 >> 4) * 256;
+  } else {
+    const int vrow = hi * 4 + (t4 >> 2);
+    val_at = vrow * R::kRow +
+             (((((lane >> 4) & 1) * 2 + ((t4 >> 1) & 1) + (wave * ND & 3) * 4) ^ R::swizzle(vrow))
+              << 4) +
+             (t4 & 1) * 8 + (wave * ND >> 2) * 256;
+  }
   // its chunk of the weights of row lane & 31 of a row tile
   const unsigned weight_at = lds + R::kWeights + qi * (kKeys * 2) + ((hi ^ ((qi >> 1) & 7)) << 4);
   // a word of its row in the row statistics
   const unsigned row_at = (tile * kRowTile + qi) * 4;
+  // in 8 bits: the exponents of its row of keys; that of key `lane` for the wave's
+  // columns; and where key `lane` stands among the weights
+  const int powers_at = R::kPowers + key_row / kOwn * 64 + key_row % kOwn * R::kGroups;
+  const int power_at =
+      R::kPowers + lane / kOwn * 64 + lane % kOwn * R::kGroups + wave * ND * 32 / kLatGroup;
+  const unsigned down = lds + R::kDown + wave * (kKeys * 2);
+  const unsigned down_at =
+      down + ((lane >> 4) * 16 + ((lane >> 2) & 1) * 8 + ((lane >> 3) & 1) * 4 + (lane & 3)) * 2;
 
   for (int i = 0; i < span.n; ++i) {
     const int key0 = span.first + i * kKeys;
@@ -592,74 +722,40 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
     };
     // this tile's copies are done when those of the stages after it may not be
     wait_copies<(R::kStages - 2) * R::kPerWave>();
-    unsigned buf;
-    if constexpr (E8) {
-      buf = lds;
-      const unsigned from = raw + wave * R::kPiece;
-      kv_u32x4 w[R::kCopies];
-      unsigned ex[R::kCopies];
+    const unsigned buf = raw;
+    if (edge) {
+      const unsigned own = buf + row0 * R::kRow + lane * 16;
+      unsigned strange = strange_turned();
 #pragma unroll
       for (int n = 0; n < R::kCopies; ++n) {
-        const int r = n * R::kRowsPerCopy + lane / R::kChunks, c = lane % R::kChunks;
-        w[n] = lds_read<kv_u32x4>(from + n * 1024 + lane * 16);
-        ex[n] = lds_read<unsigned char>(from + kOwn * L + r * (L / kLatGroup) + c / (kLatGroup / 16));
-      }
-      if (edge) {
-        unsigned strange = strange_turned();
-#pragma unroll
-        for (int n = 0; n < R::kCopies; ++n) {
-          // (no row that append writes has an exponent byte above 246; a code may
-          // pass every finite number under it)
-          bool bad = ex[n] > 246;
+        const kv_u32x4 w = lds_read<kv_u32x4>(own + n * 1024);
+        bool bad = false;
+        if constexpr (E8) {
 #pragma unroll
           for (int x = 0; x < 4; ++x)
 #pragma unroll
-            for (int y = 0; y < 32; y += 8) bad |= ((w[n][x] >> y) & 0x7Fu) == 0x7Fu;
-          strange |= rows_in(__ballot(bad), R::kChunks, n * R::kRowsPerCopy);
+            for (int y = 0; y < 32; y += 8) bad |= ((w[x] >> y) & 0x7Fu) == 0x7Fu;
+        } else {
+          bad = strange16(w);
         }
-        const unsigned hidden = hide(strange);
-        hide_turned(hidden);
-#pragma unroll
-        for (int n = 0; n < R::kCopies; ++n)
-          if ((hidden >> (n * R::kRowsPerCopy + lane / R::kChunks)) & 1) {
-            w[n] = (kv_u32x4){0, 0, 0, 0};
-            ex[n] = 127;
-          }
+        strange |= rows_in(__ballot(bad), R::kChunks, n * R::kRowsPerCopy);
       }
-      // everybody is done with the tile before
-      barrier();
-#pragma unroll
-      for (int n = 0; n < R::kCopies; ++n) {
-        const int r = n * R::kRowsPerCopy + lane / R::kChunks, c = lane % R::kChunks;
-        const float e = __builtin_bit_cast(float, ex[n] << 23);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          kv_u32x4 z;
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            z[2 * y] = __builtin_bit_cast(
-                unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[n][2 * x + y], e, false));
-            z[2 * y + 1] = __builtin_bit_cast(
-                unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[n][2 * x + y], e, true));
-          }
-          lds_write(buf + (row0 + r) * R::kRow + (((2 * c + x) ^ R::swizzle(row0 + r)) << 4), z);
-        }
+      if constexpr (E8) {
+        // (no row that append writes has an exponent byte above 246; a code may
+        // pass every finite number under it)
+        const bool bad = lane < kOwn * R::kGroups &&
+                         lds_read<unsigned char>(buf + R::kPowers + wave * 64 + lane) > 246;
+        strange |= rows_in(__ballot(bad), R::kGroups, 0);
       }
-    } else {
-      buf = raw;
-      if (edge) {
-        const unsigned own = buf + row0 * R::kRow + lane * 16;
-        unsigned strange = strange_turned();
+      const unsigned hidden = hide(strange);
+      hide_turned(hidden);
 #pragma unroll
-        for (int n = 0; n < R::kCopies; ++n)
-          strange |= rows_in(__ballot(strange16(lds_read<kv_u32x4>(own + n * 1024))), R::kChunks,
-                             n * R::kRowsPerCopy);
-        const unsigned hidden = hide(strange);
-        hide_turned(hidden);
-#pragma unroll
-        for (int n = 0; n < R::kCopies; ++n)
-          if ((hidden >> (n * R::kRowsPerCopy + lane / R::kChunks)) & 1)
-            lds_write(own + n * 1024, (kv_u32x4){0, 0, 0, 0});
+      for (int n = 0; n < R::kCopies; ++n)
+        if ((hidden >> (n * R::kRowsPerCopy + lane / R::kChunks)) & 1)
+          lds_write(own + n * 1024, (kv_u32x4){0, 0, 0, 0});
+      if constexpr (E8) {
+        if (lane < kOwn * R::kGroups && ((hidden >> (lane / R::kGroups)) & 1))
+          lds_write<unsigned char>(buf + R::kPowers + wave * 64 + lane, 127);
       }
     }
     barrier();
@@ -672,6 +768,8 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
     f32x16 sc;
     float top = -__builtin_inff();
     V8 pf[2];
+    // in 8 bits, of the wave's columns: key `lane`'s exponent byte, the tile's largest
+    int own_power = 0, top_power = 0;
     // The product takes weights of the query type, each off by up to half its step;
     // their sum takes them as they are.
     auto weigh = [&](float* sum) {
@@ -704,21 +802,52 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
         for (int f = 0; f < 8; ++f) ka[f] = at ^ (f << 5);
         settle(ta);
       }
-      V8 kf[kAhead + 1];
+      V8 kf[kAhead + 1], now;
+      kv_u32x4 kc[kAhead / 2 + 1];  // codes
+      float power[R::kGroups];
       auto read_key = [&](int f) {
-        kf[f % (kAhead + 1)] = f < NL ? lds_read<V8>(ka[f & 7] + (f >> 3) * 256)
-                                      : lds_read<V8>(ta ^ ((f - NL) << 5));
+        if (f >= NL) {
+          kf[f % (kAhead + 1)] = lds_read<V8>(ta ^ ((f - NL) << 5));
+        } else if constexpr (E8) {
+          if (f % 2 == 0)
+            kc[f / 2 % (kAhead / 2 + 1)] =
+                lds_read<kv_u32x4>(ka[(f >> 1) & 7] + (f >> 4) * 256);
+        } else {
+          kf[f % (kAhead + 1)] = lds_read<V8>(ka[f & 7] + (f >> 3) * 256);
+        }
       };
+      auto operand = [&](int f) {
+        if (E8 && f < NL) {
+          const kv_u32x4 c = kc[f / 2 % (kAhead / 2 + 1)];
+          return widen<V8>(c[f % 2 * 2], c[f % 2 * 2 + 1], power[f * 16 / kLatGroup]);
+        }
+        return kf[f % (kAhead + 1)];
+      };
+      if constexpr (E8) {
+        own_power = lds_read<unsigned char>(raw + power_at);
+        const unsigned x = R::kGroups == 4 ? lds_read<unsigned>(raw + powers_at)
+                                           : lds_read<unsigned short>(raw + powers_at);
+#pragma unroll
+        for (int g = 0; g < R::kGroups; ++g)
+          power[g] = __builtin_bit_cast(float, ((x >> (8 * g)) & 255u) << 23);
+      }
 #pragma unroll
       for (int f = 0; f < kAhead; ++f) read_key(f);
+      now = operand(0);
       auto step = [&](auto self, auto at) {
         constexpr int f = decltype(at)::value;
         if constexpr (f + kAhead < NF) read_key(f + kAhead);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (f & 1) {
-          s2 = TT::mfma32(kf[f % (kAhead + 1)], qf[f], s2);
+          s2 = TT::mfma32(now, qf[f], s2);
         } else {
-          sc = TT::mfma32(kf[f % (kAhead + 1)], qf[f], sc);
+          sc = TT::mfma32(now, qf[f], sc);
+        }
+        if constexpr (f + 1 < NF) now = operand(f + 1);
+        // (a step of the largest exponent's way through the wave behind each product)
+        if constexpr (E8 && f < 8) {
+          if constexpr (f == 1) top_power = own_power;
+          if constexpr (f >= 2) top_power = max(top_power, across<f - 2>(top_power));
         }
         // copy n goes out behind product n * NF / kPerWave
         constexpr int n0 = (f * R::kPerWave + NF - 1) / NF, n1 = ((f + 1) * R::kPerWave + NF - 1) / NF;
@@ -754,26 +883,63 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
         weigh(&sum);
       }
     }
-    // columns of the tile, the wave's share: operand k is 16 keys' (k / ND) of 32
-    // columns
-    constexpr int NV = kKeys / 16 * ND, kVAhead = 3;
+    // Columns of the tile, the wave's share: operand k is 16 keys' (k / ND) of 32
+    // columns. In 8 bits a column's keys have an exponent each, and the conversion
+    // takes one for all: the tile's largest, and what a key's own is less its weights
+    // lose, exactly, as an integer subtraction from their bits. (A weight of less than
+    // a normal number's size after it is none; so a tile in which exponents are
+    // kFar apart or more is taken in passes.)
+    constexpr int NV = kKeys / 16 * ND, kVAhead = 3, kFar = 100;
+    typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
+    bool rest = false;  // key `lane` is left for another pass
+    auto lower = [&]() {
+      const int less = top_power - own_power;
+      lds_write<unsigned short>(down_at, less < 0 || less > kFar ? 0xFFFF
+                                                                 : (unsigned short)(less << 7));
+      rest = less > kFar;
+    };
+    if constexpr (E8) {
+      top_power = __builtin_amdgcn_readlane(top_power, kWave - 1);
+      lower();
+    }
     unsigned va[ND], wa = weight_at;
     {
       unsigned at = buf + val_at;
       settle(at);
 #pragma unroll
-      for (int d = 0; d < ND; ++d) va[d] = at ^ (d << 6);
+      for (int d = 0; d < ND; ++d) va[d] = at ^ (d << (E8 ? 5 : 6));
       settle(wa);
     }
     V4 vl[kVAhead + 1], vh[kVAhead + 1];
+    lds_i32x2 vc[kVAhead + 1];
     V8 pw[2][NT];
+    u16x8 dw[2];
     auto read_value = [&](int k) {
       const int c = k / ND, d = k % ND;
-      vl[k % (kVAhead + 1)] = lds_columns<V4>(va[d] + c * 16 * R::kRow);
-      vh[k % (kVAhead + 1)] = lds_columns<V4>((va[d] ^ 32) + (c * 16 + 8) * R::kRow);
+      if constexpr (E8) {
+        vc[k % (kVAhead + 1)] = lds_columns8(va[d] + c * 16 * R::kRow);
+      } else {
+        vl[k % (kVAhead + 1)] = lds_columns<V4>(va[d] + c * 16 * R::kRow);
+        vh[k % (kVAhead + 1)] = lds_columns<V4>((va[d] ^ 32) + (c * 16 + 8) * R::kRow);
+      }
     };
     auto read_weight = [&](int c, int t) {
       pw[c & 1][t] = lds_read<V8>((wa ^ (c << 5)) + t * (kRowTile * kKeys * 2));
+      if (E8 && t == 0) dw[c & 1] = lds_read<u16x8>(down + (c * 2 + hi) * 16);
+    };
+    auto value = [&](int k) {
+      if constexpr (E8) {
+        const lds_i32x2 x = vc[k % (kVAhead + 1)];
+        return widen<V8>(x[0], x[1], __builtin_bit_cast(float, top_power << 23));
+      } else {
+        return __builtin_shufflevector(vl[k % (kVAhead + 1)], vh[k % (kVAhead + 1)], 0, 1, 2, 3, 4,
+                                       5, 6, 7);
+      }
+    };
+    auto adjust = [&](int c, int t) {
+      if constexpr (E8)
+        pw[c & 1][t] = __builtin_bit_cast(
+            V8, __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x8, pw[c & 1][t]), dw[c & 1]));
     };
 #pragma unroll
     for (int k = 0; k < kVAhead; ++k) read_value(k);
@@ -824,25 +990,60 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
       }
     }
     l += sum;
-    // O^T += C^T P^T, the reads of operands kVAhead later between the products
+    // O^T += C^T P^T, the reads of operands kVAhead later between the products; the
+    // first operands' reads are under way
+    auto products = [&]() {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int c = k / ND, d = k % ND;
-      if (k + kVAhead < NV) read_value(k + kVAhead);
-      if (c + 1 < kKeys / 16) {
-        if (ND == 1) {
+      for (int t = 0; t < NT; ++t) adjust(0, t);
+      V8 vf = value(0);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) read_weight(c + 1, t);
-        } else if (d < NT) {
-          read_weight(c + 1, d);
+      for (int k = 0; k < NV; ++k) {
+        const int c = k / ND, d = k % ND;
+        if (k + kVAhead < NV) read_value(k + kVAhead);
+        if (c + 1 < kKeys / 16) {
+          if (ND == 1) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) read_weight(c + 1, t);
+          } else if (d < NT) {
+            read_weight(c + 1, d);
+          }
         }
-      }
-      const V8 vf = __builtin_shufflevector(vl[k % (kVAhead + 1)], vh[k % (kVAhead + 1)], 0, 1, 2, 3,
-                                            4, 5, 6, 7);
-      __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) o[t][d] = TT::mfma32(vf, pw[c & 1][t], o[t][d]);
-      __builtin_amdgcn_sched_barrier(0);
+        for (int t = 0; t < NT; ++t) o[t][d] = TT::mfma32(vf, pw[c & 1][t], o[t][d]);
+        if (k + 1 < NV) vf = value(k + 1);
+        if (c + 1 < kKeys / 16) {
+          if (ND == 1) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) adjust(c + 1, t);
+          } else if (d >= ND - NT) {
+            adjust(c + 1, d - (ND - NT));
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    static_assert(ND == 1 || ND >= 2 * NT, "weights are read before they are adjusted");
+    if constexpr (!E8) {
+      products();
+    } else {
+      for (;;) {
+        products();
+        if (__builtin_expect(!__any(rest), 1)) break;
+        top_power = rest ? own_power : 0;
+        top_power = max(top_power, across<0>(top_power));
+        top_power = max(top_power, across<1>(top_power));
+        top_power = max(top_power, across<2>(top_power));
+        top_power = max(top_power, across<3>(top_power));
+        top_power = max(top_power, across<4>(top_power));
+        top_power = max(top_power, across<5>(top_power));
+        top_power = __builtin_amdgcn_readlane(top_power, kWave - 1);
+        lower();
+#pragma unroll
+        for (int k = 0; k < kVAhead; ++k) read_value(k);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) read_weight(0, t);
+      }
     }
     // (the next tile's first barrier comes before anything here is overwritten:
     // the weights, the statistics and, in 8 bits, the tile)
@@ -909,6 +1110,7 @@ __global__ __launch_bounds__(waves(L) * kWave, waves(L) / 4) void split_kernel(L
   __shared__ int64_t wsum[waves(L)];
   __shared__ int start_r;
   __shared__ int64_t start_off;
+  fetch_args<sizeof(a) + sizeof(ws)>();
   const ReqView& q = a.req;
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -987,29 +1189,18 @@ __global__ __launch_bounds__(waves(L) * kWave, waves(L) / 4) void split_kernel(L
     a.meta[1] = rows_total != total_eff ? DSPARK_DATA_BAD_LENS : 0;
   }
   if (u0 >= u1) return;
-  cur.left = u1 - u0;
+  // (uniform for the compiler too, which a copy's operands have to be)
+  cur.left = read_lane(u1 - u0, 0);
+  cur.off = read_lane(cur.off, 0);
+  cur.r = __builtin_amdgcn_readfirstlane(cur.r);
   Feeder<E8, L> feed;
-  feed.start(a, lds, cur, wave);
-#pragma unroll
-  for (int i = 0; i < R::kStages - 1; ++i) {
-    feed.begin(a, lds, wave);
-    feed.copies(wave);
-    if (i == 0) feed.look_ahead(a, lds, wave);
-    feed.end_tile(a, lds, wave);
-  }
   int stage = 0, tick = 0;
   if (tid == 0) lds_write<unsigned>(lds + R::kFlag, 0u);
-  for (;;) {
+  for (bool first = true;; first = false) {
     Job job;
     const Span span = next_span<L>(a, lds + R::kReqs, cur, &job);
     if (span.n == 0) break;
-    bool good = true;  // its tree is one
-    if (q.parents) {
-      const int lane = lane_id();
-      const int up = lane + 1 < job.s.len ? q.parents[(size_t)span.r * q.gamma + lane] : 0;
-      good = __ballot(up < 0 || up > lane) == 0;
-    }
-    segment<T, E8, L>(a, ws, span, job, good, feed, lds, stage, tick);
+    segment<T, E8, L>(a, ws, span, job, first, cur, feed, lds, stage, tick);
   }
   wait_copies<0>();
 }

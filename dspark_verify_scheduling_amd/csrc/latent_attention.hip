@@ -61,11 +61,11 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(LatentAttnArgs a, Pa
   for (int n = share * kStep + (SHARED ? 0 : wave); n < s.mtiles * kBlocks; n += shares * kStep) {
     const int mtile = n / kBlocks, block = n - mtile * kBlocks;
     const int seg = mtile / s.per;
-    const int64_t u0 = base + (int64_t)seg * s.nku, u1 = u0 + s.nku;
-    // workgroups of the first and the last unit
-    const int wa = (int)(((u0 + 1) * wgs - 1) / units), wb = (int)((u1 * wgs - 1) / units);
+    const int64_t u0 = base + (int64_t)seg * (s.nku + kSetup), u1 = u0 + s.nku + kSetup;
+    // workgroups of the first and the last unit with keys
+    const int wa = (int)(((u0 + kSetup + 1) * wgs - 1) / units), wb = (int)((u1 * wgs - 1) / units);
     if (wa == wb) continue;
-    const int slot0 = 2 * wa + (wg_start(units, wa, wgs) == u0 ? 0 : 1);
+    const int slot0 = 2 * wa + (wg_start(units, wa, wgs) >= u0 ? 0 : 1);
     const int parts = wb - wa + 1;
     const int tile = mtile - seg * s.per;
     constexpr int kAhead = 4;

@@ -99,6 +99,7 @@ template <typename T, bool E8, int L>
 __global__ __launch_bounds__(kThreads) void latent_append_kernel(LatentAppendArgs a, int per) {
   typedef typename Vec8<T>::type T8;
   constexpr int kLanes = L / 8;  // lanes that hold the latent
+  fetch_args<sizeof(a) + 4>();
   const ReqView& q = a.req;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -242,6 +243,7 @@ template <bool E8, int L>
 __global__ __launch_bounds__(kThreads) void latent_read_kernel(LatentReadArgs a) {
   constexpr int EPL = E8 ? 16 : 8;  // elements of a lane, in 16 bytes
   constexpr int kLanes = L / EPL;
+  fetch_args<sizeof(a)>();
   const ReqView& q = a.req;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);

@@ -57,6 +57,14 @@ __device__ inline V4 lds_columns(unsigned at) {
   return __builtin_bit_cast(V4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)at));
 }
 
+// The same for bytes: sixteen lanes read 8 bytes each, lanes 2 i and 2 i + 1 the halves
+// of row i's sixteen, and lane l gets column l of the eight rows.
+typedef int lds_i32x2 __attribute__((ext_vector_type(2)));
+__device__ inline lds_i32x2 lds_columns8(unsigned at) {
+  typedef __attribute__((address_space(3))) lds_i32x2 there;
+  return __builtin_amdgcn_ds_read_tr8_b64_v2i32((there*)(uintptr_t)at);
+}
+
 template <typename X>
 __device__ inline X lds_read(unsigned at) {
   return *(__attribute__((address_space(3))) const X*)(uintptr_t)at;

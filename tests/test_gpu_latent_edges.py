@@ -1,0 +1,193 @@
+"""GPU tests of the latent cache's calls where they change their way of working:
+exponents far apart in a tile, large batches of many heads, row tiles past what
+their plan sorts, workspaces with neighbours. Tolerances as in test_gpu_latent.py."""
+
+import numpy as np
+import pytest
+import torch
+
+import dspark_verify_scheduling_amd as dv
+from _gpu import DEV, say, up
+from test_gpu_latent import (R, latent_check, latent_run, latent_setup, lput, make_latent, prefill_check,
+                             prefill_run, turns, typed)
+from test_gpu_target import TYPES, Batch, bits, f64, i32, make_cache
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu(hip):
+    return hip
+
+
+@pytest.mark.parametrize("L", [512, 256])
+@pytest.mark.parametrize("where", ["draft", "cache", "everywhere"])
+def test_exponents_far_apart_in_a_tile(L, where):
+    """In 8 bits a tile's exponents differ by up to 219: a key that a row does not see,
+    or whose weight is nothing, takes nothing from the others' bits."""
+    say(f"latent attention far exponents L={L} {where}")
+    H, gamma = 6, 9
+    b = Batch(4, [10, 3], [170, 64], gamma, 16, True)
+    b.parents[0] = [0, 1, 0, 3, 3, 2, 6, 0, 8]
+    dt = TYPES["e4m3"][1]
+    rng = np.random.default_rng(3)
+    cache = make_latent("e4m3", b.nb, 16, L)
+    ql = typed(rng, (b.rows, H, L), dt).to(DEV)
+    qr = typed(rng, (b.rows, H, R), dt).to(DEV)
+    # the columns with the exponents take no part in the scores
+    ql[..., 128:256] = 0
+    qr[..., 0] = 1.0
+    for r in range(2):
+        T = b.ctx[r] + b.lens[r]
+        lat, rope = rng.normal(0, 1, (T, L)), rng.normal(0, 1, (T, R))
+        size = np.full(T, -85.0)
+        rope[:, 0] = 0
+        if where == "draft":
+            size[b.ctx[r] + 2] = 108  # seen by its descendants only
+        elif where == "cache":
+            size[[5, 40, 63]] = [60, 105, 20]  # in whole tiles
+            rope[[5, 40, 63], 0] = -4000.0     # weights of 2^-288
+        else:
+            size = rng.integers(-85, 109, T).astype(np.float64)
+        lat[:, 128:256] *= 2.0 ** size[:, None]
+        lput(cache, b.slots(r, 0, T), lat, rope)
+    o = dv.alloc_latent_attention_outputs(b.B, gamma, b.rows, H, cache, lse=True)
+    o.out.fill_(-7)
+    o.lse.fill_(-7)
+    dv.dspark_latent_attention(b.B, gamma, ql, qr, b.rows, *b.args(), cache, 0.05, o,
+                               tree_parents=b.par())
+    torch.cuda.synchronize()
+    assert o.attention_meta.tolist() == [13, 0]
+    latent_check(b, "e4m3", H, L, 0.05, cache, ql, qr, o)
+
+
+@pytest.mark.parametrize("kind,H,L", [("bf16", 128, 512), ("f16", 65, 256), ("e4m3", 33, 512)])
+def test_latent_attention_of_large_batches_and_many_heads(kind, H, L):
+    """More requests than a wave has lanes, several segments each."""
+    say(f"latent attention of 70 requests, {H} heads {kind}")
+    rng = np.random.default_rng(H)
+    lens = rng.integers(1, 6, 70).tolist()
+    ctx = rng.integers(0, 200, 70).tolist()
+    lens[3], ctx[3] = 5, 2500
+    latent_run(Batch(H, lens, ctx, 4, 16, True), kind, H, L, 0.05)
+
+
+def test_latent_attention_of_a_whole_tree_at_all_heads():
+    say("latent attention, 65 rows of 128 heads")
+    latent_run(Batch(5, [65, 1], [300, 900], 64, 64, True), "bf16", 128, 512, 0.05)
+
+
+@pytest.mark.parametrize("kind,L,H,B,ctx", [("bf16", 512, 7, 3, 900), ("e4m3", 256, 40, 2, 2100),
+                                            ("f16", 256, 3, 66, 70)])
+def test_latent_attention_keeps_to_its_workspace(kind, L, H, B, ctx):
+    say(f"latent attention workspace {kind}")
+    b = Batch(B, [3] * B, [ctx] * B, 4, 16, False)
+    cache, ql, qr = latent_setup(b, kind, H, L)
+    o = dv.alloc_latent_attention_outputs(B, 4, b.rows, H, cache, lse=True)
+    size = o.workspace.numel() * o.workspace.element_size()
+    room = torch.full((size + 8192,), 0x5A, dtype=torch.uint8, device=DEV)
+    o = o._replace(workspace=room[4096:4096 + size])
+    o.out.fill_(-7)
+    o.lse.fill_(-7)
+    dv.dspark_latent_attention(B, 4, ql, qr, b.rows, *b.args(), cache, 0.05, o)
+    torch.cuda.synchronize()
+    latent_check(b, kind, H, L, 0.05, cache, ql, qr, o)
+    assert bool((room[:4096] == 0x5A).all()) and bool((room[4096 + size:] == 0x5A).all())
+
+
+@pytest.mark.parametrize("kind,n,H,lens", [("bf16", 128, 8, [130, 0, 31]), ("e4m3", 64, 3, [1, 300]),
+                                           ("f16", 64, 16, [5] * 40)])
+def test_latent_prefill_keeps_to_its_workspace(kind, n, H, lens):
+    say(f"latent prefill workspace {kind}")
+    b = Batch(7, lens, [40] * len(lens), 1, 16, False)
+    cache, q, wk, wv, o, keys = prefill_run(b, kind, H, n, 256, 0.07, check=False)
+    size = o.workspace.numel() * o.workspace.element_size()
+    room = torch.full((size + 8192,), 0x5A, dtype=torch.uint8, device=DEV)
+    o = o._replace(workspace=room[4096:4096 + size])
+    o.out.fill_(-7)
+    o.lse.fill_(-7)
+    dv.dspark_latent_prefill(b.B, q, wk, wv, b.rows, keys, *b.args(), cache, 0.07, o)
+    torch.cuda.synchronize()
+    prefill_check(b, kind, H, n, 256, 0.07, cache, q, wk, wv, o)
+    assert bool((room[:4096] == 0x5A).all()) and bool((room[4096 + size:] == 0x5A).all())
+
+
+def test_latent_prefill_of_more_tiles_than_are_sorted():
+    say("latent prefill of 1100 requests")
+    rng = np.random.default_rng(8)
+    lens, ctx = rng.integers(1, 4, 1100).tolist(), rng.integers(0, 20, 1100).tolist()
+    lens[700] = 260
+    prefill_run(Batch(4, lens, ctx, 1, 16, False), "bf16", 8, 64, 256, 0.07)
+
+
+@pytest.mark.parametrize("kind,scale", [("bf16", 400.0), ("f16", -300.0), ("e4m3", 300.0)])
+def test_latent_prefill_large_scores(kind, scale):
+    """Scores of some thousands: a row's largest takes everything, its value comes out."""
+    say(f"latent prefill scale {scale} {kind}")
+    L, n, H, T = 256, 64, 2, 150
+    b = Batch(3, [T], [0], 1, 16, False)
+    dt = TYPES[kind][1]
+    cache = make_latent(kind, b.nb, 16, L)
+    rng = np.random.default_rng(1)
+    lat = rng.integers(-3, 4, (T, L)).astype(np.float64)
+    lat[:, 0] = rng.permutation(T) / 2  # key and score of a row, exact in every type
+    rope = np.zeros((T, R))
+    if kind == "e4m3":
+        lat[:, 0] = np.clip(np.arange(T) // 10, 0, 15)
+        lat[:, 0] += np.arange(T) / 10 % 1 >= 0.9
+        rope[:, 0] = np.arange(T)
+    lput(cache, b.slots(0, 0, T), lat, rope)
+    q = torch.zeros(b.rows, H, n + R, dtype=dt, device=DEV)
+    q[:, 0, 0], q[:, 1, 0] = 1.0, -1.0
+    if kind == "e4m3":
+        q[:, 0, 0] = q[:, 1, 0] = 0
+        q[:, 0, n], q[:, 1, n] = 1.0, -1.0
+    w = torch.zeros(H, 2 * n, L, dtype=dt, device=DEV)
+    w[:, 0, 0] = 1.0
+    for c in range(n):
+        w[:, n + c, c] = 1.0
+    o = dv.alloc_latent_prefill_outputs(1, b.rows, T, H, n, cache)
+    dv.dspark_latent_prefill(1, q, w[:, :n], w[:, n:], b.rows, T, *b.args(), cache, scale, o)
+    torch.cuda.synchronize()
+    got = f64(o.out).reshape(b.rows, H, n)
+    key = rope[:, 0] if kind == "e4m3" else lat[:, 0]
+    for row in range(T):
+        for h in range(H):
+            s = scale * (1 if h == 0 else -1) * key[:row + 1]
+            assert np.array_equal(got[row, h], lat[s.argmax(), :n]), (row, h)
+
+
+def test_axes_rows_of_a_wave_and_of_a_workgroup_agree():
+    """A call of many rows gives a wave to each, one of few a workgroup: the same bits."""
+    say("append with axes, 1500 rows at once and in parts")
+    hq, hkv, D, page, cut = 6, 3, 128, 16, 700
+    rng = np.random.default_rng(2)
+    dt = torch.bfloat16
+    rows = 1500
+    qkv = typed(rng, (rows, hq + 2 * hkv, D), dt).to(DEV)
+    w = typed(rng, (2, D), dt).to(DEV)
+    rope = up(turns(512, D))
+    pos = i32(rng.integers(0, 512, (3, rows)))
+    nb = -(-rows // page)
+    table = i32(rng.permutation(nb)[None])
+    axis = [i % 3 for i in range(D // 2)]
+    for kind in ("bf16", "e4m3"):
+        out = []
+        for parts in ([(0, rows)], [(0, cut), (cut, rows)]):
+            cache = make_cache(kind, nb, hkv, page, D)
+            for p in (cache.k, cache.v):
+                bits(p).zero_()
+            got = []
+            for lo, hi in parts:
+                n = hi - lo
+                x = qkv[lo:hi]
+                o = dv.alloc_append_outputs(n, hq, cache)
+                dv.dspark_kv_append_axes(1, x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], n,
+                                         i32([0, n]), i32([lo]), pos[:, lo:hi], axis, table, cache, o,
+                                         rope, q_weight=w[0], k_weight=w[1])
+                torch.cuda.synchronize()
+                assert o.append_meta.tolist() == [n, 0]
+                got.append(o.q_out.clone())
+            out.append([bits(torch.cat(got)), bits(cache.k).clone(), bits(cache.v).clone()])
+        for x, y in zip(*out):
+            assert torch.equal(x, y)
