@@ -9,7 +9,7 @@ namespace dspark {
 namespace lattn {
 namespace {
 
-constexpr int kJoinThreads = 256;
+constexpr int join_threads(bool shared) { return shared ? 512 : 256; }
 
 // One workgroup per (request, share of its blocks of 32 rows by 32 columns): joins
 // the parts that several workgroups of the split kernel left of a segment, a wave to
@@ -19,8 +19,9 @@ constexpr int kJoinThreads = 256;
 // against 32; 32 chains, 128 heads, two or three parts each: 19.6 against 11.8). The
 // first workgroup of each request also checks it and its pages.
 template <typename T, int L, bool SHARED>
-__global__ __launch_bounds__(kJoinThreads) void join_kernel(LatentAttnArgs a, Parts ws,
-                                                            int shares) {
+__global__ __launch_bounds__(join_threads(SHARED)) void join_kernel(LatentAttnArgs a, Parts ws,
+                                                                    int shares) {
+  constexpr int kJoinThreads = join_threads(SHARED);
   constexpr int kBlocks = L / 32, kJoinWaves = kJoinThreads / kWave;
   const ReqView& q = a.req;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
@@ -179,11 +180,12 @@ Plan plan(int B, int gamma, int num_heads, int L) {
 template <int L>
 void launch_join(const LatentAttnArgs& a, const Parts& ws, dspark_dtype dt, hipStream_t s) {
   const int tiles = (a.num_heads * (a.req.gamma + 1) + kRowTile - 1) / kRowTile;
-  const int blocks = tiles * (L / 32), waves = kJoinThreads / kWave;
+  const int blocks = tiles * (L / 32);
   const bool shared = (int64_t)a.req.B * blocks <= 1024;
+  const int waves = join_threads(shared) / kWave;
   const int most = shared ? blocks : (blocks + waves - 1) / waves;
   const int shares = std::max(1, std::min(most, 2048 / std::max(a.req.B, 1)));
-  const dim3 grid((unsigned)a.req.B * shares), block(kJoinThreads);
+  const dim3 grid((unsigned)a.req.B * shares), block(join_threads(shared));
   if (dt == DSPARK_BF16) {
     if (shared) {
       hipLaunchKernelGGL((join_kernel<__bf16, L, true>), grid, block, 0, s, a, ws, shares);
