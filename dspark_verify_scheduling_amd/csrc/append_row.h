@@ -3,6 +3,8 @@
 
 #include "kv_dev.h"
 
+#include <type_traits>
+
 namespace dspark {
 
 template <typename T>
@@ -11,6 +13,46 @@ template <>
 struct Vec8<__bf16> { typedef bf16x8 type; };
 template <>
 struct Vec8<_Float16> { typedef f16x8 type; };
+
+// x of lane ^ M, without a way through LDS where a row of sixteen lanes holds both.
+template <int M>
+__device__ __forceinline__ float lane_xor(float x) {
+  const int v = __builtin_bit_cast(int, x);
+  auto moved = [](int y, auto at) {
+    return __builtin_amdgcn_update_dpp(y, y, decltype(at)::value, 0xF, 0xF, false);
+  };
+  int z;
+  if constexpr (M == 1) {
+    z = moved(v, std::integral_constant<int, 0xB1>{});  // pairs
+  } else if constexpr (M == 2) {
+    z = moved(v, std::integral_constant<int, 0x4E>{});  // halves of a quad
+  } else if constexpr (M == 4) {
+    // eight lanes back to front, then each quad
+    z = moved(moved(v, std::integral_constant<int, 0x141>{}), std::integral_constant<int, 0x1B>{});
+  } else if constexpr (M == 8) {
+    z = moved(v, std::integral_constant<int, 0x128>{});  // sixteen lanes, turned by eight
+  } else {
+    return __shfl_xor(x, M, kWave);
+  }
+  return __builtin_bit_cast(float, z);
+}
+// The sum, or largest, of LANES neighbours.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float x) {
+  if constexpr (LANES == 1) {
+    return x;
+  } else {
+    return lanes_sum<LANES / 2>(x + lane_xor<LANES / 2>(x));
+  }
+}
+template <int LANES, int LEAST = 1>
+__device__ __forceinline__ float lanes_max(float x) {
+  if constexpr (LANES == LEAST) {
+    return x;
+  } else {
+    return lanes_max<LANES / 2, LEAST>(fmaxf(x, lane_xor<LANES / 2>(x)));
+  }
+}
 
 // A row of THREADS threads, a workgroup or a wave: LPH lanes per head take the heads
 // of q, k and v in turn, AHEAD rounds of heads loaded ahead. y = x *
@@ -67,7 +109,7 @@ struct RowAppend {
       float ss = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(x[e], x[e], ss);
-      for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor(ss, o, kWave);
+      ss = lanes_sum<LPH>(ss);
       if (kind == 0 ? a.q_weight != nullptr : kind == 1 && a.k_weight) {
         const float rstd = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
         const T8 ww = pick(kind == 0, weight[0], weight[1]);
@@ -77,10 +119,16 @@ struct RowAppend {
     }
     if (a.rope) {
       float y[8];
+      // the pair's other element: a neighbour, or the same place of another lane
+      if (a.rope_interleaved) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        // the pair's other element: a neighbour, or the same place of another lane
-        y[e] = a.rope_interleaved ? x[e ^ 1] : __shfl(x[e], swap, kWave);
+        for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
+      } else if (a.rope_dim == D) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = lane_xor<LPH / 2>(x[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = __shfl(x[e], swap, kWave);
       }
       if (turned && kind < 2) {
 #pragma unroll
@@ -98,7 +146,7 @@ struct RowAppend {
 #pragma unroll
         for (int e = 0; e < 8; ++e) amax = finite_f32(x[e]) ? fmaxf(amax, fabsf(x[e])) : amax;
       }
-      for (int o = LPH / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o, kWave));
+      amax = lanes_max<LPH>(amax);
       e8 = e4m3_exponent(amax);
       inv = pow2f(-e8);
     }

@@ -55,10 +55,8 @@ __device__ int tree_status(const LatentAppendArgs& a, int total_eff, int64_t mos
 // A lane's eight elements of a pair-wise rotation over eight lanes (64 elements).
 struct Turn {
   float co[8], si[8];
-  int swap;
   __device__ __forceinline__ void load(const float* cs, bool interleaved, int lane) {
     const int li = lane & 7;
-    swap = lane;
     if (interleaved) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -74,7 +72,6 @@ struct Turn {
         si[e] = cs[kRope / 2 + 8 * (li & 3) + e];
         si[e] = low ? -si[e] : si[e];
       }
-      swap = low ? lane + 4 : lane - 4;
     }
   }
   template <typename T>
@@ -84,7 +81,7 @@ struct Turn {
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = (float)in[e];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = interleaved ? x[e ^ 1] : __shfl(x[e], swap, kWave);
+    for (int e = 0; e < 8; ++e) y[e] = interleaved ? x[e ^ 1] : lane_xor<4>(x[e]);
     typename Vec8<T>::type out;
 #pragma unroll
     for (int e = 0; e < 8; ++e) out[e] = (T)__builtin_fmaf(x[e], co[e], y[e] * si[e]);
@@ -178,7 +175,7 @@ __global__ __launch_bounds__(kThreads) void latent_append_kernel(LatentAppendArg
       float ss = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(y[e], y[e], ss);
-      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor(ss, o, kWave);
+      ss = lanes_sum<kLanes>(ss);
       const float rstd = 1.0f / sqrtf(ss * (1.0f / L) + a.eps);
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = y[e] * rstd * (float)weight[e];
@@ -194,7 +191,7 @@ __global__ __launch_bounds__(kThreads) void latent_append_kernel(LatentAppendArg
       float amax = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) amax = finite_f32(y[e]) ? fmaxf(amax, fabsf(y[e])) : amax;
-      for (int o = kLatGroup / 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o, kWave));
+      amax = lanes_max<kLatGroup / 8>(amax);
       const int e8 = e4m3_exponent(amax);
       const float inv = pow2f(-e8);
       kv_u32x2 c;
