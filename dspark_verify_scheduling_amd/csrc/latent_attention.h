@@ -64,7 +64,8 @@ struct Parts {
 // Units that a segment counts for before its first: its start and end (queries in,
 // outputs out) take as long as some tiles do. In equal shares of the units alone, the
 // workgroups with two segments were last, by 13 us (16 trees of up to 17 rows, 32
-// heads, 8 bits: 144 us; with 2, 4, 6, 8 units a segment 126, 121, 114, 120).
+// heads, 8 bits, both kernels: 144 us; with 2, 4, 6, 8 units a segment 126, 121, 114,
+// 120).
 constexpr int kSetup = 6;
 
 // Rows of a request: m = j * heads + h for row j and head h, in tiles of kRowTile,
@@ -1097,6 +1098,15 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
 // which are keys and values at once: running maximum m, sum and outputs in float32
 // registers, m moved only when a score passes it by Soft::kSlack. Parts of a row
 // join by (m, sum, outputs) in join_kernel.
+//
+// Bound by what a workgroup does in turn for a tile of 64 keys: 128 to 144 products
+// to a SIMD (L = 512, 64 rows: 2,180 cycles of some 4,500), the scores' reads of LDS
+// beside them, then the exponentials and three meetings of its waves. 32 chains of
+// up to 4 rows at 128 heads over 1k to 8k keys: 110 us, 760 TFLOP/s; 16 trees of up to
+// 17 rows at 32 heads, 8 bits: 120 us, 650; contexts of 40k and 131k at 20 heads (L =
+// 256): 72 us, 390; one row at 32 heads over 1500 keys: 13.7 us, a chain of reads. A
+// wave with all products of 32 rows needs 512 outputs a lane beside its queries and
+// went through scratch memory (the chains: 508 us), hence columns to a wave.
 //
 // Persistent over the units of all (request, row segment)s in order: workgroup w
 // takes the w-th equal share, so ragged contexts balance by themselves and a long

@@ -15,8 +15,8 @@ constexpr int join_threads(bool shared) { return shared ? 512 : 256; }
 // the parts that several workgroups of the split kernel left of a segment, a wave to
 // a block, its parts in order and several at once, a part's statistics and outputs
 // together. SHARED: the waves take the parts of one block by turns and meet in LDS,
-// for few blocks of many parts (two contexts of 40k and 131k, 20 heads: 13 us
-// against 32; 32 chains, 128 heads, two or three parts each: 19.6 against 11.8). The
+// for few blocks of many parts (two contexts of 40k and 131k, 20 heads: 11 us
+// against 32, 13 with four waves; 32 chains, 128 heads, two or three parts each: 19.6 against 11.8). The
 // first workgroup of each request also checks it and its pages.
 template <typename T, int L, bool SHARED>
 __global__ __launch_bounds__(join_threads(SHARED)) void join_kernel(LatentAttnArgs a, Parts ws,
