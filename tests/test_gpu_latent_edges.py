@@ -191,3 +191,149 @@ def test_axes_rows_of_a_wave_and_of_a_workgroup_agree():
             out.append([bits(torch.cat(got)), bits(cache.k).clone(), bits(cache.v).clone()])
         for x, y in zip(*out):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("kind,L", [("bf16", 512), ("e4m3", 256)])
+def test_layers_and_strided_rows(kind, L):
+    """A layer of a pool of all layers' pages, queries and outputs that are parts of wider
+    rows: the results of a cache and rows of their own, and nothing beside them."""
+    say(f"latent layers and strides {kind}")
+    H, n, layers = 6, 64, 3
+    b = Batch(11, [4, 1, 5], [100, 0, 37], 4, 16, True)
+    plain, ql, qr = latent_setup(b, kind, H, L)
+    dt = ql.dtype
+    pool = make_latent(kind, b.nb, 16, L, layers, joint=True)
+    cache = pool.layer(1)
+    for name in ("latent", "rope", "scale"):
+        if getattr(plain, name) is not None:
+            getattr(cache, name).copy_(getattr(plain, name))
+    q = typed(np.random.default_rng(5), (b.rows, H, n + R), dt).to(DEV)
+    w = typed(np.random.default_rng(6), (H, 2 * n, L), dt, L ** -0.5).to(DEV)
+    keys = sum(b.ctx) + sum(b.lens)
+    got = []
+    for c, wide in ((plain, 0), (cache, 16)):
+        a = dv.alloc_latent_attention_outputs(b.B, 4, b.rows, H, c, lse=True)
+        p = dv.alloc_latent_prefill_outputs(b.B, b.rows, keys, H, n, c, lse=True)
+        rows_of, rest = [], []
+        for x in (ql, q):
+            room = torch.full((b.rows, x.shape[1] * x.shape[2] + wide), 3.0, dtype=dt, device=DEV)
+            room[:, :x.shape[1] * x.shape[2]] = x.flatten(1)
+            rows_of.append(room[:, :x.shape[1] * x.shape[2]].unflatten(1, x.shape[1:]))
+        for o, dim in ((a, L), (p, n)):
+            room = torch.full((b.rows, H * dim + wide), -7.0, dtype=dt, device=DEV)
+            rest.append(room)
+        a = a._replace(out=rest[0][:, :H * L].unflatten(1, (H, L)))
+        p = p._replace(out=rest[1][:, :H * n].unflatten(1, (H, n)))
+        dv.dspark_latent_attention(b.B, 4, rows_of[0], qr, b.rows, *b.args(), c, 0.05, a,
+                                   tree_parents=b.par())
+        dv.dspark_latent_prefill(b.B, rows_of[1], w[:, :n], w[:, n:], b.rows, keys, *b.args(), c, 0.07, p)
+        torch.cuda.synchronize()
+        total = int(b.cu[-1])
+        got.append([a.out[:total].clone(), a.lse[:total].clone(), p.out[:total].clone(),
+                    p.lse[:total].clone()])
+        for room, dim in zip(rest, (L, n)):
+            assert bool((room[total:] == -7).all()) and bool((room[:, H * dim:] == -7).all())
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("kind", ["f16", "e4m3"])
+def test_a_graph_of_a_step_takes_other_batches(kind):
+    """Captured for the largest batch, replayed with other lengths, contexts, trees and
+    paths in place: the eager results."""
+    say(f"latent graph, other batches {kind}")
+    H, n, L, gamma, B, page = 5, 64, 256, 5, 3, 16
+    dt = TYPES[kind][1]
+    batches = [Batch(s, lens, ctx, gamma, page, True, pad=30 - sum(lens)) for s, lens, ctx in (
+        (1, [6, 6, 6], [700, 90, 15]), (2, [1, 1, 1], [0, 800, 63]), (3, [2, 6, 3], [64, 5, 330]))]
+    nb, width = max(b.nb for b in batches), max(b.width for b in batches)
+    cache = make_latent(kind, nb, page, L)
+    rng = np.random.default_rng(7)
+    for pg in range(nb):
+        lput(cache, [(pg, i) for i in range(page)], rng.normal(0, 1, (page, L)), rng.normal(0, 1, (page, R)))
+    keys = 900 + 3 * (gamma + 1)
+    ql, qr = (typed(rng, (30, H, d), dt).to(DEV) for d in (L, R))
+    q = typed(rng, (30, H, n + R), dt).to(DEV)
+    w = typed(rng, (H, 2 * n, L), dt, L ** -0.5).to(DEV)
+    cu, pre = torch.zeros(B + 1, dtype=torch.int32, device=DEV), torch.zeros(B, dtype=torch.int32, device=DEV)
+    table = torch.zeros(B, width, dtype=torch.int32, device=DEV)
+    par = torch.zeros(B, gamma, dtype=torch.int32, device=DEV)
+    path, num = torch.zeros(B, gamma + 1, dtype=torch.int32, device=DEV), torch.zeros(B, dtype=torch.int32, device=DEV)
+    meta = torch.empty(2, dtype=torch.int32, device=DEV)
+    a = dv.alloc_latent_attention_outputs(B, gamma, 30, H, cache, lse=True)
+    p = dv.alloc_latent_prefill_outputs(B, 30, keys, H, n, cache, lse=True)
+
+    def fill(b):
+        cu.copy_(i32(b.cu))
+        pre.copy_(i32(b.ctx))
+        table.fill_(-1)
+        table[:, :b.width] = i32(b.table)
+        par.copy_(i32(b.parents))
+        r = np.random.default_rng(b.rows)
+        steps = np.zeros((B, gamma + 1), np.int32)
+        count = [int(r.integers(0, n)) for n in b.lens]
+        for i, c in enumerate(count):
+            steps[i, 1:c + 1] = np.sort(r.choice(np.arange(1, b.lens[i]), c, replace=False))
+        path.copy_(i32(steps))
+        num.copy_(i32(count))
+
+    def step():
+        dv.dspark_latent_attention(B, gamma, ql, qr, 30, cu, pre, table, cache, 0.05, a, tree_parents=par)
+        dv.dspark_latent_prefill(B, q, w[:, :n], w[:, n:], 30, keys, cu, pre, table, cache, 0.07, p)
+        dv.dspark_latent_commit(B, gamma, path, num, pre, table, cache, meta)
+
+    pools = [bits(cache.latent), cache.rope] + ([cache.scale] if kind == "e4m3" else [])
+    metas = [a.attention_meta, p.attention_meta, meta]
+    outs = [a.out, a.lse, p.out, p.lse] + pools + metas
+    start = [t.clone() for t in pools]
+
+    def reset():
+        for t in outs[:4]:
+            t.fill_(-7)
+        for t, y in zip(pools, start):
+            t.copy_(y)
+
+    fill(batches[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for turn in range(6):
+        b = batches[turn % 3]
+        fill(b)
+        reset()
+        step()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in outs]
+        assert all(t[1].item() == 0 for t in metas)
+        reset()
+        graph.replay()
+        torch.cuda.synchronize()
+        for k, (t, y) in enumerate(zip(outs, want)):
+            assert torch.equal(t.view(torch.uint8), y.view(torch.uint8)), (turn, k)
+        torch.randn(1 << 18, device=DEV).sum().item()
+
+
+def test_expanded_attention_on_two_streams():
+    say("latent prefill two streams")
+    one = prefill_run(Batch(3, [300, 20], [100, 7], 1, 16, False), "bf16", 8, 128, 512, 0.07, 1)
+    two = prefill_run(Batch(4, [40, 260], [900, 3], 1, 64, False), "bf16", 8, 128, 512, 0.07, 2)
+    sets = []
+    for (cache, q, wk, wv, o, keys), b in ((one, Batch(3, [300, 20], [100, 7], 1, 16, False)),
+                                           (two, Batch(4, [40, 260], [900, 3], 1, 64, False))):
+        sets.append((b, b.args(), cache, q, wk, wv, keys, o.out.clone(),
+                     dv.alloc_latent_prefill_outputs(b.B, b.rows, keys, 8, 128, cache)))
+        sets[-1][-1].out.fill_(-7)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, (b, args, cache, q, wk, wv, keys, want, o) in zip(streams, sets):
+            dv.dspark_latent_prefill(b.B, q, wk, wv, b.rows, keys, *args, cache, 0.07, o, stream=s)
+    torch.cuda.synchronize()
+    for b, args, cache, q, wk, wv, keys, want, o in sets:
+        assert torch.equal(o.out, want)
