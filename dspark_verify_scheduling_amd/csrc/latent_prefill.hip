@@ -97,6 +97,7 @@ __device__ inline int last_at(const int32_t* at, int n, int x) {
 // One workgroup: sixteen lanes check a request's words and pages, then the requests'
 // tiles and keys are summed. A few requests: three dependent reads, 4.5 us.
 __global__ __launch_bounds__(kPlanThreads) void plan_kernel(LatentPrefillArgs a, Space w) {
+  fetch_args<sizeof(a) + sizeof(w)>();
   const ReqView& q = a.req;
   const int tid = threadIdx.x;
   int total;
@@ -216,6 +217,7 @@ constexpr int kGatherThreads = 256, kGatherRows = 4;  // rows of a wave
 // by a chain of four reads: 4096 rows 7 us, 20,798 rows of an 8-bit cache 14 us.
 template <bool E8, int L>
 __global__ __launch_bounds__(kGatherThreads) void gather_kernel(LatentPrefillArgs a, Space w) {
+  fetch_args<sizeof(a) + sizeof(w)>();
   constexpr int EPL = E8 ? 16 : 8;  // elements of a lane, in 16 bytes
   constexpr int kLanes = L / EPL;
   const int lane = lane_id();
