@@ -33,7 +33,8 @@ constexpr int kDenseTile = 128; // keys of a workgroup of the expansion
 constexpr int kRowTile = 128;   // rows of a workgroup of the attention
 constexpr int kXcds = 8;
 
-// A request as the plan leaves it; len 0 where it has no rows or is left out.
+// A request as the plan leaves it; len 0 where it has no rows or is left out (keys
+// -1 then if its words of cu_seqlens are out of order).
 struct Req {
   int c0, len, prefix, keys;
 };
@@ -57,7 +58,8 @@ struct Layout {
   int64_t dense;
 };
 
-// Row tiles of a call, at most.
+// Row tiles of a call, at most: no two requests that the plan leaves in have a row
+// in common.
 int most_tiles(int B, int max_rows, int max_keys) {
   const int rows = std::min(max_rows, max_keys);
   return rows / kRowTile + std::min(B, rows);
@@ -136,16 +138,43 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(LatentPrefillArgs a,
       ok = false;
     }
     if (l == 0 && r < q.B)
-      w.req[r] = ok && e > s ? Req{s, e - s, prefix, prefix + (e - s)} : Req{0, 0, 0, 0};
+      w.req[r] = ok && e > s ? Req{s, e - s, prefix, prefix + (e - s)} : Req{0, 0, 0, e < s ? -1 : 0};
   }
   __syncthreads();
   __shared__ int64_t sums[kPlanThreads / kWave];
   const int per = (q.B + kPlanThreads - 1) / kPlanThreads;
   const int r0 = min(tid * per, q.B), r1 = min(r0 + per, q.B);
-  // requests that do not fit any more are left out: sums only grow
+  // (keys of all requests are less than 2^13 2^31)
+  constexpr int64_t kDisorder = (int64_t)1 << 48;
   int64_t mine = 0, all;
-  for (int r = r0; r < r1; ++r) mine += w.req[r].len ? w.req[r].keys : 0;
+  for (int r = r0; r < r1; ++r)
+    mine += w.req[r].len ? w.req[r].keys : w.req[r].keys < 0 ? kDisorder : 0;
   int64_t used = block_excl_scan<int64_t, kPlanThreads>(mine, sums, &all);
+  // Requests can claim the same rows only where some word is less than the one before
+  // it. Then one that has rows of a well-formed request ahead of it is left out: a row
+  // has one writer, and the launch and `order` hold all tiles.
+  if (__builtin_expect(all >= kDisorder, 0)) {
+    unsigned taken = 0;  // bit k: request r0 + k is left out
+    static_assert((DSPARK_MAX_BATCH + kPlanThreads - 1) / kPlanThreads <= 32, "bits of a thread");
+    for (int r = r0; r < r1; ++r) {
+      const Req x = w.req[r];
+      for (int p = 0; x.len && p < r; ++p) {
+        const Req y = w.req[p];
+        if (y.len && y.c0 < x.c0 + x.len && x.c0 < y.c0 + y.len) taken |= 1u << (r - r0);
+      }
+    }
+    __syncthreads();
+    mine = 0;
+    for (int r = r0; r < r1; ++r) {
+      if ((taken >> (r - r0)) & 1) {
+        w.req[r] = Req{0, 0, 0, 0};
+        bits |= DSPARK_DATA_BAD_LENS;
+      }
+      mine += w.req[r].len ? w.req[r].keys : 0;
+    }
+    used = block_excl_scan<int64_t, kPlanThreads>(mine, sums, &all);
+  }
+  // requests that do not fit any more are left out: sums only grow
   for (int r = r0; r < r1; ++r) {
     if (!w.req[r].len) continue;
     used += w.req[r].keys;

@@ -1092,7 +1092,9 @@ size_t dspark_latent_attention_workspace_size(int32_t B, int32_t gamma, int32_t 
  *   max_rows)), whose prefix is negative, or whose keys with those of the requests
  *   before it pass max_keys, sets DSPARK_DATA_BAD_LENS; one that ends beyond its
  *   table row or has a page id outside [0, num_blocks) DSPARK_DATA_BAD_PAGE. None
- *   of such a request's rows is written.
+ *   of such a request's rows is written. Where cu_seqlens is out of order, a
+ *   request that has rows in common with a well-formed one ahead of it (max_keys
+ *   apart) sets DSPARK_DATA_BAD_LENS and is left out too.
  */
 dspark_status dspark_latent_prefill(int32_t B, int32_t num_heads, int32_t nope, dspark_dtype dt,
                                     const void* q, int64_t q_ld, const void* w_k,
