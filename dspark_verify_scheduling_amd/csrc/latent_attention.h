@@ -166,9 +166,13 @@ struct Ring {
   static constexpr int kFlag = kFix + kMaxRows * 4;        // some maximum moves; of two tiles
   // rows with NaN or infinity, kOwn bits for each wave
   static constexpr int kOdd = kFlag + 8;
-  static constexpr int kReqs = kOdd + 8;  // rows of up to kWave requests, 3 words each
+  // up to kWave requests' rows, 3 words each, or, where they are more, bits of those
+  // that are left out for rows of others (see split_kernel)
+  static constexpr int kReqs = kOdd + 8;
+  static constexpr int kReqBytes =
+      12 * kWave > DSPARK_MAX_BATCH / 8 ? 12 * kWave : DSPARK_MAX_BATCH / 8;
   // what a key's weights lose in exponent, 16 bits a key for each wave; 8 bits
-  static constexpr int kDown = kReqs + 12 * kWave;
+  static constexpr int kDown = kReqs + kReqBytes;
   static constexpr int kBytes = kDown + (E8 ? W * kKeys * 2 : 0);
   static_assert(kStage % 256 == 0 && kDown % 16 == 0, "a swizzle is an exclusive or of addresses");
   static_assert(kBytes <= 163840 - 256, "a CU's LDS");
@@ -204,8 +208,14 @@ struct Cursor {
   int begun;     // 0 before the share's first segment
 };
 
+// Whether request r's bit of the words at `bits` in LDS is set.
+__device__ __forceinline__ bool left_out(unsigned bits, int r) {
+  return (lds_read<unsigned>(bits + (r >> 5) * 4) >> (r & 31)) & 1;
+}
+
 // The next segment of a share. `reqs`: the requests' rows in LDS where a wave's
-// lanes hold the batch (len 0: malformed); otherwise they are read from memory.
+// lanes hold the batch (len 0: left out); otherwise they are read from memory, and
+// there are the bits of those that are left out though they are well formed.
 template <int L>
 __device__ __forceinline__ Span next_span(const LatentAttnArgs& a, unsigned reqs, Cursor& c,
                                           Job* job) {
@@ -221,7 +231,9 @@ __device__ __forceinline__ Span next_span(const LatentAttnArgs& a, unsigned reqs
     } else {
       int total;
       const int total_eff = rows_in_use(a.req, &total);
-      if (!rows_of(a.req, a.kv.page_shift, c.r, total_eff, &c0, &len, &prefix)) len = 0;
+      if (!rows_of(a.req, a.kv.page_shift, c.r, total_eff, &c0, &len, &prefix) ||
+          left_out(reqs, c.r))
+        len = 0;
     }
     c0 = __builtin_amdgcn_readfirstlane(c0);
     len = __builtin_amdgcn_readfirstlane(len);
@@ -1111,6 +1123,10 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
 // Persistent over the units of all (request, row segment)s in order: workgroup w
 // takes the w-th equal share, so ragged contexts balance by themselves and a long
 // one is split over many workgroups. The ring of tiles runs on across segments.
+//
+// Requests can claim the same rows only where some word of cu_seqlens is less than the
+// one before it. Then one that has rows of a well-formed request ahead of it is left out:
+// it has no units, by which the joining kernel knows it. A row has one writer.
 template <typename T, bool E8, int L>
 __global__ __launch_bounds__(waves(L) * kWave, waves(L) / 4) void split_kernel(LatentAttnArgs a,
                                                                                Parts ws) {
@@ -1137,7 +1153,16 @@ __global__ __launch_bounds__(waves(L) * kWave, waves(L) / 4) void split_kernel(L
   const int wgs_all = gridDim.x;
   if (q.B <= kWave) {
     int c0 = 0, len = 0, prefix = 0;
-    if (lane_id() < q.B && !rows_of(q, shift, lane_id(), total_eff, &c0, &len, &prefix)) len = 0;
+    const int lane = lane_id();
+    if (lane < q.B && !rows_of(q, shift, lane, total_eff, &c0, &len, &prefix)) len = 0;
+    if (__builtin_expect(__any(lane < q.B && q.cu[lane + 1] < q.cu[lane]), 0)) {
+      bool taken = false;
+      for (int p = 0; p + 1 < q.B; ++p) {
+        const int at = read_lane(c0, p), n = read_lane(len, p);
+        taken |= p < lane && n && len && at < c0 + len && c0 < at + n;
+      }
+      if (taken) len = 0;
+    }
     if (wave == 0) {
       lds_write(lds + R::kReqs + 12 * lane_id(), c0);
       lds_write(lds + R::kReqs + 12 * lane_id() + 4, len);
@@ -1156,17 +1181,40 @@ __global__ __launch_bounds__(waves(L) * kWave, waves(L) / 4) void split_kernel(L
     cur.off = u0 - read_lane(incl - mine, cur.r);
     barrier();
   } else {
+    const unsigned lost = lds + R::kReqs;
+    for (int i = tid; i < DSPARK_MAX_BATCH / 32; i += kThreads) lds_write(lost + i * 4, 0u);
+    __syncthreads();
     auto units = [&](int r) {
       int c0, len, prefix;
-      return rows_of(q, shift, r, total_eff, &c0, &len, &prefix)
+      return rows_of(q, shift, r, total_eff, &c0, &len, &prefix) && !left_out(lost, r)
                  ? units_of<L>(a.num_heads, c0, len, prefix)
                  : (int64_t)0;
     };
     const int per = (q.B + kThreads - 1) / kThreads;
     const int r0 = min(tid * per, q.B), r1 = min(r0 + per, q.B);
+    // (all units are less than 2^13 requests of 2^8 segments of 2^26)
+    constexpr int64_t kDisorder = (int64_t)1 << 48;
     int64_t mine = 0;
-    for (int r = r0; r < r1; ++r) mine += units(r);
+    for (int r = r0; r < r1; ++r) mine += units(r) + (q.cu[r + 1] < q.cu[r] ? kDisorder : 0);
     int64_t at = block_excl_scan<int64_t, kThreads>(mine, wsum, &total);
+    if (__builtin_expect(total >= kDisorder, 0)) {
+      for (int r = r0; r < r1; ++r) {
+        int c0, len, c1, n, prefix;
+        bool taken = false;
+        if (rows_of(q, shift, r, total_eff, &c0, &len, &prefix))
+          for (int p = 0; p < r; ++p)
+            taken |= rows_of(q, shift, p, total_eff, &c1, &n, &prefix) && c1 < c0 + len &&
+                     c0 < c1 + n;
+        if (taken)
+          __hip_atomic_fetch_or(
+              (__attribute__((address_space(3))) unsigned*)(uintptr_t)(lost + (r >> 5) * 4),
+              1u << (r & 31), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+      }
+      __syncthreads();
+      mine = 0;
+      for (int r = r0; r < r1; ++r) mine += units(r);
+      at = block_excl_scan<int64_t, kThreads>(mine, wsum, &total);
+    }
     if (blockIdx.x == 0) {
       int64_t b = at;
       for (int r = r0; r < r1; ++r) {

@@ -26,7 +26,7 @@ __global__ __launch_bounds__(join_threads(SHARED)) void join_kernel(LatentAttnAr
   const ReqView& q = a.req;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int share = blockIdx.x % shares, r = blockIdx.x / shares;
-  const int64_t units = ws.base[q.B], base = ws.base[r];
+  const int64_t units = ws.base[q.B], base = ws.base[r], end = ws.base[r + 1];
   int total;
   const int total_eff = rows_in_use(q, &total);
   int c0, len, prefix;
@@ -41,6 +41,8 @@ __global__ __launch_bounds__(join_threads(SHARED)) void join_kernel(LatentAttnAr
     if (!good) {
       bits = request_status(q, r, total_eff);
       if (!bits) bits = DSPARK_DATA_BAD_PAGE;
+    } else if (end == base) {
+      bits = DSPARK_DATA_BAD_LENS;  // rows of a request ahead of it
     } else if (!tree) {
       bits = DSPARK_DATA_BAD_TREE;
     } else {
@@ -52,7 +54,7 @@ __global__ __launch_bounds__(join_threads(SHARED)) void join_kernel(LatentAttnAr
     }
     if (bits) atomicOr(a.meta + 1, bits);
   }
-  if (!good || !tree) return;
+  if (!good || !tree || end == base) return;
   const Shape s = shape_of<L>(a.num_heads, c0, len, prefix);
   const int wgs = wgs_in_use(units, ws.wgs);
   const int qi = lane & 31;

@@ -1043,7 +1043,9 @@ dspark_status dspark_latent_commit(int32_t B, int32_t gamma, const int32_t* path
  *   workspace          dspark_latent_attention_workspace_size() bytes, 256-byte
  *                      aligned; contents irrelevant, no state between calls;
  *                      calls that share it must not overlap in time
- * Data errors: as for dspark_tree_attention.
+ * Data errors: as for dspark_tree_attention. Where cu_seqlens is out of order, a
+ *   request that has rows in common with a well-formed one ahead of it (its tree
+ *   and page ids apart) sets DSPARK_DATA_BAD_LENS and is left out too.
  */
 dspark_status dspark_latent_attention(int32_t B, int32_t gamma, int32_t num_heads,
                                       dspark_dtype dt, const void* q_latent, int64_t ql_ld,

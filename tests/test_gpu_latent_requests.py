@@ -7,9 +7,10 @@ import pytest
 import torch
 
 import dspark_verify_scheduling_amd as dv
+import oracle
 from _gpu import DEV, say
-from test_gpu_latent import R, latent_setup, prefill_check, typed
-from test_gpu_target import TYPES, Batch, i32
+from test_gpu_latent import R, attention_bound, latent_setup, lget, prefill_check, typed
+from test_gpu_target import TYPES, Batch, W, f64, i32, within
 
 pytestmark = pytest.mark.gpu
 
@@ -22,23 +23,23 @@ def _need_gpu(hip):
 # ------------------------------------------------------------------ lengths out of order
 
 def disorder(cu, ctx, most=10 ** 9):
-    """A batch of these words, whose last is the largest, and who has which rows: the
-    lengths of those that have any, and the requests that are well formed but have rows in
-    common with a well-formed one ahead."""
-    total, mine, lost, own = cu[-1], [], [], set()
-    for r, c in enumerate(ctx):
-        rows = set(range(cu[r], cu[r + 1]))
-        good = 0 <= cu[r] <= cu[r + 1] <= total and c >= 0 and len(rows) <= most
-        if good and any(m & rows for m in mine):
-            lost.append(r)
-        mine.append(rows if good else set())
-    lens = [0 if r in lost else len(m) for r, m in enumerate(mine)]
+    """A batch of these words, whose last is the largest, the lengths of its requests as
+    far as they are well formed and have no rows of a well-formed one ahead, and which
+    rows are nobody's."""
+    cu, total = [int(c) for c in cu], int(cu[-1])
+    lens, seen, nobody = [], [], torch.ones(total + 3, dtype=torch.bool)
+    for s, e, c in zip(cu, cu[1:], ctx):
+        good = 0 <= s <= e <= total and c >= 0 and e - s <= most
+        free = good and not any(s < y and x < e for x, y in seen)
+        if good:
+            seen.append((s, e))
+        lens.append(e - s if free else 0)
+        if free:
+            nobody[s:e] = False
     # pages for everybody's rows, as if they were in order
-    b = Batch(3, [max(0, e - s) for s, e in zip(cu, cu[1:])], [max(c, 0) for c in ctx], 1, 16, False)
-    b.cu, b.lens, b.rows = np.asarray(cu, np.int32), lens, total + 3
-    for r, n in enumerate(lens):
-        own |= mine[r] if n else set()
-    return b, lost, torch.tensor([n not in own for n in range(b.rows)], device=DEV)
+    b = Batch(3, [max(0, e - s) for s, e in zip(cu, cu[1:])], [max(c, 0) for c in ctx], 8, 16, False)
+    b.cu, b.rows = np.asarray(cu, np.int32), total + 3
+    return b, lens, nobody.to(DEV)
 
 
 OUT_OF_ORDER = [  # words, contexts
@@ -59,14 +60,12 @@ def test_latent_prefill_where_lengths_go_back(case, kind):
     cu, ctx = OUT_OF_ORDER[case]
     say(f"latent prefill, words out of order, case {case} {kind}")
     H, n, L = 3, 64, 256
-    b, lost, nobody = disorder(cu, ctx)
-    full, b.lens = b.lens, [max(0, e - s) for s, e in zip(cu, cu[1:])]
+    b, lens, nobody = disorder(cu, ctx)
     cache, _, _ = latent_setup(b, kind, 1, L)
-    b.lens = full
+    keys, b.lens = sum(b.ctx) + sum(b.lens), lens
     rng, dt = np.random.default_rng(1), TYPES[kind][1]
     q = typed(rng, (b.rows, H, n + R), dt).to(DEV)
     w = typed(rng, (H, 2 * n, L), dt, L ** -0.5).to(DEV)
-    keys = sum(c + max(0, e - s) for c, s, e in zip(b.ctx, cu, cu[1:]))
     o = dv.alloc_latent_prefill_outputs(b.B, b.rows, keys, H, n, cache, lse=True)
     for _ in range(3):
         o.workspace.fill_(0xFF)
@@ -78,3 +77,60 @@ def test_latent_prefill_where_lengths_go_back(case, kind):
         assert o.attention_meta.tolist() == [cu[-1], dv.DATA_BAD_LENS]
         prefill_check(b, kind, H, n, L, 0.07, cache, q, w[:, :n], w[:, n:], o)
         assert bool((o.out[nobody] == -7).all()) and bool((o.lse[nobody] == -7).all())
+
+
+def swapped(B, gamma, seed):
+    """Words in order but for some that have changed places with one a few further."""
+    rng = np.random.default_rng(seed)
+    cu = np.concatenate([[0], np.cumsum(rng.integers(1, gamma + 2, B))])
+    for i in rng.integers(0, B - 4, max(1, B // 20)):
+        j = i + int(rng.integers(1, 4))
+        cu[i], cu[j] = cu[j], cu[i]
+    return cu.tolist(), rng.integers(0, 60, B).tolist()
+
+
+SHORT_OUT_OF_ORDER = [  # words, contexts; up to 9 rows a request
+    ([0, 5, 0, 5, 6], [40, 3, 100, 0]),
+    ([0, 9] * 12, [70] * 23),
+    ([3, 9, 5, 12, 10, 14], [30, 0, 9, 0, 64]),
+    ([4, 9, 0, 4, 2, 9, 11], [3, 0, 70, 0, 8, 0]),
+    ([0, 6, 6, 0, 6, 7], [-1, 0, 0, 12, 0]),      # malformed ones claim nothing:
+    ([0, 20, 12, 20, 21], [50, 0, 31, 64]),       # too many rows
+    ([0] + [2, 1] * 150 + [3, 8], [1] * 302),
+    swapped(64, 8, 1), swapped(65, 8, 2), swapped(300, 4, 3), swapped(2500, 2, 4),
+]
+
+
+@pytest.mark.parametrize("kind,L,H", [("bf16", 512, 5), ("f16", 256, 33), ("e4m3", 512, 40)])
+@pytest.mark.parametrize("case", range(len(SHORT_OUT_OF_ORDER)))
+def test_latent_attention_where_lengths_go_back(case, kind, L, H):
+    cu, ctx = SHORT_OUT_OF_ORDER[case]
+    say(f"latent attention, words out of order, case {case} {kind} L={L}")
+    if len(ctx) > 400:
+        H = 2
+    b, lens, nobody = disorder(cu, ctx, 9)
+    assert 0 < sum(lens) and len(lens) > sum(n > 0 for n in lens)
+    if len(ctx) > 400:  # pages of others' will do
+        b.nb = b.nb // 4
+        b.table = np.where(b.table >= 0, b.table % b.nb, b.table)
+    cache, ql, qr = latent_setup(b, kind, H, L)
+    o = dv.alloc_latent_attention_outputs(b.B, 8, b.rows, H, cache, lse=True)
+    for _ in range(3):
+        o.workspace.fill_(0xFF)
+        o.out.fill_(-7)
+        o.lse.fill_(-7)
+        dv.dspark_latent_attention(b.B, 8, ql, qr, b.rows, i32(cu), i32(ctx), i32(b.table), cache, 0.05, o)
+        torch.cuda.synchronize()
+        assert o.attention_meta.tolist() == [cu[-1], dv.DATA_BAD_LENS]
+        assert bool((o.out[nobody] == -7).all()) and bool((o.lse[nobody] == -7).all())
+    got, got_lse, u = f64(o.out), f64(o.lse), TYPES[kind][2]
+    for r, n in enumerate(lens):
+        if not n:
+            continue
+        T, s = ctx[r] + n, slice(cu[r], cu[r + 1])
+        lat, rope = lget(cache, b.slots(r, 0, T))
+        ref, lse, mean_abs, top = oracle.latent_attention(f64(ql[s]), f64(qr[s]), lat, rope, ctx[r], None, 0.05)
+        bound, lse_bound = attention_bound(ref, lse, mean_abs, (L + R + 16) * W * top,
+                                           np.abs(lat).max(), T, u, kind)
+        within(got[s], ref, bound, (r, "out"))
+        within(got_lse[s], lse, lse_bound, (r, "lse"))
