@@ -137,8 +137,11 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(LatentPrefillArgs a,
       bits |= DSPARK_DATA_BAD_PAGE;
       ok = false;
     }
-    if (l == 0 && r < q.B)
-      w.req[r] = ok && e > s ? Req{s, e - s, prefix, prefix + (e - s)} : Req{0, 0, 0, e < s ? -1 : 0};
+    if (l == 0 && r < q.B) {
+      // (held to 32 bits: so many keys pass any max_keys)
+      const int keys = (int)min((int64_t)prefix + (e - s), (int64_t)0x7FFFFFFF);
+      w.req[r] = ok && e > s ? Req{s, e - s, prefix, keys} : Req{0, 0, 0, e < s ? -1 : 0};
+    }
   }
   __syncthreads();
   __shared__ int64_t sums[kPlanThreads / kWave];

@@ -79,6 +79,29 @@ def test_latent_prefill_where_lengths_go_back(case, kind):
         assert bool((o.out[nobody] == -7).all()) and bool((o.lse[nobody] == -7).all())
 
 
+def test_latent_prefill_of_more_keys_than_32_bits_count():
+    """A request whose last cache index passes 2^31 is left out for its keys, as any that
+    passes max_keys; the one ahead of it is not."""
+    say("latent prefill, keys past 2^31")
+    H, n, L, page = 2, 64, 256, 256
+    b = Batch(2, [20, 10], [30, 0], 1, page, False)
+    cache, _, _ = latent_setup(b, "bf16", 1, L)
+    q = typed(b.rng, (b.rows, H, n + R), torch.bfloat16).to(DEV)
+    w = typed(b.rng, (H, 2 * n, L), torch.bfloat16, L ** -0.5).to(DEV)
+    table = torch.zeros(2, 2 ** 31 // page + 1, dtype=torch.int32, device=DEV)
+    table[:, :b.width] = i32(np.maximum(b.table, 0))
+    o = dv.alloc_latent_prefill_outputs(2, b.rows, 60, H, n, cache, lse=True)
+    for prefix, rows in ((2 ** 31 - 5, (0,)), (2 ** 31 - 11, (0,)), (0, (0, 1))):
+        o.out.fill_(-7)
+        o.lse.fill_(-7)
+        dv.dspark_latent_prefill(2, q, w[:, :n], w[:, n:], b.rows, 60, i32(b.cu), i32([30, prefix]), table,
+                                 cache, 0.07, o)
+        torch.cuda.synchronize()
+        assert o.attention_meta.tolist() == [30, dv.DATA_BAD_LENS if prefix else 0]
+        prefill_check(b, "bf16", H, n, L, 0.07, cache, q, w[:, :n], w[:, n:], o,
+                      [r for r in (0, 1) if r not in rows])
+
+
 def swapped(B, gamma, seed):
     """Words in order but for some that have changed places with one a few further."""
     rng = np.random.default_rng(seed)
