@@ -10,12 +10,22 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Positions of all packed rows on all axes, a share to each thread.
+// Positions of all packed rows on all axes, a share to each thread. Rows before any
+// request's, where the first starts late, are nobody's.
 __device__ int position_status(const AppendAxesArgs& a, int total_eff) {
+  const ReqView& q = a.base.req;
   int bits = 0;
-  if (a.base.req.B == 0) return bits;
+  if (q.B == 0) return bits;
+  __shared__ int first;
+  if (threadIdx.x == 0) first = total_eff;
+  __syncthreads();
+  int lo = max(q.cu[0], 0);
+  if (lo > 0)  // (words out of order: not the least then)
+    for (int r = threadIdx.x; r < q.B; r += kThreads) lo = min(lo, max(q.cu[r], 0));
+  atomicMin(&first, lo);
+  __syncthreads();
 #pragma unroll 4
-  for (int n = threadIdx.x; n < total_eff; n += kThreads) {
+  for (int64_t n = (int64_t)first + threadIdx.x; n < total_eff; n += kThreads) {
     int p[DSPARK_MAX_AXES];  // all axes' loads before the first is looked at
 #pragma unroll
     for (int x = 0; x < DSPARK_MAX_AXES; ++x)

@@ -10,7 +10,7 @@ import dspark_verify_scheduling_amd as dv
 import oracle
 from _gpu import DEV, say
 from test_gpu_latent import R, attention_bound, latent_setup, lget, prefill_check, typed
-from test_gpu_target import TYPES, Batch, W, f64, i32, within
+from test_gpu_target import TYPES, Batch, W, f64, i32, make_cache, within
 
 pytestmark = pytest.mark.gpu
 
@@ -18,6 +18,47 @@ pytestmark = pytest.mark.gpu
 @pytest.fixture(scope="module", autouse=True)
 def _need_gpu(hip):
     return hip
+
+
+# ------------------------------------------------------------------ requests that start late
+
+@pytest.mark.parametrize("B", [1, 3, 300])
+def test_axes_positions_of_nobody_do_not_count(B):
+    """Requests of a part of the packed rows: positions before the first one's rows are not
+    looked at; a bad one of theirs still counts where words are out of order."""
+    say(f"append axes, rows that start late, B={B}")
+    start, D = 40, 64
+    b = Batch(B, [3] * B, [7] * B, 1, 16, False)
+    b.cu = b.cu + start
+    b.rows += start
+    cache = make_cache("bf16", b.nb, 1, 16, D)
+    x = typed(b.rng, (b.rows, 1, D), torch.bfloat16).to(DEV)
+    pos = torch.zeros(2, b.rows, dtype=torch.int32, device=DEV)
+    pos[:, :start] = -1
+    rope = torch.zeros(5, D, device=DEV)
+
+    def call(cu):
+        o = dv.alloc_append_outputs(b.rows, 1, cache)
+        o.q_out.fill_(-7)
+        dv.dspark_kv_append_axes(B, x, x, x, b.rows, i32(cu), i32(b.ctx), pos, [i % 2 for i in range(D // 2)],
+                                 i32(b.table), cache, o, rope)
+        torch.cuda.synchronize()
+        return o
+
+    total = int(b.cu[-1])
+    o = call(b.cu)
+    assert o.append_meta.tolist() == [total, 0]
+    assert bool((o.q_out[:start] == -7).all()) and bool((o.q_out[start:total] == 0).all())
+    pos[1, total - 1] = 5
+    assert call(b.cu).append_meta.tolist() == [total, dv.DATA_BAD_POS]
+    pos[1, total - 1] = 0
+    pos[0, start + 4 if B > 1 else start] = -2
+    assert call(b.cu).append_meta.tolist() == [total, dv.DATA_BAD_POS]
+    if B > 1:  # the first request's word is beyond the others'
+        for word in (total, 2 ** 31 - 1):
+            cu = b.cu.copy()
+            cu[0] = word
+            assert call(cu).append_meta.tolist() == [total, dv.DATA_BAD_LENS | dv.DATA_BAD_POS]
 
 
 # ------------------------------------------------------------------ lengths out of order
