@@ -87,14 +87,18 @@ dspark_status check_queries(const char* fn, int32_t num_heads, int32_t least, ds
   return DSPARK_OK;
 }
 
-// Rows whose heads have a stride of their own.
+// Rows whose heads have a stride of their own: a row's heads lie together, or a head's
+// rows do (as a product for each head leaves them).
 dspark_status check_head_rows(const char* fn, const char* name, const void* p, int64_t ld,
                               int64_t head_ld, int32_t heads, int64_t dim, int32_t max_rows) {
-  if (heads > 1 && (head_ld < dim || head_ld % 8 != 0 || head_ld > (1LL << 32)))
+  if (heads <= 1) return check_rows(fn, name, p, ld, dim, max_rows);
+  if (head_ld < dim || head_ld % 8 != 0 || head_ld > (1LL << 40))
     return fail(DSPARK_E_INVALID,
                 "%s: the head stride %lld of %s must be >= %lld elements and a multiple of 8", fn,
                 (long long)head_ld, name, (long long)dim);
-  return check_rows(fn, name, p, ld, heads > 1 ? (heads - 1) * head_ld + dim : dim, max_rows);
+  const int64_t row = (heads - 1) * head_ld + dim;
+  const bool by_head = ld < row && (max_rows < 2 || ld <= (head_ld - dim) / (max_rows - 1));
+  return check_rows(fn, name, p, ld, by_head ? dim : row, max_rows);
 }
 
 }  // namespace

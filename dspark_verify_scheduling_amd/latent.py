@@ -19,7 +19,8 @@ from .target import _CODE, _I32, _TORCH, AttentionOutputs, _device, _on, _stride
 
 
 def _heads(t: torch.Tensor, name: str, dtype, rows: int, heads: int, dim: int, dev: int):
-    """Pointer, row stride and head stride of [rows, heads, dim] with dense elements."""
+    """Pointer, row stride and head stride of [rows, heads, dim] with dense elements,
+    whose rows or whose heads may be the outer ones."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.get_device() != dev:
@@ -172,7 +173,8 @@ def dspark_latent_append(B: int, kv: torch.Tensor, max_rows: int, cu_seqlens: to
     """Norm (``weight`` [latent_dim]) and rotation (``rope`` [positions, 64]
     float32, cosines then sines) of the packed rows ``kv`` [max_rows, latent_dim
     + 64], their write into the cache, and the rotation of ``q_rope`` [max_rows,
-    num_heads, 64]; ``out.q_rope`` may be ``q_rope``. ``gamma`` 0: requests have
+    num_heads, 64], also as [num_heads, max_rows, 64] transposed; ``out.q_rope`` may
+    be ``q_rope``. ``gamma`` 0: requests have
     any number of rows; otherwise up to gamma + 1, in a chain or in the trees of
     ``tree_parents`` [B, gamma]."""
     dev = _device(cache)
@@ -303,7 +305,8 @@ def dspark_latent_attention(B: int, gamma: int, q_latent: torch.Tensor, q_rope: 
     """Attention of the packed rows over the latents of each request's context
     and its own tree (``tree_parents`` [B, gamma]; None: a chain). ``q_latent``
     [max_rows, num_heads, latent_dim] are the queries taken through the heads'
-    key weights, ``q_rope`` [max_rows, num_heads, 64] their turned parts; the
+    key weights, ``q_rope`` [max_rows, num_heads, 64] their turned parts, both also
+    transposed from a product for each head; the
     outputs are means of latents, for the heads' value weights."""
     dev = _device(cache)
     dt, L = cache.row_dtype, cache.latent_dim

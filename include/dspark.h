@@ -972,7 +972,8 @@ typedef struct dspark_latent_cache {
  *   dt                 type of kv, weight and q_rope: BF16 or F16; the cache
  *                      holds the same type, or E4M3 with BF16
  *   kv, kv_ld          rows of latent_dim + DSPARK_LATENT_ROPE elements
- *   q_rope             row n, head h at q_rope + n * q_ld + h * q_head_ld
+ *   q_rope             row n, head h at q_rope + n * q_ld + h * q_head_ld; a row's
+ *                      heads lie together (q_ld beyond the last) or a head's rows do
  *   q_rope_out         rows as q_rope; q_rope itself (with its strides) is allowed
  *   All rows 16-byte aligned, strides multiples of 8 elements.
  *   weight             [latent_dim] or NULL, 16-byte aligned
@@ -1034,7 +1035,8 @@ dspark_status dspark_latent_commit(int32_t B, int32_t gamma, const int32_t* path
  *   num_heads          1..DSPARK_LATENT_MAX_HEADS
  *   dt                 BF16 or F16; the cache holds the same type, or E4M3 with BF16
  *   q_latent           row n, head h at q_latent + n * ql_ld + h * ql_head_ld:
- *                      latent_dim elements; q_rope alike (DSPARK_LATENT_ROPE)
+ *                      latent_dim elements; q_rope alike (DSPARK_LATENT_ROPE).
+ *                      Strides as for dspark_latent_append's q_rope
  *   out                row n at out + n * out_ld: num_heads dense heads of latent_dim
  *   All 16-byte aligned, strides multiples of 8 elements.
  *   scale              finite

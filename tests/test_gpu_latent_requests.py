@@ -198,3 +198,42 @@ def test_latent_attention_where_lengths_go_back(case, kind, L, H):
                                            np.abs(lat).max(), T, u, kind)
         within(got[s], ref, bound, (r, "out"))
         within(got_lse[s], lse, lse_bound, (r, "lse"))
+
+
+# ------------------------------------------------------------------ orders of rows and heads
+
+@pytest.mark.parametrize("kind,L,H", [("bf16", 512, 20), ("f16", 256, 3), ("e4m3", 512, 128)])
+def test_queries_of_a_product_for_each_head(kind, L, H):
+    """Queries as a product for each head leaves them, a head's rows together, give what
+    the same queries in rows do, bit for bit; so does the append, in place too."""
+    say(f"latent queries by head {kind} L={L} H={H}")
+    b = Batch(4, [5, 1, 3], [100, 0, 700], 4, 16, True)
+    cache, ql, qr = latent_setup(b, kind, H, L)
+    n = int(b.cu[-1])
+    ql[n:], qr[n:] = 0, 0
+    rope = torch.randn(800, R, device=DEV)
+    kv = typed(b.rng, (b.rows, L + R), ql.dtype).to(DEV)
+    by_head = [x.transpose(0, 1).contiguous().transpose(0, 1) for x in (ql, qr)]
+    assert by_head[0].stride(0) == L and by_head[1].stride(1) == b.rows * R
+    got = []
+    for latent, turned, place in ((ql, qr.contiguous(), False), (*by_head, False), (*by_head, True)):
+        ap = dv.alloc_latent_append_outputs(b.rows, H, cache)
+        if place:
+            ap = ap._replace(q_rope=turned)
+        elif latent is not ql:
+            ap = ap._replace(q_rope=torch.empty_like(turned.transpose(0, 1)).transpose(0, 1))
+            assert ap.q_rope.stride(0) == R
+        if not place:
+            ap.q_rope.fill_(-7)
+        dv.dspark_latent_append(b.B, kv, b.rows, *b.args(), cache, ap, q_rope=turned, rope=rope, gamma=4,
+                                tree_parents=b.par())
+        o = dv.alloc_latent_attention_outputs(b.B, 4, b.rows, H, cache, lse=True)
+        dv.dspark_latent_attention(b.B, 4, latent, ap.q_rope, b.rows, *b.args(), cache, 0.05, o,
+                                   tree_parents=b.par())
+        torch.cuda.synchronize()
+        assert ap.append_meta.tolist() == [n, 0] and o.attention_meta.tolist() == [n, 0]
+        assert bool((ap.q_rope[n:] == (0 if place else -7)).all())
+        got.append([ap.q_rope[:n].clone(), o.out[:n].clone(), o.lse[:n].clone()])
+    for other in got[1:]:
+        for x, y in zip(got[0], other):
+            assert torch.equal(x, y)
