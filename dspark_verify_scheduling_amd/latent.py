@@ -363,6 +363,8 @@ def dspark_latent_prefill(B: int, q: torch.Tensor, w_k: torch.Tensor, w_v: torch
     weights = []
     for name, t in (("w_k", w_k), ("w_v", w_v)):
         ptr, head, row = _heads(t, name, dt, hq, n, L, dev)
+        if t.shape[0] != hq:
+            raise ValueError(f"{name} holds {t.shape[0]} heads, q has {hq}")
         if row != L:
             raise ValueError(f"the rows of {name} must be dense")
         weights.append((ptr, head))

@@ -237,3 +237,23 @@ def test_queries_of_a_product_for_each_head(kind, L, H):
     for other in got[1:]:
         for x, y in zip(got[0], other):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("which", ["w_k", "w_v"])
+def test_weights_of_other_heads_are_refused(which):
+    """A share of the heads needs its share of the weights: more than q has heads would be
+    the first heads' without a word."""
+    say(f"latent prefill, {which} of other heads")
+    n, L = 64, 256
+    b = Batch(2, [5], [0], 1, 16, False)
+    cache, _, _ = latent_setup(b, "bf16", 1, L)
+    q = torch.zeros(b.rows, 2, n + R, dtype=torch.bfloat16, device=DEV)
+    w = torch.zeros(4, n, L, dtype=torch.bfloat16, device=DEV)
+    o = dv.alloc_latent_prefill_outputs(1, b.rows, 5, 2, n, cache)
+    for heads in (4, 1):
+        weights = {"w_k": w[:2], "w_v": w[:2], which: w[:heads]}
+        with pytest.raises(ValueError, match=which):
+            dv.dspark_latent_prefill(1, q, weights["w_k"], weights["w_v"], b.rows, 5, *b.args(), cache, 0.1, o)
+    dv.dspark_latent_prefill(1, q, w[:2], w[2:], b.rows, 5, *b.args(), cache, 0.1, o)
+    torch.cuda.synchronize()
+    assert o.attention_meta.tolist() == [5, 0]
