@@ -354,7 +354,9 @@ def dspark_latent_prefill(B: int, q: torch.Tensor, w_k: torch.Tensor, w_v: torch
     over their requests' cached tokens and themselves, with keys and values
     expanded by ``w_k`` and ``w_v`` [num_heads, nope, latent_dim] (which may be
     parts of one weight). ``max_keys``: cached tokens of all requests together,
-    their rows included, at most."""
+    their rows included, at most. The workspace grows with heads times keys; a share of
+    the heads at a time (``q[:, a:b]``, ``w_k[a:b]``, ``w_v[a:b]``, an output
+    ``out[:, a:b]``) needs that share of it."""
     dev = _device(cache)
     dt, L = cache.row_dtype, cache.latent_dim
     hq, dim = (q.shape[1], q.shape[2]) if q.dim() == 3 else (0, 0)

@@ -1092,6 +1092,13 @@ size_t dspark_latent_attention_workspace_size(int32_t B, int32_t gamma, int32_t 
  *   All 16-byte aligned, strides multiples of 8 elements.
  *   lse, prefill_meta, workspace  as for dspark_latent_attention, with
  *                      dspark_latent_prefill_workspace_size()
+ * The workspace holds every head's keys and values, 4 * nope bytes for each of
+ * max_keys, beside the rows they come from. Heads do not meet: a caller who has less
+ * room makes the call for a share of the heads at a time (q, w_k, w_v and out from
+ * the share's first head on, with their strides as they are, and an lse of its own).
+ * For up to DSPARK_MAX_GAMMA + 1 rows a request dspark_latent_attention needs fewer
+ * operations, 2 * (2 * latent_dim + DSPARK_LATENT_ROPE) for a row, head and key: the
+ * expansion alone is 4 * latent_dim * nope for a head and key.
  * Data errors: a request whose rows lie outside [0, min(cu_seqlens[B],
  *   max_rows)), whose prefix is negative, or whose keys with those of the requests
  *   before it pass max_keys, sets DSPARK_DATA_BAD_LENS; one that ends beyond its

@@ -257,3 +257,33 @@ def test_weights_of_other_heads_are_refused(which):
     dv.dspark_latent_prefill(1, q, w[:2], w[2:], b.rows, 5, *b.args(), cache, 0.1, o)
     torch.cuda.synchronize()
     assert o.attention_meta.tolist() == [5, 0]
+
+
+@pytest.mark.parametrize("kind,H,cuts", [("bf16", 8, (0, 3, 8)), ("e4m3", 5, (0, 1, 2, 5))])
+def test_prompts_by_shares_of_the_heads(kind, H, cuts):
+    """A call for some heads at a time, in a workspace of their size, gives what one call
+    for all does, bit for bit."""
+    say(f"latent prefill by shares of heads {kind}")
+    n, L = 64, 256
+    b = Batch(6, [150, 1, 40], [30, 200, 0], 1, 16, False)
+    cache, _, _ = latent_setup(b, kind, 1, L)
+    dt = TYPES[kind][1]
+    q = typed(b.rng, (b.rows, H, n + R), dt).to(DEV)
+    w = typed(b.rng, (H, 2 * n, L), dt, L ** -0.5).to(DEV)
+    keys = sum(b.ctx) + sum(b.lens)
+    whole = dv.alloc_latent_prefill_outputs(3, b.rows, keys, H, n, cache, lse=True)
+    parts = torch.full_like(whole.out, -7)
+    for o in (whole.out, whole.lse):
+        o.fill_(-7)
+    dv.dspark_latent_prefill(3, q, w[:, :n], w[:, n:], b.rows, keys, *b.args(), cache, 0.07, whole)
+    for lo, hi in zip(cuts, cuts[1:]):
+        o = dv.alloc_latent_prefill_outputs(3, b.rows, keys, hi - lo, n, cache, lse=True)
+        assert o.workspace.numel() < whole.workspace.numel()
+        o.lse.fill_(-7)
+        o = o._replace(out=parts[:, lo:hi])
+        dv.dspark_latent_prefill(3, q[:, lo:hi], w[lo:hi, :n], w[lo:hi, n:], b.rows, keys, *b.args(), cache,
+                                 0.07, o)
+        torch.cuda.synchronize()
+        assert o.attention_meta.tolist() == [int(b.cu[-1]), 0]
+        assert torch.equal(o.lse, whole.lse[:, lo:hi])
+    assert torch.equal(parts, whole.out)
