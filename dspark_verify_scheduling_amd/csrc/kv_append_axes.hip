@@ -41,10 +41,14 @@ __device__ int position_status(const AppendAxesArgs& a, int total_eff) {
 // row's request and page by itself, and a row's waves take its heads in turn. Pair i
 // turns by row positions[axis of i] of the table, so a lane gathers its eight
 // cosines and sines from up to num_axes table rows, once for all heads.
-// Bound by its arithmetic where rows are many, two thirds of the time in 205 vector
-// instructions to a round of four heads: 13,001 rows of 32 + 2 * 8 heads of 128 into
-// an 8-bit cache, 80 us, 3.7 TB/s. Bound by dependent reads where they are few: 8
-// rows 7.1 us. A wave to a row there takes 12 rounds one after the other; a
+// Bound by its arithmetic where rows are many, 2,460 vector instructions a row and four
+// fifths of a CU's busy cycles: 13,001 rows of 32 + 2 * 8 heads of 128 into an 8-bit
+// cache, 81 us, 3.6 TB/s. Bound by dependent reads where they are few: 8 rows 7.1 us.
+// (The one workgroup that checks all positions is hidden beside the rows, 256,000 of 1 +
+// 2 heads of 64 among them: 215 us with it and without.) A workgroup to a row, or a wave:
+// 128 rows of 32 + 2 * 8 heads in 8 bits 15.5 and 16.5 us, of 28 + 2 * 4 in 16 bits 14.8
+// and 11.9; 1,024 rows 25.3 and 29, 23.8 and 23.5; 2,048 rows 32.7 and 31.3, 30.3 and
+// 26.4. A wave to a row where rows are few takes 12 rounds one after the other; a
 // workgroup to a row where they are many has four waves look the same request up (the
 // first case: 199 us for the call with the cache's read, 133 with a wave; 96 with two
 // rounds under way, nothing in scratch memory and no exchange through LDS).

@@ -1111,14 +1111,18 @@ __device__ __forceinline__ void segment(const LatentAttnArgs& a, const Parts& ws
 // registers, m moved only when a score passes it by Soft::kSlack. Parts of a row
 // join by (m, sum, outputs) in join_kernel.
 //
-// Bound by what a workgroup does in turn for a tile of 64 keys: 128 to 144 products
-// to a SIMD (L = 512, 64 rows: 2,180 cycles of some 4,500), the scores' reads of LDS
-// beside them, then the exponentials and three meetings of its waves. 32 chains of
-// up to 4 rows at 128 heads over 1k to 8k keys: 110 us, 760 TFLOP/s; 16 trees of up to
-// 17 rows at 32 heads, 8 bits: 120 us, 650; contexts of 40k and 131k at 20 heads (L =
-// 256): 72 us, 390; one row at 32 heads over 1500 keys: 13.7 us, a chain of reads. A
+// Bound by what a workgroup does in turn for a tile of 64 keys: 68 products of 32
+// cycles to a SIMD (L = 512, 64 rows; 144 at L = 256, 128 rows, for its two waves), the
+// scores' reads of LDS beside them, then the exponentials, around two meetings of its
+// waves and four where a maximum moves. 32 chains of up to 4 rows at 128 heads over 1k to
+// 8k keys: 110 us, 760 TFLOP/s, 5,140 cycles a tile with the starts and ends of segments,
+// 42 % of them products, and 640 MB past the L2; 16 trees of up to 17 rows at 32 heads,
+// 8 bits: 119 us, 660, 6,070 cycles, 36 %; contexts of 40k and 131k at 20 heads (L = 256):
+// 71 us, 280, nine tiles to a workgroup and more than half of the products for rows that
+// are not there; one row at 32 heads over 1500 keys: 14.0 us, a chain of reads. A
 // wave with all products of 32 rows needs 512 outputs a lane beside its queries and
-// went through scratch memory (the chains: 508 us), hence columns to a wave.
+// went through scratch memory (the chains: 508 us), hence columns to a wave. (At L = 256
+// 45 registers are spilled and read back around the loop, none in it.)
 //
 // Persistent over the units of all (request, row segment)s in order: workgroup w
 // takes the w-th equal share, so ragged contexts balance by themselves and a long

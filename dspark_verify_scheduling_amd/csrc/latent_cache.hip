@@ -92,7 +92,10 @@ struct Turn {
 // `per` packed rows to a workgroup, kWaves / per waves to a row: the first takes
 // its latent, and the rotated part with the query heads go eight at a time to the
 // waves in turn. 16,401 rows of 512 + 64 and 64 query heads into an 8-bit cache: 52
-// us, 5.7 TB/s read and written. A few rows: 4.1 us of dependent reads.
+// us, 5.8 TB/s read and written. A few rows: 4.1 us of dependent reads. All waves to a
+// row, or a row to each: 1,024 rows at 64 heads and 8 bits 7.7 and 8.7 us, at 20 heads
+// 5.4 and 5.3, at 8 heads (L = 256) 5.1 and 4.6; 3,000 rows 15.8 and 13.1, 10.2 and 7.3,
+// 9.0 and 5.7; at 128 heads a row to a workgroup is 7 % better there too.
 template <typename T, bool E8, int L>
 __global__ __launch_bounds__(kThreads) void latent_append_kernel(LatentAppendArgs a, int per) {
   typedef typename Vec8<T>::type T8;
@@ -236,7 +239,7 @@ constexpr int kReadRows = 4;  // of a wave, under way at once
 
 // kReadRows rows to a wave: their requests and pages are found together, then each
 // row is one 16-byte load a lane for the latent and one of eight lanes for the
-// rotated part. 16,401 rows of an 8-bit cache: 10.6 us, 2.8 TB/s, of which 4.5 are a
+// rotated part. 16,401 rows of an 8-bit cache: 10.9 us, 2.7 TB/s, of which 4.4 are a
 // single row's.
 template <bool E8, int L>
 __global__ __launch_bounds__(kThreads) void latent_read_kernel(LatentReadArgs a) {
@@ -318,7 +321,8 @@ __global__ __launch_bounds__(kThreads) void latent_read_kernel(LatentReadArgs a)
 
 // A workgroup per (request, a few layers), as many as its threads hold; a thread owns
 // 16-byte columns of a row's latent and rotated part or one byte of its exponents
-// (256 requests, 27 layers, 8 bits, two rows each to move: 11 us a call),
+// (256 requests, 27 layers, 8 bits, two rows each to move: 10.8 us, 1.6 TB/s; bound by
+// the path's look-up, three dependent reads in each of six workgroups of a request),
 // and moves the path's rows of that column in ascending order (as commit_kernel of
 // the key/value cache does, with the same reason why batches of loads may run
 // ahead of their stores).

@@ -330,9 +330,10 @@ constexpr int kExpandThreads = 256;
 // four elements in a row of one key; they are turned through LDS into whole lines.
 // 32 of the L products to a step, through a ring of three stages, so that two
 // workgroups share a CU and one's first loads and last stores run beside the other's
-// products. Bound by the products: 34 GFLOP (4096 keys, 32 heads) 43 to 50 us, 349
-// GFLOP (20,798 keys, 64 heads) 400 to 427 us, 820 to 870 TFLOP/s. (One workgroup of
-// 256 keys to a CU: 62 and 554 us.)
+// products. 34 GFLOP (4096 keys, 32 heads) 47 us, 740 TFLOP/s; 349 GFLOP (20,798 keys, 64
+// heads) 418 us, 840; 43 % of a CU's busy cycles are products of its SIMDs, with a barrier
+// after every 16 of a wave and the turn through LDS at the end. (One workgroup of 256 keys
+// to a CU: 62 and 554 us where these took 43 and 404.)
 // Keys and values round to the query type here, as a model's own projection leaves
 // them; kept in 32 bits they would be twice the reads of attend() and no operand.
 template <typename T, int L, int N>
@@ -479,10 +480,10 @@ struct Ring {
 //   S^T = K Q^T, O^T += V^T P^T
 // as the other attention kernels have it: a lane holds one row's scores, and its
 // weights are in place as the operand of the second product.
-// Bound by exponentials and products, which the CU's two workgroups trade: a prompt
-// of 4096 rows at 32 heads (172 GFLOP) 191 to 222 us; chunks of 300 to 1100 rows over
-// up to 8300 keys at 64 heads (563 GFLOP) 517 to 546 us, where half of the reads miss
-// an L2. (Tiles of a head side by side, 4, 8, 16 before the next head's: 256, 268, 278
+// Bound by exponentials and products, which the CU's two workgroups trade, half of its
+// busy cycles products: a prompt of 4096 rows at 32 heads (172 GFLOP) 205 us, 840 TFLOP/s;
+// chunks of 300 to 1100 rows over up to 8300 keys at 64 heads (563 GFLOP) 524 us, 1,070,
+// where 31 % of the look-ups in an L2 miss (the prompt: 16 %). (Tiles of a head side by side, 4, 8, 16 before the next head's: 256, 268, 278
 // us instead of 243 for the prompt's whole call, the chunks' 4 % better to 2 % worse.)
 template <typename T, int N>
 __global__ __launch_bounds__(kAttendWaves * kWave, 2) void attend_kernel(LatentPrefillArgs a,
